@@ -58,6 +58,19 @@ cudaError_t launch_attn(const uint16_t*, const uint16_t*, const uint16_t*, int64
                         void*, cudaStream_t);
 size_t attn_workspace_bytes(int64_t nk, int hkv, int d);
 int read_and_clear_attn_error();
+cudaError_t launch_rope(const gdn_rope_table&, const int32_t*, int64_t, int, const uint16_t*, int64_t, int, uint16_t*,
+                        int64_t, const uint16_t*, int64_t, int, uint16_t*, int64_t, cudaStream_t);
+cudaError_t launch_kv_write(const gdn_kv_cache&, const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t,
+                            const int32_t*, const int64_t*, int64_t, cudaStream_t);
+cudaError_t launch_kv_read(const gdn_kv_cache&, const int64_t*, int64_t, uint16_t*, int64_t, uint16_t*, int64_t,
+                           cudaStream_t);
+cudaError_t launch_attn_cache(const gdn_kv_cache&, const uint16_t*, int64_t, const int32_t*, int64_t, int, const uint64_t*,
+                              const int32_t*, int64_t, int, const int32_t*, int, int, float, uint16_t*, int64_t, void*,
+                              cudaStream_t);
+size_t attn_cache_workspace_bytes(const gdn_kv_cache&, int64_t, int);
+int read_and_clear_rope_error();
+int read_and_clear_kv_error();
+int read_and_clear_attn_cache_error();
 int read_and_clear_gemm_error();
 int read_and_clear_delta_error();
 int read_and_clear_q4k_error();
@@ -102,6 +115,34 @@ int cuda_fail(cudaError_t e, const char* what) {
     } while (0)
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int check_cache(const gdn_kv_cache* c, const char* who) {
+    if (!c) return fail(GDN_EINVAL, "%s: cache is NULL", who);
+    if (c->dtype != GDN_KV_BF16 && c->dtype != GDN_KV_I8 && c->dtype != GDN_KV_E4M3)
+        return fail(GDN_EINVAL, "%s: unknown cache dtype %d", who, c->dtype);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 256)
+        return fail(GDN_EINVAL, "%s: 1 <= n_kv_heads <= 256 required (got %d)", who, c->n_kv_heads);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(GDN_EINVAL, "%s: head_dim must be 64, 128 or 256 (got %d)", who, c->head_dim);
+    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+        return fail(GDN_EINVAL, "%s: page_tokens must be 16, 32, 64 or 128 (got %d)", who, c->page_tokens);
+    if (c->n_pages < 1 || c->n_pages > 0x7fffffff / c->n_kv_heads)
+        return fail(GDN_EINVAL, "%s: n_pages >= 1 and n_pages * n_kv_heads < 2^31 required (got %lld)", who,
+                    (long long)c->n_pages);
+    if (!c->k || !c->v) return fail(GDN_EINVAL, "%s: NULL cache pages", who);
+    if (!aligned(c->k, 128) || !aligned(c->v, 128)) return fail(GDN_EINVAL, "%s: cache pages must be 128-byte aligned", who);
+    if (c->dtype == GDN_KV_BF16) {
+        if (c->k_scale || c->v_scale) return fail(GDN_EINVAL, "%s: a bf16 cache has no scales", who);
+    } else {
+        if (!c->k_scale || !c->v_scale) return fail(GDN_EINVAL, "%s: NULL cache scales", who);
+        if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+            return fail(GDN_EINVAL, "%s: cache scales must be 16-byte aligned", who);
+    }
+    return GDN_OK;
+}
+
+// bf16 rows of n_heads * d elements, ld elements apart.
+bool rows_ok(const void* p, int64_t ld, int64_t width) { return p && aligned(p, 2) && ld >= width; }
 
 struct Sizes {
     int64_t H, hk, hv, d, c_qk, c_v, c_conv, n_bf16, r_in;
@@ -948,6 +989,139 @@ int gdn_attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v, in
     return GDN_OK;
 }
 
+int gdn_rope_make(int rot, int layout, double base, int scaling, double factor, int64_t orig_len, double fast, double slow,
+                  double amp, gdn_rope_table* table) {
+    if (!table) return fail(GDN_EINVAL, "gdn_rope_make: table is NULL");
+    if (rot < 2 || rot % 2 || rot > 2 * GDN_ROPE_MAX_PAIRS)
+        return fail(GDN_EINVAL, "gdn_rope_make: rot even in [2, %d] required (got %d)", 2 * GDN_ROPE_MAX_PAIRS, rot);
+    if (layout != GDN_ROPE_HALF && layout != GDN_ROPE_INTERLEAVED)
+        return fail(GDN_EINVAL, "gdn_rope_make: unknown layout %d", layout);
+    if (scaling != GDN_ROPE_PLAIN && scaling != GDN_ROPE_LINEAR && scaling != GDN_ROPE_PARTS)
+        return fail(GDN_EINVAL, "gdn_rope_make: unknown scaling %d", scaling);
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(GDN_EINVAL, "gdn_rope_make: base > 1 required");
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(GDN_EINVAL, "gdn_rope_make: factor >= 1 required");
+    if (!(amp >= 0.0) || !std::isfinite(amp)) return fail(GDN_EINVAL, "gdn_rope_make: amp >= 0 required");
+    if (scaling == GDN_ROPE_PARTS && (orig_len < 1 || !(slow > 0.0) || !(fast > slow) || !std::isfinite(fast)))
+        return fail(GDN_EINVAL, "gdn_rope_make: orig_len >= 1 and 0 < slow < fast required");
+    const double two_pi = 6.283185307179586476925;
+    gdn_rope_table t{};
+    t.rot = rot;
+    t.layout = layout;
+    t.amp = static_cast<float>(amp > 0.0 ? amp : scaling == GDN_ROPE_PARTS ? 0.1 * std::log(factor) + 1.0 : 1.0);
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == GDN_ROPE_LINEAR) f /= factor;
+        if (scaling == GDN_ROPE_PARTS) {
+            const double r = static_cast<double>(orig_len) * f / two_pi;
+            const double g = std::fmin(std::fmax((r - slow) / (fast - slow), 0.0), 1.0);
+            f = g * f + (1.0 - g) * f / factor;
+        }
+        t.step[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));   // f <= 1: below 2^62
+    }
+    *table = t;
+    return GDN_OK;
+}
+
+int gdn_rope(const gdn_rope_table* table, const int32_t* positions, int64_t n_tokens, int head_dim, const uint16_t* q,
+             int64_t ld_q, int n_q_heads, uint16_t* q_out, int64_t ld_qo, const uint16_t* k, int64_t ld_k, int n_k_heads,
+             uint16_t* k_out, int64_t ld_ko, void* stream) {
+    if (!table) return fail(GDN_EINVAL, "gdn_rope: table is NULL");
+    if (table->rot < 2 || table->rot % 2 || table->rot > 2 * GDN_ROPE_MAX_PAIRS ||
+        (table->layout != GDN_ROPE_HALF && table->layout != GDN_ROPE_INTERLEAVED))
+        return fail(GDN_EINVAL, "gdn_rope: the table is not one of gdn_rope_make");
+    if (head_dim < 2 || head_dim % 2 || head_dim > 512 || head_dim < table->rot)
+        return fail(GDN_EINVAL, "gdn_rope: head_dim even in [rot, 512] required (got %d, rot %d)", head_dim, table->rot);
+    if (n_tokens < 0 || n_tokens > 0x7fffffff) return fail(GDN_EINVAL, "gdn_rope: 0 <= n_tokens < 2^31 required");
+    if (n_q_heads < 1 || n_q_heads > 256 || n_k_heads < 0 || n_k_heads > 256)
+        return fail(GDN_EINVAL, "gdn_rope: 1 .. 256 query heads and 0 .. 256 key heads required (got %d, %d)", n_q_heads,
+                    n_k_heads);
+    if (n_tokens == 0) return GDN_OK;
+    if (!positions || !aligned(positions, 4)) return fail(GDN_EINVAL, "gdn_rope: positions");
+    const int64_t wq = static_cast<int64_t>(n_q_heads) * head_dim, wk = static_cast<int64_t>(n_k_heads) * head_dim;
+    if (!rows_ok(q, ld_q, wq) || !rows_ok(q_out, ld_qo, wq) || (q == q_out && ld_q != ld_qo))
+        return fail(GDN_EINVAL, "gdn_rope: q layout");
+    if (n_k_heads && (!rows_ok(k, ld_k, wk) || !rows_ok(k_out, ld_ko, wk) || (k == k_out && ld_k != ld_ko)))
+        return fail(GDN_EINVAL, "gdn_rope: k layout");
+    GDN_LAUNCH(launch_rope(*table, positions, n_tokens, head_dim, q, ld_q, n_q_heads, q_out, ld_qo, k, ld_k, n_k_heads,
+                           k_out, ld_ko, static_cast<cudaStream_t>(stream)),
+               "gdn_rope");
+    return GDN_OK;
+}
+
+int gdn_kv_write(const gdn_kv_cache* cache, const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v,
+                 int64_t n_rows, const int32_t* rows, const int64_t* slots, int64_t n_tokens, void* stream) {
+    int r = check_cache(cache, "gdn_kv_write");
+    if (r) return r;
+    const int64_t w = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+    if (n_tokens < 0 || n_tokens > 0x7fffffff || n_rows < 0 || n_rows > 0x7fffffff)
+        return fail(GDN_EINVAL, "gdn_kv_write: 0 <= n_tokens, n_rows < 2^31 required");
+    if (!rows && n_tokens > n_rows)
+        return fail(GDN_EINVAL, "gdn_kv_write: %lld tokens of %lld rows", (long long)n_tokens, (long long)n_rows);
+    if (n_tokens == 0) return GDN_OK;
+    if (!slots || !aligned(slots, 8) || !aligned(rows, 4)) return fail(GDN_EINVAL, "gdn_kv_write: slots or rows");
+    if (!rows_ok(k, ld_k, w) || !rows_ok(v, ld_v, w)) return fail(GDN_EINVAL, "gdn_kv_write: k or v layout");
+    GDN_LAUNCH(launch_kv_write(*cache, k, ld_k, v, ld_v, n_rows, rows, slots, n_tokens, static_cast<cudaStream_t>(stream)),
+               "gdn_kv_write");
+    return GDN_OK;
+}
+
+int gdn_kv_read(const gdn_kv_cache* cache, const int64_t* slots, int64_t n_tokens, uint16_t* k, int64_t ld_k, uint16_t* v,
+                int64_t ld_v, void* stream) {
+    int r = check_cache(cache, "gdn_kv_read");
+    if (r) return r;
+    const int64_t w = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+    if (n_tokens < 0 || n_tokens > 0x7fffffff) return fail(GDN_EINVAL, "gdn_kv_read: 0 <= n_tokens < 2^31 required");
+    if (n_tokens == 0) return GDN_OK;
+    if (!slots || !aligned(slots, 8)) return fail(GDN_EINVAL, "gdn_kv_read: slots");
+    if (!rows_ok(k, ld_k, w) || !rows_ok(v, ld_v, w)) return fail(GDN_EINVAL, "gdn_kv_read: k or v layout");
+    GDN_LAUNCH(launch_kv_read(*cache, slots, n_tokens, k, ld_k, v, ld_v, static_cast<cudaStream_t>(stream)), "gdn_kv_read");
+    return GDN_OK;
+}
+
+size_t gdn_attn_cache_workspace_size(const gdn_kv_cache* cache, int64_t n_tokens, int n_q_heads) {
+    if (check_cache(cache, "gdn_attn_cache_workspace_size")) return 0;
+    if (n_tokens < 1 || n_tokens > GDN_MAX_SEQS * GDN_MAX_NEW || n_q_heads < 1 || n_q_heads % cache->n_kv_heads ||
+        n_q_heads / cache->n_kv_heads > 16)
+        return 0;
+    return attn_cache_workspace_bytes(*cache, n_tokens, n_q_heads);
+}
+
+int gdn_attn_cache(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, const int32_t* cu_q, int64_t n_tokens,
+                   int max_q, const uint64_t* tree, const int32_t* block_table, int64_t ld_table, int max_blocks,
+                   const int32_t* lens, int n_seqs, int n_q_heads, float scale, uint16_t* o, int64_t ld_o, void* workspace,
+                   size_t ws_bytes, void* stream) {
+    int r = check_cache(cache, "gdn_attn_cache");
+    if (r) return r;
+    if (n_seqs < 1 || n_seqs > GDN_MAX_SEQS)
+        return fail(GDN_EINVAL, "gdn_attn_cache: 1 <= n_seqs <= %d required (got %d)", GDN_MAX_SEQS, n_seqs);
+    if (max_q < 1 || max_q > GDN_MAX_NEW)
+        return fail(GDN_EINVAL, "gdn_attn_cache: 1 <= max_q <= %d required (got %d)", GDN_MAX_NEW, max_q);
+    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 16)
+        return fail(GDN_EINVAL, "gdn_attn_cache: n_q_heads a multiple of n_kv_heads, at most 16 each (got %d, %d)", n_q_heads,
+                    cache->n_kv_heads);
+    if (n_tokens < 0 || n_tokens > static_cast<int64_t>(n_seqs) * max_q || (!cu_q && n_tokens != static_cast<int64_t>(n_seqs) * max_q))
+        return fail(GDN_EINVAL, "gdn_attn_cache: %lld new tokens in %d sequences of at most %d", (long long)n_tokens, n_seqs,
+                    max_q);
+    if (n_tokens == 0) return GDN_OK;
+    const int64_t w = static_cast<int64_t>(n_q_heads) * cache->head_dim;
+    if (!q || !o || !block_table || !lens || !workspace) return fail(GDN_EINVAL, "gdn_attn_cache: NULL pointer");
+    if (ld_q < w || ld_o < w || ld_q % 8 || ld_o % 8 || !aligned(q, 16) || !aligned(o, 16))
+        return fail(GDN_EINVAL, "gdn_attn_cache: q and o rows 16-byte aligned, at least %lld elements apart", (long long)w);
+    if (!aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(tree, 8) || !aligned(workspace, 256))
+        return fail(GDN_EINVAL, "gdn_attn_cache: alignment");
+    if (max_blocks < 1 || max_blocks > 0x7fffffff / cache->page_tokens || ld_table < max_blocks)
+        return fail(GDN_EINVAL, "gdn_attn_cache: 1 <= max_blocks <= ld_table and max_blocks * page_tokens < 2^31 required");
+    if (!std::isfinite(scale)) return fail(GDN_EINVAL, "gdn_attn_cache: scale is not finite");
+    const size_t need = attn_cache_workspace_bytes(*cache, n_tokens, n_q_heads);
+    if (ws_bytes < need) return fail(GDN_ENOMEM, "gdn_attn_cache: workspace %zu B < %zu B", ws_bytes, need);
+    const float sc = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
+    const cudaError_t e = launch_attn_cache(*cache, q, ld_q, cu_q, n_tokens, max_q, tree, block_table, ld_table, max_blocks, lens,
+                                            n_seqs, n_q_heads, sc, o, ld_o, workspace, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorInvalidValue) return fail(GDN_EINVAL, "gdn_attn_cache: tensor map rejected");
+    if (e != cudaSuccess) return cuda_fail(e, "gdn_attn_cache");
+    return GDN_OK;
+}
+
 int gdn_sync_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
@@ -960,16 +1134,22 @@ int gdn_sync_status(void* stream) {
     const int rcode = read_and_clear_decode_error();
     const int ccode = read_and_clear_conv_error();
     const int ncode = read_and_clear_norm_error();
+    const int pcode = read_and_clear_rope_error();
+    const int kcode = read_and_clear_kv_error();
+    const int xcode = read_and_clear_attn_cache_error();
+    if (kcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped");
+    if (xcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_attn_cache: an offset, length or page out of range was skipped");
     const int words[] = {read_and_clear_q4k_error(), read_and_clear_q6k_error(), read_and_clear_quant_error(),
-                         gcode, ccode, dcode, ncode, rcode, acode};
+                         gcode, ccode, dcode, ncode, rcode, acode, pcode};
     const char* units[] = {"Q4_K decode", "Q6_K decode", "activation quantisation", "projection", "conv",
-                           "delta-rule", "gated-norm", "decode-step", "attention"};
+                           "delta-rule", "gated-norm", "decode-step", "attention", "rotary"};
     for (int i = 0; i < static_cast<int>(sizeof(words) / sizeof(words[0])); ++i)
         if (words[i] == ERR_INDEX)
             return fail(GDN_EINDEX, "an index check of the %s kernel failed (the store was skipped; debug library)",
                         units[i]);
     if (gcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the projection kernel ran out");
     if (acode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the attention kernel ran out");
+    if (xcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the cache attention kernel ran out");
     if (ncode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the gated-norm kernel ran out");
     if (dcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the delta-rule kernel ran out");
     if (rcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in a decode-step kernel ran out");

@@ -20,6 +20,11 @@ GDN_W_Q4K, GDN_W_F32 = 0, 1
 GDN_CHUNK = 64
 GDN_MAX_SEQS = 256
 GDN_N_STAGE_EVENTS = 8
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_PARTS = 0, 1, 2
+GDN_ROPE_MAX_PAIRS = 128
+GDN_KV_BF16, GDN_KV_I8, GDN_KV_E4M3 = 0, 1, 2
+GDN_MAX_NEW = 64
 GDN_NOALLOC_SCRATCH_BYTES = 48 << 20
 STAGE_NAMES = ["dequant", "act_quant", "in_proj", "conv", "delta_rule", "gated_norm", "out_proj"]
 
@@ -35,7 +40,20 @@ class GdnLayer(ctypes.Structure):
     ]
 
 
+class GdnRopeTable(ctypes.Structure):
+    """Mirror of ``struct gdn_rope_table``."""
+    _fields_ = [("rot", c_int32), ("layout", c_int32), ("amp", c_float), ("reserved0", c_int32),
+                ("step", ctypes.c_uint64 * GDN_ROPE_MAX_PAIRS)]
+
+
+class GdnKvCache(ctypes.Structure):
+    """Mirror of ``struct gdn_kv_cache``."""
+    _fields_ = [("dtype", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_tokens", c_int32),
+                ("n_pages", c_int64), ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
 _P = c_void_p
+_D = ctypes.c_double
 _SIGNATURES = {
     "q4k_pack": (c_int32, [_P, c_int64, c_int64, _P]),
     "q4k_deq_i8": (c_int32, [_P, c_int64, c_int64, _P, _P, _P]),
@@ -54,6 +72,13 @@ _SIGNATURES = {
     "gdn_prefill_ckpt": (c_int32, [_P, _P, c_int64, _P, _P, _P, _P, c_int64, _P, _P, _P, c_size_t, _P]),
     "gdn_attn_workspace_size": (c_size_t, [c_int64, c_int32, c_int32]),
     "gdn_attn_prefill": (c_int32, [_P, _P, _P, c_int64, c_int64, c_int32, c_int32, c_int32, c_float, _P, _P, c_size_t, _P]),
+    "gdn_rope_make": (c_int32, [c_int32, c_int32, _D, c_int32, _D, c_int64, _D, _D, _D, _P]),
+    "gdn_rope": (c_int32, [_P, _P, c_int64, c_int32, _P, c_int64, c_int32, _P, c_int64, _P, c_int64, c_int32, _P, c_int64, _P]),
+    "gdn_kv_write": (c_int32, [_P, _P, c_int64, _P, c_int64, c_int64, _P, _P, c_int64, _P]),
+    "gdn_kv_read": (c_int32, [_P, _P, c_int64, _P, c_int64, _P, c_int64, _P]),
+    "gdn_attn_cache_workspace_size": (c_size_t, [_P, c_int64, c_int32]),
+    "gdn_attn_cache": (c_int32, [_P, _P, c_int64, _P, c_int64, c_int32, _P, _P, c_int64, c_int32, _P, c_int32, c_int32, c_float, _P,
+                                 c_int64, _P, c_size_t, _P]),
     "gdn_sync_status": (c_int32, [_P]),
     "gdn_last_error": (ctypes.c_char_p, []),
     "gdn_set_stage_events": (c_int32, [ctypes.POINTER(c_void_p), c_int32]),

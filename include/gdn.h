@@ -63,13 +63,26 @@ extern "C" {
 #define GDN_ECUDA (-3)    /* a CUDA call or kernel launch failed */
 #define GDN_ETIMEOUT (-4) /* a bounded device-side wait ran out; the kernel returned early */
 #define GDN_ERANGE (-5)   /* a value beyond the fp16 operand range (|x| > 65504) reached the recurrence */
-#define GDN_EINDEX (-6)   /* debug library only: a kernel's index check failed (the store was skipped) */
+#define GDN_EINDEX (-6)   /* an index held in device memory (a cache slot, row, page or length) was out of range and skipped;
+                             in the debug library also: a kernel's own index check failed (the store was skipped) */
 
 #define GDN_W_Q4K 0 /* weights are GGUF Q4_K superblocks, activations bf16 */
 #define GDN_W_F32 1 /* weights and activations fp32, no quantisation anywhere */
 
 #define GDN_CHUNK 64 /* tokens per chunk of the chunked delta rule */
 #define GDN_MAX_SEQS 256 /* sequences per gdn_prefill_batch or gdn_decode call */
+#define GDN_ROPE_HALF 0        /* pair i is (x[i], x[i + rot/2]) */
+#define GDN_ROPE_INTERLEAVED 1 /* pair i is (x[2i], x[2i + 1]) */
+#define GDN_ROPE_PLAIN 0       /* position scaling: none */
+#define GDN_ROPE_LINEAR 1      /* every frequency divided by the factor */
+#define GDN_ROPE_PARTS 2       /* slow pairs divided by the factor, fast ones kept, a ramp between */
+#define GDN_ROPE_MAX_PAIRS 128 /* pairs of one head: rot <= 256 */
+
+#define GDN_KV_BF16 0 /* cached rows as they came */
+#define GDN_KV_I8 1   /* int8 codes, one fp32 scale per (token, head) row: amax / 127 */
+#define GDN_KV_E4M3 2 /* 8-bit floating point codes, one fp32 scale per row: amax / 448 */
+#define GDN_MAX_NEW 64 /* new tokens of one sequence per gdn_attn_cache call (the bits of a mask word) */
+
 #define GDN_DECODE_GEMV_TOKENS 8 /* tokens per launch of the decode step's fused weight-decode GEMV (dp4a form; the Q4_K tensor-core form takes twice as many) */
 
 /*
@@ -353,11 +366,140 @@ int gdn_attn_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, in
                      void *stream);
 
 /*
+ * Serving the full-attention layers: rotary positions, a paged key/value
+ * cache, and the attention of new tokens over it.  A prompt is rotated
+ * (gdn_rope), attended (gdn_attn_prefill) and stored (gdn_kv_write); each
+ * further step rotates its new tokens, stores them and attends over the cache
+ * (gdn_attn_cache): one token per sequence, a chain, or a tree of drafts, of
+ * which the accepted path is then stored again at its final slots (the `rows`
+ * of gdn_kv_write).  gdn_kv_read gives a held prompt back in the layout of
+ * gdn_attn_prefill, for a prompt that extends it.
+ */
+
+/*
+ * gdn_rope_make -- the rotation table of a rotary embedding (host only, no
+ * GPU).  Pair i < rot/2 turns by the angle pos * f_i with
+ *     f_i = base^(-2i/rot)                       GDN_ROPE_PLAIN
+ *     f_i / factor                               GDN_ROPE_LINEAR
+ *     g f_i + (1 - g) f_i / factor               GDN_ROPE_PARTS
+ * where g = clamp((r - slow) / (fast - slow), 0, 1) and r = orig_len f_i / 2 pi
+ * is the number of turns pair i makes over the original context (the
+ * published "NTK by parts" interpolation, whose usual bounds are slow = 1,
+ * fast = 32).  amp multiplies both outputs; 0 means 1, and for GDN_ROPE_PARTS
+ * the published 0.1 ln(factor) + 1.
+ * step[i] = f_i / 2 pi as a fraction of 2^64, so pos * step[i] mod 2^64 is the
+ * angle in turns, exactly reduced, for any 32-bit position.
+ * rot even, 2 <= rot <= 256; base > 1; factor >= 1; PARTS: orig_len >= 1 and
+ * 0 < slow < fast.
+ */
+typedef struct gdn_rope_table {
+    int32_t rot;    /* rotated leading elements of each head; the rest pass through */
+    int32_t layout; /* GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED */
+    float amp;
+    int32_t reserved0;
+    uint64_t step[GDN_ROPE_MAX_PAIRS];
+} gdn_rope_table;
+int gdn_rope_make(int rot, int layout, double base, int scaling, double factor, int64_t orig_len, double fast,
+                  double slow, double amp, gdn_rope_table *table);
+
+/*
+ * gdn_rope -- rotate the query and key heads of n_tokens tokens in one launch.
+ *   table      HOST, from gdn_rope_make; copied into the launch
+ *   positions  device int32 [n_tokens], any value (negative turns backwards)
+ *   q, q_out   device bf16, head h of token t at t*ld + h*head_dim (ld_q, ld_qo
+ *              elements between tokens); q_out may equal q with the same ld:
+ *              in place, the pass-through elements are then not touched.
+ *              Other overlaps are not allowed.
+ *   k, k_out   as q; n_k_heads = 0 and NULL for queries alone
+ * Angles from the exactly reduced turns, products in fp32, each output rounded
+ * to bf16 once.  head_dim even, 2 .. 512, >= rot; 1 .. 256 heads each.
+ * n_tokens = 0 is allowed and does nothing.
+ */
+int gdn_rope(const gdn_rope_table *table, const int32_t *positions, int64_t n_tokens, int head_dim, const uint16_t *q,
+             int64_t ld_q, int n_q_heads, uint16_t *q_out, int64_t ld_qo, const uint16_t *k, int64_t ld_k,
+             int n_k_heads, uint16_t *k_out, int64_t ld_ko, void *stream);
+
+/*
+ * A paged cache of keys and values.  Token slot s is row s % page_tokens of
+ * page s / page_tokens.  The memory is the caller's.
+ */
+typedef struct gdn_kv_cache {
+    int32_t dtype;       /* GDN_KV_BF16, GDN_KV_I8 or GDN_KV_E4M3 */
+    int32_t n_kv_heads;  /* 1 .. 256 */
+    int32_t head_dim;    /* 64, 128 or 256 */
+    int32_t page_tokens; /* 16, 32, 64 or 128 */
+    int64_t n_pages;     /* >= 1, n_pages * n_kv_heads < 2^31 */
+    void *k, *v;         /* [n_pages][n_kv_heads][page_tokens][head_dim] of 2 or 1 bytes, 128-byte aligned */
+    float *k_scale, *v_scale; /* [n_pages][n_kv_heads][page_tokens], 16-byte aligned; NULL for GDN_KV_BF16 */
+} gdn_kv_cache;
+
+/*
+ * gdn_kv_write -- store the keys and values of n_tokens tokens, quantised on
+ * the way.  Per (token, head) row, in IEEE fp32: scale = amax / 127 (int8) or
+ * amax / 448 (e4m3), code = x / scale rounded to nearest even; a row of zeros
+ * (and a quotient that is not a number) has codes 0.
+ *   k, v    device bf16 [n_rows][n_kv_heads][head_dim], ld_k / ld_v elements
+ *           between rows
+ *   rows    device int32 [n_tokens] or NULL: token t is row rows[t] (NULL: row
+ *           t; n_tokens <= n_rows)
+ *   slots   device int64 [n_tokens]: where token t goes; negative: nowhere.
+ *           Slots given twice hold one of the tokens.
+ * A row outside [0, n_rows) or a slot past the cache is skipped and reported
+ * as GDN_EINDEX by gdn_sync_status.  n_tokens = 0 does nothing.
+ */
+int gdn_kv_write(const gdn_kv_cache *cache, const uint16_t *k, int64_t ld_k, const uint16_t *v, int64_t ld_v,
+                 int64_t n_rows, const int32_t *rows, const int64_t *slots, int64_t n_tokens, void *stream);
+
+/*
+ * gdn_kv_read -- the values the slots hold (code * scale, rounded to bf16
+ * once) as contiguous rows: k, v device bf16 [n_tokens][n_kv_heads][head_dim],
+ * ld_k / ld_v elements between tokens.  A negative slot reads as zeros; a
+ * slot past the cache too, and is reported as GDN_EINDEX.
+ */
+int gdn_kv_read(const gdn_kv_cache *cache, const int64_t *slots, int64_t n_tokens, uint16_t *k, int64_t ld_k,
+                uint16_t *v, int64_t ld_v, void *stream);
+
+/*
+ * gdn_attn_cache -- attention of each sequence's new tokens over its cached
+ * ones.  Sequence s has lens[s] tokens in the cache, the last n_s of them the
+ * new tokens of this call (already written), n_s = cu_q[s+1] - cu_q[s].  For
+ * query head h (key/value head h / (n_q_heads / n_kv_heads)) of new token i:
+ *     o = sum_j softmax_j(scale * q . k_j) v_j
+ * over the lens[s] - n_s earlier tokens and those new tokens j of the sequence
+ * for which bit j of the token's mask word is set (no masks: j <= i).  A token
+ * that sees nothing gets zeros; what it does not see does not enter its
+ * result, whatever the cache holds there.
+ *   q, o         device bf16 [n_tokens][n_q_heads][head_dim], ld_q / ld_o
+ *                elements between tokens (multiples of 8, 16-byte aligned)
+ *   cu_q         device int32 [n_seqs + 1], cu_q[0] = 0, non-decreasing, at
+ *                most max_q apart, cu_q[n_seqs] = n_tokens; NULL: max_q each
+ *   tree         device uint64 [n_tokens] mask words, or NULL
+ *   block_table  device int32 [n_seqs] rows of max_blocks, ld_table apart: the
+ *                page of tokens [b * page_tokens, (b+1) * page_tokens) of
+ *                sequence s
+ *   lens         device int32 [n_seqs], at most max_blocks * page_tokens
+ *   max_q        1 .. GDN_MAX_NEW; n_q_heads / n_kv_heads <= 16
+ *   scale <= 0 means head_dim^-1/2
+ *   workspace    device, 256-byte aligned, ws_bytes >=
+ *                gdn_attn_cache_workspace_size(cache, n_tokens, n_q_heads)
+ * Nothing is read back to the host, so a captured graph may be replayed with
+ * other lengths, pages and masks.  A length out of range is clamped to it, a
+ * sequence whose offsets are out of range is left out, and the tokens of a
+ * page outside the cache count as not seen; each is reported as GDN_EINDEX.  Scores, maxima, sums and the result are fp32 until the one
+ * rounding to bf16.  1 <= n_seqs <= GDN_MAX_SEQS.
+ */
+size_t gdn_attn_cache_workspace_size(const gdn_kv_cache *cache, int64_t n_tokens, int n_q_heads);
+int gdn_attn_cache(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, const int32_t *cu_q, int64_t n_tokens,
+                   int max_q, const uint64_t *tree, const int32_t *block_table, int64_t ld_table, int max_blocks,
+                   const int32_t *lens, int n_seqs, int n_q_heads, float scale, uint16_t *o, int64_t ld_o, void *workspace, size_t ws_bytes,
+                   void *stream);
+
+/*
  * gdn_sync_status -- wait for `stream`, then report (and clear) the device
  * error words the kernels set: GDN_OK, GDN_ETIMEOUT (a bounded wait ran out),
  * GDN_ERANGE (a value beyond the fp16 operand range of the recurrence: the
- * results of that call are not valid) or GDN_ECUDA (a CUDA error from the
- * stream).
+ * results of that call are not valid), GDN_EINDEX (an index that a kernel
+ * skipped) or GDN_ECUDA (a CUDA error from the stream).
  */
 int gdn_sync_status(void *stream);
 
