@@ -121,21 +121,18 @@ class Lib:
             fn = getattr(self.dll, name)
             fn.restype = res
             fn.argtypes = args
+            setattr(self, name, self._bind(name, fn, res is c_int32))   # size queries return sizes, not statuses
 
     def last_error(self) -> str:
         return self.dll.gdn_last_error().decode()
 
-    def _call(self, name, *args, check=True):
-        r = getattr(self.dll, name)(*args)
-        if check and r != GDN_OK:
-            raise GdnError(name, r, self.last_error())
-        return r
-
-    def __getattr__(self, name):
-        if name in _SIGNATURES:
-            status = _SIGNATURES[name][0] is c_int32     # size queries return sizes, not statuses
-            return lambda *a, check=status: self._call(name, *a, check=check)
-        raise AttributeError(name)
+    def _bind(self, name, fn, status):
+        def call(*args, check=status):
+            r = fn(*args)
+            if check and r != GDN_OK:
+                raise GdnError(name, r, self.last_error())
+            return r
+        return call
 
 
 _LIBS = {}
@@ -167,9 +164,10 @@ def ptr(t) -> int:
 
 
 def stream_handle(stream=None) -> int:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 def make_layer_struct(spec, dev: dict, eps_l2=1e-6, eps_rms=1e-6, q_scale=None, gate_log_a=None, gate_b=None) -> GdnLayer:
