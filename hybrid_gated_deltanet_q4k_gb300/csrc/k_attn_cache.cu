@@ -14,12 +14,17 @@
 // others).  A pair that lies in one run is written at once; the others leave
 // (maximum, sum, fp32 accumulator) partials that a second kernel joins.
 //
-// Inside a CTA each of the eight warps walks every eighth tile of 16 keys on
-// its own: its lane 0 copies the tile's keys and values by TMA into the warp's
-// own ring, the warp multiplies them on the tensor cores (m16n8k16) with the
-// scores and probabilities never leaving registers, and keeps its own running
+// Inside a CTA each warp walks every 8th or 16th tile of 16 keys on its own:
+// its lane 0 copies the tile's keys and values by TMA into the warp's own ring,
+// the warp multiplies them on the tensor cores and keeps its own running
 // maximum, sum and accumulator; there is no barrier between warps until the
-// end of a pair, where the eight results are joined in shared memory.
+// end of a pair, where their results are joined in shared memory.  The
+// products are m16n8k16 with the cache as the 16-wide operand and eight rows as
+// the other, S^T = K Q^T and O^T = V^T P^T: one new token of up to eight query
+// heads then takes half the instructions and accumulators of the form with the
+// rows on the wide side, which leaves registers for 16 warps.  The scores never
+// leave registers: a transpose of 8 x 8 tiles (movmatrix) turns them into the
+// second product's operand.
 //
 // 8-bit codes become fp16 in registers (exact), with the row scales kept out
 // of the products: a key's scale multiplies its score, and a value's scale
@@ -43,12 +48,11 @@ namespace gdn {
 
 static __device__ int g_attn_cache_error;
 
-constexpr int AC_WARPS = 8;
-constexpr int AC_THREADS = 32 * AC_WARPS;
 constexpr int AC_TILE = 16;             // keys per tile
-constexpr int AC_BLOCK = AC_WARPS;      // tiles of a block: one per warp
+constexpr int AC_BLOCK = 8;             // tiles of a block
 constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
-constexpr int AC_RING = 128 * 1024;     // bytes of tiles in flight per CTA
+constexpr int AC_RING = 192 * 1024;     // bytes of tiles in flight per CTA
+constexpr int AC_JOIN_THREADS = 256;
 constexpr float AC_MARGIN = 8.0f;
 constexpr float AC_LIFT = 7.0f;         // fp16 probabilities times 2^7
 constexpr float LOG2E = 1.4426950408889634f;
@@ -63,7 +67,7 @@ struct AttCacheArgs {
     const int32_t *cu, *table, *lens;
     const uint64_t* tree;
     int n_seqs, max_q, max_blocks;
-    int runs, ranks;    // runs of tiles, and row tiles of a pair (a CTA per run and rank)
+    int runs, ranks;    // runs of tiles, and row tiles of a pair (a CTA per run and rank of rows)
     float sl2;          // scale * log2(e)
     float* part;        // [runs * ranks][2][rows][D + 2] partials
 };
@@ -90,8 +94,8 @@ __device__ __forceinline__ int64_t ac_blocks(const AcSeq& s) {
     return s.nq == 0 ? 0 : s.len == 0 ? 1 : (static_cast<int64_t>(s.len) + KEYS - 1) / KEYS;
 }
 
-// The blocks before each sequence (of one head): pre[0 .. n_seqs], by all AC_THREADS threads.
-static_assert(GDN_MAX_SEQS <= AC_THREADS, "a thread per sequence");
+// The blocks before each sequence (of one head): pre[0 .. n_seqs], by all threads of a CTA.
+static_assert(GDN_MAX_SEQS <= AC_JOIN_THREADS, "a thread per sequence");
 __device__ __forceinline__ void ac_prefix(const AttCacheArgs& a, int64_t* pre, int64_t* wsum, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int64_t v = t < a.n_seqs ? ac_blocks(ac_seq(a, t, report)) : 0;
@@ -102,7 +106,7 @@ __device__ __forceinline__ void ac_prefix(const AttCacheArgs& a, int64_t* pre, i
     }
     if (lane == 31) wsum[warp] = v;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) v += wsum[w];
+    for (int w = 0; w < min(warp, GDN_MAX_SEQS / 32); ++w) v += wsum[w];
     if (t < a.n_seqs) pre[t + 1] = v;
     if (t == 0) pre[0] = 0;
     __syncthreads();
@@ -159,6 +163,13 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Whole warp: an 8 x 8 matrix of 16-bit values, two of row lane / 4 per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
@@ -172,26 +183,31 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // A row of a tile is cut into slabs of 128 bytes (one of 64 for 8-bit heads of
 // 64), each slab [16 keys][128 bytes] with the TMA's 128-byte (64-byte)
 // swizzle, so that eight keys' 16-byte pieces fall into different banks.
-template <int D, int T, int MT>
+template <int D, int T, int NR>
 struct AcSmem {
     static constexpr int ES = T == GDN_KV_BF16 ? 2 : 1;
     static constexpr int ROW = D * ES;
     static constexpr int SLAB = ROW < 128 ? ROW : 128;      // bytes of a row in one slab
     static constexpr int NSLAB = ROW / SLAB;
     static constexpr int HALF = AC_TILE * ROW;              // the keys, or the values, of a tile
-    static constexpr int ST = AC_RING / AC_WARPS / (2 * HALF);   // tiles in flight per warp
-    static constexpr int ROWS = 16 * MT;
+    // 16 warps where a thread's accumulators are at most 64 registers and a
+    // warp's share of the ring holds a tile and a half
+    static constexpr int WARPS = D * NR <= 256 && NR <= 2 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int NS = AC_RING / WARPS / HALF < 8 ? AC_RING / WARPS / HALF : 8;   // half tiles in flight per warp
+    static constexpr int ROWS = 8 * NR;
     static constexpr int OLD = D + 8;                       // padded rows of the joined accumulators
-    static constexpr int JOIN = AC_WARPS * ROWS * OLD * 4;
-    static constexpr int R0 = 0;                            // ring; the accumulators at the end of a pair
-    static constexpr int S0 = AC_RING > JOIN ? AC_RING : JOIN;   // row scales of the tiles in flight: [warp][stage][2][16]
-    static constexpr int M0 = S0 + AC_WARPS * ST * 2 * AC_TILE * 4;   // maxima and sums: [warp][rows][2]
-    static constexpr int P0 = M0 + AC_WARPS * ROWS * 2 * 4;      // blocks before each sequence
+    static constexpr int R0 = 0;                            // ring [warp][slot]; the accumulators at the end of a pair
+    static constexpr int S0 = AC_RING;                      // row scales of the half tiles: [warp][slot][16]
+    static constexpr int M0 = S0 + WARPS * NS * AC_TILE * 4;     // maxima and sums: [warp][rows][2]
+    static constexpr int P0 = M0 + WARPS * ROWS * 2 * 4;         // blocks before each sequence
     static constexpr int W0 = P0 + (GDN_MAX_SEQS + 2) * 8;
-    static constexpr int F0 = W0 + AC_WARPS * 8;                 // pages in range: [warp][stage]
-    static constexpr int Q0 = (F0 + AC_WARPS * ST * 4 + 15) & ~15;   // q fragments [row tile][step][lane] x 16 bytes
-    static constexpr int B0 = Q0 + MT * (D / 16) * 512;          // mbarriers [warp][stage][keys, values]
-    static constexpr int BYTES = B0 + AC_WARPS * ST * 2 * 8;
+    static constexpr int F0 = W0 + WARPS * 8;                    // pages in range: [warp][slot]
+    static constexpr int X0 = F0 + WARPS * NS * 4;               // score factor of each row
+    static constexpr int Q0 = (X0 + ROWS * 4 + 15) & ~15;        // q fragments [row tile][step][lane] x 8 bytes
+    static constexpr int B0 = Q0 + NR * (D / 16) * 256;          // mbarriers [warp][slot]
+    static constexpr int BYTES = B0 + WARPS * NS * 8;
+    static_assert(WARPS * ROWS * OLD * 4 <= AC_RING, "the joined accumulators fit the ring");
     static_assert(BYTES + 1024 <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -206,12 +222,12 @@ __device__ __forceinline__ uint32_t ac_piece(int r, int c) {
 
 // ------------------------------------------------------------ the kernel
 
-template <int D, int T, int MT>
-__global__ void __launch_bounds__(AC_THREADS, 1)
+// NR tiles of eight rows per CTA.
+template <int D, int T, int NR>
+__global__ void __launch_bounds__(AcSmem<D, T, NR>::THREADS, 1)
 attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ AttCacheArgs a) {
-    using L = AcSmem<D, T, MT>;
-    constexpr int NT = D / 8;             // output column tiles
+    using L = AcSmem<D, T, NR>;
     constexpr int KT = D / 16;            // 16-wide steps of a row
     constexpr bool Q8 = T != GDN_KV_BF16;
     extern __shared__ __align__(1024) unsigned char smb[];
@@ -220,15 +236,16 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     int64_t* pre = reinterpret_cast<int64_t*>(base + L::P0);
     float* join = reinterpret_cast<float*>(base + L::R0);
     float2* ml = reinterpret_cast<float2*>(base + L::M0);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::B0) + warp * L::ST * 2;
-    unsigned char* ring = base + L::R0 + warp * L::ST * 2 * L::HALF;
-    float* scales = reinterpret_cast<float*>(base + L::S0) + warp * L::ST * 2 * AC_TILE;
-    int* page_in = reinterpret_cast<int*>(base + L::F0) + warp * L::ST;
-    uint4* qsm = reinterpret_cast<uint4*>(base + L::Q0);
+    float* row_factor = reinterpret_cast<float*>(base + L::X0);
+    uint2* qsm = reinterpret_cast<uint2*>(base + L::Q0);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::B0) + warp * L::NS;
+    unsigned char* ring = base + L::R0 + warp * L::NS * L::HALF;
+    float* scales = reinterpret_cast<float*>(base + L::S0) + warp * L::NS * AC_TILE;
+    int* page_in = reinterpret_cast<int*>(base + L::F0) + warp * L::NS;
 
     pdl_trigger();
     if (lane == 0) {
-        for (int i = 0; i < L::ST * 2; ++i) mbar_init_cta(bars + i, 1);
+        for (int i = 0; i < L::NS; ++i) mbar_init_cta(bars + i, 1);
         mbar_init_fence();
     }
     const int run = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
@@ -244,8 +261,14 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const int mid = (s + hi + 1) >> 1;
         if (pre[mid] * a.heads <= at) s = mid; else hi = mid - 1;
     }
-    uint32_t uses = 0;          // tiles this warp has taken: stage uses % ST, phase uses / ST
+    int slot = 0;               // the next half tile of this warp's ring and its phase
+    uint32_t par = 0;
     bool dead = false;          // a wait ran out
+
+    // the lanes' rows of the ldmatrix operands: keys (lane & 7) + 8 ((lane >> 3) & 1), piece + (lane >> 4);
+    // bf16 values swap the two
+    const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+    const int vr = Q8 ? kr : (lane & 7) + ((lane >> 4) << 3), vc = Q8 ? kc : (lane >> 3) & 1;
 
     while (at < end) {
         while (pre[s + 1] * a.heads <= at) ++s;
@@ -262,290 +285,245 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const int ctx = q.len - q.nq;      // keys every row sees
         const int32_t* table = a.table + s * a.ld_table;
 
-        // ---- copies: tile u of the piece goes to stage uses % ST
-        const int mine = t1 - t0 - warp > 0 ? (t1 - t0 - warp + AC_WARPS - 1) / AC_WARPS : 0;   // tiles of this warp
+        // ---- copies: half tile j (keys of tile j / 2, then its values) follows j - NS in its slot
+        const int mine = t1 - t0 - warp > 0 ? (t1 - t0 - warp + L::WARPS - 1) / L::WARPS : 0;   // tiles of this warp
         auto page_of = [&](int i) {
-            return table[min(((t0 + warp + i * AC_WARPS) * AC_TILE) >> a.page_shift, a.max_blocks - 1)];
+            return table[min(((t0 + warp + i * L::WARPS) * AC_TILE) >> a.page_shift, a.max_blocks - 1)];
         };
-        auto issue = [&](int i, int page, int half) {   // lane 0
-            const int tile = t0 + warp + i * AC_WARPS, st = static_cast<int>((uses + i) % L::ST);
-            const int row = (tile * AC_TILE) & (a.page - 1);
-            const bool in = page >= 0 && page < a.n_pages;
-            const int p = in ? page : 0;                // an unseen page: any rows, all of them masked
-            page_in[st] = in;
-            uint64_t* bar = bars + st * 2 + half;
-            mbar_expect_tx(bar, L::HALF + (Q8 ? AC_TILE * 4 : 0));
-            tma_load_4d(ring + (st * 2 + half) * L::HALF, half ? &mv : &mk, bar, 0, row, 0, p * a.heads + head);
+        auto issue = [&](int j, int sl, int page) {   // lane 0
+            const int row = ((t0 + warp + (j >> 1) * L::WARPS) * AC_TILE) & (a.page - 1);
+            const bool in = page >= 0 && page < a.n_pages, val = j & 1;
+            const int pair = (in ? page : 0) * a.heads + head;   // an unseen page: any rows, all of them masked
+            page_in[sl] = in;
+            mbar_expect_tx(bars + sl, L::HALF + (Q8 ? AC_TILE * 4 : 0));
+            tma_load_4d(ring + sl * L::HALF, val ? &mv : &mk, bars + sl, 0, row, 0, pair);
             if constexpr (Q8)
-                bulk_load_1d(scales + (st * 2 + half) * AC_TILE,
-                             (half ? a.sv : a.sk) + (static_cast<int64_t>(p) * a.heads + head) * a.page + row, AC_TILE * 4, bar);
+                bulk_load_1d(scales + sl * AC_TILE, (val ? a.sv : a.sk) + static_cast<int64_t>(pair) * a.page + row,
+                             AC_TILE * 4, bars + sl);
         };
         if (lane == 0 && !dead) {
-            for (int i = 0; i < L::ST && i < mine; ++i) {
-                const int p = page_of(i);
-                issue(i, p, 0);
-                issue(i, p, 1);
+            int sl = slot;
+            for (int j = 0; j < L::NS && j < 2 * mine; ++j) {
+                issue(j, sl, page_of(j >> 1));
+                sl = sl + 1 == L::NS ? 0 : sl + 1;
             }
         }
-        int page_next = L::ST < mine ? page_of(L::ST) : 0;   // read one tile ahead of its copies
+        // pages of the tiles whose keys (a) and values (b) the next two free slots take
+        int page_a = page_of(min(L::NS / 2, max(mine - 1, 0))), page_b = page_of(min((L::NS + 1) / 2, max(mine - 1, 0)));
 
-        // ---- q fragments: rows 16 mt + g and + 8, the same for every warp, in
-        // shared memory (in registers they would spill).  The d elements a
-        // thread holds at step kt are those its key fragments hold.
-        float qs[MT][2];
-        uint64_t seen[MT][2];
+        // ---- q fragments: row 8 nr + g, the same for every warp, in shared
+        // memory.  The d elements a thread holds at step kt are those its key
+        // fragments hold.
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            uint32_t qf[KT][4];
+        for (int nr = 0; nr < NR; ++nr) {
+            const int r = 8 * nr + g, rr = row0 + r, i = rr / a.ratio;
+            const bool on = r < rows;
+            const uint16_t* src = a.q + static_cast<int64_t>(q.tok + (on ? i : 0)) * a.ld_q +
+                                  (head * a.ratio + (on ? rr - i * a.ratio : 0)) * D;
+            if constexpr (!Q8) {
+                for (int kt = warp; kt < KT; kt += L::WARPS)
+                    qsm[(nr * KT + kt) * 32 + lane] =
+                        on ? make_uint2(*reinterpret_cast<const uint32_t*>(src + 16 * kt + 2 * t),
+                                        *reinterpret_cast<const uint32_t*>(src + 16 * kt + 8 + 2 * t))
+                           : make_uint2(0u, 0u);
+                if (warp == 0 && t == 0) row_factor[r] = a.sl2;
+            } else {
+                float amax = 0.0f;
+                uint2 w[KT];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int r = 16 * mt + 8 * hh + g, rr = row0 + r, i = rr / a.ratio;
-                const bool on = r < rows;
-                const uint16_t* src = a.q + static_cast<int64_t>(q.tok + (on ? i : 0)) * a.ld_q +
-                                      (head * a.ratio + (on ? rr - i * a.ratio : 0)) * D;
-                seen[mt][hh] = !on ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
-                if constexpr (!Q8) {
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        qf[kt][hh] = on ? *reinterpret_cast<const uint32_t*>(src + 16 * kt + 2 * t) : 0u;
-                        qf[kt][2 + hh] = on ? *reinterpret_cast<const uint32_t*>(src + 16 * kt + 8 + 2 * t) : 0u;
-                    }
-                    qs[mt][hh] = a.sl2;
-                } else {
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        const uint2 w = on ? *reinterpret_cast<const uint2*>(src + 16 * kt + 4 * t) : make_uint2(0u, 0u);
-                        qf[kt][hh] = w.x;
-                        qf[kt][2 + hh] = w.y;
-                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
-                                                 fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
-                    }
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    // 2^e with amax 2^e in [2^14, 2^15): exact both ways within the exponents that keep 2^e finite
-                    const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
-                    qs[mt][hh] = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const uint32_t w = qf[kt][e + hh];
-                            qf[kt][e + hh] = f16x2_bits(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                        }
+                for (int kt = 0; kt < KT; ++kt) {
+                    w[kt] = on ? *reinterpret_cast<const uint2*>(src + 16 * kt + 4 * t) : make_uint2(0u, 0u);
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[kt].x << 16)), fabsf(__uint_as_float(w[kt].x & 0xffff0000u))),
+                                             fmaxf(fabsf(__uint_as_float(w[kt].y << 16)), fabsf(__uint_as_float(w[kt].y & 0xffff0000u)))));
                 }
-            }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^e with amax 2^e in [2^14, 2^15): exact both ways within the exponents that keep 2^e finite
+                const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+                if (warp == 0 && t == 0) row_factor[r] = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                if (kt % AC_WARPS == warp)
-                    qsm[(mt * KT + kt) * 32 + lane] = make_uint4(qf[kt][0], qf[kt][1], qf[kt][2], qf[kt][3]);
+                for (int kt = 0; kt < KT; ++kt)
+                    if (kt % L::WARPS == warp)
+                        qsm[(nr * KT + kt) * 32 + lane] =
+                            make_uint2(f16x2_bits(__uint_as_float(w[kt].x << 16) * up, __uint_as_float(w[kt].x & 0xffff0000u) * up),
+                                       f16x2_bits(__uint_as_float(w[kt].y << 16) * up, __uint_as_float(w[kt].y & 0xffff0000u) * up));
+            }
         }
         __syncthreads();
 
-        float o[MT][NT][4], m[MT][2], l[MT][2];
+        // ---- this thread's rows of the scores: 8 nr + 2t and + 1
+        float qs[NR][2], m[NR][2], l[NR][2], o[NR][KT][4];
+        uint64_t seen[NR][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.0f;
+        for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nr + 2 * t + e, i = (row0 + r) / a.ratio;
+                qs[nr][e] = row_factor[r];
+                seen[nr][e] = r >= rows ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
+                m[nr][e] = -INFINITY;
+                l[nr][e] = 0.0f;
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+            for (int c = 0; c < KT; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nr][c][e] = 0.0f;
         }
 
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
-            const int st = static_cast<int>((uses + i) % L::ST);
-            const uint32_t par = ((uses + i) / L::ST) & 1;
-            const int key0 = (t0 + warp + i * AC_WARPS) * AC_TILE;
+            const int key0 = (t0 + warp + i * L::WARPS) * AC_TILE;
             int lim = q.len - key0;   // keys of this tile below `lim` exist
-            const uint32_t kb = smem_addr(ring + st * 2 * L::HALF), vb = kb + L::HALF;
+            const uint32_t kb = smem_addr(ring + slot * L::HALF);
 
-            if (!dead && !mbar_wait_bounded(bars + st * 2, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
+            if (!dead && !mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
-            if (!page_in[st]) {
+            if (!page_in[slot]) {
                 if (lane == 0 && lim > 0) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
                 lim = 0;
             }
             const bool edge = key0 + AC_TILE > ctx || lim < AC_TILE;   // some row may not see some key
 
-            // ---- scores
-            auto qfrag = [&](int mt, int kt, uint32_t (&f)[4]) {
-                const uint4 w = qsm[(mt * KT + kt) * 32 + lane];
-                f[0] = w.x;
-                f[1] = w.y;
-                f[2] = w.z;
-                f[3] = w.w;
-            };
-            float sc[MT][2][4];
+            // ---- scores of keys g and g + 8 for this thread's rows
+            float sc[NR][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) sc[nr][e] = 0.0f;
             if constexpr (!Q8) {
-                // matrices: keys 0-7 and 8-15, each by the two 8-wide halves of the step
-                const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
-                    uint32_t b[4];
-                    ldsm_x4(kb + ac_piece<L>(kr, 2 * kt + kc), b);
+                    uint32_t f[4];
+                    ldsm_x4(kb + ac_piece<L>(kr, 2 * kt + kc), f);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        uint32_t f[4];
-                        qfrag(mt, kt, f);
-                        mma16816<T>(sc[mt][0], f, b[0], b[1]);
-                        mma16816<T>(sc[mt][1], f, b[2], b[3]);
+                    for (int nr = 0; nr < NR; ++nr) {
+                        const uint2 b = qsm[(nr * KT + kt) * 32 + lane];
+                        mma16816<T>(sc[nr], f, b.x, b.y);
                     }
                 }
             } else {
-                // matrices: keys 0-7 and 8-15 of 16 codes, then of the next 16; a thread gets codes 4t .. 4t+3
-                const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+                // 16 codes of eight keys per register set: a thread gets codes 4t .. 4t+3 of key g
 #pragma unroll
                 for (int kt = 0; kt < KT; kt += 2) {
-                    uint32_t b[4];
-                    ldsm_x4(kb + ac_piece<L>(kr, kt + kc), b);
+                    uint32_t w[4];
+                    ldsm_x4(kb + ac_piece<L>(kr, kt + kc), w);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        uint32_t k0[2], k1[2];
+                        const uint32_t x = T == GDN_KV_I8 ? w[2 * u] ^ 0x80808080u : w[2 * u];
+                        const uint32_t y = T == GDN_KV_I8 ? w[2 * u + 1] ^ 0x80808080u : w[2 * u + 1];
+                        const uint32_t f[4] = {codes_f16<T, 0, 1>(x), codes_f16<T, 0, 1>(y), codes_f16<T, 2, 3>(x),
+                                               codes_f16<T, 2, 3>(y)};
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const uint32_t w = T == GDN_KV_I8 ? b[2 * u + n] ^ 0x80808080u : b[2 * u + n];
-                            k0[n] = codes_f16<T, 0, 1>(w);
-                            k1[n] = codes_f16<T, 2, 3>(w);
-                        }
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t f[4];
-                            qfrag(mt, kt + u, f);
-                            mma16816<T>(sc[mt][0], f, k0[0], k1[0]);
-                            mma16816<T>(sc[mt][1], f, k0[1], k1[1]);
+                        for (int nr = 0; nr < NR; ++nr) {
+                            const uint2 b = qsm[(nr * KT + kt + u) * 32 + lane];
+                            mma16816<T>(sc[nr], f, b.x, b.y);
                         }
                     }
                 }
             }
-            // scores to units of log 2; keys 2t, 2t+1, 8+2t, 9+2t of this thread
-            float kv[2][2], lv[2][2];
+            float kv[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
             if constexpr (Q8) {
-                const float* ks = scales + st * 2 * AC_TILE;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 x = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * t);
-                    kv[n][0] = x.x;
-                    kv[n][1] = x.y;
-                }
+                kv[0] = scales[slot * AC_TILE + g];
+                kv[1] = scales[slot * AC_TILE + 8 + g];
             }
             __syncwarp();
-            const bool more = i + L::ST < mine;
-            if (lane == 0 && more) issue(i + L::ST, page_next, 0);
+            if (lane == 0 && 2 * i + L::NS < 2 * mine) issue(2 * i + L::NS, slot, page_a);
+            if (++slot == L::NS) {
+                slot = 0;
+                par ^= 1;
+            }
+            const uint32_t vb = smem_addr(ring + slot * L::HALF);
 
-            if (!mbar_wait_bounded(bars + st * 2 + 1, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
+            if (!mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             if constexpr (Q8) {
-                const float* vs = scales + (st * 2 + 1) * AC_TILE;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 x = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * t);
-                    // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
-                    lv[n][0] = lg2(fmaxf_nan(x.x, 7.7e-34f));
-                    lv[n][1] = lg2(fmaxf_nan(x.y, 7.7e-34f));
-                }
+                // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
+                lv[0] = lg2(fmaxf_nan(scales[slot * AC_TILE + g], 7.7e-34f));
+                lv[1] = lg2(fmaxf_nan(scales[slot * AC_TILE + 8 + g], 7.7e-34f));
             }
 
-            // ---- softmax of the tile
-            uint32_t pf[MT][4];
+            // ---- softmax of the tile: x in units of log 2, y with the value's scale
+            bool up = false;
+            float y[NR][4];
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = sc[nr][e] * qs[nr][e & 1];
+                    if constexpr (Q8) x *= kv[e >> 1];
+                    y[nr][e] = Q8 ? x + lv[e >> 1] : x;
+                    if (edge) {
+                        const int j = 8 * (e >> 1) + g, d = key0 + j - ctx;
+                        if (j >= lim || (d >= 0 && !((seen[nr][e & 1] >> (d & 63)) & 1))) x = y[nr][e] = -INFINITY;
+                    }
+                    sc[nr][e] = x;
+                    up |= y[nr][e] > m[nr][e & 1] + AC_MARGIN;   // from a maximum of -inf: any finite score
+                }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float bm = fmaxf(y[nr][e], y[nr][2 + e]);
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+                        const float old = m[nr][e], mn = fmaxf(old, bm);
+                        const float c = old == -INFINITY ? 0.0f : ex2_ftz(old - mn);
+                        m[nr][e] = mn;
+                        l[nr][e] *= c;
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) {
+                            o[nr][k][e] *= c;
+                            o[nr][k][2 + e] *= c;
+                        }
+                    }
+            }
+            uint32_t pf[NR][2];      // probabilities of (key g, rows 2t, 2t+1) and (key g + 8, ..)
+            float pk[NR][4];
             bool faint = false;      // an fp16 probability that lost bits
-            float pk[MT][2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = sc[mt][n][e] * qs[mt][e >> 1];
-                        if constexpr (Q8) x *= kv[n][e & 1];
-                        if (edge) {
-                            const int j = 8 * n + 2 * t + (e & 1), d = key0 + j - ctx;
-                            if (j >= lim || (d >= 0 && !((seen[mt][e >> 1] >> (d & 63)) & 1))) x = -INFINITY;
-                        }
-                        sc[mt][n][e] = x;
-                    }
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    float y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = sc[mt][e >> 1][2 * hh + (e & 1)];
-                        y[e] = x;
-                        if constexpr (Q8)
-                            if (x != -INFINITY) y[e] = x + lv[e >> 1][e & 1];
-                    }
-                    float bm = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                    const float old = m[mt][hh];
-                    const bool up = bm > old + AC_MARGIN || (old == -INFINITY && bm > old);
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float mn = up ? bm : old, c = old == -INFINITY ? 0.0f : ex2_ftz(old - mn);
-                        m[mt][hh] = mn;
-                        l[mt][hh] *= c;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            o[mt][n][2 * hh] *= c;
-                            o[mt][n][2 * hh + 1] *= c;
-                        }
-                    }
-                    const float mm = m[mt][hh] == -INFINITY ? 0.0f : m[mt][hh];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = sc[mt][e >> 1][2 * hh + (e & 1)];
-                        if constexpr (Q8) {
-                            const float p = ex2_ftz(y[e] - mm + AC_LIFT);
-                            pk[mt][e >> 1][2 * hh + (e & 1)] = p;
-                            faint |= p != 0.0f && p < 6.1035156e-5f;
-                            l[mt][hh] += ex2_ftz(x - mm + AC_LIFT);
-                        } else {
-                            pk[mt][e >> 1][2 * hh + (e & 1)] = ex2_ftz(y[e] - mm);
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : m[nr][e & 1];
+                    if constexpr (Q8) {
+                        const float p = ex2_ftz(y[nr][e] - mm + AC_LIFT);
+                        pk[nr][e] = p;
+                        faint |= p != 0.0f && p < 6.1035156e-5f;
+                        l[nr][e & 1] += ex2_ftz(sc[nr][e] - mm + AC_LIFT);
+                    } else {
+                        pk[nr][e] = ex2_ftz(y[nr][e] - mm);
                     }
                 }
-                // the first product's accumulators are the second one's A fragments
-                if constexpr (Q8) {
-                    pf[mt][0] = f16x2_bits(pk[mt][0][0], pk[mt][0][1]);
-                    pf[mt][1] = f16x2_bits(pk[mt][0][2], pk[mt][0][3]);
-                    pf[mt][2] = f16x2_bits(pk[mt][1][0], pk[mt][1][1]);
-                    pf[mt][3] = f16x2_bits(pk[mt][1][2], pk[mt][1][3]);
-                } else {
-                    pf[mt][0] = bf16x2(pk[mt][0][0], pk[mt][0][1]);
-                    pf[mt][1] = bf16x2(pk[mt][0][2], pk[mt][0][3]);
-                    pf[mt][2] = bf16x2(pk[mt][1][0], pk[mt][1][1]);
-                    pf[mt][3] = bf16x2(pk[mt][1][2], pk[mt][1][3]);
-                    // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        l[mt][e & 1] += __uint_as_float(pf[mt][e] << 16) + __uint_as_float(pf[mt][e] & 0xffff0000u);
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (Q8) {
+                        pf[nr][h] = f16x2_bits(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                    } else {
+                        pf[nr][h] = bf16x2(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                        // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
+                        l[nr][0] += __uint_as_float(pf[nr][h] << 16);
+                        l[nr][1] += __uint_as_float(pf[nr][h] & 0xffff0000u);
+                    }
                 }
             }
 
-            // ---- values: column tiles 2c and 2c+1 of each 16 columns
-            const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
-            constexpr int STEP = Q8 ? 4 : 2;     // column tiles per ldmatrix
+            // ---- values
             uint32_t odd = 0;                    // a value that is not finite at the edge
-            uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys exist
+            uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys (2t, 2t+1; + 8) exist
             if (edge) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    km[n] = (8 * n + 2 * t < lim ? 0xffffu : 0u) | (8 * n + 2 * t + 1 < lim ? 0xffff0000u : 0u);
+                for (int h = 0; h < 2; ++h)
+                    km[h] = (8 * h + 2 * t < lim ? 0xffffu : 0u) | (8 * h + 2 * t + 1 < lim ? 0xffff0000u : 0u);
             }
-            // fragment register of keys 2t, 2t+1 (n = 0) or 8+2t, 9+2t: what does not exist, and
-            // what is not finite (its rows see it below), is taken as zero
-            auto clean = [&](uint32_t w, int n) {
+            // what does not exist, and what is not finite (its rows see it below), is taken as zero
+            auto clean = [&](uint32_t w, int h) {
                 constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
-                w &= km[n];
+                w &= km[h];
                 if (T != GDN_KV_I8) {
                     if ((w & EXP) == EXP) {
                         w &= 0xffff0000u;
@@ -558,137 +536,146 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 }
                 return w;
             };
-            auto values = [&](int n, uint32_t (&f)[STEP][2]) {   // fragments of column tiles n .. n + STEP - 1
-                uint32_t b[4];
-                ldsm_x4_trans(vb + ac_piece<L>(vr, (Q8 ? n / 2 : n) + vc), b);
+            // fragments of columns 16c .. 16c + 15 (8-bit: and of the next 16)
+            constexpr int STEP = Q8 ? 2 : 1;
+            auto values = [&](int c, uint32_t (&f)[STEP][4]) {
+                uint32_t w[4];
+                ldsm_x4_trans(vb + ac_piece<L>(vr, (Q8 ? c : 2 * c) + vc), w);
                 if constexpr (Q8) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t w = T == GDN_KV_I8 ? b[u] ^ 0x80808080u : b[u];
-                        f[(u >> 1) * 2][u & 1] = codes_f16<T, 0, 2>(w);
-                        f[(u >> 1) * 2 + 1][u & 1] = codes_f16<T, 1, 3>(w);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t x = T == GDN_KV_I8 ? w[2 * u] ^ 0x80808080u : w[2 * u];
+                        const uint32_t z = T == GDN_KV_I8 ? w[2 * u + 1] ^ 0x80808080u : w[2 * u + 1];
+                        f[u][0] = codes_f16<T, 0, 2>(x);     // columns 2g of keys 0-7, 2g + 1, then keys 8-15
+                        f[u][1] = codes_f16<T, 1, 3>(x);
+                        f[u][2] = codes_f16<T, 0, 2>(z);
+                        f[u][3] = codes_f16<T, 1, 3>(z);
                     }
                 } else {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) f[u >> 1][u & 1] = b[u];
+                    for (int u = 0; u < 4; ++u) f[0][u] = w[u];
                 }
                 if (edge) {
 #pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        f[u][0] = clean(f[u][0], 0);
-                        f[u][1] = clean(f[u][1], 1);
-                    }
+                    for (int u = 0; u < STEP; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[u][e] = clean(f[u][e], e >> 1);
                 }
             };
+            // the second product's operand: (keys 2t, 2t+1; row g)
+            uint32_t pt[NR][2];
 #pragma unroll
-            for (int n = 0; n < NT; n += STEP) {
-                uint32_t f[STEP][2];
-                values(n, f);
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
+#pragma unroll
+            for (int c = 0; c < KT; c += STEP) {
+                uint32_t f[STEP][4];
+                values(c, f);
 #pragma unroll
                 for (int u = 0; u < STEP; ++u)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma16816<T>(o[mt][n + u], pf[mt], f[u][0], f[u][1]);
+                    for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
             }
             if constexpr (Q8) {
                 if (__any_sync(0xffffffffu, faint)) {
-                    uint32_t rf[MT][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[mt][e]));
-                            const float* p = &pk[mt][e >> 1][2 * (e & 1)];
-                            rf[mt][e] = bf16x2(p[0] - r.x, p[1] - r.y);
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[nr][h]));
+                            pt[nr][h] = transpose8(bf16x2(pk[nr][2 * h] - r.x, pk[nr][2 * h + 1] - r.y));
                         }
 #pragma unroll
-                    for (int n = 0; n < NT; n += STEP) {
-                        uint32_t f[STEP][2];
-                        values(n, f);
+                    for (int c = 0; c < KT; c += STEP) {
+                        uint32_t f[STEP][4];
+                        values(c, f);
 #pragma unroll
                         for (int u = 0; u < STEP; ++u) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&f[u][e]));
-                                f[u][e] = bf16x2(c.x, c.y);
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[u][e]));
+                                f[u][e] = bf16x2(v.x, v.y);
                             }
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) mma16816<GDN_KV_BF16>(o[mt][n + u], rf[mt], f[u][0], f[u][1]);
+                            for (int nr = 0; nr < NR; ++nr) mma16816<GDN_KV_BF16>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
                         }
                     }
                 }
             }
             if (T != GDN_KV_I8 && edge && __any_sync(0xffffffffu, odd)) {
                 // rows that see such a key add its term by themselves
-                const unsigned char* vt = ring + (st * 2 + 1) * L::HALF;
+                const unsigned char* vt = ring + slot * L::HALF;
 #pragma unroll 1
                 for (int j = 0; j < min(lim, AC_TILE); ++j) {
-                    const int d = key0 + j - ctx, src = (lane & ~3) | ((j & 7) >> 1);
+                    const int d = key0 + j - ctx, src = ((j & 7) << 2) | t;
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const float p0 = __shfl_sync(0xffffffffu, j < 8 ? pk[mt][0][2 * hh] : pk[mt][1][2 * hh], src);
-                            const float p1 = __shfl_sync(0xffffffffu, j < 8 ? pk[mt][0][2 * hh + 1] : pk[mt][1][2 * hh + 1], src);
-                            const bool see = d < 0 || ((seen[mt][hh] >> (d & 63)) & 1);
-                            if (!see) continue;
+                        for (int e = 0; e < 2; ++e) {
+                            const float p = __shfl_sync(0xffffffffu, j < 8 ? pk[nr][e] : pk[nr][2 + e], src);
+                            if (d >= 0 && !((seen[nr][e] >> (d & 63)) & 1)) continue;
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                            for (int c = 0; c < KT; ++c)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
+                                for (int h = 0; h < 2; ++h) {
+                                    const int col = 16 * c + (Q8 ? 2 * g + h : 8 * h + g);
                                     float v;
-                                    if constexpr (Q8) {
-                                        const int col = 16 * (n >> 1) + 4 * t + 2 * e + (n & 1);
+                                    if constexpr (Q8)
                                         v = __half2float(__half(__nv_cvt_fp8_to_halfraw(vt[ac_piece<L>(j, col >> 4) + (col & 15)], __NV_E4M3)));
-                                    } else {
-                                        const int col = 8 * n + 2 * t + e;
+                                    else
                                         v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + ac_piece<L>(j, col >> 3) + 2 * (col & 7)));
-                                    }
-                                    if (!(fabsf(v) < INFINITY)) o[mt][n][2 * hh + e] += (j & 1 ? p1 : p0) * v;
+                                    if (!(fabsf(v) < INFINITY)) o[nr][c][2 * h + e] += p * v;
                                 }
                         }
                 }
             }
             __syncwarp();
-            if (lane == 0 && more) issue(i + L::ST, page_next, 1);
-            if (i + L::ST + 1 < mine) page_next = page_of(i + L::ST + 1);
+            if (lane == 0 && 2 * i + 1 + L::NS < 2 * mine) issue(2 * i + 1 + L::NS, slot, page_b);
+            if (++slot == L::NS) {
+                slot = 0;
+                par ^= 1;
+            }
+            const int next = page_of(min(i + 1 + (L::NS + 1) / 2, mine - 1));
+            page_a = L::NS % 2 ? page_b : next;
+            page_b = next;
         }
-        uses += mine;
 
         // ---- join the warps
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                l[mt][hh] += __shfl_xor_sync(0xffffffffu, l[mt][hh], 1);
-                l[mt][hh] += __shfl_xor_sync(0xffffffffu, l[mt][hh], 2);
-                if (t == 0) ml[warp * L::ROWS + 16 * mt + 8 * hh + g] = make_float2(m[mt][hh], l[mt][hh]);
+            for (int e = 0; e < 2; ++e) {
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 4);
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
+                if (g == 0) ml[warp * L::ROWS + 8 * nr + 2 * t + e] = make_float2(m[nr][e], l[nr][e]);
             }
         __syncthreads();   // every warp is done with its ring
-        const int live = min(t1 - t0, AC_WARPS);
+        const int live = min(t1 - t0, L::WARPS);
         if (warp < live) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int r = 16 * mt + 8 * hh + g;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nr + 2 * t + e;
                     if (r >= rows) continue;
                     float* dst = join + (warp * L::ROWS + r) * L::OLD;
-                    if constexpr (Q8) {
 #pragma unroll
-                        for (int n = 0; n < NT; n += 2)
-                            *reinterpret_cast<float4*>(dst + 8 * n + 4 * t) =
-                                make_float4(o[mt][n][2 * hh], o[mt][n + 1][2 * hh], o[mt][n][2 * hh + 1], o[mt][n + 1][2 * hh + 1]);
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[mt][n][2 * hh], o[mt][n][2 * hh + 1]);
+                    for (int c = 0; c < KT; ++c) {
+                        if constexpr (Q8) {
+                            *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[nr][c][e], o[nr][c][2 + e]);
+                        } else {
+                            dst[16 * c + g] = o[nr][c][e];
+                            dst[16 * c + 8 + g] = o[nr][c][2 + e];
+                        }
                     }
                 }
         }
         __syncthreads();
         const bool whole = b0 == 0 && b1 == blocks;
         float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (b0 > 0 ? 0 : 1)) * L::ROWS * (D + 2);
-        for (int e = tid; e < rows * (D / 2); e += AC_THREADS) {
+        for (int e = tid; e < rows * (D / 2); e += L::THREADS) {
             const int r = e / (D / 2), c = (e % (D / 2)) * 2;
             float mx = -INFINITY;
             for (int w = 0; w < live; ++w) mx = fmaxf_nan(mx, ml[w * L::ROWS + r].x);
@@ -718,16 +705,21 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     }
     if (dead) {
         // a wait ran out: let copies already issued land (bounded) before the shared memory is released
-        for (int i = 0; i < L::ST * 2; ++i)
-            for (uint32_t par = 0; par < 2; ++par) mbar_wait_bounded(bars + i, par, nullptr, 0, 20000000ull);
+        for (int i = 0; i < L::NS; ++i)
+            for (uint32_t p = 0; p < 2; ++p) mbar_wait_bounded(bars + i, p, nullptr, 0, 20000000ull);
     }
 }
 
-// Joins the partials of the pairs that lie in more than one run.  D/4 threads
-// per row, a block for 1024/D rows of one pair.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(AC_THREADS) attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a) {
-    __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[AC_WARPS];
+// Joins the partials of the pairs that lie in more than one run: a block per
+// pair and `step`-th row, D/4 threads across a row and the runs dealt over the
+// others, since one row's chain of loads would take longer than its bytes.
+template <int D>
+__global__ void __launch_bounds__(AC_JOIN_THREADS)
+attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
+    constexpr int W = D / 4, G = AC_JOIN_THREADS / W;
+    __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[AC_JOIN_THREADS / 32];
+    __shared__ float2 ml[AC_MAX_RUNS];
+    __shared__ float4 acc[G][W];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     ac_prefix(a, pre, wsum, false);
@@ -735,33 +727,49 @@ __global__ void __launch_bounds__(AC_THREADS) attn_cache_join_kernel(const __gri
     const int64_t first = pre[s] * a.heads + head * blocks;
     if (blocks == 0 || first / per == (first + blocks - 1) / per) return;   // written by its one run
     const AcSeq q = ac_seq(a, s, false);
-    const int rr = blockIdx.y * (1024 / D) + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
-    if (rr >= q.nq * a.ratio) return;
-    const int rank = rr / ROWS, r = rr % ROWS;
-    const int c0 = static_cast<int>(first / per), c1 = static_cast<int>((first + blocks - 1) / per);
-    auto piece = [&](int run) {
-        const int which = run * per > first ? 0 : 1;
-        return a.part + ((static_cast<int64_t>(run) * a.ranks + rank) * 2 + which) * ROWS * (D + 2) + r * (D + 2);
-    };
-    float mx = -INFINITY;
-    for (int run = c0; run <= c1; ++run) mx = fmaxf_nan(mx, piece(run)[0]);
-    float lt = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int run = c0; run <= c1; ++run) {
-        const float* p = piece(run);
-        const float f = p[0] == -INFINITY ? 0.0f : ex2_ftz(p[0] - mx);
-        lt = fmaf(f, p[1], lt);
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(p + 2 + c + e);
-            x[e] = fmaf(f, v.x, x[e]);
-            x[e + 1] = fmaf(f, v.y, x[e + 1]);
+    const int c0 = static_cast<int>(first / per), n = static_cast<int>((first + blocks - 1) / per) - c0 + 1;
+    const int c = threadIdx.x % W, grp = threadIdx.x / W;
+    for (int rr = blockIdx.y; rr < q.nq * a.ratio; rr += gridDim.y) {
+        const int rank = rr / rank_rows, r = rr % rank_rows;
+        auto piece = [&](int k) {
+            const int run = c0 + k, which = run * per > first ? 0 : 1;
+            return a.part + ((static_cast<int64_t>(run) * a.ranks + rank) * 2 + which) * rank_rows * (D + 2) + r * (D + 2);
+        };
+        if (threadIdx.x < n) ml[threadIdx.x] = *reinterpret_cast<const float2*>(piece(threadIdx.x));
+        __syncthreads();
+        float mx = -INFINITY;
+        for (int k = 0; k < n; ++k) mx = fmaxf_nan(mx, ml[k].x);
+        float lt = 0.0f;
+        for (int k = 0; k < n; ++k) lt = fmaf(ml[k].x == -INFINITY ? 0.0f : ex2_ftz(ml[k].x - mx), ml[k].y, lt);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = grp; k < n; k += G) {
+            const float f = ml[k].x == -INFINITY ? 0.0f : ex2_ftz(ml[k].x - mx);
+            const float2* p = reinterpret_cast<const float2*>(piece(k) + 2 + 4 * c);
+            const float2 u = p[0], v = p[1];
+            x.x = fmaf(f, u.x, x.x);
+            x.y = fmaf(f, u.y, x.y);
+            x.z = fmaf(f, v.x, x.z);
+            x.w = fmaf(f, v.y, x.w);
         }
+        acc[grp][c] = x;
+        __syncthreads();
+        if (grp == 0) {
+            for (int k = 1; k < G; ++k) {
+                const float4 v = acc[k][c];
+                x.x += v.x;
+                x.y += v.y;
+                x.z += v.z;
+                x.w += v.w;
+            }
+            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+            const int i = rr / a.ratio;
+            if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
+                *reinterpret_cast<uint2*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + 4 * c) =
+                    make_uint2(bf16x2(x.x * inv, x.y * inv), bf16x2(x.z * inv, x.w * inv));
+        }
+        __syncthreads();
     }
-    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-    const int i = rr / a.ratio;
-    if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
-        *reinterpret_cast<uint2*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + c) =
-            make_uint2(bf16x2(x[0] * inv, x[1] * inv), bf16x2(x[2] * inv, x[3] * inv));
 }
 
 // ------------------------------------------------------------ host
@@ -798,53 +806,50 @@ static bool ac_map(CUtensorMap* map, const void* ptr, const gdn_kv_cache& c) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of one CTA: 16, 32 or 64, as many as the accumulators of a warp leave
-// room for (4096 fp32 at most).
-static int ac_rows(int d, int64_t rows) {
-    const int most = 4096 / d;
-    return rows <= 16 || most == 16 ? 16 : rows <= 32 || most == 32 ? 32 : 64;
-}
+// Most rows of one CTA: what the accumulators of a warp leave room for.
+static int ac_most_rows(int d) { return 4096 / d; }
 
 size_t attn_cache_workspace_bytes(const gdn_kv_cache& c, int64_t n_tokens, int hq) {
     (void)n_tokens;
     (void)hq;
-    const int rows = 4096 / c.head_dim;
-    return static_cast<size_t>(AC_MAX_RUNS) * 2 * rows * (c.head_dim + 2) * 4;
+    return static_cast<size_t>(AC_MAX_RUNS) * 2 * ac_most_rows(c.head_dim) * (c.head_dim + 2) * 4;
 }
 
-template <int D, int T, int MT>
+template <int D, int T, int NR>
 static cudaError_t ac_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st) {
-    using L = AcSmem<D, T, MT>;
+    using L = AcSmem<D, T, NR>;
     static PerDeviceOnce once;
     if (once.run([](int) {
-            cudaFuncSetAttribute(attn_cache_kernel<D, T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES + 1024);
+            cudaFuncSetAttribute(attn_cache_kernel<D, T, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES + 1024);
         }) < 0)
         return cudaErrorInvalidDevice;
     CUtensorMap mk, mv;
     if (!ac_map(&mk, c.k, c) || !ac_map(&mv, c.v, c)) return cudaErrorInvalidValue;
-    const int rows = a.max_q * a.ratio;
+    const int rows = a.max_q * a.ratio, pairs = a.n_seqs * a.heads;
     a.ranks = (rows + L::ROWS - 1) / L::ROWS;
     a.runs = AC_MAX_RUNS / a.ranks;
-    attn_cache_kernel<D, T, MT><<<static_cast<unsigned>(a.runs * a.ranks), AC_THREADS, L::BYTES + 1024, st>>>(mk, mv, a);
+    attn_cache_kernel<D, T, NR><<<static_cast<unsigned>(a.runs * a.ranks), L::THREADS, L::BYTES + 1024, st>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // a row per block, up to a few blocks per SM
+    const int y = pairs >= 8 * AC_MAX_RUNS ? 1 : 8 * AC_MAX_RUNS / pairs < rows ? 8 * AC_MAX_RUNS / pairs : rows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.n_seqs * a.heads), static_cast<unsigned>((rows + 1024 / D - 1) / (1024 / D)), 1);
-    cfg.blockDim = dim3(AC_THREADS, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y), 1);
+    cfg.blockDim = dim3(AC_JOIN_THREADS, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<D, L::ROWS>, a);
+    return cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<D>, a, static_cast<int>(L::ROWS));
 }
 
-template <int D, int MT>
+template <int D, int NR>
 static cudaError_t ac_launch_t(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st) {
-    if (c.dtype == GDN_KV_BF16) return ac_launch<D, GDN_KV_BF16, MT>(c, a, st);
-    if (c.dtype == GDN_KV_I8) return ac_launch<D, GDN_KV_I8, MT>(c, a, st);
-    return ac_launch<D, GDN_KV_E4M3, MT>(c, a, st);
+    if (c.dtype == GDN_KV_BF16) return ac_launch<D, GDN_KV_BF16, NR>(c, a, st);
+    if (c.dtype == GDN_KV_I8) return ac_launch<D, GDN_KV_I8, NR>(c, a, st);
+    return ac_launch<D, GDN_KV_E4M3, NR>(c, a, st);
 }
 
 cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t ld_q, const int32_t* cu, int64_t n_tokens,
@@ -875,10 +880,11 @@ cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t 
     a.max_blocks = max_blocks;
     a.sl2 = scale * LOG2E;
     a.part = static_cast<float*>(workspace);
-    const int rows = ac_rows(c.head_dim, static_cast<int64_t>(max_q) * a.ratio);
-    if (c.head_dim == 256) return ac_launch_t<256, 1>(c, a, st);
-    if (c.head_dim == 128) return rows == 16 ? ac_launch_t<128, 1>(c, a, st) : ac_launch_t<128, 2>(c, a, st);
-    return rows == 16 ? ac_launch_t<64, 1>(c, a, st) : rows == 32 ? ac_launch_t<64, 2>(c, a, st) : ac_launch_t<64, 4>(c, a, st);
+    const int rows = max_q * a.ratio;
+    if (c.head_dim == 256) return rows <= 8 ? ac_launch_t<256, 1>(c, a, st) : ac_launch_t<256, 2>(c, a, st);
+    if (c.head_dim == 128)
+        return rows <= 8 ? ac_launch_t<128, 1>(c, a, st) : rows <= 16 ? ac_launch_t<128, 2>(c, a, st) : ac_launch_t<128, 4>(c, a, st);
+    return rows <= 8 ? ac_launch_t<64, 1>(c, a, st) : rows <= 16 ? ac_launch_t<64, 2>(c, a, st) : ac_launch_t<64, 4>(c, a, st);
 }
 
 int read_and_clear_attn_cache_error() {
