@@ -150,11 +150,15 @@ class DeviceLayer:
                                          gl.stream_handle(stream), check=check)
 
 
-def _heads(t: torch.Tensor, name: str) -> int:
-    """Elements between the tokens of a bf16 tensor [tokens][heads][head_dim] whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+def _heads(t: torch.Tensor, name: str, width=None) -> int:
+    """Elements between the tokens of a bf16 tensor [tokens][heads][head_dim] whose heads are contiguous (and
+    whose heads and head_dim are ``width``, if given)."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or not t.is_cuda:
         raise ValueError(f"{name}: a bf16 device tensor [tokens][heads][head_dim] is required")
-    n, h, d = t.shape
+    n, h, d = shape
+    if width is not None and (h, d) != width:
+        raise ValueError(f"{name}: [tokens][{width[0]}][{width[1]}] is required")
     sn, sh, sd = t.stride()
     if n and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -162,7 +166,7 @@ def _heads(t: torch.Tensor, name: str) -> int:
 
 
 def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous {dtype} on the device are required")
 
 
@@ -239,6 +243,7 @@ class KvCache:
         c.k, c.v, c.k_scale, c.v_scale = gl.ptr(k), gl.ptr(v), gl.ptr(k_scale), gl.ptr(v_scale)
         self.struct = c
         self._ref = ctypes.byref(c)
+        self._width = (self.n_kv_heads, self.head_dim)
 
     @classmethod
     def new(cls, kind: str, n_pages: int, n_kv_heads: int, page_tokens: int, head_dim: int, device: str = "cuda",
@@ -256,17 +261,11 @@ class KvCache:
         t = torch.arange(first, first + n, device=pages.device)
         return pages[t // self.page_tokens].long() * self.page_tokens + t % self.page_tokens
 
-    def _rows(self, t: torch.Tensor, name: str) -> int:
-        ld = _heads(t, name)
-        if t.shape[1:] != (self.n_kv_heads, self.head_dim):
-            raise ValueError(f"{name}: [tokens][{self.n_kv_heads}][{self.head_dim}] is required")
-        return ld
-
     def write(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor | None = None, stream=None,
               check=True) -> int:
         """Enqueue gdn_kv_write: rows of k and v (bf16 [n][n_kv_heads][head_dim]) into slots (int64); with
         rows (int32), token t is row rows[t]: the accepted tokens of a drafted tree."""
-        ld_k, ld_v = self._rows(k, "k"), self._rows(v, "v")
+        ld_k, ld_v = _heads(k, "k", self._width), _heads(v, "v", self._width)
         n = slots.numel()
         _vector(slots, torch.int64, n, "slots")
         if v.shape[0] != k.shape[0]:
@@ -278,7 +277,7 @@ class KvCache:
 
     def read(self, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None, check=True) -> int:
         """Enqueue gdn_kv_read: the values of the slots (int64) into k and v (bf16 [n][n_kv_heads][head_dim])."""
-        ld_k, ld_v = self._rows(k, "k"), self._rows(v, "v")
+        ld_k, ld_v = _heads(k, "k", self._width), _heads(v, "v", self._width)
         n = slots.numel()
         _vector(slots, torch.int64, n, "slots")
         if k.shape[0] != n or v.shape[0] != n:

@@ -31,11 +31,12 @@
 // goes into the exponent of its probability, p' = 2^(x + log2 vs - m), which
 // enters the product as fp16; the softmax sum adds p = 2^(x - m) in fp32.
 // Scores x are in units of log 2.  A maximum is raised only past a margin of
-// 2^8, so the accumulators are seldom rescaled; fp16 probabilities carry a
-// factor 2^7 (at most 2^15 with the margin).  Those below 2^-14, where fp16
-// loses bits, matter only to elements that are zero in every more probable
-// row; a tile that has one multiplies the rounding errors p' - fp16(p') in
-// bf16, whose exponents reach as far as fp32's, in a second pass.  q goes to fp16 times a power of two per row that puts its largest
+// 2^4, so the accumulators are seldom rescaled; fp16 probabilities carry a
+// factor 2^11 (at most 2^15 with the margin).  Those below 2^-14, where fp16
+// loses bits (2^-25 of the largest), matter only to elements that are zero in
+// every more probable row; a tile that has one multiplies the rounding errors
+// p' - fp16(p') in bf16, whose exponents reach as far as fp32's, in a second
+// pass, and leaves out the first where fp16 holds nothing.  q goes to fp16 times a power of two per row that puts its largest
 // element in [2^14, 2^15): elements below 2^-38 of it are lost.
 #include "common.cuh"
 #include "tma.cuh"
@@ -53,8 +54,8 @@ constexpr int AC_BLOCK = 8;             // tiles of a block
 constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
 constexpr int AC_RING = 192 * 1024;     // bytes of tiles in flight per CTA
 constexpr int AC_JOIN_THREADS = 256;
-constexpr float AC_MARGIN = 8.0f;
-constexpr float AC_LIFT = 7.0f;         // fp16 probabilities times 2^7
+constexpr float AC_MARGIN = 4.0f;
+constexpr float AC_LIFT = 11.0f;        // fp16 probabilities times 2^11
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct AttCacheArgs {
@@ -192,7 +193,7 @@ struct AcSmem {
     static constexpr int HALF = AC_TILE * ROW;              // the keys, or the values, of a tile
     // 16 warps where a thread's accumulators are at most 64 registers and a
     // warp's share of the ring holds a tile and a half
-    static constexpr int WARPS = D * NR <= 256 && NR <= 2 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
+    static constexpr int WARPS = D * NR <= 256 && NR == 1 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int NS = AC_RING / WARPS / HALF < 8 ? AC_RING / WARPS / HALF : 8;   // half tiles in flight per warp
     static constexpr int ROWS = 8 * NR;
@@ -269,6 +270,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     // bf16 values swap the two
     const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
     const int vr = Q8 ? kr : (lane & 7) + ((lane >> 4) << 3), vc = Q8 ? kc : (lane >> 3) & 1;
+    // piece c + kc (c even) of a half tile at `b`: the swizzle is one exclusive or on the address
+    const uint32_t koff = ac_piece<L>(kr, kc), voff = ac_piece<L>(vr, vc);
+    auto piece_at = [](uint32_t b, int c) { return (b ^ ((c & 7) << 4)) + (c >> 3) * (AC_TILE * 128); };
 
     while (at < end) {
         while (pre[s + 1] * a.heads <= at) ++s;
@@ -375,7 +379,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         for (int i = 0; i < mine; ++i) {
             const int key0 = (t0 + warp + i * L::WARPS) * AC_TILE;
             int lim = q.len - key0;   // keys of this tile below `lim` exist
-            const uint32_t kb = smem_addr(ring + slot * L::HALF);
+            const uint32_t kb = smem_addr(ring + slot * L::HALF) + koff;
 
             if (!dead && !mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
@@ -396,7 +400,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     uint32_t f[4];
-                    ldsm_x4(kb + ac_piece<L>(kr, 2 * kt + kc), f);
+                    ldsm_x4(piece_at(kb, 2 * kt), f);
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) {
                         const uint2 b = qsm[(nr * KT + kt) * 32 + lane];
@@ -408,7 +412,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
                 for (int kt = 0; kt < KT; kt += 2) {
                     uint32_t w[4];
-                    ldsm_x4(kb + ac_piece<L>(kr, kt + kc), w);
+                    ldsm_x4(piece_at(kb, kt), w);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint32_t x = T == GDN_KV_I8 ? w[2 * u] ^ 0x80808080u : w[2 * u];
@@ -434,7 +438,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 slot = 0;
                 par ^= 1;
             }
-            const uint32_t vb = smem_addr(ring + slot * L::HALF);
+            const uint32_t vb = smem_addr(ring + slot * L::HALF) + voff;
 
             if (!mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
@@ -445,23 +449,28 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 lv[1] = lg2(fmaxf_nan(scales[slot * AC_TILE + 8 + g], 7.7e-34f));
             }
 
-            // ---- softmax of the tile: x in units of log 2, y with the value's scale
+            // ---- softmax of the tile: y = x + log2 of the value's scale
             bool up = false;
             float y[NR][4];
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x = sc[nr][e] * qs[nr][e & 1];
-                    if constexpr (Q8) x *= kv[e >> 1];
-                    y[nr][e] = Q8 ? x + lv[e >> 1] : x;
+                    if constexpr (Q8)
+                        y[nr][e] = fmaf(sc[nr][e], qs[nr][e & 1] * kv[e >> 1], lv[e >> 1]);
+                    else
+                        y[nr][e] = sc[nr][e] * qs[nr][e & 1];
                     if (edge) {
                         const int j = 8 * (e >> 1) + g, d = key0 + j - ctx;
-                        if (j >= lim || (d >= 0 && !((seen[nr][e & 1] >> (d & 63)) & 1))) x = y[nr][e] = -INFINITY;
+                        if (j >= lim || (d >= 0 && !((seen[nr][e & 1] >> (d & 63)) & 1))) y[nr][e] = -INFINITY;
                     }
-                    sc[nr][e] = x;
                     up |= y[nr][e] > m[nr][e & 1] + AC_MARGIN;   // from a maximum of -inf: any finite score
                 }
+            if (edge) {      // a scale that is no number has reached the rows that see its key in y
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (!(fabsf(lv[h]) < INFINITY)) lv[h] = 0.0f;
+            }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
@@ -489,12 +498,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : m[nr][e & 1];
+                    const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : Q8 ? m[nr][e & 1] - AC_LIFT : m[nr][e & 1];
                     if constexpr (Q8) {
-                        const float p = ex2_ftz(y[nr][e] - mm + AC_LIFT);
+                        const float x = y[nr][e] - mm, p = ex2_ftz(x);
                         pk[nr][e] = p;
                         faint |= p != 0.0f && p < 6.1035156e-5f;
-                        l[nr][e & 1] += ex2_ftz(sc[nr][e] - mm + AC_LIFT);
+                        l[nr][e & 1] += ex2_ftz(x - lv[e >> 1]);
                     } else {
                         pk[nr][e] = ex2_ftz(y[nr][e] - mm);
                     }
@@ -540,7 +549,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             constexpr int STEP = Q8 ? 2 : 1;
             auto values = [&](int c, uint32_t (&f)[STEP][4]) {
                 uint32_t w[4];
-                ldsm_x4_trans(vb + ac_piece<L>(vr, (Q8 ? c : 2 * c) + vc), w);
+                ldsm_x4_trans(piece_at(vb, Q8 ? c : 2 * c), w);
                 if constexpr (Q8) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -568,17 +577,29 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
+            bool first = true;
+            if constexpr (Q8) {
+                faint = __any_sync(0xffffffffu, faint);
+                if (faint) {         // does fp16 hold anything of this tile?
+                    uint32_t any = 0;
 #pragma unroll
-            for (int c = 0; c < KT; c += STEP) {
-                uint32_t f[STEP][4];
-                values(c, f);
+                    for (int nr = 0; nr < NR; ++nr) any |= pt[nr][0] | pt[nr][1];
+                    first = __any_sync(0xffffffffu, any != 0);
+                }
+            }
+            if (first) {
 #pragma unroll
-                for (int u = 0; u < STEP; ++u)
+                for (int c = 0; c < KT; c += STEP) {
+                    uint32_t f[STEP][4];
+                    values(c, f);
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
+                    for (int u = 0; u < STEP; ++u)
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
+                }
             }
             if constexpr (Q8) {
-                if (__any_sync(0xffffffffu, faint)) {
+                if (faint) {
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll

@@ -158,16 +158,19 @@ def ptr(t) -> int:
     """Device (or host) address of a torch tensor / numpy array, 0 for None."""
     if t is None:
         return 0
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
-    return t.ctypes.data
+    except AttributeError:
+        return t.ctypes.data
 
 
 def stream_handle(stream=None) -> int:
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    if torch.cuda.is_initialized():     # the handle alone: no stream object is made for a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def make_layer_struct(spec, dev: dict, eps_l2=1e-6, eps_rms=1e-6, q_scale=None, gate_log_a=None, gate_b=None) -> GdnLayer:
