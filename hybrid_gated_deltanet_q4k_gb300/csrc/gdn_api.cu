@@ -1109,8 +1109,8 @@ int gdn_attn_cache(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, c
         return fail(GDN_EINVAL, "gdn_attn_cache: q and o rows 16-byte aligned, at least %lld elements apart", (long long)w);
     if (!aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(tree, 8) || !aligned(workspace, 256))
         return fail(GDN_EINVAL, "gdn_attn_cache: alignment");
-    if (max_blocks < 1 || max_blocks > 0x7fffffff / cache->page_tokens || ld_table < max_blocks)
-        return fail(GDN_EINVAL, "gdn_attn_cache: 1 <= max_blocks <= ld_table and max_blocks * page_tokens < 2^31 required");
+    if (max_blocks < 1 || max_blocks > (1 << 30) / cache->page_tokens || ld_table < max_blocks)
+        return fail(GDN_EINVAL, "gdn_attn_cache: 1 <= max_blocks <= ld_table and max_blocks * page_tokens <= 2^30 required");
     if (!std::isfinite(scale)) return fail(GDN_EINVAL, "gdn_attn_cache: scale is not finite");
     const size_t need = attn_cache_workspace_bytes(*cache, n_tokens, n_q_heads);
     if (ws_bytes < need) return fail(GDN_ENOMEM, "gdn_attn_cache: workspace %zu B < %zu B", ws_bytes, need);

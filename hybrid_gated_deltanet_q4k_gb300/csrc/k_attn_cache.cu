@@ -11,10 +11,12 @@
 // pairs, and each CTA takes one contiguous run of them: every SM gets the same
 // bytes whatever the lengths are, with nothing planned on the host (lengths
 // and offsets are read on the device, so a captured graph may be replayed with
-// others).  A pair that lies in one run is written at once; the others leave
-// (maximum, sum, fp32 accumulator) partials that a second kernel joins.
+// others).  Each pair counts some blocks more than it has, for the time that
+// starting and joining it takes.  A pair that lies in one run is written at
+// once; the others leave (maximum, sum, fp32 accumulator) partials that a
+// second kernel joins.
 //
-// Inside a CTA each warp walks every 8th or 16th tile of 16 keys on its own:
+// Inside a CTA each warp walks every 8th or 16th tile (16 to 64 keys) on its own:
 // its lane 0 copies the tile's keys and values by TMA into the warp's own ring,
 // the warp multiplies them on the tensor cores and keeps its own running
 // maximum, sum and accumulator; there is no barrier between warps until the
@@ -49,8 +51,7 @@ namespace gdn {
 
 static __device__ int g_attn_cache_error;
 
-constexpr int AC_TILE = 16;             // keys per tile
-constexpr int AC_BLOCK = 8;             // tiles of a block
+constexpr int AC_BLOCK = 128;           // keys of a block
 constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
 constexpr int AC_RING = 192 * 1024;     // bytes of tiles in flight per CTA
 constexpr int AC_JOIN_THREADS = 256;
@@ -68,7 +69,9 @@ struct AttCacheArgs {
     const int32_t *cu, *table, *lens;
     const uint64_t* tree;
     int n_seqs, max_q, max_blocks;
-    int runs, ranks;    // runs of tiles, and row tiles of a pair (a CTA per run and rank of rows)
+    int runs, ranks;    // runs of blocks, and row tiles of a pair (a CTA per run and rank of rows)
+    int start;          // blocks that each pair counts more than it has
+    int box;            // keys of one copy
     float sl2;          // scale * log2(e)
     float* part;        // [runs * ranks][2][rows][D + 2] partials
 };
@@ -89,25 +92,30 @@ __device__ __forceinline__ AcSeq ac_seq(const AttCacheArgs& a, int s, bool repor
     if (report && (!ok || r.len != len)) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
     return r;
 }
-// Blocks of each of its pairs: at least one where there is a row to write.
-__device__ __forceinline__ int64_t ac_blocks(const AcSeq& s) {
-    constexpr int KEYS = AC_BLOCK * AC_TILE;
-    return s.nq == 0 ? 0 : s.len == 0 ? 1 : (static_cast<int64_t>(s.len) + KEYS - 1) / KEYS;
-}
+// Blocks of each of its pairs (at least one where there is a row to write), and as they count.
+__device__ __forceinline__ int ac_blocks(const AcSeq& s) { return s.len == 0 ? 1 : (s.len - 1) / AC_BLOCK + 1; }
 
-// The blocks before each sequence (of one head): pre[0 .. n_seqs], by all threads of a CTA.
+// The counted blocks before each sequence (of one head), pre[0 .. n_seqs], and
+// the sequences, by all threads of a CTA.
 static_assert(GDN_MAX_SEQS <= AC_JOIN_THREADS, "a thread per sequence");
-__device__ __forceinline__ void ac_prefix(const AttCacheArgs& a, int64_t* pre, int64_t* wsum, bool report) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    int64_t v = t < a.n_seqs ? ac_blocks(ac_seq(a, t, report)) : 0;
+__device__ __forceinline__ void ac_prefix(const AttCacheArgs& a, int64_t* pre, AcSeq* seq, int64_t* wsum, bool report) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = (a.n_seqs + 31) / 32;
+    int64_t v = 0;
+    if (t < a.n_seqs) {
+        const AcSeq q = ac_seq(a, t, report);
+        seq[t] = q;
+        v = q.nq == 0 ? 0 : ac_blocks(q) + a.start;
+    }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
-    if (lane == 31) wsum[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < min(warp, GDN_MAX_SEQS / 32); ++w) v += wsum[w];
+    if (warps > 1) {
+        if (lane == 31 && warp < warps) wsum[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < min(warp, warps); ++w) v += wsum[w];
+    }
     if (t < a.n_seqs) pre[t + 1] = v;
     if (t == 0) pre[0] = 0;
     __syncthreads();
@@ -182,33 +190,40 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // ------------------------------------------------------------ shared memory
 
 // A row of a tile is cut into slabs of 128 bytes (one of 64 for 8-bit heads of
-// 64), each slab [16 keys][128 bytes] with the TMA's 128-byte (64-byte)
-// swizzle, so that eight keys' 16-byte pieces fall into different banks.
+// 64), each slab [keys][128 bytes] with the TMA's 128-byte (64-byte) swizzle,
+// so that eight keys' 16-byte pieces fall into different banks.
 template <int D, int T, int NR>
 struct AcSmem {
     static constexpr int ES = T == GDN_KV_BF16 ? 2 : 1;
     static constexpr int ROW = D * ES;
     static constexpr int SLAB = ROW < 128 ? ROW : 128;      // bytes of a row in one slab
     static constexpr int NSLAB = ROW / SLAB;
-    static constexpr int HALF = AC_TILE * ROW;              // the keys, or the values, of a tile
+    static constexpr int SUB = ROW >= 256 ? 1 : 256 / ROW;  // 16-key steps of a tile: 4 KB or more, so that a
+    static constexpr int KEYS = 16 * SUB;                   // tile's waits and copies are worth their instructions
+    static constexpr int HALF = KEYS * ROW;                 // the keys, or the values, of a tile
+    static constexpr int TILES = AC_BLOCK / KEYS;           // tiles of a block
+    static constexpr int START = 768 / ROW > 0 ? 768 / ROW : 1;   // blocks' worth of starting a pair: 4 us of 45 GB/s
     // 16 warps where a thread's accumulators are at most 64 registers and a
     // warp's share of the ring holds a tile and a half
-    static constexpr int WARPS = D * NR <= 256 && NR == 1 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
+    static constexpr int WARPS = D * NR <= 256 && NR <= 2 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int NS = AC_RING / WARPS / HALF < 8 ? AC_RING / WARPS / HALF : 8;   // half tiles in flight per warp
     static constexpr int ROWS = 8 * NR;
     static constexpr int OLD = D + 8;                       // padded rows of the joined accumulators
     static constexpr int R0 = 0;                            // ring [warp][slot]; the accumulators at the end of a pair
-    static constexpr int S0 = AC_RING;                      // row scales of the half tiles: [warp][slot][16]
-    static constexpr int M0 = S0 + WARPS * NS * AC_TILE * 4;     // maxima and sums: [warp][rows][2]
+    static constexpr int S0 = AC_RING;                      // row scales of the half tiles: [warp][slot][keys]
+    static constexpr int M0 = S0 + WARPS * NS * KEYS * 4;        // maxima and sums: [warp][rows][2]
     static constexpr int P0 = M0 + WARPS * ROWS * 2 * 4;         // blocks before each sequence
-    static constexpr int W0 = P0 + (GDN_MAX_SEQS + 2) * 8;
-    static constexpr int F0 = W0 + WARPS * 8;                    // pages in range: [warp][slot]
-    static constexpr int X0 = F0 + WARPS * NS * 4;               // score factor of each row
+    static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;       // the sequences
+    static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
+    static constexpr int F0 = W0 + WARPS * 8;                    // pages in range, a bit per copy: [warp][slot]
+    static constexpr int N0 = F0 + WARPS * NS * 4;               // mask word of each row
+    static constexpr int X0 = N0 + ROWS * 8;                     // score factor of each row
     static constexpr int Q0 = (X0 + ROWS * 4 + 15) & ~15;        // q fragments [row tile][step][lane] x 8 bytes
     static constexpr int B0 = Q0 + NR * (D / 16) * 256;          // mbarriers [warp][slot]
     static constexpr int BYTES = B0 + WARPS * NS * 8;
     static_assert(WARPS * ROWS * OLD * 4 <= AC_RING, "the joined accumulators fit the ring");
+    static_assert(SUB == 1 || NSLAB == 1, "copies of a tile follow each other");
     static_assert(BYTES + 1024 <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -216,7 +231,7 @@ struct AcSmem {
 template <class L>
 __device__ __forceinline__ uint32_t ac_piece(int r, int c) {
     if constexpr (L::SLAB == 128)
-        return static_cast<uint32_t>((c >> 3) * (AC_TILE * 128) + r * 128 + (((c ^ r) & 7) << 4));
+        return static_cast<uint32_t>((c >> 3) * (L::KEYS * 128) + r * 128 + (((c ^ r) & 7) << 4));
     else
         return static_cast<uint32_t>(r * 64 + (((c ^ (r >> 1)) & 3) << 4));
 }
@@ -230,27 +245,31 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                   const __grid_constant__ AttCacheArgs a) {
     using L = AcSmem<D, T, NR>;
     constexpr int KT = D / 16;            // 16-wide steps of a row
+    constexpr int SUB = L::SUB;
     constexpr bool Q8 = T != GDN_KV_BF16;
     extern __shared__ __align__(1024) unsigned char smb[];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smb) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     int64_t* pre = reinterpret_cast<int64_t*>(base + L::P0);
+    AcSeq* seq = reinterpret_cast<AcSeq*>(base + L::T0);
     float* join = reinterpret_cast<float*>(base + L::R0);
     float2* ml = reinterpret_cast<float2*>(base + L::M0);
+    uint64_t* seen = reinterpret_cast<uint64_t*>(base + L::N0);
     float* row_factor = reinterpret_cast<float*>(base + L::X0);
     uint2* qsm = reinterpret_cast<uint2*>(base + L::Q0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::B0) + warp * L::NS;
     unsigned char* ring = base + L::R0 + warp * L::NS * L::HALF;
-    float* scales = reinterpret_cast<float*>(base + L::S0) + warp * L::NS * AC_TILE;
-    int* page_in = reinterpret_cast<int*>(base + L::F0) + warp * L::NS;
+    float* scales = reinterpret_cast<float*>(base + L::S0) + warp * L::NS * L::KEYS;
+    uint32_t* page_in = reinterpret_cast<uint32_t*>(base + L::F0) + warp * L::NS;
 
-    pdl_trigger();
     if (lane == 0) {
         for (int i = 0; i < L::NS; ++i) mbar_init_cta(bars + i, 1);
         mbar_init_fence();
     }
+    pdl_wait();
+    pdl_trigger();   // after the wait: what precedes this kernel is complete when the next one's CTAs start
     const int run = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
-    ac_prefix(a, pre, reinterpret_cast<int64_t*>(base + L::W0), blockIdx.x == 0);
+    ac_prefix(a, pre, seq, reinterpret_cast<int64_t*>(base + L::W0), blockIdx.x == 0);
     const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total);
     int64_t at = run * per;
     const int64_t end = at + per < total ? at + per : total;
@@ -270,47 +289,60 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     // bf16 values swap the two
     const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
     const int vr = Q8 ? kr : (lane & 7) + ((lane >> 4) << 3), vc = Q8 ? kc : (lane >> 3) & 1;
-    // piece c + kc (c even) of a half tile at `b`: the swizzle is one exclusive or on the address
+    // piece c + kc (c even) of 16 keys at `b`: the swizzle is one exclusive or on the address
     const uint32_t koff = ac_piece<L>(kr, kc), voff = ac_piece<L>(vr, vc);
-    auto piece_at = [](uint32_t b, int c) { return (b ^ ((c & 7) << 4)) + (c >> 3) * (AC_TILE * 128); };
+    auto piece_at = [](uint32_t b, int c) { return (b ^ ((c & 7) << 4)) + (c >> 3) * (L::KEYS * 128); };
 
     while (at < end) {
         while (pre[s + 1] * a.heads <= at) ++s;
-        const AcSeq q = ac_seq(a, s, false);
-        const int blocks = static_cast<int>(pre[s + 1] - pre[s]);
-        const int head = static_cast<int>((at - pre[s] * a.heads) / blocks);
-        const int64_t first = pre[s] * a.heads + static_cast<int64_t>(head) * blocks;
-        const int b0 = static_cast<int>(at - first);
-        const int b1 = end - first < blocks ? static_cast<int>(end - first) : blocks;
-        at = first + b1;
-        const int t0 = b0 * AC_BLOCK, t1 = min(b1 * AC_BLOCK, max(1, (q.len + AC_TILE - 1) / AC_TILE));   // tiles
+        const AcSeq q = seq[s];
+        const int counted = static_cast<int>(pre[s + 1] - pre[s]), blocks = counted - a.start;
+        const int head = static_cast<int>((at - pre[s] * a.heads) / counted);
+        const int64_t first = pre[s] * a.heads + static_cast<int64_t>(head) * counted;
+        const int b0 = max(static_cast<int>(at - first) - a.start, 0);
+        const int b1 = end - first < counted ? max(static_cast<int>(end - first) - a.start, 0) : blocks;
+        at = first + counted < end ? first + counted : end;
         const int row0 = rank * L::ROWS, rows = min(q.nq * a.ratio - row0, L::ROWS);
-        if (rows <= 0) continue;
+        if (rows <= 0 || b0 >= b1) continue;
+        const int t0 = b0 * L::TILES, t1 = min(b1 * L::TILES, q.len == 0 ? 1 : (q.len - 1) / L::KEYS + 1);   // tiles
         const int ctx = q.len - q.nq;      // keys every row sees
         const int32_t* table = a.table + s * a.ld_table;
 
-        // ---- copies: half tile j (keys of tile j / 2, then its values) follows j - NS in its slot
+        // ---- copies: half tile j (keys of tile j / 2, then its values)
+        // follows j - NS in its slot.  A tile may lie in several pages: lane p
+        // copies the rows of the p-th.
         const int mine = t1 - t0 - warp > 0 ? (t1 - t0 - warp + L::WARPS - 1) / L::WARPS : 0;   // tiles of this warp
+        const int copies = L::KEYS / a.box, mycopy = lane < copies ? lane * a.box : 0;
         auto page_of = [&](int i) {
-            return table[min(((t0 + warp + i * L::WARPS) * AC_TILE) >> a.page_shift, a.max_blocks - 1)];
+            return table[min(((t0 + warp + i * L::WARPS) * L::KEYS + mycopy) >> a.page_shift, a.max_blocks - 1)];
         };
-        auto issue = [&](int j, int sl, int page) {   // lane 0
-            const int row = ((t0 + warp + (j >> 1) * L::WARPS) * AC_TILE) & (a.page - 1);
+        auto issue = [&](int j, int sl, int page) {   // whole warp
+            const int row = ((t0 + warp + (j >> 1) * L::WARPS) * L::KEYS + mycopy) & (a.page - 1);
             const bool in = page >= 0 && page < a.n_pages, val = j & 1;
             const int pair = (in ? page : 0) * a.heads + head;   // an unseen page: any rows, all of them masked
-            page_in[sl] = in;
-            mbar_expect_tx(bars + sl, L::HALF + (Q8 ? AC_TILE * 4 : 0));
-            tma_load_4d(ring + sl * L::HALF, val ? &mv : &mk, bars + sl, 0, row, 0, pair);
-            if constexpr (Q8)
-                bulk_load_1d(scales + sl * AC_TILE, (val ? a.sv : a.sk) + static_cast<int64_t>(pair) * a.page + row,
-                             AC_TILE * 4, bars + sl);
-        };
-        if (lane == 0 && !dead) {
-            int sl = slot;
-            for (int j = 0; j < L::NS && j < 2 * mine; ++j) {
-                issue(j, sl, page_of(j >> 1));
-                sl = sl + 1 == L::NS ? 0 : sl + 1;
+            const uint32_t ok = __ballot_sync(0xffffffffu, in);
+            if (lane < copies) {
+                if (lane == 0) {
+                    page_in[sl] = ok;
+                    mbar_expect_tx(bars + sl, L::HALF + (Q8 ? L::KEYS * 4 : 0));
+                }
+                tma_load_4d(ring + sl * L::HALF + mycopy * L::SLAB, val ? &mv : &mk, bars + sl, 0, row, 0, pair);
+                if constexpr (Q8)
+                    bulk_load_1d(scales + sl * L::KEYS + mycopy, (val ? a.sv : a.sk) + static_cast<int64_t>(pair) * a.page + row,
+                                 a.box * 4, bars + sl);
             }
+        };
+        if (!dead) {
+            int pg[(L::NS + 1) / 2];     // all pages before the first copy: one latency
+#pragma unroll
+            for (int i = 0; i < (L::NS + 1) / 2; ++i) pg[i] = page_of(min(i, max(mine - 1, 0)));
+            int sl = slot;
+#pragma unroll
+            for (int j = 0; j < L::NS; ++j)
+                if (j < 2 * mine) {
+                    issue(j, sl, pg[j >> 1]);
+                    sl = sl + 1 == L::NS ? 0 : sl + 1;
+                }
         }
         // pages of the tiles whose keys (a) and values (b) the next two free slots take
         int page_a = page_of(min(L::NS / 2, max(mine - 1, 0))), page_b = page_of(min((L::NS + 1) / 2, max(mine - 1, 0)));
@@ -324,13 +356,13 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const bool on = r < rows;
             const uint16_t* src = a.q + static_cast<int64_t>(q.tok + (on ? i : 0)) * a.ld_q +
                                   (head * a.ratio + (on ? rr - i * a.ratio : 0)) * D;
+            float factor = a.sl2;
             if constexpr (!Q8) {
                 for (int kt = warp; kt < KT; kt += L::WARPS)
                     qsm[(nr * KT + kt) * 32 + lane] =
                         on ? make_uint2(*reinterpret_cast<const uint32_t*>(src + 16 * kt + 2 * t),
                                         *reinterpret_cast<const uint32_t*>(src + 16 * kt + 8 + 2 * t))
                            : make_uint2(0u, 0u);
-                if (warp == 0 && t == 0) row_factor[r] = a.sl2;
             } else {
                 float amax = 0.0f;
                 uint2 w[KT];
@@ -345,7 +377,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 // 2^e with amax 2^e in [2^14, 2^15): exact both ways within the exponents that keep 2^e finite
                 const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
-                if (warp == 0 && t == 0) row_factor[r] = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+                factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
                     if (kt % L::WARPS == warp)
@@ -353,22 +385,19 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                             make_uint2(f16x2_bits(__uint_as_float(w[kt].x << 16) * up, __uint_as_float(w[kt].x & 0xffff0000u) * up),
                                        f16x2_bits(__uint_as_float(w[kt].y << 16) * up, __uint_as_float(w[kt].y & 0xffff0000u) * up));
             }
+            if (warp == 0 && t == 0) {
+                row_factor[r] = factor;
+                seen[r] = !on ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
+            }
         }
         __syncthreads();
 
         // ---- this thread's rows of the scores: 8 nr + 2t and + 1
-        float qs[NR][2], m[NR][2], l[NR][2], o[NR][KT][4];
-        uint64_t seen[NR][2];
+        float m[NR][2], l[NR][2], o[NR][KT][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nr + 2 * t + e, i = (row0 + r) / a.ratio;
-                qs[nr][e] = row_factor[r];
-                seen[nr][e] = r >= rows ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
-                m[nr][e] = -INFINITY;
-                l[nr][e] = 0.0f;
-            }
+            m[nr][0] = m[nr][1] = -INFINITY;
+            l[nr][0] = l[nr][1] = 0.0f;
 #pragma unroll
             for (int c = 0; c < KT; ++c)
 #pragma unroll
@@ -377,63 +406,68 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
-            const int key0 = (t0 + warp + i * L::WARPS) * AC_TILE;
-            int lim = q.len - key0;   // keys of this tile below `lim` exist
+            const int key0 = (t0 + warp + i * L::WARPS) * L::KEYS;
             const uint32_t kb = smem_addr(ring + slot * L::HALF) + koff;
 
             if (!dead && !mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
-            if (!page_in[slot]) {
-                if (lane == 0 && lim > 0) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
-                lim = 0;
-            }
-            const bool edge = key0 + AC_TILE > ctx || lim < AC_TILE;   // some row may not see some key
+            const uint32_t ok = page_in[slot] | (~0u << copies);
+            const bool edge = key0 + L::KEYS > ctx || ok != ~0u;   // some row may not see some key
+            if (ok != ~0u && lane < copies && !((ok >> lane) & 1) && key0 + mycopy < q.len)
+                atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+            // keys of 16-key step u below limit(u) exist; those of an unseen page do not
+            auto limit = [&](int u) {
+                return (ok >> (16 * u / a.box)) & 1 ? q.len - key0 - 16 * u : 0;
+            };
 
-            // ---- scores of keys g and g + 8 for this thread's rows
-            float sc[NR][4];
+            // ---- scores of keys g and g + 8 (of each 16) for this thread's rows
+            float y[SUB][NR][4], kv[SUB][2];
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+            for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nr][e] = 0.0f;
-            if constexpr (!Q8) {
+                for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    uint32_t f[4];
-                    ldsm_x4(piece_at(kb, 2 * kt), f);
+                    for (int e = 0; e < 4; ++e) y[u][nr][e] = 0.0f;
+                const uint32_t ku = kb + u * (16 * L::SLAB);
+                if constexpr (!Q8) {
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) {
-                        const uint2 b = qsm[(nr * KT + kt) * 32 + lane];
-                        mma16816<T>(sc[nr], f, b.x, b.y);
-                    }
-                }
-            } else {
-                // 16 codes of eight keys per register set: a thread gets codes 4t .. 4t+3 of key g
-#pragma unroll
-                for (int kt = 0; kt < KT; kt += 2) {
-                    uint32_t w[4];
-                    ldsm_x4(piece_at(kb, kt), w);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t x = T == GDN_KV_I8 ? w[2 * u] ^ 0x80808080u : w[2 * u];
-                        const uint32_t y = T == GDN_KV_I8 ? w[2 * u + 1] ^ 0x80808080u : w[2 * u + 1];
-                        const uint32_t f[4] = {codes_f16<T, 0, 1>(x), codes_f16<T, 0, 1>(y), codes_f16<T, 2, 3>(x),
-                                               codes_f16<T, 2, 3>(y)};
+                    for (int kt = 0; kt < KT; ++kt) {
+                        uint32_t f[4];
+                        ldsm_x4(piece_at(ku, 2 * kt), f);
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr) {
-                            const uint2 b = qsm[(nr * KT + kt + u) * 32 + lane];
-                            mma16816<T>(sc[nr], f, b.x, b.y);
+                            const uint2 b = qsm[(nr * KT + kt) * 32 + lane];
+                            mma16816<T>(y[u][nr], f, b.x, b.y);
+                        }
+                    }
+                } else {
+                    // 16 codes of eight keys per register set: a thread gets codes 4t .. 4t+3 of key g
+#pragma unroll
+                    for (int kt = 0; kt < KT; kt += 2) {
+                        uint32_t w[4];
+                        ldsm_x4(piece_at(ku, kt), w);
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint32_t x = T == GDN_KV_I8 ? w[2 * v] ^ 0x80808080u : w[2 * v];
+                            const uint32_t z = T == GDN_KV_I8 ? w[2 * v + 1] ^ 0x80808080u : w[2 * v + 1];
+                            const uint32_t f[4] = {codes_f16<T, 0, 1>(x), codes_f16<T, 0, 1>(z), codes_f16<T, 2, 3>(x),
+                                                   codes_f16<T, 2, 3>(z)};
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) {
+                                const uint2 b = qsm[(nr * KT + kt + v) * 32 + lane];
+                                mma16816<T>(y[u][nr], f, b.x, b.y);
+                            }
                         }
                     }
                 }
-            }
-            float kv[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
-            if constexpr (Q8) {
-                kv[0] = scales[slot * AC_TILE + g];
-                kv[1] = scales[slot * AC_TILE + 8 + g];
+                if constexpr (Q8) {
+                    kv[u][0] = scales[slot * L::KEYS + 16 * u + g];
+                    kv[u][1] = scales[slot * L::KEYS + 16 * u + 8 + g];
+                }
             }
             __syncwarp();
-            if (lane == 0 && 2 * i + L::NS < 2 * mine) issue(2 * i + L::NS, slot, page_a);
+            if (2 * i + L::NS < 2 * mine) issue(2 * i + L::NS, slot, page_a);
             if (++slot == L::NS) {
                 slot = 0;
                 par ^= 1;
@@ -443,40 +477,48 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (!mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
-            if constexpr (Q8) {
-                // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
-                lv[0] = lg2(fmaxf_nan(scales[slot * AC_TILE + g], 7.7e-34f));
-                lv[1] = lg2(fmaxf_nan(scales[slot * AC_TILE + 8 + g], 7.7e-34f));
-            }
 
             // ---- softmax of the tile: y = x + log2 of the value's scale
             bool up = false;
-            float y[NR][4];
+            float lv[SUB][2];
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+            for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (Q8)
-                        y[nr][e] = fmaf(sc[nr][e], qs[nr][e & 1] * kv[e >> 1], lv[e >> 1]);
-                    else
-                        y[nr][e] = sc[nr][e] * qs[nr][e & 1];
-                    if (edge) {
-                        const int j = 8 * (e >> 1) + g, d = key0 + j - ctx;
-                        if (j >= lim || (d >= 0 && !((seen[nr][e & 1] >> (d & 63)) & 1))) y[nr][e] = -INFINITY;
+                for (int h = 0; h < 2; ++h)   // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
+                    lv[u][h] = Q8 ? lg2(fmaxf_nan(scales[slot * L::KEYS + 16 * u + 8 * h + g], 7.7e-34f)) : 0.0f;
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    const float2 qs = *reinterpret_cast<const float2*>(row_factor + 8 * nr + 2 * t);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = e & 1 ? qs.y : qs.x;
+                        y[u][nr][e] = Q8 ? fmaf(y[u][nr][e], f * kv[u][e >> 1], lv[u][e >> 1]) : y[u][nr][e] * f;
                     }
-                    up |= y[nr][e] > m[nr][e & 1] + AC_MARGIN;   // from a maximum of -inf: any finite score
-                }
-            if (edge) {      // a scale that is no number has reached the rows that see its key in y
+                    if (edge) {
+                        const int lim = limit(u);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (!(fabsf(lv[h]) < INFINITY)) lv[h] = 0.0f;
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 8 * (e >> 1) + g, d = key0 + 16 * u + j - ctx;
+                            if (j >= lim || (d >= 0 && !((seen[8 * nr + 2 * t + (e & 1)] >> (d & 63)) & 1))) y[u][nr][e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) up |= y[u][nr][e] > m[nr][e & 1] + AC_MARGIN;   // from -inf: any finite score
+                }
+                if (edge) {      // a scale that is no number has reached the rows that see its key in y
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!(fabsf(lv[u][h]) < INFINITY)) lv[u][h] = 0.0f;
+                }
             }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float bm = fmaxf(y[nr][e], y[nr][2 + e]);
+                        float bm = fmaxf(y[0][nr][e], y[0][nr][2 + e]);
+#pragma unroll
+                        for (int u = 1; u < SUB; ++u) bm = fmaxf(bm, fmaxf(y[u][nr][e], y[u][nr][2 + e]));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
@@ -491,168 +533,173 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         }
                     }
             }
-            uint32_t pf[NR][2];      // probabilities of (key g, rows 2t, 2t+1) and (key g + 8, ..)
-            float pk[NR][4];
-            bool faint = false;      // an fp16 probability that lost bits
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : Q8 ? m[nr][e & 1] - AC_LIFT : m[nr][e & 1];
-                    if constexpr (Q8) {
-                        const float x = y[nr][e] - mm, p = ex2_ftz(x);
-                        pk[nr][e] = p;
-                        faint |= p != 0.0f && p < 6.1035156e-5f;
-                        l[nr][e & 1] += ex2_ftz(x - lv[e >> 1]);
-                    } else {
-                        pk[nr][e] = ex2_ftz(y[nr][e] - mm);
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (Q8) {
-                        pf[nr][h] = f16x2_bits(pk[nr][2 * h], pk[nr][2 * h + 1]);
-                    } else {
-                        pf[nr][h] = bf16x2(pk[nr][2 * h], pk[nr][2 * h + 1]);
-                        // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
-                        l[nr][0] += __uint_as_float(pf[nr][h] << 16);
-                        l[nr][1] += __uint_as_float(pf[nr][h] & 0xffff0000u);
-                    }
-                }
-            }
 
-            // ---- values
-            uint32_t odd = 0;                    // a value that is not finite at the edge
-            uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys (2t, 2t+1; + 8) exist
-            if (edge) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    km[h] = (8 * h + 2 * t < lim ? 0xffffu : 0u) | (8 * h + 2 * t + 1 < lim ? 0xffff0000u : 0u);
-            }
-            // what does not exist, and what is not finite (its rows see it below), is taken as zero
-            auto clean = [&](uint32_t w, int h) {
-                constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
-                w &= km[h];
-                if (T != GDN_KV_I8) {
-                    if ((w & EXP) == EXP) {
-                        w &= 0xffff0000u;
-                        odd = 1;
-                    }
-                    if ((w & (EXP << 16)) == (EXP << 16)) {
-                        w &= 0xffffu;
-                        odd = 1;
-                    }
-                }
-                return w;
-            };
-            // fragments of columns 16c .. 16c + 15 (8-bit: and of the next 16)
-            constexpr int STEP = Q8 ? 2 : 1;
-            auto values = [&](int c, uint32_t (&f)[STEP][4]) {
-                uint32_t w[4];
-                ldsm_x4_trans(piece_at(vb, Q8 ? c : 2 * c), w);
-                if constexpr (Q8) {
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t pf[NR][2];      // probabilities of (key g, rows 2t, 2t+1) and (key g + 8, ..)
+                float pk[NR][4];
+                bool faint = false;      // an fp16 probability that lost bits
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t x = T == GDN_KV_I8 ? w[2 * u] ^ 0x80808080u : w[2 * u];
-                        const uint32_t z = T == GDN_KV_I8 ? w[2 * u + 1] ^ 0x80808080u : w[2 * u + 1];
-                        f[u][0] = codes_f16<T, 0, 2>(x);     // columns 2g of keys 0-7, 2g + 1, then keys 8-15
-                        f[u][1] = codes_f16<T, 1, 3>(x);
-                        f[u][2] = codes_f16<T, 0, 2>(z);
-                        f[u][3] = codes_f16<T, 1, 3>(z);
-                    }
-                } else {
+                for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) f[0][u] = w[u];
-                }
-                if (edge) {
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[u][e] = clean(f[u][e], e >> 1);
-                }
-            };
-            // the second product's operand: (keys 2t, 2t+1; row g)
-            uint32_t pt[NR][2];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
-            bool first = true;
-            if constexpr (Q8) {
-                faint = __any_sync(0xffffffffu, faint);
-                if (faint) {         // does fp16 hold anything of this tile?
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) any |= pt[nr][0] | pt[nr][1];
-                    first = __any_sync(0xffffffffu, any != 0);
-                }
-            }
-            if (first) {
-#pragma unroll
-                for (int c = 0; c < KT; c += STEP) {
-                    uint32_t f[STEP][4];
-                    values(c, f);
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u)
-#pragma unroll
-                        for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
-                }
-            }
-            if constexpr (Q8) {
-                if (faint) {
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[nr][h]));
-                            pt[nr][h] = transpose8(bf16x2(pk[nr][2 * h] - r.x, pk[nr][2 * h + 1] - r.y));
+                    for (int e = 0; e < 4; ++e) {
+                        const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : Q8 ? m[nr][e & 1] - AC_LIFT : m[nr][e & 1];
+                        const float x = y[u][nr][e] - mm, p = ex2_ftz(x);
+                        pk[nr][e] = p;
+                        if constexpr (Q8) {
+                            faint |= p != 0.0f && p < 6.1035156e-5f;
+                            l[nr][e & 1] += ex2_ftz(x - lv[u][e >> 1]);
                         }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (Q8) {
+                            pf[nr][h] = f16x2_bits(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                        } else {
+                            pf[nr][h] = bf16x2(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                            // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
+                            l[nr][0] += __uint_as_float(pf[nr][h] << 16);
+                            l[nr][1] += __uint_as_float(pf[nr][h] & 0xffff0000u);
+                        }
+                    }
+                }
+
+                // ---- values
+                const uint32_t vu = vb + u * (16 * L::SLAB);
+                uint32_t odd = 0;                    // a value that is not finite at the edge
+                uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys (2t, 2t+1; + 8) exist
+                if (edge) {
+                    const int lim = limit(u);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        km[h] = (8 * h + 2 * t < lim ? 0xffffu : 0u) | (8 * h + 2 * t + 1 < lim ? 0xffff0000u : 0u);
+                }
+                // what does not exist, and what is not finite (its rows see it below), is taken as zero
+                auto clean = [&](uint32_t w, int h) {
+                    constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
+                    w &= km[h];
+                    if (T != GDN_KV_I8) {
+                        if ((w & EXP) == EXP) {
+                            w &= 0xffff0000u;
+                            odd = 1;
+                        }
+                        if ((w & (EXP << 16)) == (EXP << 16)) {
+                            w &= 0xffffu;
+                            odd = 1;
+                        }
+                    }
+                    return w;
+                };
+                // fragments of columns 16c .. 16c + 15 (8-bit: and of the next 16)
+                constexpr int STEP = Q8 ? 2 : 1;
+                auto values = [&](int c, uint32_t (&f)[STEP][4]) {
+                    uint32_t w[4];
+                    ldsm_x4_trans(piece_at(vu, Q8 ? c : 2 * c), w);
+                    if constexpr (Q8) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint32_t x = T == GDN_KV_I8 ? w[2 * v] ^ 0x80808080u : w[2 * v];
+                            const uint32_t z = T == GDN_KV_I8 ? w[2 * v + 1] ^ 0x80808080u : w[2 * v + 1];
+                            f[v][0] = codes_f16<T, 0, 2>(x);     // columns 2g of keys 0-7, 2g + 1, then keys 8-15
+                            f[v][1] = codes_f16<T, 1, 3>(x);
+                            f[v][2] = codes_f16<T, 0, 2>(z);
+                            f[v][3] = codes_f16<T, 1, 3>(z);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[0][e] = w[e];
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int v = 0; v < STEP; ++v)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[v][e] = clean(f[v][e], e >> 1);
+                    }
+                };
+                // the second product's operand: (keys 2t, 2t+1; row g)
+                uint32_t pt[NR][2];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
+                bool first_pass = true;
+                if constexpr (Q8) {
+                    faint = __any_sync(0xffffffffu, faint);
+                    if (faint) {         // does fp16 hold anything of these keys?
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) any |= pt[nr][0] | pt[nr][1];
+                        first_pass = __any_sync(0xffffffffu, any != 0);
+                    }
+                }
+                if (first_pass) {
 #pragma unroll
                     for (int c = 0; c < KT; c += STEP) {
                         uint32_t f[STEP][4];
                         values(c, f);
 #pragma unroll
-                        for (int u = 0; u < STEP; ++u) {
+                        for (int v = 0; v < STEP; ++v)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[u][e]));
-                                f[u][e] = bf16x2(v.x, v.y);
+                            for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
+                    }
+                }
+                if constexpr (Q8) {
+                    if (faint) {
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[nr][h]));
+                                pt[nr][h] = transpose8(bf16x2(pk[nr][2 * h] - r.x, pk[nr][2 * h + 1] - r.y));
                             }
 #pragma unroll
-                            for (int nr = 0; nr < NR; ++nr) mma16816<GDN_KV_BF16>(o[nr][c + u], f[u], pt[nr][0], pt[nr][1]);
+                        for (int c = 0; c < KT; c += STEP) {
+                            uint32_t f[STEP][4];
+                            values(c, f);
+#pragma unroll
+                            for (int v = 0; v < STEP; ++v) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[v][e]));
+                                    f[v][e] = bf16x2(x.x, x.y);
+                                }
+#pragma unroll
+                                for (int nr = 0; nr < NR; ++nr)
+                                    mma16816<GDN_KV_BF16>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
+                            }
                         }
                     }
                 }
-            }
-            if (T != GDN_KV_I8 && edge && __any_sync(0xffffffffu, odd)) {
-                // rows that see such a key add its term by themselves
-                const unsigned char* vt = ring + slot * L::HALF;
+                if (T != GDN_KV_I8 && edge && __any_sync(0xffffffffu, odd)) {
+                    // rows that see such a key add its term by themselves
+                    const unsigned char* vt = ring + slot * L::HALF;
 #pragma unroll 1
-                for (int j = 0; j < min(lim, AC_TILE); ++j) {
-                    const int d = key0 + j - ctx, src = ((j & 7) << 2) | t;
+                    for (int j = 0; j < min(limit(u), 16); ++j) {
+                        const int d = key0 + 16 * u + j - ctx, src = ((j & 7) << 2) | t;
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
+                        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float p = __shfl_sync(0xffffffffu, j < 8 ? pk[nr][e] : pk[nr][2 + e], src);
-                            if (d >= 0 && !((seen[nr][e] >> (d & 63)) & 1)) continue;
+                            for (int e = 0; e < 2; ++e) {
+                                const float p = __shfl_sync(0xffffffffu, j < 8 ? pk[nr][e] : pk[nr][2 + e], src);
+                                if (d >= 0 && !((seen[8 * nr + 2 * t + e] >> (d & 63)) & 1)) continue;
 #pragma unroll
-                            for (int c = 0; c < KT; ++c)
+                                for (int c = 0; c < KT; ++c)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int col = 16 * c + (Q8 ? 2 * g + h : 8 * h + g);
-                                    float v;
-                                    if constexpr (Q8)
-                                        v = __half2float(__half(__nv_cvt_fp8_to_halfraw(vt[ac_piece<L>(j, col >> 4) + (col & 15)], __NV_E4M3)));
-                                    else
-                                        v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + ac_piece<L>(j, col >> 3) + 2 * (col & 7)));
-                                    if (!(fabsf(v) < INFINITY)) o[nr][c][2 * h + e] += p * v;
-                                }
-                        }
+                                    for (int h = 0; h < 2; ++h) {
+                                        const int col = 16 * c + (Q8 ? 2 * g + h : 8 * h + g), key = 16 * u + j;
+                                        float v;
+                                        if constexpr (Q8)
+                                            v = __half2float(__half(__nv_cvt_fp8_to_halfraw(vt[ac_piece<L>(key, col >> 4) + (col & 15)], __NV_E4M3)));
+                                        else
+                                            v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + ac_piece<L>(key, col >> 3) + 2 * (col & 7)));
+                                        if (!(fabsf(v) < INFINITY)) o[nr][c][2 * h + e] += p * v;
+                                    }
+                            }
+                    }
                 }
             }
             __syncwarp();
-            if (lane == 0 && 2 * i + 1 + L::NS < 2 * mine) issue(2 * i + 1 + L::NS, slot, page_b);
+            if (2 * i + 1 + L::NS < 2 * mine) issue(2 * i + 1 + L::NS, slot, page_b);
             if (++slot == L::NS) {
                 slot = 0;
                 par ^= 1;
@@ -700,7 +747,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const int r = e / (D / 2), c = (e % (D / 2)) * 2;
             float mx = -INFINITY;
             for (int w = 0; w < live; ++w) mx = fmaxf_nan(mx, ml[w * L::ROWS + r].x);
-            float lt = 0.0f, x = 0.0f, y = 0.0f;
+            float lt = 0.0f, x = 0.0f, z = 0.0f;
             for (int w = 0; w < live; ++w) {
                 const float2 v = ml[w * L::ROWS + r];
                 // weight 0, not left out: a NaN (of a score, or 0 times an infinite value) stays
@@ -708,16 +755,16 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 const float2 ov = *reinterpret_cast<const float2*>(join + (w * L::ROWS + r) * L::OLD + c);
                 lt = fmaf(f, v.y, lt);
                 x = fmaf(f, ov.x, x);
-                y = fmaf(f, ov.y, y);
+                z = fmaf(f, ov.y, z);
             }
             if (whole) {
                 const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
                 const int rr = row0 + r, i = rr / a.ratio;
                 if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
                     *reinterpret_cast<uint32_t*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + c) =
-                        bf16x2(x * inv, y * inv);
+                        bf16x2(x * inv, z * inv);
             } else {
-                *reinterpret_cast<float2*>(part + r * (D + 2) + 2 + c) = make_float2(x, y);
+                *reinterpret_cast<float2*>(part + r * (D + 2) + 2 + c) = make_float2(x, z);
                 if (c == 0) *reinterpret_cast<float2*>(part + r * (D + 2)) = make_float2(mx, lt);
             }
         }
@@ -732,23 +779,26 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 }
 
 // Joins the partials of the pairs that lie in more than one run: a block per
-// pair and `step`-th row, D/4 threads across a row and the runs dealt over the
-// others, since one row's chain of loads would take longer than its bytes.
+// pair and row (every gridDim.y-th row), D/4 threads across a row and the runs
+// dealt over the others, since one row's chain of loads would take longer than
+// its bytes.
 template <int D>
 __global__ void __launch_bounds__(AC_JOIN_THREADS)
 attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
     constexpr int W = D / 4, G = AC_JOIN_THREADS / W;
     __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[AC_JOIN_THREADS / 32];
+    __shared__ AcSeq seq[GDN_MAX_SEQS];
     __shared__ float2 ml[AC_MAX_RUNS];
     __shared__ float4 acc[G][W];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    ac_prefix(a, pre, wsum, false);
-    const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total), blocks = pre[s + 1] - pre[s];
-    const int64_t first = pre[s] * a.heads + head * blocks;
-    if (blocks == 0 || first / per == (first + blocks - 1) / per) return;   // written by its one run
-    const AcSeq q = ac_seq(a, s, false);
-    const int c0 = static_cast<int>(first / per), n = static_cast<int>((first + blocks - 1) / per) - c0 + 1;
+    ac_prefix(a, pre, seq, wsum, false);     // inputs of the call: complete before the kernel that is waited for began
+    pdl_wait();
+    const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total), counted = pre[s + 1] - pre[s];
+    // the pair's own blocks, after those that count for its start
+    const int64_t first = pre[s] * a.heads + head * counted + a.start, last = first + counted - a.start - 1;
+    if (counted == 0 || first / per == last / per) return;   // written by its one run
+    const AcSeq q = seq[s];
+    const int c0 = static_cast<int>(first / per), n = static_cast<int>(last / per) - c0 + 1;
     const int c = threadIdx.x % W, grp = threadIdx.x / W;
     for (int rr = blockIdx.y; rr < q.nq * a.ratio; rr += gridDim.y) {
         const int rank = rr / rank_rows, r = rr % rank_rows;
@@ -809,9 +859,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 ac_map_encoder() {
 }
 
 // The pages as [n_pages * heads][slabs][page rows][slab bytes]; a box is the
-// 16 rows of a tile in all slabs.  The page index is its own dimension, so no
+// rows that a tile has in one page, in all slabs.  The page index is its own dimension, so no
 // coordinate grows with the cache's bytes.
-static bool ac_map(CUtensorMap* map, const void* ptr, const gdn_kv_cache& c) {
+static bool ac_map(CUtensorMap* map, const void* ptr, const gdn_kv_cache& c, int box_rows) {
     auto enc = ac_map_encoder();
     if (!enc) return false;
     const bool wide = c.dtype == GDN_KV_BF16;
@@ -820,7 +870,7 @@ static bool ac_map(CUtensorMap* map, const void* ptr, const gdn_kv_cache& c) {
                           static_cast<cuuint64_t>(row / slab), static_cast<cuuint64_t>(c.n_pages * c.n_kv_heads)};
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(slab),
                              static_cast<cuuint64_t>(row) * c.page_tokens};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(dims[0]), AC_TILE, static_cast<cuuint32_t>(dims[2]), 1};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(dims[0]), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(dims[2]), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims,
                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, slab == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -845,25 +895,19 @@ static cudaError_t ac_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
         }) < 0)
         return cudaErrorInvalidDevice;
     CUtensorMap mk, mv;
-    if (!ac_map(&mk, c.k, c) || !ac_map(&mv, c.v, c)) return cudaErrorInvalidValue;
+    a.box = c.page_tokens < L::KEYS ? c.page_tokens : L::KEYS;
+    a.start = L::START;
+    if (!ac_map(&mk, c.k, c, a.box) || !ac_map(&mv, c.v, c, a.box)) return cudaErrorInvalidValue;
     const int rows = a.max_q * a.ratio, pairs = a.n_seqs * a.heads;
     a.ranks = (rows + L::ROWS - 1) / L::ROWS;
     a.runs = AC_MAX_RUNS / a.ranks;
-    attn_cache_kernel<D, T, NR><<<static_cast<unsigned>(a.runs * a.ranks), L::THREADS, L::BYTES + 1024, st>>>(mk, mv, a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_dependent(attn_cache_kernel<D, T, NR>, dim3(static_cast<unsigned>(a.runs * a.ranks)), dim3(L::THREADS),
+                                     L::BYTES + 1024, st, mk, mv, a);
     if (e != cudaSuccess) return e;
     // a row per block, up to a few blocks per SM
     const int y = pairs >= 8 * AC_MAX_RUNS ? 1 : 8 * AC_MAX_RUNS / pairs < rows ? 8 * AC_MAX_RUNS / pairs : rows;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y), 1);
-    cfg.blockDim = dim3(AC_JOIN_THREADS, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_cache_join_kernel<D>, a, static_cast<int>(L::ROWS));
+    return launch_dependent(attn_cache_join_kernel<D>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y)),
+                            dim3(AC_JOIN_THREADS), 0, st, a, static_cast<int>(L::ROWS));
 }
 
 template <int D, int NR>

@@ -99,6 +99,8 @@ __device__ __forceinline__ void e4m3_pair(uint32_t w, float& lo, float& hi) {
 template <int D, int T, bool VEC>
 __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const __grid_constant__ KvArgs a) {
     constexpr int G = D / 8, RB = KV_THREADS / G;
+    pdl_wait();
+    pdl_trigger();
     const int sub = threadIdx.x % G, side = blockIdx.y;
     const uint16_t* src = side ? a.v : a.k;
     const int64_t ld = side ? a.ld_v : a.ld_k, n_rows = a.n * a.heads;
@@ -162,6 +164,8 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const __grid_const
 template <int D, int T, bool VEC>
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const __grid_constant__ KvArgs a) {
     constexpr int G = D / 8, RB = KV_THREADS / G;
+    pdl_wait();
+    pdl_trigger();
     const int sub = threadIdx.x % G, side = blockIdx.y;
     const void* codes = side ? a.cv : a.ck;
     const float* scales = side ? a.sv : a.sk;
@@ -237,11 +241,9 @@ static cudaError_t kv_launch(bool write, const KvArgs& a, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((a.n * a.heads + ROWS - 1) / ROWS), 2);
     const bool vec = a.ld_k % 8 == 0 && a.ld_v % 8 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.v) % 16 == 0;
-    if (write)
-        vec ? kv_write_kernel<D, T, true><<<grid, KV_THREADS, 0, st>>>(a) : kv_write_kernel<D, T, false><<<grid, KV_THREADS, 0, st>>>(a);
-    else
-        vec ? kv_read_kernel<D, T, true><<<grid, KV_THREADS, 0, st>>>(a) : kv_read_kernel<D, T, false><<<grid, KV_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    auto kernel = write ? (vec ? kv_write_kernel<D, T, true> : kv_write_kernel<D, T, false>)
+                        : (vec ? kv_read_kernel<D, T, true> : kv_read_kernel<D, T, false>);
+    return launch_dependent(kernel, grid, dim3(KV_THREADS), 0, st, a);
 }
 
 template <int D>

@@ -51,6 +51,8 @@ template <int K>
 __global__ void __launch_bounds__(ROPE_THREADS)
 rope_vec_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant__ RopeArgs a) {
     extern __shared__ float2 table[];   // [tokens of the run][rot / 2]
+    pdl_wait();
+    pdl_trigger();
     const int half = t.rot / 2, heads = a.hq + a.hk, c = threadIdx.x;
     const int64_t rows = a.n * heads, r0 = static_cast<int64_t>(blockIdx.x) * (blockDim.y * K);
     const int64_t t0 = r0 / heads, r1 = min(r0 + static_cast<int64_t>(blockDim.y) * K, rows);
@@ -121,6 +123,8 @@ rope_vec_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant_
 __global__ void __launch_bounds__(ROPE_THREADS)
 rope_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant__ RopeArgs a) {
     __shared__ float2 cs[GDN_ROPE_MAX_PAIRS];
+    pdl_wait();
+    pdl_trigger();
     const int64_t tok = blockIdx.x;
     const int half = t.rot / 2, per = half + a.d - t.rot;
     const int pos = a.pos[tok];
@@ -151,20 +155,17 @@ cudaError_t launch_rope(const gdn_rope_table& t, const int32_t* pos, int64_t n, 
     auto pieces = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
     const int units = d / 16;
     if (t.rot % 16 || d % 16 || !pieces(q, ld_q) || !pieces(qo, ld_qo) || !pieces(k, ld_k) || !pieces(ko, ld_ko)) {
-        rope_kernel<<<static_cast<unsigned>(n), ROPE_THREADS, 0, st>>>(t, a);
-        return cudaGetLastError();
+        return launch_dependent(rope_kernel, dim3(static_cast<unsigned>(n)), dim3(ROPE_THREADS), 0, st, t, a);
     }
     const dim3 block(static_cast<unsigned>(units), static_cast<unsigned>(ROPE_THREADS / units));
     const int64_t rows = n * (hq + hk);
     auto smem = [&](int kk) { return ((block.y * kk - 1) / (hq + hk) + 2) * (t.rot / 2) * sizeof(float2); };
     auto grid = [&](int kk) { return static_cast<unsigned>((rows + block.y * kk - 1) / (block.y * kk)); };
     if (smem(4) <= 40960 && grid(4) >= 608)
-        rope_vec_kernel<4><<<grid(4), block, smem(4), st>>>(t, a);
-    else if (smem(2) <= 40960 && grid(2) >= 608)
-        rope_vec_kernel<2><<<grid(2), block, smem(2), st>>>(t, a);
-    else
-        rope_vec_kernel<1><<<grid(1), block, smem(1), st>>>(t, a);
-    return cudaGetLastError();
+        return launch_dependent(rope_vec_kernel<4>, dim3(grid(4)), block, smem(4), st, t, a);
+    if (smem(2) <= 40960 && grid(2) >= 608)
+        return launch_dependent(rope_vec_kernel<2>, dim3(grid(2)), block, smem(2), st, t, a);
+    return launch_dependent(rope_vec_kernel<1>, dim3(grid(1)), block, smem(1), st, t, a);
 }
 
 int read_and_clear_rope_error() {

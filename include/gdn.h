@@ -477,7 +477,8 @@ int gdn_kv_read(const gdn_kv_cache *cache, const int64_t *slots, int64_t n_token
  *   block_table  device int32 [n_seqs] rows of max_blocks, ld_table apart: the
  *                page of tokens [b * page_tokens, (b+1) * page_tokens) of
  *                sequence s
- *   lens         device int32 [n_seqs], at most max_blocks * page_tokens
+ *   lens         device int32 [n_seqs], at most max_blocks * page_tokens,
+ *                which is at most 2^30
  *   max_q        1 .. GDN_MAX_NEW; n_q_heads / n_kv_heads <= 16
  *   scale <= 0 means head_dim^-1/2
  *   workspace    device, 256-byte aligned, ws_bytes >=
