@@ -71,6 +71,7 @@ size_t attn_cache_workspace_bytes(const gdn_kv_cache&, int64_t, int);
 int read_and_clear_rope_error();
 int read_and_clear_kv_error();
 int read_and_clear_attn_cache_error();
+int read_and_clear_attn_tree_error();
 int read_and_clear_gemm_error();
 int read_and_clear_delta_error();
 int read_and_clear_q4k_error();
@@ -1136,7 +1137,8 @@ int gdn_sync_status(void* stream) {
     const int ncode = read_and_clear_norm_error();
     const int pcode = read_and_clear_rope_error();
     const int kcode = read_and_clear_kv_error();
-    const int xcode = read_and_clear_attn_cache_error();
+    const int fcode = read_and_clear_attn_cache_error(), tcode = read_and_clear_attn_tree_error();
+    const int xcode = fcode ? fcode : tcode;
     if (kcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped");
     if (xcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_attn_cache: an offset, length or page out of range was skipped");
     const int words[] = {read_and_clear_q4k_error(), read_and_clear_q6k_error(), read_and_clear_quant_error(),

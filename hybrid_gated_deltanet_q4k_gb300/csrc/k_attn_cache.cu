@@ -40,90 +40,11 @@
 // p' - fp16(p') in bf16, whose exponents reach as far as fp32's, in a second
 // pass, and leaves out the first where fp16 holds nothing.  q goes to fp16 times a power of two per row that puts its largest
 // element in [2^14, 2^15): elements below 2^-38 of it are lost.
-#include "common.cuh"
-#include "tma.cuh"
-
-#include <cuda_fp8.h>
-
-#include <mutex>
+#include "attn_cache.cuh"
 
 namespace gdn {
 
-static __device__ int g_attn_cache_error;
-
-constexpr int AC_BLOCK = 128;           // keys of a block
-constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
 constexpr int AC_RING = 192 * 1024;     // bytes of tiles in flight per CTA
-constexpr int AC_JOIN_THREADS = 256;
-constexpr float AC_MARGIN = 4.0f;
-constexpr float AC_LIFT = 11.0f;        // fp16 probabilities times 2^11
-constexpr float LOG2E = 1.4426950408889634f;
-
-struct AttCacheArgs {
-    int64_t n_pages;
-    int heads, page, page_shift, ratio, hq;
-    const float *sk, *sv;
-    const uint16_t* q;
-    uint16_t* o;
-    int64_t ld_q, ld_o, ld_table, n_tokens;
-    const int32_t *cu, *table, *lens;
-    const uint64_t* tree;
-    int n_seqs, max_q, max_blocks;
-    int runs, ranks;    // runs of blocks, and row tiles of a pair (a CTA per run and rank of rows)
-    int start;          // blocks that each pair counts more than it has
-    int box;            // keys of one copy
-    float sl2;          // scale * log2(e)
-    float* part;        // [runs * ranks][2][rows][D + 2] partials
-};
-
-// A sequence as the kernels see it, its device-held numbers forced into range.
-struct AcSeq {
-    int tok, nq, len;
-};
-__device__ __forceinline__ AcSeq ac_seq(const AttCacheArgs& a, int s, bool report) {
-    AcSeq r;
-    const int lo = a.cu ? a.cu[s] : s * a.max_q, hi = a.cu ? a.cu[s + 1] : lo + a.max_q;
-    const int64_t cap = static_cast<int64_t>(a.max_blocks) * a.page;
-    const int len = a.lens[s];
-    const bool ok = lo >= 0 && hi >= lo && hi <= a.n_tokens && hi - lo <= a.max_q;
-    r.tok = ok ? lo : 0;
-    r.nq = ok ? hi - lo : 0;
-    r.len = len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
-    if (report && (!ok || r.len != len)) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
-    return r;
-}
-// Blocks of each of its pairs (at least one where there is a row to write), and as they count.
-__device__ __forceinline__ int ac_blocks(const AcSeq& s) { return s.len == 0 ? 1 : (s.len - 1) / AC_BLOCK + 1; }
-
-// The counted blocks before each sequence (of one head), pre[0 .. n_seqs], and
-// the sequences, by all threads of a CTA.
-static_assert(GDN_MAX_SEQS <= AC_JOIN_THREADS, "a thread per sequence");
-__device__ __forceinline__ void ac_prefix(const AttCacheArgs& a, int64_t* pre, AcSeq* seq, int64_t* wsum, bool report) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = (a.n_seqs + 31) / 32;
-    int64_t v = 0;
-    if (t < a.n_seqs) {
-        const AcSeq q = ac_seq(a, t, report);
-        seq[t] = q;
-        v = q.nq == 0 ? 0 : ac_blocks(q) + a.start;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    if (warps > 1) {
-        if (lane == 31 && warp < warps) wsum[warp] = v;
-        __syncthreads();
-        for (int w = 0; w < min(warp, warps); ++w) v += wsum[w];
-    }
-    if (t < a.n_seqs) pre[t + 1] = v;
-    if (t == 0) pre[0] = 0;
-    __syncthreads();
-}
-// Blocks per run, from the total over all pairs.
-__device__ __forceinline__ int64_t ac_run_blocks(const AttCacheArgs& a, int64_t total) {
-    return total < a.runs ? 1 : (total + a.runs - 1) / a.runs;
-}
 
 // ------------------------------------------------------------ tensor-core steps
 
@@ -146,45 +67,11 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
-// Two codes of w (bytes I and J) as fp16 values; int8 codes come with the top bit flipped.
-template <int T, int I, int J>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-    if constexpr (T == GDN_KV_I8) {
-        const uint32_t b = __byte_perm(w, 0x64646464u, 0x4040u | (J << 8) | I);   // 1024 + (code + 128)
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const uint32_t b = __byte_perm(w, 0, (J << 4) | I);
-        uint32_t r;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(b)));
-        return r;
-    }
-}
-
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Whole warp: an 8 x 8 matrix of 16-bit values, two of row lane / 4 per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
-        : "memory");
 }
 
 // ------------------------------------------------------------ shared memory
@@ -275,12 +162,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const int64_t end = at + per < total ? at + per : total;
     if (at >= end) return;
 
-    // the sequence of the first block: the last s with pre[s] * heads <= at
-    int s = 0;
-    for (int hi = a.n_seqs - 1; s < hi;) {
-        const int mid = (s + hi + 1) >> 1;
-        if (pre[mid] * a.heads <= at) s = mid; else hi = mid - 1;
-    }
+    int s = ac_seq_of(a, pre, at);
     int slot = 0;               // the next half tile of this warp's ring and its phase
     uint32_t par = 0;
     bool dead = false;          // a wait ran out
@@ -293,20 +175,15 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const uint32_t koff = ac_piece<L>(kr, kc), voff = ac_piece<L>(vr, vc);
     auto piece_at = [](uint32_t b, int c) { return (b ^ ((c & 7) << 4)) + (c >> 3) * (L::KEYS * 128); };
 
-    while (at < end) {
-        while (pre[s + 1] * a.heads <= at) ++s;
-        const AcSeq q = seq[s];
-        const int counted = static_cast<int>(pre[s + 1] - pre[s]), blocks = counted - a.start;
-        const int head = static_cast<int>((at - pre[s] * a.heads) / counted);
-        const int64_t first = pre[s] * a.heads + static_cast<int64_t>(head) * counted;
-        const int b0 = max(static_cast<int>(at - first) - a.start, 0);
-        const int b1 = end - first < counted ? max(static_cast<int>(end - first) - a.start, 0) : blocks;
-        at = first + counted < end ? first + counted : end;
+    AcPiece pc;
+    while (ac_next(a, pre, seq, at, end, s, pc)) {
+        const AcSeq q = pc.q;
+        const int head = pc.head, b0 = pc.b0, b1 = pc.b1;
         const int row0 = rank * L::ROWS, rows = min(q.nq * a.ratio - row0, L::ROWS);
-        if (rows <= 0 || b0 >= b1) continue;
+        if (rows <= 0) continue;
         const int t0 = b0 * L::TILES, t1 = min(b1 * L::TILES, q.len == 0 ? 1 : (q.len - 1) / L::KEYS + 1);   // tiles
         const int ctx = q.len - q.nq;      // keys every row sees
-        const int32_t* table = a.table + s * a.ld_table;
+        const int32_t* table = a.table + pc.s * a.ld_table;
 
         // ---- copies: half tile j (keys of tile j / 2, then its values)
         // follows j - NS in its slot.  A tile may lie in several pages: lane p
@@ -741,7 +618,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 }
         }
         __syncthreads();
-        const bool whole = b0 == 0 && b1 == blocks;
+        const bool whole = b0 == 0 && b1 == pc.blocks;
         float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (b0 > 0 ? 0 : 1)) * L::ROWS * (D + 2);
         for (int e = tid; e < rows * (D / 2); e += L::THREADS) {
             const int r = e / (D / 2), c = (e % (D / 2)) * 2;
@@ -845,45 +722,26 @@ attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
 
 // ------------------------------------------------------------ host
 
-static PFN_cuTensorMapEncodeTiled_v12000 ac_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
+cudaError_t launch_attn_tree(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st);   // k_attn_tree.cu
+constexpr int AC_TREE_TILE = 128;       // its rows per CTA
 
-// The pages as [n_pages * heads][slabs][page rows][slab bytes]; a box is the
-// rows that a tile has in one page, in all slabs.  The page index is its own dimension, so no
-// coordinate grows with the cache's bytes.
-static bool ac_map(CUtensorMap* map, const void* ptr, const gdn_kv_cache& c, int box_rows) {
-    auto enc = ac_map_encoder();
-    if (!enc) return false;
-    const bool wide = c.dtype == GDN_KV_BF16;
-    const int row = c.head_dim * (wide ? 2 : 1), slab = row < 128 ? row : 128;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(wide ? slab / 2 : slab), static_cast<cuuint64_t>(c.page_tokens),
-                          static_cast<cuuint64_t>(row / slab), static_cast<cuuint64_t>(c.n_pages * c.n_kv_heads)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(slab),
-                             static_cast<cuuint64_t>(row) * c.page_tokens};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(dims[0]), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(dims[2]), 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims,
-               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, slab == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Most rows of one CTA: what the accumulators of a warp leave room for.
-static int ac_most_rows(int d) { return 4096 / d; }
+// The kernel for many rows from this many rows of a pair on (max_q times the
+// heads of a key/value head), where it is the faster one.
+constexpr int AC_TREE_ROWS = 33;
 
 size_t attn_cache_workspace_bytes(const gdn_kv_cache& c, int64_t n_tokens, int hq) {
-    (void)n_tokens;
-    (void)hq;
-    return static_cast<size_t>(AC_MAX_RUNS) * 2 * ac_most_rows(c.head_dim) * (c.head_dim + 2) * 4;
+    // partials of the rows of one CTA: 4096 / D at most in the kernel for few rows
+    const int rows = n_tokens * (hq / c.n_kv_heads) >= AC_TREE_ROWS ? AC_TREE_TILE : 4096 / c.head_dim;
+    return static_cast<size_t>(AC_MAX_RUNS) * 2 * rows * (c.head_dim + 2) * 4;
+}
+
+template <int D>
+static cudaError_t ac_join(const AttCacheArgs& a, int rank_rows, cudaStream_t st) {
+    // a row per block, up to a few blocks per SM
+    const int rows = a.max_q * a.ratio, pairs = a.n_seqs * a.heads;
+    const int y = pairs >= 8 * AC_MAX_RUNS ? 1 : 8 * AC_MAX_RUNS / pairs < rows ? 8 * AC_MAX_RUNS / pairs : rows;
+    return launch_dependent(attn_cache_join_kernel<D>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y)),
+                            dim3(AC_JOIN_THREADS), 0, st, a, rank_rows);
 }
 
 template <int D, int T, int NR>
@@ -897,17 +755,13 @@ static cudaError_t ac_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
     CUtensorMap mk, mv;
     a.box = c.page_tokens < L::KEYS ? c.page_tokens : L::KEYS;
     a.start = L::START;
-    if (!ac_map(&mk, c.k, c, a.box) || !ac_map(&mv, c.v, c, a.box)) return cudaErrorInvalidValue;
-    const int rows = a.max_q * a.ratio, pairs = a.n_seqs * a.heads;
-    a.ranks = (rows + L::ROWS - 1) / L::ROWS;
+    if (!ac_map(&mk, c.k, c, a.box, L::NSLAB) || !ac_map(&mv, c.v, c, a.box, L::NSLAB)) return cudaErrorInvalidValue;
+    a.ranks = (a.max_q * a.ratio + L::ROWS - 1) / L::ROWS;
     a.runs = AC_MAX_RUNS / a.ranks;
     cudaError_t e = launch_dependent(attn_cache_kernel<D, T, NR>, dim3(static_cast<unsigned>(a.runs * a.ranks)), dim3(L::THREADS),
                                      L::BYTES + 1024, st, mk, mv, a);
     if (e != cudaSuccess) return e;
-    // a row per block, up to a few blocks per SM
-    const int y = pairs >= 8 * AC_MAX_RUNS ? 1 : 8 * AC_MAX_RUNS / pairs < rows ? 8 * AC_MAX_RUNS / pairs : rows;
-    return launch_dependent(attn_cache_join_kernel<D>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y)),
-                            dim3(AC_JOIN_THREADS), 0, st, a, static_cast<int>(L::ROWS));
+    return ac_join<D>(a, L::ROWS, st);
 }
 
 template <int D, int NR>
@@ -928,6 +782,7 @@ cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t 
     a.page_shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
     a.ratio = hq / c.n_kv_heads;
     a.hq = hq;
+    a.v = c.v;
     a.sk = c.k_scale;
     a.sv = c.v_scale;
     a.q = q;
@@ -941,11 +796,16 @@ cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t 
     a.lens = lens;
     a.tree = tree;
     a.n_seqs = n_seqs;
-    a.max_q = max_q;
+    a.max_q = max_q < n_tokens ? max_q : static_cast<int>(n_tokens);
     a.max_blocks = max_blocks;
     a.sl2 = scale * LOG2E;
     a.part = static_cast<float*>(workspace);
-    const int rows = max_q * a.ratio;
+    const int rows = a.max_q * a.ratio;
+    if (rows >= AC_TREE_ROWS) {
+        const cudaError_t e = launch_attn_tree(c, a, st);
+        if (e != cudaSuccess) return e;
+        return c.head_dim == 64 ? ac_join<64>(a, AC_TREE_TILE, st) : c.head_dim == 128 ? ac_join<128>(a, AC_TREE_TILE, st) : ac_join<256>(a, AC_TREE_TILE, st);
+    }
     if (c.head_dim == 256) return rows <= 8 ? ac_launch_t<256, 1>(c, a, st) : ac_launch_t<256, 2>(c, a, st);
     if (c.head_dim == 128)
         return rows <= 8 ? ac_launch_t<128, 1>(c, a, st) : rows <= 16 ? ac_launch_t<128, 2>(c, a, st) : ac_launch_t<128, 4>(c, a, st);

@@ -1,0 +1,650 @@
+// Cache attention of many rows (trees of drafts, long chains): the same
+// operator, partition and partials as the kernel for few rows, on the
+// fifth-generation tensor cores, 128 rows per CTA.
+//
+// With R rows of a (sequence, key/value head) pair every cached byte of an
+// 8-bit cache is worth 4 R flops (of bf16, 2 R): from some tens of rows on the
+// kernel for few rows, which reads the cache once per 8 to 32 rows, is bound by
+// L2 and its own instructions, while 128 rows of one tcgen05 instruction cost
+// the cache one read.  Pairs of more than 128 rows take several CTAs with the
+// same run of blocks; they walk it at the same time, so the cache comes from L2
+// for all but one.
+//
+// Per block of BN keys (64 for heads of 256, else 128; row r = TMEM lane r):
+//   S = Q K^T      M = 128, N = BN, K = D; both from shared memory, into TMEM
+//   softmax warps  two threads per row, BN / 2 scores each; P back into TMEM
+//                  (two buffers), the running maximum raised only past a margin
+//   O += P V       M = 128, N = D, K = BN; P from TMEM, V [key][d] as the
+//                  MN-major operand, the image that the copy writes: no transpose
+// The pages are bf16: TMA writes the operand images (128-byte swizzle).  8-bit
+// codes go through a ring of raw tiles that four warps turn into fp16 images
+// (exact); the row scales stay out of the products, as in the other kernel: a
+// key's multiplies its scores, a value's goes into the exponent of p'.  fp16
+// probabilities are p' 2^11, exact to 2^-11 down to 2^-25 of the largest and
+// zero below 2^-36 of it.
+//
+// Warps: 0 copies the keys (8-bit: both), 1 allocates TMEM and issues the
+// products in whichever order they become ready, 2-9 softmax, 10 copies the
+// values (8-bit: 10-13 convert).  Every wait is bounded; after one runs out the
+// CTA stops issuing, lets copies and products finish and returns with the error
+// word set.
+#include "attn_cache.cuh"
+#include "tcgen05.cuh"
+
+namespace gdn {
+
+constexpr int AT_ROWS = 128;
+constexpr int AT_SM_WARPS = 8;
+constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
+
+template <int D, int T>
+struct AtSmem {
+    static constexpr bool Q8 = T != GDN_KV_BF16;
+    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int THREADS = 32 * (2 + AT_SM_WARPS + (Q8 ? 4 : 1));
+    static constexpr int ROW = D * (Q8 ? 1 : 2);
+    static constexpr int SLAB = ROW < 128 ? ROW : 128;      // bytes of a cached row in one slab of the copies
+    static constexpr int NSLAB = ROW / SLAB;
+    static constexpr int RAW = BN * ROW;                    // a tile as cached
+    static constexpr int S16 = D / 64;                      // slabs of an operand image: [rows][64 x 16 bit]
+    static constexpr int TILE = BN * D * 2;                 // a K or V image
+    static constexpr int QB = AT_ROWS * D * 2;
+    // images of K (and of V) held at once, raw tiles in flight
+    static constexpr int ST = Q8 ? 1 : D == 64 ? 4 : 2;
+    static constexpr int RS = !Q8 ? 1 : D == 256 ? 5 : D == 128 ? 6 : 8;
+    static constexpr int Q0 = 0;
+    static constexpr int K0 = QB;
+    static constexpr int V0 = K0 + ST * TILE;
+    static constexpr int R0 = V0 + ST * TILE;
+    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN / 2]
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // row maxima: [2 rounds][2 halves][128]
+    static constexpr int L0 = X0 + 4 * AT_ROWS * 4;         // row sums of each half
+    static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
+    static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
+    static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
+    static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
+    static constexpr int QF = 0, SF = 1, SC = 2, PF = 3, PV = 5, FIN = 7, KF = 8, KE = KF + ST, VF = KE + ST, VE = VF + ST,
+                         RF = VE + ST, RE = RF + RS, NBAR = RE + RS;
+    static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite
+    static constexpr int BYTES = MISC + 16;
+    // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
+    static constexpr int DYN = BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024;
+    static_assert(DYN <= 227 * 1024, "shared memory of a CTA");
+    static constexpr uint32_t PCOL = BN, OCOL = 2 * BN;     // TMEM columns: S 0 .. BN-1, P two buffers of BN / 2, O
+    static_assert(2 * BN + D <= 512, "TMEM columns");
+};
+
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (*abort) return false;
+    if (mbar_wait_bounded(bar, parity, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) return true;
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool at_ready(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void at_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
+
+template <int D, int T>
+__global__ void __launch_bounds__(AtSmem<D, T>::THREADS, 1)
+attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ AttCacheArgs a) {
+    using L = AtSmem<D, T>;
+    constexpr int BN = L::BN, ST = L::ST, RS = L::RS, HN = BN / 2;
+    constexpr bool Q8 = L::Q8;
+    extern __shared__ __align__(1024) unsigned char smb[];
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smb) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::B0);
+    int64_t* pre = reinterpret_cast<int64_t*>(base + L::P0);
+    AcSeq* seq = reinterpret_cast<AcSeq*>(base + L::T0);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(base + L::MISC);
+    volatile int* abort = reinterpret_cast<volatile int*>(base + L::MISC + 4);
+    unsigned long long* odd = reinterpret_cast<unsigned long long*>(base + L::MISC + 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t sbase = smem_addr(base);
+
+    if (tid == 0) {
+        for (int i = 0; i < L::NBAR; ++i) {
+            int n = 1;
+            if (i == L::QF || i == L::SC || i == L::PF || i == L::PF + 1) n = AT_SM_THREADS;
+            if (Q8 && ((i >= L::KF && i < L::KE) || (i >= L::VF && i < L::VE))) n = 128;   // the converting threads
+            if (Q8 && i >= L::RE) n = 128;
+            mbar_init_cta(bars + i, n);
+        }
+        mbar_init_fence();
+        *abort = 0;
+        *odd = 0;
+    }
+    if (warp == 1) t5::alloc(tslot, 512);
+    pdl_wait();
+    pdl_trigger();
+    t5::fence_before();
+    ac_prefix(a, pre, seq, reinterpret_cast<int64_t*>(base + L::W0), blockIdx.x == 0);   // ends with a barrier
+    t5::fence_after();
+    const uint32_t tmem = *tslot;
+    const int run = blockIdx.x / a.ranks, row0 = (blockIdx.x % a.ranks) * AT_ROWS;
+    const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total);
+    int64_t at = run * per;
+    const int64_t end = at + per < total ? at + per : total;
+    int s = at < end ? ac_seq_of(a, pre, at) : 0;
+    AcPiece pc;
+    // every role walks the same pieces; a piece is `nb` tiles of BN keys from tile t0
+    int t0 = 0, nb = 0, rows = 0;
+    auto next = [&]() {
+        while (ac_next(a, pre, seq, at, end, s, pc)) {
+            rows = min(pc.q.nq * a.ratio - row0, AT_ROWS);
+            if (rows <= 0) continue;
+            t0 = pc.b0 * (AC_BLOCK / BN);
+            nb = min(pc.b1 * (AC_BLOCK / BN), pc.q.len == 0 ? 1 : (pc.q.len - 1) / BN + 1) - t0;
+            return true;
+        }
+        return false;
+    };
+    // copies of a tile: the rows of each of its pages, by slab; lane = page * NSLAB + slab
+    const int copies = BN / a.box;
+    uint32_t n = 0;   // tiles so far, over all pieces
+
+    if (warp == 0 || (!Q8 && warp == 10)) {
+        // ------------------------------------------------------------ TMA
+        const int p = lane / L::NSLAB, slab = lane % L::NSLAB;
+        const bool on = lane < copies * L::NSLAB;
+        const int off = on ? p * a.box : 0;
+        bool ok = true;
+        while (ok && next()) {
+            const int32_t* table = a.table + pc.s * a.ld_table;
+            auto page_of = [&](int j) { return table[min(((t0 + j) * BN + off) >> a.page_shift, a.max_blocks - 1)]; };
+            auto load = [&](const CUtensorMap* map, uint64_t* bar, int dst, int bytes, int j, int page) {
+                const int row = ((t0 + j) * BN + off) & (a.page - 1);
+                const int pg = page >= 0 && page < a.n_pages ? page : 0;   // an unseen page: any rows, all of them masked
+                if (lane == 0) mbar_expect_tx(bar, bytes);
+                if (on) tma_load_4d(base + dst + slab * (BN * L::SLAB) + off * L::SLAB, map, bar, 0, row, slab, pg * a.heads + pc.head);
+            };
+            int page = page_of(0);
+            for (int j = 0; ok && j < nb; ++j) {
+                const int ahead = page_of(min(j + 1, nb - 1));
+                if constexpr (Q8) {
+                    // raw tiles: keys, then values
+                    for (int v = 0; ok && v < 2; ++v) {
+                        const uint32_t m = 2 * n + v, sl = m % RS;
+                        if (m >= RS) ok = __all_sync(0xffffffffu, at_wait(bars + L::RE + sl, (m / RS - 1) & 1, abort));
+                        if (ok) load(v ? &mv : &mk, bars + L::RF + sl, L::R0 + sl * L::RAW, L::RAW, j, page);
+                    }
+                } else {
+                    const bool v = warp == 10;
+                    const uint32_t sl = n % ST;
+                    if (n >= ST) ok = __all_sync(0xffffffffu, at_wait(bars + (v ? L::VE : L::KE) + sl, (n / ST - 1) & 1, abort));
+                    if (ok) load(v ? &mv : &mk, bars + (v ? L::VF : L::KF) + sl, (v ? L::V0 : L::K0) + sl * L::TILE, L::TILE, j, page);
+                }
+                page = ahead;
+                ++n;
+            }
+        }
+    } else if (Q8 && warp >= 10) {
+        // ------------------------------------------------------------ codes to fp16 images
+        bool ok = true;
+        const int ct = tid - 320;
+        while (ok && next()) {
+            for (int j = 0; ok && j < nb; ++j) {
+                for (int v = 0; ok && v < 2; ++v) {
+                    const uint32_t m = 2 * n + v, sl = m % RS;
+                    ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort);
+                    if (ok && n >= 1) ok = at_wait(bars + (v ? L::VE : L::KE), (n - 1) & 1, abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const unsigned char* src = base + L::R0 + sl * L::RAW;
+                    unsigned char* dst = base + (v ? L::V0 : L::K0);
+                    // 16 codes per step; consecutive threads take consecutive keys
+#pragma unroll 4
+                    for (int e = ct; e < BN * (D / 16); e += 128) {
+                        const int key = e % BN, c = e / BN;
+                        uint4 w;
+                        if constexpr (L::SLAB == 128)
+                            w = *reinterpret_cast<const uint4*>(src + (c >> 3) * (BN * 128) + key * 128 + (((c ^ key) & 7) << 4));
+                        else
+                            w = *reinterpret_cast<const uint4*>(src + key * 64 + (((c ^ (key >> 1)) & 3) << 4));
+                        if constexpr (T == GDN_KV_I8) {
+                            w.x ^= 0x80808080u;
+                            w.y ^= 0x80808080u;
+                            w.z ^= 0x80808080u;
+                            w.w ^= 0x80808080u;
+                        }
+                        unsigned char* row = dst + (c >> 2) * (BN * 128) + key * 128;
+                        const int c0 = (2 * c) & 7;
+                        *reinterpret_cast<uint4*>(row + (((c0 ^ key) & 7) << 4)) =
+                            make_uint4(codes_f16<T, 0, 1>(w.x), codes_f16<T, 2, 3>(w.x), codes_f16<T, 0, 1>(w.y), codes_f16<T, 2, 3>(w.y));
+                        *reinterpret_cast<uint4*>(row + ((((c0 + 1) ^ key) & 7) << 4)) =
+                            make_uint4(codes_f16<T, 0, 1>(w.z), codes_f16<T, 2, 3>(w.z), codes_f16<T, 0, 1>(w.w), codes_f16<T, 2, 3>(w.w));
+                    }
+                    fence_proxy_async_smem();
+                    at_arrive(bars + (v ? L::VF : L::KF));
+                    at_arrive(bars + L::RE + sl);
+                }
+                ++n;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // S of a tile needs its K image and the softmax to have read the last
+        // S; P V needs P and the V image.  One thread polls both; a stall past
+        // 2 s sets the error word.
+        if (lane == 0) {
+            constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
+            constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
+            bool ok = true;
+            uint32_t piece = 0;
+            while (ok && next()) {
+                ok = at_wait(bars + L::QF, piece & 1, abort);
+                ++piece;
+                t5::fence_after();
+                int ns = 0, np = 0;
+                uint64_t t_last = globaltimer_ns();
+                while (ok && np < nb) {
+                    bool did = false;
+                    const uint32_t is = n + ns, ip = n + np;
+                    if (ns < nb && ns <= np + 1 && (is == 0 || at_ready(bars + L::SC, (is - 1) & 1)) &&
+                        at_ready(bars + L::KF + is % ST, (is / ST) & 1)) {
+                        t5::fence_after();
+                        const uint32_t kt = sbase + L::K0 + (is % ST) * L::TILE;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const int sl = kk >> 2, w = kk & 3;
+                            t5::mma_f16(tmem, t5::desc_sw128(sbase + L::Q0 + sl * (AT_ROWS * 128) + w * 32),
+                                        t5::desc_sw128(kt + sl * (BN * 128) + w * 32), IDS, kk > 0 ? 1u : 0u);
+                        }
+                        t5::commit(bars + L::SF);
+                        t5::commit(bars + L::KE + is % ST);
+                        ++ns;
+                        did = true;
+                    } else if (np < ns && at_ready(bars + L::PF + (ip & 1), (ip >> 1) & 1) &&
+                               at_ready(bars + L::VF + ip % ST, (ip / ST) & 1)) {
+                        t5::fence_after();
+                        const uint32_t vt = sbase + L::V0 + (ip % ST) * L::TILE, pa = tmem + L::PCOL + (ip & 1) * HN;
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            t5::mma_f16_ts(tmem + L::OCOL, pa + kk * 8, t5::desc_sw128_mn(vt + kk * 2048, BN * 128), IDO,
+                                           (np > 0 || kk > 0) ? 1u : 0u);
+                        t5::commit(bars + L::PV + (ip & 1));
+                        t5::commit(bars + L::VE + ip % ST);
+                        ++np;
+                        did = true;
+                    }
+                    if (did) {
+                        t_last = globaltimer_ns();
+                    } else if (*abort || globaltimer_ns() - t_last > 2000000000ull) {
+                        if (!*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
+                        *abort = 1;
+                        ok = false;
+                    }
+                }
+                n += nb;
+            }
+            // every product issued has completed before TMEM is released
+            t5::commit(bars + L::FIN);
+            mbar_wait_bounded(bars + L::FIN, 0, nullptr, 0, 200000000ull);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int quad = warp & 3, half = (warp - 2) >> 2, r = 32 * quad + lane, st = tid - 64;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+        float* xmax = reinterpret_cast<float*>(base + L::X0);
+        float* lsum = reinterpret_cast<float*>(base + L::L0);
+        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * BN;   // this warp's: HN key factors, HN log2 value scales
+        float* vlog = kfac + HN;
+        bool ok = true;
+        while (next()) {
+            const AcSeq q = pc.q;
+            const int ctx = q.len - q.nq, rr = row0 + r, tok = rr / a.ratio;
+            const bool on = r < rows;
+            const int hq = pc.head * a.ratio + rr - tok * a.ratio;
+            const int32_t* table = a.table + pc.s * a.ld_table;
+            uint64_t seen = !on ? 0 : a.tree ? a.tree[q.tok + tok] : tok >= 63 ? ~0ull : (1ull << (tok + 1)) - 1;
+
+            // ---- Q to shared memory: this thread half a row.  The last piece's products have read theirs.
+            float factor = a.sl2;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(q.tok + (on ? tok : 0)) * a.ld_q +
+                                                                  (on ? hq : 0) * D + half * (D / 2));
+                unsigned char* dst = base + L::Q0 + r * 128;
+                float up = 1.0f;
+                if constexpr (Q8) {
+                    float amax = 0.0f;
+#pragma unroll 4
+                    for (int c = 0; c < D / 16; ++c) {
+                        const uint4 w = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+                    }
+                    lsum[half * AT_ROWS + r] = amax;
+                    at_bar_softmax();
+                    amax = fmaxf(amax, lsum[(half ^ 1) * AT_ROWS + r]);
+                    const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
+                    up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+                    factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+                }
+#pragma unroll 4
+                for (int c = 0; c < D / 16; ++c) {
+                    uint4 w = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (Q8) {
+                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = f16x2_bits(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+                        w = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    const int cc = half * (D / 16) + c;
+                    *reinterpret_cast<uint4*>(dst + (cc >> 3) * (AT_ROWS * 128) + (((cc ^ r) & 7) << 4)) = w;
+                }
+                fence_proxy_async_smem();
+                at_arrive(bars + L::QF);
+            }
+
+            // ---- pages (by lane, of the tile's copies) and, for 8-bit caches, the scales of this
+            // half's keys (by lane), read ahead
+            const int pl = (lane < copies ? lane : 0) * a.box;
+            auto page_of = [&](int j) { return table[min(((t0 + min(j, nb - 1)) * BN + pl) >> a.page_shift, a.max_blocks - 1)]; };
+            constexpr int KL = HN / 32;     // keys per lane
+            float ksn[KL], vsn[KL];
+            auto scales_of = [&](int j, int page) {
+#pragma unroll
+                for (int x = 0; x < KL; ++x) {
+                    const int key = half * HN + 32 * x + lane;
+                    int pg = __shfl_sync(0xffffffffu, page, key / a.box);
+                    if (pg < 0 || pg >= a.n_pages) pg = 0;
+                    const int64_t row = (static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (((t0 + min(j, nb - 1)) * BN + key) & (a.page - 1));
+                    ksn[x] = a.sk[row];
+                    vsn[x] = a.sv[row];
+                }
+            };
+            int page = page_of(0), page1 = page_of(1);
+            if constexpr (Q8) scales_of(0, page);
+
+            float m = -INFINITY, l = 0.0f;
+            uint64_t none = 0;      // new keys this row sees with probability zero
+            for (int j = 0; j < nb; ++j) {
+                const uint32_t i = n + j;
+                const int key0 = (t0 + j) * BN;
+                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 && page < a.n_pages) | (copies < 32 ? ~0u << copies : 0u);
+                const bool edge = key0 + BN > ctx || good != ~0u;
+                if (good != ~0u && warp == 2 && lane < copies && !((good >> lane) & 1) && key0 + pl < q.len)
+                    atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+                if constexpr (Q8) {
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < KL; ++x) {
+                        kfac[32 * x + lane] = ksn[x];
+                        float lv = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
+                        vlog[32 * x + lane] = lv;
+                    }
+                    __syncwarp();
+                    scales_of(j + 1, page1);
+                }
+                page = page1;
+                page1 = page_of(j + 2);
+                auto exists = [&](int key) { return key0 + key < q.len && ((good >> (key / a.box)) & 1); };
+
+                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF, i & 1, abort));
+                float x[HN];
+                if (ok) {
+                    t5::fence_after();
+#pragma unroll
+                    for (int c = 0; c < HN; c += 32) {
+                        float s0[32];
+                        t5::ld32(trow + half * HN + c, s0);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c + e] = s0[e];
+                    }
+                }
+                t5::fence_before();
+                at_arrive(bars + L::SC);   // S is in registers: the next may overwrite it
+
+                float bm = -INFINITY;
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < HN; c += 4) {
+                        if constexpr (Q8) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(kfac + c), v4 = *reinterpret_cast<const float4*>(vlog + c);
+                            x[c] = fmaf(x[c], factor * k4.x, v4.x);
+                            x[c + 1] = fmaf(x[c + 1], factor * k4.y, v4.y);
+                            x[c + 2] = fmaf(x[c + 2], factor * k4.z, v4.z);
+                            x[c + 3] = fmaf(x[c + 3], factor * k4.w, v4.w);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[c + e] *= factor;
+                        }
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < HN; ++c) {
+                            const int key = half * HN + c, d = key0 + key - ctx;
+                            if (!exists(key) || (d >= 0 && !((seen >> (d & 63)) & 1))) x[c] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < HN; ++c) bm = fmaxf(bm, x[c]);
+                }
+                // the row's maximum over both halves
+                xmax[((i & 1) * 2 + half) * AT_ROWS + r] = bm;
+                at_bar_softmax();
+                bm = fmaxf(bm, xmax[((i & 1) * 2 + (half ^ 1)) * AT_ROWS + r]);
+                // P buffer i & 1 is free once P V of tile i - 2 has finished
+                if (i >= 2) ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + (i & 1), ((i - 2) >> 1) & 1, abort));
+                if (ok && j > 0 && __any_sync(0xffffffffu, bm > m + AC_MARGIN)) {
+                    // O is rescaled once P V of tile i - 1 has finished
+                    ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
+                    if (ok) {
+                        const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
+                        m = mn;
+                        l *= f;
+                        t5::fence_after();
+#pragma unroll 1
+                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                            float ov[32];
+                            t5::ld32(trow + L::OCOL + c0, ov);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ov[e] *= f;
+                            t5::st32(trow + L::OCOL + c0, ov);
+                        }
+                    }
+                } else if (j == 0) {
+                    m = bm;
+                }
+                if (ok) {
+                    const float mm = m == -INFINITY ? 0.0f : Q8 ? m - AC_LIFT : m;
+                    uint32_t pk[HN / 2];
+#pragma unroll
+                    for (int c = 0; c < HN; c += 2) {
+                        const float y0 = x[c] - mm, y1 = x[c + 1] - mm, p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+                        if constexpr (Q8) {
+                            const float2 lv = *reinterpret_cast<const float2*>(vlog + c);
+                            float e0 = ex2_ftz(y0 - lv.x), e1 = ex2_ftz(y1 - lv.y);
+                            if (edge) {     // a scale that is no number reaches only the rows that see its key
+                                if (y0 == -INFINITY) e0 = 0.0f;
+                                if (y1 == -INFINITY) e1 = 0.0f;
+                            }
+                            l += e0 + e1;
+                            pk[c / 2] = f16x2_bits(p0, p1);
+                        } else {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                            // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
+                            l += __uint_as_float(pk[c / 2] << 16) + __uint_as_float(pk[c / 2] & 0xffff0000u);
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int d = key0 + half * HN + c + e - ctx;
+                                if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
+                            }
+                        }
+                    }
+                    if (edge) {
+                        // values of keys that do not exist become zero, and so do those of
+                        // new keys that are not finite: the rows that see them add them at the end
+                        ok = __all_sync(0xffffffffu, at_wait(bars + L::VF + i % ST, (i / ST) & 1, abort));
+                        unsigned char* vt = base + L::V0 + (i % ST) * L::TILE;
+                        if (ok)
+                            for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS) {
+                                const int key = e % BN, c = e / BN, d = key0 + key - ctx;
+                                uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * (BN * 128) + key * 128 + (((c ^ key) & 7) << 4));
+                                if (!exists(key)) {
+                                    *p = make_uint4(0u, 0u, 0u, 0u);
+                                } else if (d >= 0 && T != GDN_KV_I8) {
+                                    constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
+                                    uint32_t u[4] = {p->x, p->y, p->z, p->w}, any = 0;
+#pragma unroll
+                                    for (int h = 0; h < 4; ++h) {
+                                        if ((u[h] & EXP) == EXP) u[h] &= 0xffff0000u, any = 1;
+                                        if ((u[h] & (EXP << 16)) == (EXP << 16)) u[h] &= 0xffffu, any = 1;
+                                    }
+                                    if (any) {
+                                        *p = make_uint4(u[0], u[1], u[2], u[3]);
+                                        atomicOr(odd, 1ull << (d & 63));
+                                    }
+                                }
+                            }
+                        fence_proxy_async_smem();
+                    }
+                    t5::fence_after();   // after the wait for P V of tile i - 2
+                    const uint32_t pc0 = trow + L::PCOL + (i & 1) * HN + half * (HN / 2);
+                    if constexpr (HN == 32)
+                        t5::st16u(pc0, pk);
+                    else
+                        t5::st32u(pc0, pk);
+                    t5::fence_before();
+                }
+                at_arrive(bars + L::PF + (i & 1));
+            }
+            n += nb;
+
+            // ---- the piece's rows out
+            const uint32_t i1 = n - 1;
+            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + (i1 & 1), (i1 >> 1) & 1, abort));
+            lsum[half * AT_ROWS + r] = l;
+            uint64_t* none_of = reinterpret_cast<uint64_t*>(xmax);   // the maxima have been read: every thread's P is in
+            none_of[half * AT_ROWS + r] = none;
+            at_bar_softmax();
+            const uint64_t odd_keys = *odd & seen;
+            none |= none_of[(half ^ 1) * AT_ROWS + r];
+            const float lt = lsum[r] + lsum[AT_ROWS + r];
+            if (ok) {
+                t5::fence_after();
+                const bool whole = pc.b0 == 0 && pc.b1 == pc.blocks;
+                const float inv = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
+                const bool store = on && GDN_IN_RANGE(g_attn_cache_error, q.tok + tok < a.n_tokens && hq < a.hq);
+                uint16_t* orow = a.o + (q.tok + tok) * a.ld_o + hq * D;
+                float* part = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (pc.b0 > 0 ? 0 : 1)) * AT_ROWS + r) * (D + 2);
+#pragma unroll 1
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                    float ov[32];
+                    t5::ld32(trow + L::OCOL + c0, ov);
+                    if (odd_keys && store) {
+                        // values that are not finite: infinite or NaN whatever their (positive) weight is
+#pragma unroll 1
+                        for (int d = 0; d < 64; ++d) {
+                            if (!((odd_keys >> d) & 1)) continue;
+                            const int key = ctx + d, pg = table[min(key >> a.page_shift, a.max_blocks - 1)];
+                            if (key < 0 || key < pc.b0 * AC_BLOCK || key >= pc.b1 * AC_BLOCK || pg < 0 || pg >= a.n_pages) continue;
+                            const int64_t vr = ((static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key & (a.page - 1))) * D + c0;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float v;
+                                if constexpr (Q8)
+                                    v = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(a.v)[vr + e], __NV_E4M3)));
+                                else
+                                    v = bf16_bits_to_float(static_cast<const uint16_t*>(a.v)[vr + e]);
+                                if (!(fabsf(v) < INFINITY)) ov[e] += ((none >> d) & 1 ? 0.0f : 1.0f) * v;
+                            }
+                        }
+                    }
+                    if (!store) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(ov[e + 2 * h] * inv, ov[e + 2 * h + 1] * inv);
+                                u[h] = *reinterpret_cast<const uint32_t*>(&b2);
+                            }
+                            *reinterpret_cast<uint4*>(orow + c0 + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2*>(part + 2 + c0 + e) = make_float2(ov[e], ov[e + 1]);
+                    }
+                }
+                if (!whole && on && half == 0) *reinterpret_cast<float2*>(part) = make_float2(m, lt);
+                t5::fence_before();
+            }
+            at_bar_softmax();           // every row has read what the others left it
+            if (st == 0) *odd = 0;
+        }
+    }
+
+    if (*abort && tid == 0) {
+        // a wait ran out: let copies already issued land (bounded) before the shared memory is released
+        for (int i = L::KF; i < L::NBAR; ++i)
+            for (uint32_t par = 0; par < 2; ++par) mbar_wait_bounded(bars + i, par, nullptr, 0, 20000000ull);
+    }
+    t5::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        t5::fence_after();
+        t5::dealloc(tmem, 512);
+    }
+}
+
+template <int D, int T>
+static cudaError_t at_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st) {
+    using L = AtSmem<D, T>;
+    static PerDeviceOnce once;
+    if (once.run([](int) {
+            cudaFuncSetAttribute(attn_tree_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::DYN);
+        }) < 0)
+        return cudaErrorInvalidDevice;
+    CUtensorMap mk, mv;
+    a.box = c.page_tokens < L::BN ? c.page_tokens : L::BN;
+    a.start = 768 / L::ROW > 0 ? 768 / L::ROW : 1;
+    if (!ac_map(&mk, c.k, c, a.box, 1) || !ac_map(&mv, c.v, c, a.box, 1)) return cudaErrorInvalidValue;
+    a.ranks = (a.max_q * a.ratio + AT_ROWS - 1) / AT_ROWS;
+    a.runs = AC_MAX_RUNS / a.ranks;
+    return launch_dependent(attn_tree_kernel<D, T>, dim3(static_cast<unsigned>(a.runs * a.ranks)), dim3(L::THREADS), L::DYN, st,
+                            mk, mv, a);
+}
+
+template <int D>
+static cudaError_t at_launch_t(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st) {
+    if (c.dtype == GDN_KV_BF16) return at_launch<D, GDN_KV_BF16>(c, a, st);
+    if (c.dtype == GDN_KV_I8) return at_launch<D, GDN_KV_I8>(c, a, st);
+    return at_launch<D, GDN_KV_E4M3>(c, a, st);
+}
+
+// Fills in a.box, a.start, a.ranks and a.runs; the partials have AT_ROWS rows.
+cudaError_t launch_attn_tree(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_t st) {
+    if (c.head_dim == 64) return at_launch_t<64>(c, a, st);
+    if (c.head_dim == 128) return at_launch_t<128>(c, a, st);
+    return at_launch_t<256>(c, a, st);
+}
+
+int read_and_clear_attn_tree_error() {
+    int v = 0, z = 0;
+    cudaMemcpyFromSymbol(&v, g_attn_cache_error, sizeof(int));
+    if (v) cudaMemcpyToSymbol(g_attn_cache_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace gdn

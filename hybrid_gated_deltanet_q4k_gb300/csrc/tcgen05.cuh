@@ -49,6 +49,18 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
            (static_cast<uint64_t>(2) << 61);
 }
 
+// Shared-memory descriptor of an MN-major operand stored with the 128-byte
+// swizzle: at each K index a row of 128 bytes holds 64 consecutive 16-bit
+// values of the M (or N) dimension; groups of 8 rows (1024 bytes) follow each
+// other (stride 1024 B >> 4 at bits 32-45), the next 64 values lie
+// `atom_bytes` further (leading offset >> 4 at bits 16-29); descriptor version
+// 1 (bit 46), swizzle mode 2 (bits 61-63).  A K step of 16 rows adds 2048 B >>
+// 4 = 128 to the start field.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t atom_bytes) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((atom_bytes >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
 // Shared-memory descriptor of an MN-major operand stored with the 64-byte
 // swizzle: at each K index a row of 64 bytes holds 32 consecutive fp16 of the
 // M (or N) dimension, the 16-byte chunk c of row k at chunk c ^ ((k >> 1) & 3);
@@ -186,6 +198,16 @@ __device__ __forceinline__ void st32u(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// Sixteen columns, likewise.
+__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
