@@ -11,9 +11,12 @@
 // for all but one.
 //
 // Per block of BN keys (64 for heads of 256, else 128; row r = TMEM lane r):
-//   S = Q K^T      M = 128, N = BN, K = D; both from shared memory, into TMEM
+//   S = Q K^T      M = 128, N = BN, K = D; Q in TMEM (from shared memory its
+//                  reads alone would take three times the product), K shared
 //   softmax warps  two threads per row, BN / 2 scores each; P back into TMEM
-//                  (two buffers), the running maximum raised only past a margin
+//                  (two buffers).  The running maximum is raised only past a
+//                  margin: the two threads swap their maxima when one of their
+//                  64 rows asks for it, a vote in the barrier between them
 //   O += P V       M = 128, N = D, K = BN; P from TMEM, V [key][d] as the
 //                  MN-major operand, the image that the copy writes: no transpose
 // The pages are bf16: TMA writes the operand images (128-byte swizzle).  8-bit
@@ -48,17 +51,15 @@ struct AtSmem {
     static constexpr int RAW = BN * ROW;                    // a tile as cached
     static constexpr int S16 = D / 64;                      // slabs of an operand image: [rows][64 x 16 bit]
     static constexpr int TILE = BN * D * 2;                 // a K or V image
-    static constexpr int QB = AT_ROWS * D * 2;
     // images of K (and of V) held at once, raw tiles in flight
-    static constexpr int ST = Q8 ? 1 : D == 64 ? 4 : 2;
-    static constexpr int RS = !Q8 ? 1 : D == 256 ? 5 : D == 128 ? 6 : 8;
-    static constexpr int Q0 = 0;
-    static constexpr int K0 = QB;
+    static constexpr int ST = Q8 ? 2 : D == 64 ? 6 : 3;
+    static constexpr int RS = !Q8 ? 1 : D == 64 ? 8 : 5;
+    static constexpr int K0 = 0;
     static constexpr int V0 = K0 + ST * TILE;
     static constexpr int R0 = V0 + ST * TILE;
     static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN / 2]
-    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // row maxima: [2 rounds][2 halves][128]
-    static constexpr int L0 = X0 + 4 * AT_ROWS * 4;         // row sums of each half
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
+    static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
     static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
@@ -70,11 +71,13 @@ struct AtSmem {
     // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
     static constexpr int DYN = BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024;
     static_assert(DYN <= 227 * 1024, "shared memory of a CTA");
-    static constexpr uint32_t PCOL = BN, OCOL = 2 * BN;     // TMEM columns: S 0 .. BN-1, P two buffers of BN / 2, O
-    static_assert(2 * BN + D <= 512, "TMEM columns");
+    // TMEM columns: S 0 .. BN - 1, P two buffers of BN / 2, Q, O
+    static constexpr uint32_t PCOL = BN, QCOL = 2 * BN, OCOL = 2 * BN + D / 2;
+    static_assert(OCOL + D <= 512, "TMEM columns");
 };
 
 __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_test(bar, parity)) return true;
     if (*abort) return false;
     if (mbar_wait_bounded(bar, parity, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) return true;
     *abort = 1;
@@ -94,7 +97,26 @@ __device__ __forceinline__ bool at_ready(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void at_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
+// One arrival for a warp whose lanes have all done their part.
+__device__ __forceinline__ void at_arrive_warp(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) at_arrive(bar);
+}
+// All softmax threads; the two warps that share 32 rows (barriers 1 .. 4), as they are and with a vote.
+__device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 5, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
+__device__ __forceinline__ void at_bar_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
+__device__ __forceinline__ bool at_vote_rows(int quad, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.or.pred p, %1, 64, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r)
+        : "r"(1 + quad), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
 
 template <int D, int T>
 __global__ void __launch_bounds__(AtSmem<D, T>::THREADS, 1)
@@ -117,9 +139,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
             int n = 1;
-            if (i == L::QF || i == L::SC || i == L::PF || i == L::PF + 1) n = AT_SM_THREADS;
-            if (Q8 && ((i >= L::KF && i < L::KE) || (i >= L::VF && i < L::VE))) n = 128;   // the converting threads
-            if (Q8 && i >= L::RE) n = 128;
+            if (i == L::QF || i == L::SC || i == L::PF || i == L::PF + 1) n = AT_SM_WARPS;
+            if (Q8 && ((i >= L::KF && i < L::KE) || (i >= L::VF && i < L::VE) || i >= L::RE)) n = 4;   // the converting warps
             mbar_init_cta(bars + i, n);
         }
         mbar_init_fence();
@@ -199,11 +220,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 for (int v = 0; ok && v < 2; ++v) {
                     const uint32_t m = 2 * n + v, sl = m % RS;
                     ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort);
-                    if (ok && n >= 1) ok = at_wait(bars + (v ? L::VE : L::KE), (n - 1) & 1, abort);
+                    if (ok && n >= ST) ok = at_wait(bars + (v ? L::VE : L::KE) + n % ST, (n / ST - 1) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const unsigned char* src = base + L::R0 + sl * L::RAW;
-                    unsigned char* dst = base + (v ? L::V0 : L::K0);
+                    unsigned char* dst = base + (v ? L::V0 : L::K0) + (n % ST) * L::TILE;
                     // 16 codes per step; consecutive threads take consecutive keys
 #pragma unroll 4
                     for (int e = ct; e < BN * (D / 16); e += 128) {
@@ -227,8 +248,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             make_uint4(codes_f16<T, 0, 1>(w.z), codes_f16<T, 2, 3>(w.z), codes_f16<T, 0, 1>(w.w), codes_f16<T, 2, 3>(w.w));
                     }
                     fence_proxy_async_smem();
-                    at_arrive(bars + (v ? L::VF : L::KF));
-                    at_arrive(bars + L::RE + sl);
+                    at_arrive_warp(bars + (v ? L::VF : L::KF) + n % ST, lane);
+                    at_arrive_warp(bars + L::RE + sl, lane);
                 }
                 ++n;
             }
@@ -259,8 +280,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const int sl = kk >> 2, w = kk & 3;
-                            t5::mma_f16(tmem, t5::desc_sw128(sbase + L::Q0 + sl * (AT_ROWS * 128) + w * 32),
-                                        t5::desc_sw128(kt + sl * (BN * 128) + w * 32), IDS, kk > 0 ? 1u : 0u);
+                            t5::mma_f16_ts(tmem, tmem + L::QCOL + kk * 8, t5::desc_sw128(kt + sl * (BN * 128) + w * 32), IDS,
+                                           kk > 0 ? 1u : 0u);
                         }
                         t5::commit(bars + L::SF);
                         t5::commit(bars + L::KE + is % ST);
@@ -302,6 +323,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         float* lsum = reinterpret_cast<float*>(base + L::L0);
         float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * BN;   // this warp's: HN key factors, HN log2 value scales
         float* vlog = kfac + HN;
+        constexpr int CH = HN / 32;                       // 32 scores at a time
+        constexpr int KEEP = Q8 && CH == 2 ? 1 : CH;      // of them in registers; the others are read twice
         bool ok = true;
         while (next()) {
             const AcSeq q = pc.q;
@@ -309,14 +332,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const bool on = r < rows;
             const int hq = pc.head * a.ratio + rr - tok * a.ratio;
             const int32_t* table = a.table + pc.s * a.ld_table;
-            uint64_t seen = !on ? 0 : a.tree ? a.tree[q.tok + tok] : tok >= 63 ? ~0ull : (1ull << (tok + 1)) - 1;
+            const uint64_t seen = !on ? 0 : a.tree ? a.tree[q.tok + tok] : tok >= 63 ? ~0ull : (1ull << (tok + 1)) - 1;
 
-            // ---- Q to shared memory: this thread half a row.  The last piece's products have read theirs.
+            // ---- Q to TMEM: this thread half a row.  The last piece's products have read theirs.
             float factor = a.sl2;
             {
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(q.tok + (on ? tok : 0)) * a.ld_q +
                                                                   (on ? hq : 0) * D + half * (D / 2));
-                unsigned char* dst = base + L::Q0 + r * 128;
                 float up = 1.0f;
                 if constexpr (Q8) {
                     float amax = 0.0f;
@@ -328,175 +350,218 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         for (int e = 0; e < 4; ++e)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
                     }
-                    lsum[half * AT_ROWS + r] = amax;
-                    at_bar_softmax();
-                    amax = fmaxf(amax, lsum[(half ^ 1) * AT_ROWS + r]);
+                    xmax[half * AT_ROWS + r] = amax;
+                    at_bar_rows(quad);
+                    amax = fmaxf(amax, xmax[(half ^ 1) * AT_ROWS + r]);
+                    at_bar_rows(quad);
                     const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
                     up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                     factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
                 }
-#pragma unroll 4
-                for (int c = 0; c < D / 16; ++c) {
-                    uint4 w = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                    if constexpr (Q8) {
-                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+                for (int c = 0; c < D / 16; c += 4) {
+                    uint32_t u[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            u[e] = f16x2_bits(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-                        w = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 w = on ? src[c + e] : make_uint4(0u, 0u, 0u, 0u);
+                        u[4 * e] = w.x;
+                        u[4 * e + 1] = w.y;
+                        u[4 * e + 2] = w.z;
+                        u[4 * e + 3] = w.w;
                     }
-                    const int cc = half * (D / 16) + c;
-                    *reinterpret_cast<uint4*>(dst + (cc >> 3) * (AT_ROWS * 128) + (((cc ^ r) & 7) << 4)) = w;
+                    if constexpr (Q8) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[e] = f16x2_bits(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+                    }
+                    t5::st16u(trow + L::QCOL + half * (D / 4) + 4 * c, u);
                 }
-                fence_proxy_async_smem();
-                at_arrive(bars + L::QF);
+                t5::fence_before();
+                at_arrive_warp(bars + L::QF, lane);
             }
 
-            // ---- pages (by lane, of the tile's copies) and, for 8-bit caches, the scales of this
-            // half's keys (by lane), read ahead
-            const int pl = (lane < copies ? lane : 0) * a.box;
-            auto page_of = [&](int j) { return table[min(((t0 + min(j, nb - 1)) * BN + pl) >> a.page_shift, a.max_blocks - 1)]; };
+            // ---- do all pages of the piece lie in the cache?
+            bool all_in = true;
+            {
+                const int lo = (t0 * BN) >> a.page_shift, hi = (min((t0 + nb) * BN, q.len) - 1) >> a.page_shift;
+                for (int b = lo + lane; b <= hi; b += 32) {
+                    const int pg = table[b];
+                    all_in &= pg >= 0 && pg < a.n_pages;
+                }
+                all_in = __all_sync(0xffffffffu, all_in);
+                if (!all_in && warp == 2 && lane == 0) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+            }
+            auto page_at = [&](int key) { return table[min(key >> a.page_shift, a.max_blocks - 1)]; };
+
+            // ---- 8-bit: the scales of this half's keys (by lane), read a tile ahead, their pages two
             constexpr int KL = HN / 32;     // keys per lane
             float ksn[KL], vsn[KL];
-            auto scales_of = [&](int j, int page) {
+            int pgn[KL];
+            auto key_of = [&](int j, int x) { return (t0 + min(j, nb - 1)) * BN + half * HN + 32 * x + lane; };
+            auto scales_of = [&](int j) {
 #pragma unroll
                 for (int x = 0; x < KL; ++x) {
-                    const int key = half * HN + 32 * x + lane;
-                    int pg = __shfl_sync(0xffffffffu, page, key / a.box);
-                    if (pg < 0 || pg >= a.n_pages) pg = 0;
-                    const int64_t row = (static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (((t0 + min(j, nb - 1)) * BN + key) & (a.page - 1));
+                    const int pg = pgn[x] >= 0 && pgn[x] < a.n_pages ? pgn[x] : 0;
+                    const int64_t row = (static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key_of(j, x) & (a.page - 1));
                     ksn[x] = a.sk[row];
                     vsn[x] = a.sv[row];
+                    pgn[x] = page_at(key_of(j + 1, x));
                 }
             };
-            int page = page_of(0), page1 = page_of(1);
-            if constexpr (Q8) scales_of(0, page);
+            if constexpr (Q8) {
+#pragma unroll
+                for (int x = 0; x < KL; ++x) pgn[x] = page_at(key_of(0, x));
+                scales_of(0);
+            }
 
             float m = -INFINITY, l = 0.0f;
             uint64_t none = 0;      // new keys this row sees with probability zero
             for (int j = 0; j < nb; ++j) {
                 const uint32_t i = n + j;
                 const int key0 = (t0 + j) * BN;
-                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 && page < a.n_pages) | (copies < 32 ? ~0u << copies : 0u);
-                const bool edge = key0 + BN > ctx || good != ~0u;
-                if (good != ~0u && warp == 2 && lane < copies && !((good >> lane) & 1) && key0 + pl < q.len)
-                    atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+                const bool edge = key0 + BN > ctx || !all_in;   // some row may not see some key
+                auto exists = [&](int key) {
+                    if (key0 + key >= q.len) return false;
+                    if (all_in) return true;
+                    const int pg = page_at(key0 + key);
+                    return pg >= 0 && pg < a.n_pages;
+                };
                 if constexpr (Q8) {
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < KL; ++x) {
                         kfac[32 * x + lane] = ksn[x];
-                        float lv = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
-                        vlog[32 * x + lane] = lv;
+                        vlog[32 * x + lane] = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
                     }
                     __syncwarp();
-                    scales_of(j + 1, page1);
+                    scales_of(j + 1);
                 }
-                page = page1;
-                page1 = page_of(j + 2);
-                auto exists = [&](int key) { return key0 + key < q.len && ((good >> (key / a.box)) & 1); };
 
                 ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF, i & 1, abort));
-                float x[HN];
-                if (ok) {
-                    t5::fence_after();
+                // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
+                float xs[KEEP][32];
+                auto scores = [&](int ch, float (&x)[32]) {
+                    t5::ld32(trow + half * HN + 32 * ch, x);
+                    if constexpr (Q8) {
+                        const F2 f = f2(factor, factor);
 #pragma unroll
-                    for (int c = 0; c < HN; c += 32) {
-                        float s0[32];
-                        t5::ld32(trow + half * HN + c, s0);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[c + e] = s0[e];
-                    }
-                }
-                t5::fence_before();
-                at_arrive(bars + L::SC);   // S is in registers: the next may overwrite it
-
-                float bm = -INFINITY;
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < HN; c += 4) {
-                        if constexpr (Q8) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(kfac + c), v4 = *reinterpret_cast<const float4*>(vlog + c);
-                            x[c] = fmaf(x[c], factor * k4.x, v4.x);
-                            x[c + 1] = fmaf(x[c + 1], factor * k4.y, v4.y);
-                            x[c + 2] = fmaf(x[c + 2], factor * k4.z, v4.z);
-                            x[c + 3] = fmaf(x[c + 3], factor * k4.w, v4.w);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[c + e] *= factor;
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(kfac + 32 * ch + c);
+                            const float4 v4 = *reinterpret_cast<const float4*>(vlog + 32 * ch + c);
+                            f2_split(f2_fma(f2(x[c], x[c + 1]), f2_mul(f, f2(k4.x, k4.y)), f2(v4.x, v4.y)), x[c], x[c + 1]);
+                            f2_split(f2_fma(f2(x[c + 2], x[c + 3]), f2_mul(f, f2(k4.z, k4.w)), f2(v4.z, v4.w)), x[c + 2], x[c + 3]);
                         }
                     }
                     if (edge) {
 #pragma unroll
-                        for (int c = 0; c < HN; ++c) {
-                            const int key = half * HN + c, d = key0 + key - ctx;
+                        for (int c = 0; c < 32; ++c) {
+                            const int key = half * HN + 32 * ch + c, d = key0 + key - ctx;
                             if (!exists(key) || (d >= 0 && !((seen >> (d & 63)) & 1))) x[c] = -INFINITY;
                         }
                     }
+                };
+                float bm = -INFINITY;
+                if (ok) {
+                    t5::fence_after();
 #pragma unroll
-                    for (int c = 0; c < HN; ++c) bm = fmaxf(bm, x[c]);
+                    for (int ch = 0; ch < CH; ++ch) {
+                        float(&x)[32] = xs[KEEP == CH ? ch : 0];
+                        scores(ch, x);
+                        float b0 = fmaxf(x[0], x[1]), b1 = fmaxf(x[2], x[3]);
+#pragma unroll
+                        for (int c = 4; c < 32; c += 4) {
+                            b0 = fmaxf(b0, fmaxf(x[c], x[c + 1]));
+                            b1 = fmaxf(b1, fmaxf(x[c + 2], x[c + 3]));
+                        }
+                        bm = fmaxf(bm, fmaxf(b0, b1));
+                    }
+                    if constexpr (!Q8) bm *= factor;
                 }
-                // the row's maximum over both halves
-                xmax[((i & 1) * 2 + half) * AT_ROWS + r] = bm;
-                at_bar_softmax();
-                bm = fmaxf(bm, xmax[((i & 1) * 2 + (half ^ 1)) * AT_ROWS + r]);
+                if constexpr (KEEP == CH) {   // S is in registers: the next may overwrite it
+                    t5::fence_before();
+                    at_arrive_warp(bars + L::SC, lane);
+                }
+                if (at_vote_rows(quad, j == 0 || bm > m + AC_MARGIN)) {
+                    // the row's maximum over both halves
+                    xmax[half * AT_ROWS + r] = bm;
+                    at_bar_rows(quad);
+                    bm = fmaxf(bm, xmax[(half ^ 1) * AT_ROWS + r]);
+                    at_bar_rows(quad);
+                    if (j == 0) {
+                        m = bm;
+                    } else {
+                        // O is rescaled once P V of tile i - 1 has finished
+                        ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
+                        if (ok) {
+                            const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
+                            m = mn;
+                            l *= f;
+                            t5::fence_after();
+#pragma unroll 1
+                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                                float ov[32];
+                                t5::ld32(trow + L::OCOL + c0, ov);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) ov[e] *= f;
+                                t5::st32(trow + L::OCOL + c0, ov);
+                            }
+                        }
+                    }
+                }
                 // P buffer i & 1 is free once P V of tile i - 2 has finished
                 if (i >= 2) ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + (i & 1), ((i - 2) >> 1) & 1, abort));
-                if (ok && j > 0 && __any_sync(0xffffffffu, bm > m + AC_MARGIN)) {
-                    // O is rescaled once P V of tile i - 1 has finished
-                    ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
-                    if (ok) {
-                        const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
-                        m = mn;
-                        l *= f;
-                        t5::fence_after();
-#pragma unroll 1
-                        for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
-                            float ov[32];
-                            t5::ld32(trow + L::OCOL + c0, ov);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) ov[e] *= f;
-                            t5::st32(trow + L::OCOL + c0, ov);
-                        }
-                    }
-                } else if (j == 0) {
-                    m = bm;
-                }
                 if (ok) {
                     const float mm = m == -INFINITY ? 0.0f : Q8 ? m - AC_LIFT : m;
-                    uint32_t pk[HN / 2];
+                    const F2 nm = f2(-mm, -mm), ff = f2(factor, factor);
+                    F2 l2 = f2(0.0f, 0.0f);
+                    t5::fence_after();
 #pragma unroll
-                    for (int c = 0; c < HN; c += 2) {
-                        const float y0 = x[c] - mm, y1 = x[c + 1] - mm, p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
-                        if constexpr (Q8) {
-                            const float2 lv = *reinterpret_cast<const float2*>(vlog + c);
-                            float e0 = ex2_ftz(y0 - lv.x), e1 = ex2_ftz(y1 - lv.y);
-                            if (edge) {     // a scale that is no number reaches only the rows that see its key
-                                if (y0 == -INFINITY) e0 = 0.0f;
-                                if (y1 == -INFINITY) e1 = 0.0f;
-                            }
-                            l += e0 + e1;
-                            pk[c / 2] = f16x2_bits(p0, p1);
-                        } else {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                            // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
-                            l += __uint_as_float(pk[c / 2] << 16) + __uint_as_float(pk[c / 2] & 0xffff0000u);
-                        }
-                        if (edge) {
+                    for (int ch = 0; ch < CH; ++ch) {
+                        float(&x)[32] = xs[KEEP == CH ? ch : 0];
+                        if (KEEP < CH) scores(ch, x);
+                        uint32_t pk[16];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int d = key0 + half * HN + c + e - ctx;
-                                if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
+                        for (int c = 0; c < 32; c += 2) {
+                            float y0, y1;
+                            f2_split(Q8 ? f2_add(f2(x[c], x[c + 1]), nm) : f2_fma(f2(x[c], x[c + 1]), ff, nm), y0, y1);
+                            const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+                            if constexpr (Q8) {
+                                const float2 lv = *reinterpret_cast<const float2*>(vlog + 32 * ch + c);
+                                float e0, e1;
+                                f2_split(f2_sub(f2(y0, y1), f2(lv.x, lv.y)), e0, e1);
+                                e0 = ex2_ftz(e0);
+                                e1 = ex2_ftz(e1);
+                                if (edge) {     // a scale that is no number reaches only the rows that see its key
+                                    if (y0 == -INFINITY) e0 = 0.0f;
+                                    if (y1 == -INFINITY) e1 = 0.0f;
+                                }
+                                l2 = f2_add(l2, f2(e0, e1));
+                                pk[c / 2] = f16x2_bits(p0, p1);
+                            } else {
+                                l2 = f2_add(l2, f2(p0, p1));
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                                pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int d = key0 + half * HN + 32 * ch + c + e - ctx;
+                                    if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
+                                }
                             }
                         }
+                        t5::st16u(trow + L::PCOL + (i & 1) * HN + half * (HN / 2) + 16 * ch, pk);
                     }
+                    float s0, s1;
+                    f2_split(l2, s0, s1);
+                    l += s0 + s1;
                     if (edge) {
                         // values of keys that do not exist become zero, and so do those of
                         // new keys that are not finite: the rows that see them add them at the end
                         ok = __all_sync(0xffffffffu, at_wait(bars + L::VF + i % ST, (i / ST) & 1, abort));
                         unsigned char* vt = base + L::V0 + (i % ST) * L::TILE;
                         if (ok)
+#pragma unroll 1
                             for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS) {
                                 const int key = e % BN, c = e / BN, d = key0 + key - ctx;
                                 uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * (BN * 128) + key * 128 + (((c ^ key) & 7) << 4));
@@ -518,15 +583,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             }
                         fence_proxy_async_smem();
                     }
-                    t5::fence_after();   // after the wait for P V of tile i - 2
-                    const uint32_t pc0 = trow + L::PCOL + (i & 1) * HN + half * (HN / 2);
-                    if constexpr (HN == 32)
-                        t5::st16u(pc0, pk);
-                    else
-                        t5::st32u(pc0, pk);
-                    t5::fence_before();
                 }
-                at_arrive(bars + L::PF + (i & 1));
+                t5::fence_before();
+                if constexpr (KEEP < CH) at_arrive_warp(bars + L::SC, lane);
+                at_arrive_warp(bars + L::PF + (i & 1), lane);
             }
             n += nb;
 
