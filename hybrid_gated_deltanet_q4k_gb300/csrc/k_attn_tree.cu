@@ -10,15 +10,18 @@
 // same run of blocks; they walk it at the same time, so the cache comes from L2
 // for all but one.
 //
-// Per block of BN keys (64 for heads of 256, else 128; row r = TMEM lane r):
-//   S = Q K^T      M = 128, N = BN, K = D; Q in TMEM (from shared memory its
-//                  reads alone would take three times the product), K shared
-//   softmax warps  two threads per row, BN / 2 scores each; P back into TMEM
-//                  (two buffers).  The running maximum is raised only past a
-//                  margin: the two threads swap their maxima when one of their
-//                  64 rows asks for it, a vote in the barrier between them
-//   O += P V       M = 128, N = D, K = BN; P from TMEM, V [key][d] as the
+// Per tile of 64 keys (row r = TMEM lane r):
+//   S = Q K^T      M = 128, N = 64, K = D; Q in TMEM (from shared memory its
+//                  reads alone would take three times the product), K shared;
+//                  two S buffers
+//   softmax        a thread per row; two groups of four warps take the tiles in
+//                  turn, so that one's exponentials run beside the other's
+//                  waits; P goes over its own S
+//   O += P V       M = 128, N = D, K = 64; P from TMEM, V [key][d] as the
 //                  MN-major operand, the image that the copy writes: no transpose
+// The running maximum is raised only past a margin; the groups hand it on: a
+// warp waits for the decision of the tile before (not for its exponentials)
+// before it takes its own.
 // The pages are bf16: TMA writes the operand images (128-byte swizzle).  8-bit
 // codes go through a ring of raw tiles that four warps turn into fp16 images
 // (exact); the row scales stay out of the products, as in the other kernel: a
@@ -27,12 +30,14 @@
 // zero below 2^-36 of it.
 //
 // Warps: 0 copies the keys (8-bit: both), 1 allocates TMEM and issues the
-// products in whichever order they become ready, 2-9 softmax, 10 copies the
-// values (8-bit: 10-13 convert).  Every wait is bounded; after one runs out the
+// products (S of a tile two ahead of its P V), 2-5 and 6-9 softmax, 10 copies
+// the values (8-bit: 10-13 convert).  Every wait is bounded; after one runs out the
 // CTA stops issuing, lets copies and products finish and returns with the error
 // word set.
 #include "attn_cache.cuh"
 #include "tcgen05.cuh"
+
+#include <type_traits>
 
 namespace gdn {
 
@@ -43,7 +48,7 @@ constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
 template <int D, int T>
 struct AtSmem {
     static constexpr bool Q8 = T != GDN_KV_BF16;
-    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int BN = 64;
     static constexpr int THREADS = 32 * (2 + AT_SM_WARPS + (Q8 ? 4 : 1));
     static constexpr int ROW = D * (Q8 ? 1 : 2);
     static constexpr int SLAB = ROW < 128 ? ROW : 128;      // bytes of a cached row in one slab of the copies
@@ -52,27 +57,28 @@ struct AtSmem {
     static constexpr int S16 = D / 64;                      // slabs of an operand image: [rows][64 x 16 bit]
     static constexpr int TILE = BN * D * 2;                 // a K or V image
     // images of K (and of V) held at once, raw tiles in flight
-    static constexpr int ST = Q8 ? 2 : D == 64 ? 6 : 3;
-    static constexpr int RS = !Q8 ? 1 : D == 64 ? 8 : 5;
+    static constexpr int ST = Q8 ? 2 : D == 256 ? 3 : 6;
+    static constexpr int RS = !Q8 ? 1 : D == 256 ? 5 : 10;
     static constexpr int K0 = 0;
     static constexpr int V0 = K0 + ST * TILE;
     static constexpr int R0 = V0 + ST * TILE;
-    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN / 2]
-    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
-    static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
+    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN]
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 2 * BN * 4 : 0);   // maximum of each row; masks of zero weights [2][128]
+    static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each group
     static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
     static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
-    static constexpr int QF = 0, SF = 1, SC = 2, PF = 3, PV = 5, FIN = 7, KF = 8, KE = KF + ST, VF = KE + ST, VE = VF + ST,
+    // Q in; S, P and P V by buffer; decisions by group and 32 rows; images and raw tiles, full and empty
+    static constexpr int QF = 0, SF = 1, PF = 3, PV = 5, FIN = 7, DR = 8, KF = 16, KE = KF + ST, VF = KE + ST, VE = VF + ST,
                          RF = VE + ST, RE = RF + RS, NBAR = RE + RS;
     static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite
     static constexpr int BYTES = MISC + 16;
     // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
     static constexpr int DYN = BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024;
     static_assert(DYN <= 227 * 1024, "shared memory of a CTA");
-    // TMEM columns: S 0 .. BN - 1, P two buffers of BN / 2, Q, O
-    static constexpr uint32_t PCOL = BN, QCOL = 2 * BN, OCOL = 2 * BN + D / 2;
+    // TMEM columns: two buffers of S (BN columns) with P over their first BN / 2, Q, O
+    static constexpr uint32_t QCOL = 2 * BN, OCOL = 2 * BN + D / 2;
     static_assert(OCOL + D <= 512, "TMEM columns");
 };
 
@@ -102,28 +108,15 @@ __device__ __forceinline__ void at_arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) at_arrive(bar);
 }
-// All softmax threads; the two warps that share 32 rows (barriers 1 .. 4), as they are and with a vote.
-__device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 5, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
-__device__ __forceinline__ void at_bar_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
-__device__ __forceinline__ bool at_vote_rows(int quad, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.or.pred p, %1, 64, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(r)
-        : "r"(1 + quad), "r"(x ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
+// All softmax threads.
+__device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
 
 template <int D, int T>
 __global__ void __launch_bounds__(AtSmem<D, T>::THREADS, 1)
 attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttCacheArgs a) {
     using L = AtSmem<D, T>;
-    constexpr int BN = L::BN, ST = L::ST, RS = L::RS, HN = BN / 2;
+    constexpr int BN = L::BN, ST = L::ST, RS = L::RS;
     constexpr bool Q8 = L::Q8;
     extern __shared__ __align__(1024) unsigned char smb[];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smb) + 1023) & ~uintptr_t(1023));
@@ -139,7 +132,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
             int n = 1;
-            if (i == L::QF || i == L::SC || i == L::PF || i == L::PF + 1) n = AT_SM_WARPS;
+            if (i == L::QF) n = AT_SM_WARPS;
+            if (i == L::PF || i == L::PF + 1) n = AT_SM_WARPS / 2;
             if (Q8 && ((i >= L::KF && i < L::KE) || (i >= L::VF && i < L::VE) || i >= L::RE)) n = 4;   // the converting warps
             mbar_init_cta(bars + i, n);
         }
@@ -256,9 +250,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        // S of a tile needs its K image and the softmax to have read the last
-        // S; P V needs P and the V image.  One thread polls both; a stall past
-        // 2 s sets the error word.
+        // S of a tile needs its K image and its buffer (P V two tiles before has
+        // read P there); P V needs P and the V image.  One thread polls both and
+        // issues what is ready; a stall past 2 s sets the error word.
         if (lane == 0) {
             constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
             constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
@@ -267,45 +261,41 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             while (ok && next()) {
                 ok = at_wait(bars + L::QF, piece & 1, abort);
                 ++piece;
-                t5::fence_after();
-                int ns = 0, np = 0;
-                uint64_t t_last = globaltimer_ns();
+                int ns = 0, np = 0, spins = 0;
+                uint64_t t_last = 0;
                 while (ok && np < nb) {
-                    bool did = false;
                     const uint32_t is = n + ns, ip = n + np;
-                    if (ns < nb && ns <= np + 1 && (is == 0 || at_ready(bars + L::SC, (is - 1) & 1)) &&
+                    if (ns < nb && ns < np + 2 && (ns < 2 || at_ready(bars + L::PV + (is & 1), ((is - 2) >> 1) & 1)) &&
                         at_ready(bars + L::KF + is % ST, (is / ST) & 1)) {
                         t5::fence_after();
                         const uint32_t kt = sbase + L::K0 + (is % ST) * L::TILE;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const int sl = kk >> 2, w = kk & 3;
-                            t5::mma_f16_ts(tmem, tmem + L::QCOL + kk * 8, t5::desc_sw128(kt + sl * (BN * 128) + w * 32), IDS,
-                                           kk > 0 ? 1u : 0u);
-                        }
-                        t5::commit(bars + L::SF);
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            t5::mma_f16_ts(tmem + (is & 1) * BN, tmem + L::QCOL + kk * 8,
+                                           t5::desc_sw128(kt + (kk >> 2) * (BN * 128) + (kk & 3) * 32), IDS, kk > 0 ? 1u : 0u);
+                        t5::commit(bars + L::SF + (is & 1));
                         t5::commit(bars + L::KE + is % ST);
                         ++ns;
-                        did = true;
+                        spins = 0;
                     } else if (np < ns && at_ready(bars + L::PF + (ip & 1), (ip >> 1) & 1) &&
                                at_ready(bars + L::VF + ip % ST, (ip / ST) & 1)) {
                         t5::fence_after();
-                        const uint32_t vt = sbase + L::V0 + (ip % ST) * L::TILE, pa = tmem + L::PCOL + (ip & 1) * HN;
+                        const uint32_t vt = sbase + L::V0 + (ip % ST) * L::TILE;
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
-                            t5::mma_f16_ts(tmem + L::OCOL, pa + kk * 8, t5::desc_sw128_mn(vt + kk * 2048, BN * 128), IDO,
-                                           (np > 0 || kk > 0) ? 1u : 0u);
+                            t5::mma_f16_ts(tmem + L::OCOL, tmem + (ip & 1) * BN + kk * 8, t5::desc_sw128_mn(vt + kk * 2048, BN * 128),
+                                           IDO, (np > 0 || kk > 0) ? 1u : 0u);
                         t5::commit(bars + L::PV + (ip & 1));
                         t5::commit(bars + L::VE + ip % ST);
                         ++np;
-                        did = true;
-                    }
-                    if (did) {
-                        t_last = globaltimer_ns();
-                    } else if (*abort || globaltimer_ns() - t_last > 2000000000ull) {
-                        if (!*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
-                        *abort = 1;
-                        ok = false;
+                        spins = 0;
+                    } else if (++spins >= 1024) {
+                        if (spins == 1024) t_last = globaltimer_ns();
+                        if (*abort || globaltimer_ns() - t_last > 2000000000ull) {
+                            if (!*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
+                            *abort = 1;
+                            ok = false;
+                        }
                     }
                 }
                 n += nb;
@@ -317,14 +307,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int quad = warp & 3, half = (warp - 2) >> 2, r = 32 * quad + lane, st = tid - 64;
+        // group `half` takes the tiles of its parity (and half of the columns of q and o)
+        const int quad = warp & 3, half = (warp - 2) >> 2, r = 32 * quad + lane, st = (tid - 64) & 127;
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-        float* xmax = reinterpret_cast<float*>(base + L::X0);
+        float* row_max = reinterpret_cast<float*>(base + L::X0);
         float* lsum = reinterpret_cast<float*>(base + L::L0);
-        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * BN;   // this warp's: HN key factors, HN log2 value scales
-        float* vlog = kfac + HN;
-        constexpr int CH = HN / 32;                       // 32 scores at a time
-        constexpr int KEEP = Q8 && CH == 2 ? 1 : CH;      // of them in registers; the others are read twice
+        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * 2 * BN;   // this warp's: BN key factors, BN log2 value scales
+        float* vlog = kfac + BN;
+        constexpr int CH = BN / 32;                       // 32 scores at a time
         bool ok = true;
         while (next()) {
             const AcSeq q = pc.q;
@@ -350,10 +340,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         for (int e = 0; e < 4; ++e)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
                     }
-                    xmax[half * AT_ROWS + r] = amax;
-                    at_bar_rows(quad);
-                    amax = fmaxf(amax, xmax[(half ^ 1) * AT_ROWS + r]);
-                    at_bar_rows(quad);
+                    lsum[half * AT_ROWS + r] = amax;
+                    at_bar_softmax();
+                    amax = fmaxf(amax, lsum[(half ^ 1) * AT_ROWS + r]);
                     const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
                     up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                     factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
@@ -393,11 +382,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             auto page_at = [&](int key) { return table[min(key >> a.page_shift, a.max_blocks - 1)]; };
 
-            // ---- 8-bit: the scales of this half's keys (by lane), read a tile ahead, their pages two
-            constexpr int KL = HN / 32;     // keys per lane
+            // ---- 8-bit: the scales of the tile's keys (by lane), read one of this group's tiles ahead, their pages two
+            constexpr int KL = BN / 32;     // keys per lane
             float ksn[KL], vsn[KL];
             int pgn[KL];
-            auto key_of = [&](int j, int x) { return (t0 + min(j, nb - 1)) * BN + half * HN + 32 * x + lane; };
+            auto key_of = [&](int j, int x) { return (t0 + min(j, nb - 1)) * BN + 32 * x + lane; };
             auto scales_of = [&](int j) {
 #pragma unroll
                 for (int x = 0; x < KL; ++x) {
@@ -405,21 +394,26 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     const int64_t row = (static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key_of(j, x) & (a.page - 1));
                     ksn[x] = a.sk[row];
                     vsn[x] = a.sv[row];
-                    pgn[x] = page_at(key_of(j + 1, x));
+                    pgn[x] = page_at(key_of(j + 2, x));
                 }
             };
+            const int j0 = (n & 1) == static_cast<uint32_t>(half) ? 0 : 1;    // this group's first tile
             if constexpr (Q8) {
 #pragma unroll
-                for (int x = 0; x < KL; ++x) pgn[x] = page_at(key_of(0, x));
-                scales_of(0);
+                for (int x = 0; x < KL; ++x) pgn[x] = page_at(key_of(j0, x));
+                scales_of(j0);
             }
 
             float m = -INFINITY, l = 0.0f;
             uint64_t none = 0;      // new keys this row sees with probability zero
-            for (int j = 0; j < nb; ++j) {
+            // A tile; EDGE: some row may not see some key.  Two copies of the code, since
+            // the tests inside its loops would cost the plain tiles five times their exponentials.
+            auto tile = [&](int j, auto edge_tag) {
+                constexpr bool edge = decltype(edge_tag)::value;
+                constexpr int KEEP = edge || Q8 ? 1 : CH;   // scores in registers (fewer: the others are read twice)
                 const uint32_t i = n + j;
                 const int key0 = (t0 + j) * BN;
-                const bool edge = key0 + BN > ctx || !all_in;   // some row may not see some key
+                const uint32_t sbuf = trow + (i & 1) * BN;
                 auto exists = [&](int key) {
                     if (key0 + key >= q.len) return false;
                     if (all_in) return true;
@@ -434,14 +428,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         vlog[32 * x + lane] = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
                     }
                     __syncwarp();
-                    scales_of(j + 1);
+                    scales_of(j + 2);
                 }
 
-                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF, i & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + (i & 1), (i >> 1) & 1, abort));
                 // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
                 float xs[KEEP][32];
                 auto scores = [&](int ch, float (&x)[32]) {
-                    t5::ld32(trow + half * HN + 32 * ch, x);
+                    t5::ld32(sbuf + 32 * ch, x);
                     if constexpr (Q8) {
                         const F2 f = f2(factor, factor);
 #pragma unroll
@@ -452,10 +446,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             f2_split(f2_fma(f2(x[c + 2], x[c + 3]), f2_mul(f, f2(k4.z, k4.w)), f2(v4.z, v4.w)), x[c + 2], x[c + 3]);
                         }
                     }
-                    if (edge) {
+                    if constexpr (edge) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const int key = half * HN + 32 * ch + c, d = key0 + key - ctx;
+                            const int key = 32 * ch + c, d = key0 + key - ctx;
                             if (!exists(key) || (d >= 0 && !((seen >> (d & 63)) & 1))) x[c] = -INFINITY;
                         }
                     }
@@ -477,28 +471,25 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     }
                     if constexpr (!Q8) bm *= factor;
                 }
-                if constexpr (KEEP == CH) {   // S is in registers: the next may overwrite it
-                    t5::fence_before();
-                    at_arrive_warp(bars + L::SC, lane);
-                }
-                if (at_vote_rows(quad, j == 0 || bm > m + AC_MARGIN)) {
-                    // the row's maximum over both halves
-                    xmax[half * AT_ROWS + r] = bm;
-                    at_bar_rows(quad);
-                    bm = fmaxf(bm, xmax[(half ^ 1) * AT_ROWS + r]);
-                    at_bar_rows(quad);
-                    if (j == 0) {
-                        m = bm;
-                    } else {
+                // ---- the maximum after the tile before (the other group's), then this tile's
+                if (j > 0) {
+                    ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::DR + 4 * (half ^ 1) + quad, ((i - 1) >> 1) & 1, abort));
+                    const float mo = row_max[r];
+                    if (__any_sync(0xffffffffu, mo != m)) {
+                        l *= m == -INFINITY ? 0.0f : ex2_ftz(m - mo);
+                        m = mo;
+                    }
+                    if (ok && __any_sync(0xffffffffu, bm > m + AC_MARGIN)) {
                         // O is rescaled once P V of tile i - 1 has finished
-                        ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
+                        ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
                         if (ok) {
                             const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
                             m = mn;
                             l *= f;
+                            row_max[r] = m;
                             t5::fence_after();
 #pragma unroll 1
-                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                            for (int c0 = 0; c0 < D; c0 += 32) {
                                 float ov[32];
                                 t5::ld32(trow + L::OCOL + c0, ov);
 #pragma unroll
@@ -507,14 +498,15 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             }
                         }
                     }
+                } else {
+                    m = bm;
+                    row_max[r] = m;
                 }
-                // P buffer i & 1 is free once P V of tile i - 2 has finished
-                if (i >= 2) ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + (i & 1), ((i - 2) >> 1) & 1, abort));
+                at_arrive_warp(bars + L::DR + 4 * half + quad, lane);
                 if (ok) {
                     const float mm = m == -INFINITY ? 0.0f : Q8 ? m - AC_LIFT : m;
                     const F2 nm = f2(-mm, -mm), ff = f2(factor, factor);
                     F2 l2 = f2(0.0f, 0.0f);
-                    t5::fence_after();
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch) {
                         float(&x)[32] = xs[KEEP == CH ? ch : 0];
@@ -531,7 +523,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                                 f2_split(f2_sub(f2(y0, y1), f2(lv.x, lv.y)), e0, e1);
                                 e0 = ex2_ftz(e0);
                                 e1 = ex2_ftz(e1);
-                                if (edge) {     // a scale that is no number reaches only the rows that see its key
+                                if constexpr (edge) {     // a scale that is no number reaches only the rows that see its key
                                     if (y0 == -INFINITY) e0 = 0.0f;
                                     if (y1 == -INFINITY) e1 = 0.0f;
                                 }
@@ -542,27 +534,27 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                                 const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
                                 pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
                             }
-                            if (edge) {
+                            if constexpr (edge) {
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const int d = key0 + half * HN + 32 * ch + c + e - ctx;
+                                    const int d = key0 + 32 * ch + c + e - ctx;
                                     if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
                                 }
                             }
                         }
-                        t5::st16u(trow + L::PCOL + (i & 1) * HN + half * (HN / 2) + 16 * ch, pk);
+                        t5::st16u(sbuf + 16 * ch, pk);   // over scores that have been read
                     }
                     float s0, s1;
                     f2_split(l2, s0, s1);
                     l += s0 + s1;
-                    if (edge) {
+                    if constexpr (edge) {
                         // values of keys that do not exist become zero, and so do those of
                         // new keys that are not finite: the rows that see them add them at the end
                         ok = __all_sync(0xffffffffu, at_wait(bars + L::VF + i % ST, (i / ST) & 1, abort));
                         unsigned char* vt = base + L::V0 + (i % ST) * L::TILE;
                         if (ok)
 #pragma unroll 1
-                            for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS) {
+                            for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS / 2) {
                                 const int key = e % BN, c = e / BN, d = key0 + key - ctx;
                                 uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * (BN * 128) + key * 128 + (((c ^ key) & 7) << 4));
                                 if (!exists(key)) {
@@ -585,16 +577,29 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     }
                 }
                 t5::fence_before();
-                if constexpr (KEEP < CH) at_arrive_warp(bars + L::SC, lane);
                 at_arrive_warp(bars + L::PF + (i & 1), lane);
+            };
+            for (int j = j0; j < nb; j += 2) {
+                if ((t0 + j + 1) * BN > ctx || !all_in)
+                    tile(j, std::true_type{});
+                else
+                    tile(j, std::false_type{});
             }
             n += nb;
 
             // ---- the piece's rows out
             const uint32_t i1 = n - 1;
-            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::PV + (i1 & 1), (i1 >> 1) & 1, abort));
+            // the last S first: the phase of P V before the last one, of the same barrier, is then over
+            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + (i1 & 1), (i1 >> 1) & 1, abort) &&
+                                             at_wait(bars + L::PV + (i1 & 1), (i1 >> 1) & 1, abort));
+            // the last decision, for the group that did not take it
+            at_bar_softmax();
+            const float mo = row_max[r];
+            l *= m == -INFINITY ? 0.0f : ex2_ftz(m - mo);
+            m = mo;
             lsum[half * AT_ROWS + r] = l;
-            uint64_t* none_of = reinterpret_cast<uint64_t*>(xmax);   // the maxima have been read: every thread's P is in
+            at_bar_softmax();
+            uint64_t* none_of = reinterpret_cast<uint64_t*>(row_max);   // the maxima have been read
             none_of[half * AT_ROWS + r] = none;
             at_bar_softmax();
             const uint64_t odd_keys = *odd & seen;
