@@ -125,6 +125,12 @@ __device__ __forceinline__ uint32_t ac_piece(int r, int c) {
 
 // ------------------------------------------------------------ the kernel
 
+// A truth value that is known to the compiler.
+template <bool V>
+struct Flag {
+    __device__ constexpr operator bool() const { return V; }
+};
+
 // NR tiles of eight rows per CTA.
 template <int D, int T, int NR>
 __global__ void __launch_bounds__(AcSmem<D, T, NR>::THREADS, 1)
@@ -290,7 +296,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             const uint32_t ok = page_in[slot] | (~0u << copies);
-            const bool edge = key0 + L::KEYS > ctx || ok != ~0u;   // some row may not see some key
+            const bool edge_tile = key0 + L::KEYS > ctx || ok != ~0u;
             if (ok != ~0u && lane < copies && !((ok >> lane) & 1) && key0 + mycopy < q.len)
                 atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
             // keys of 16-key step u below limit(u) exist; those of an unseen page do not
@@ -355,225 +361,238 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
 
-            // ---- softmax of the tile: y = x + log2 of the value's scale
-            bool up = false;
-            float lv[SUB][2];
+            // The rest of the tile; edge: some row may not see some key.
+            auto finish = [&](auto edge) {
+                // ---- softmax of the tile: y = x + log2 of the value's scale
+                bool up = false;
+                float lv[SUB][2];
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
+                for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)   // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
-                    lv[u][h] = Q8 ? lg2(fmaxf_nan(scales[slot * L::KEYS + 16 * u + 8 * h + g], 7.7e-34f)) : 0.0f;
+                    for (int h = 0; h < 2; ++h)   // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
+                        lv[u][h] = Q8 ? lg2(fmaxf_nan(scales[slot * L::KEYS + 16 * u + 8 * h + g], 7.7e-34f)) : 0.0f;
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    const float2 qs = *reinterpret_cast<const float2*>(row_factor + 8 * nr + 2 * t);
+                    for (int nr = 0; nr < NR; ++nr) {
+                        const float2 qs = *reinterpret_cast<const float2*>(row_factor + 8 * nr + 2 * t);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f = e & 1 ? qs.y : qs.x;
-                        y[u][nr][e] = Q8 ? fmaf(y[u][nr][e], f * kv[u][e >> 1], lv[u][e >> 1]) : y[u][nr][e] * f;
+                        for (int e = 0; e < 4; ++e) {
+                            const float f = e & 1 ? qs.y : qs.x;
+                            y[u][nr][e] = Q8 ? fmaf(y[u][nr][e], f * kv[u][e >> 1], lv[u][e >> 1]) : y[u][nr][e] * f;
+                        }
+                        if (edge) {
+                            const int lim = limit(u);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = 8 * (e >> 1) + g, d = key0 + 16 * u + j - ctx;
+                                if (j >= lim || (d >= 0 && !((seen[8 * nr + 2 * t + (e & 1)] >> (d & 63)) & 1))) y[u][nr][e] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) up |= y[u][nr][e] > m[nr][e & 1] + AC_MARGIN;   // from -inf: any finite score
                     }
+                    if (edge) {      // a scale that is no number has reached the rows that see its key in y
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (!(fabsf(lv[u][h]) < INFINITY)) lv[u][h] = 0.0f;
+                    }
+                }
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float bm = fmaxf(y[0][nr][e], y[0][nr][2 + e]);
+#pragma unroll
+                            for (int u = 1; u < SUB; ++u) bm = fmaxf(bm, fmaxf(y[u][nr][e], y[u][nr][2 + e]));
+                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+                            const float old = m[nr][e], mn = fmaxf(old, bm);
+                            const float c = old == -INFINITY ? 0.0f : ex2_ftz(old - mn);
+                            m[nr][e] = mn;
+                            l[nr][e] *= c;
+#pragma unroll
+                            for (int k = 0; k < KT; ++k) {
+                                o[nr][k][e] *= c;
+                                o[nr][k][2 + e] *= c;
+                            }
+                        }
+                }
+
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t pf[NR][2];      // probabilities of (key g, rows 2t, 2t+1) and (key g + 8, ..)
+                    float pk[NR][4];
+                    bool faint = false;      // an fp16 probability that lost bits
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : Q8 ? m[nr][e & 1] - AC_LIFT : m[nr][e & 1];
+                            const float x = y[u][nr][e] - mm, p = ex2_ftz(x);
+                            pk[nr][e] = p;
+                            if constexpr (Q8) {
+                                faint |= p != 0.0f && p < 6.1035156e-5f;
+                                l[nr][e & 1] += ex2_ftz(x - lv[u][e >> 1]);
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (Q8) {
+                                pf[nr][h] = f16x2_bits(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                            } else {
+                                pf[nr][h] = bf16x2(pk[nr][2 * h], pk[nr][2 * h + 1]);
+                                // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
+                                l[nr][0] += __uint_as_float(pf[nr][h] << 16);
+                                l[nr][1] += __uint_as_float(pf[nr][h] & 0xffff0000u);
+                            }
+                        }
+                    }
+
+                    // ---- values
+                    const uint32_t vu = vb + u * (16 * L::SLAB);
+                    uint32_t odd = 0;                    // a value that is not finite at the edge
+                    uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys (2t, 2t+1; + 8) exist
                     if (edge) {
                         const int lim = limit(u);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 8 * (e >> 1) + g, d = key0 + 16 * u + j - ctx;
-                            if (j >= lim || (d >= 0 && !((seen[8 * nr + 2 * t + (e & 1)] >> (d & 63)) & 1))) y[u][nr][e] = -INFINITY;
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            km[h] = (8 * h + 2 * t < lim ? 0xffffu : 0u) | (8 * h + 2 * t + 1 < lim ? 0xffff0000u : 0u);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) up |= y[u][nr][e] > m[nr][e & 1] + AC_MARGIN;   // from -inf: any finite score
-                }
-                if (edge) {      // a scale that is no number has reached the rows that see its key in y
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (!(fabsf(lv[u][h]) < INFINITY)) lv[u][h] = 0.0f;
-                }
-            }
-            if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float bm = fmaxf(y[0][nr][e], y[0][nr][2 + e]);
-#pragma unroll
-                        for (int u = 1; u < SUB; ++u) bm = fmaxf(bm, fmaxf(y[u][nr][e], y[u][nr][2 + e]));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-                        const float old = m[nr][e], mn = fmaxf(old, bm);
-                        const float c = old == -INFINITY ? 0.0f : ex2_ftz(old - mn);
-                        m[nr][e] = mn;
-                        l[nr][e] *= c;
-#pragma unroll
-                        for (int k = 0; k < KT; ++k) {
-                            o[nr][k][e] *= c;
-                            o[nr][k][2 + e] *= c;
-                        }
-                    }
-            }
-
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                uint32_t pf[NR][2];      // probabilities of (key g, rows 2t, 2t+1) and (key g + 8, ..)
-                float pk[NR][4];
-                bool faint = false;      // an fp16 probability that lost bits
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float mm = m[nr][e & 1] == -INFINITY ? 0.0f : Q8 ? m[nr][e & 1] - AC_LIFT : m[nr][e & 1];
-                        const float x = y[u][nr][e] - mm, p = ex2_ftz(x);
-                        pk[nr][e] = p;
-                        if constexpr (Q8) {
-                            faint |= p != 0.0f && p < 6.1035156e-5f;
-                            l[nr][e & 1] += ex2_ftz(x - lv[u][e >> 1]);
-                        }
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (Q8) {
-                            pf[nr][h] = f16x2_bits(pk[nr][2 * h], pk[nr][2 * h + 1]);
-                        } else {
-                            pf[nr][h] = bf16x2(pk[nr][2 * h], pk[nr][2 * h + 1]);
-                            // the sum takes the probabilities as rounded, so their rounding cancels where few keys matter
-                            l[nr][0] += __uint_as_float(pf[nr][h] << 16);
-                            l[nr][1] += __uint_as_float(pf[nr][h] & 0xffff0000u);
-                        }
-                    }
-                }
-
-                // ---- values
-                const uint32_t vu = vb + u * (16 * L::SLAB);
-                uint32_t odd = 0;                    // a value that is not finite at the edge
-                uint32_t km[2] = {~0u, ~0u};         // halves of the fragments whose keys (2t, 2t+1; + 8) exist
-                if (edge) {
-                    const int lim = limit(u);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        km[h] = (8 * h + 2 * t < lim ? 0xffffu : 0u) | (8 * h + 2 * t + 1 < lim ? 0xffff0000u : 0u);
-                }
-                // what does not exist, and what is not finite (its rows see it below), is taken as zero
-                auto clean = [&](uint32_t w, int h) {
-                    constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
-                    w &= km[h];
-                    if (T != GDN_KV_I8) {
-                        if ((w & EXP) == EXP) {
-                            w &= 0xffff0000u;
-                            odd = 1;
-                        }
-                        if ((w & (EXP << 16)) == (EXP << 16)) {
-                            w &= 0xffffu;
-                            odd = 1;
-                        }
-                    }
-                    return w;
-                };
-                // fragments of columns 16c .. 16c + 15 (8-bit: and of the next 16)
-                constexpr int STEP = Q8 ? 2 : 1;
-                auto values = [&](int c, uint32_t (&f)[STEP][4]) {
-                    uint32_t w[4];
-                    ldsm_x4_trans(piece_at(vu, Q8 ? c : 2 * c), w);
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const uint32_t x = T == GDN_KV_I8 ? w[2 * v] ^ 0x80808080u : w[2 * v];
-                            const uint32_t z = T == GDN_KV_I8 ? w[2 * v + 1] ^ 0x80808080u : w[2 * v + 1];
-                            f[v][0] = codes_f16<T, 0, 2>(x);     // columns 2g of keys 0-7, 2g + 1, then keys 8-15
-                            f[v][1] = codes_f16<T, 1, 3>(x);
-                            f[v][2] = codes_f16<T, 0, 2>(z);
-                            f[v][3] = codes_f16<T, 1, 3>(z);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[0][e] = w[e];
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int v = 0; v < STEP; ++v)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[v][e] = clean(f[v][e], e >> 1);
-                    }
-                };
-                // the second product's operand: (keys 2t, 2t+1; row g)
-                uint32_t pt[NR][2];
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
-                bool first_pass = true;
-                if constexpr (Q8) {
-                    faint = __any_sync(0xffffffffu, faint);
-                    if (faint) {         // does fp16 hold anything of these keys?
-                        uint32_t any = 0;
-#pragma unroll
-                        for (int nr = 0; nr < NR; ++nr) any |= pt[nr][0] | pt[nr][1];
-                        first_pass = __any_sync(0xffffffffu, any != 0);
-                    }
-                }
-                if (first_pass) {
-#pragma unroll
-                    for (int c = 0; c < KT; c += STEP) {
-                        uint32_t f[STEP][4];
-                        values(c, f);
-#pragma unroll
-                        for (int v = 0; v < STEP; ++v)
-#pragma unroll
-                            for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
-                    }
-                }
-                if constexpr (Q8) {
-                    if (faint) {
-#pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[nr][h]));
-                                pt[nr][h] = transpose8(bf16x2(pk[nr][2 * h] - r.x, pk[nr][2 * h + 1] - r.y));
+                    // what does not exist, and what is not finite (its rows see it below), is taken as zero
+                    auto clean = [&](uint32_t w, int h) {
+                        constexpr uint32_t EXP = Q8 ? 0x7c00u : 0x7f80u;
+                        w &= km[h];
+                        if (T != GDN_KV_I8) {
+                            if ((w & EXP) == EXP) {
+                                w &= 0xffff0000u;
+                                odd = 1;
                             }
+                            if ((w & (EXP << 16)) == (EXP << 16)) {
+                                w &= 0xffffu;
+                                odd = 1;
+                            }
+                        }
+                        return w;
+                    };
+                    // fragments of columns 16c .. 16c + 15 (8-bit: and of the next 16)
+                    constexpr int STEP = Q8 ? 2 : 1;
+                    auto values = [&](int c, uint32_t (&f)[STEP][4]) {
+                        uint32_t w[4];
+                        ldsm_x4_trans(piece_at(vu, Q8 ? c : 2 * c), w);
+                        if constexpr (Q8) {
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                const uint32_t x = T == GDN_KV_I8 ? w[2 * v] ^ 0x80808080u : w[2 * v];
+                                const uint32_t z = T == GDN_KV_I8 ? w[2 * v + 1] ^ 0x80808080u : w[2 * v + 1];
+                                f[v][0] = codes_f16<T, 0, 2>(x);     // columns 2g of keys 0-7, 2g + 1, then keys 8-15
+                                f[v][1] = codes_f16<T, 1, 3>(x);
+                                f[v][2] = codes_f16<T, 0, 2>(z);
+                                f[v][3] = codes_f16<T, 1, 3>(z);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[0][e] = w[e];
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int v = 0; v < STEP; ++v)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[v][e] = clean(f[v][e], e >> 1);
+                        }
+                    };
+                    // the second product's operand: (keys 2t, 2t+1; row g)
+                    uint32_t pt[NR][2];
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) pt[nr][h] = transpose8(pf[nr][h]);
+                    bool first_pass = true;
+                    if constexpr (Q8) {
+                        faint = __any_sync(0xffffffffu, faint);
+                        if (faint) {         // does fp16 hold anything of these keys?
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) any |= pt[nr][0] | pt[nr][1];
+                            first_pass = __any_sync(0xffffffffu, any != 0);
+                        }
+                    }
+                    if (first_pass) {
 #pragma unroll
                         for (int c = 0; c < KT; c += STEP) {
                             uint32_t f[STEP][4];
                             values(c, f);
 #pragma unroll
-                            for (int v = 0; v < STEP; ++v) {
+                            for (int v = 0; v < STEP; ++v)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[v][e]));
-                                    f[v][e] = bf16x2(x.x, x.y);
+                                for (int nr = 0; nr < NR; ++nr) mma16816<T>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
+                        }
+                    }
+                    if constexpr (Q8) {
+                        if (faint) {
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[nr][h]));
+                                    pt[nr][h] = transpose8(bf16x2(pk[nr][2 * h] - r.x, pk[nr][2 * h + 1] - r.y));
                                 }
 #pragma unroll
-                                for (int nr = 0; nr < NR; ++nr)
-                                    mma16816<GDN_KV_BF16>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
+                            for (int c = 0; c < KT; c += STEP) {
+                                uint32_t f[STEP][4];
+                                values(c, f);
+#pragma unroll
+                                for (int v = 0; v < STEP; ++v) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[v][e]));
+                                        f[v][e] = bf16x2(x.x, x.y);
+                                    }
+#pragma unroll
+                                    for (int nr = 0; nr < NR; ++nr)
+                                        mma16816<GDN_KV_BF16>(o[nr][c + v], f[v], pt[nr][0], pt[nr][1]);
+                                }
                             }
                         }
                     }
-                }
-                if (T != GDN_KV_I8 && edge && __any_sync(0xffffffffu, odd)) {
-                    // rows that see such a key add its term by themselves
-                    const unsigned char* vt = ring + slot * L::HALF;
+                    if (T != GDN_KV_I8 && edge && __any_sync(0xffffffffu, odd)) {
+                        // rows that see such a key add its term by themselves
+                        const unsigned char* vt = ring + slot * L::HALF;
 #pragma unroll 1
-                    for (int j = 0; j < min(limit(u), 16); ++j) {
-                        const int d = key0 + 16 * u + j - ctx, src = ((j & 7) << 2) | t;
+                        for (int j = 0; j < min(limit(u), 16); ++j) {
+                            const int d = key0 + 16 * u + j - ctx, src = ((j & 7) << 2) | t;
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
+                            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float p = __shfl_sync(0xffffffffu, j < 8 ? pk[nr][e] : pk[nr][2 + e], src);
-                                if (d >= 0 && !((seen[8 * nr + 2 * t + e] >> (d & 63)) & 1)) continue;
+                                for (int e = 0; e < 2; ++e) {
+                                    const float p = __shfl_sync(0xffffffffu, j < 8 ? pk[nr][e] : pk[nr][2 + e], src);
+                                    if (d >= 0 && !((seen[8 * nr + 2 * t + e] >> (d & 63)) & 1)) continue;
 #pragma unroll
-                                for (int c = 0; c < KT; ++c)
+                                    for (int c = 0; c < KT; ++c)
 #pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        const int col = 16 * c + (Q8 ? 2 * g + h : 8 * h + g), key = 16 * u + j;
-                                        float v;
-                                        if constexpr (Q8)
-                                            v = __half2float(__half(__nv_cvt_fp8_to_halfraw(vt[ac_piece<L>(key, col >> 4) + (col & 15)], __NV_E4M3)));
-                                        else
-                                            v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + ac_piece<L>(key, col >> 3) + 2 * (col & 7)));
-                                        if (!(fabsf(v) < INFINITY)) o[nr][c][2 * h + e] += p * v;
-                                    }
-                            }
+                                        for (int h = 0; h < 2; ++h) {
+                                            const int col = 16 * c + (Q8 ? 2 * g + h : 8 * h + g), key = 16 * u + j;
+                                            float v;
+                                            if constexpr (Q8)
+                                                v = __half2float(__half(__nv_cvt_fp8_to_halfraw(vt[ac_piece<L>(key, col >> 4) + (col & 15)], __NV_E4M3)));
+                                            else
+                                                v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + ac_piece<L>(key, col >> 3) + 2 * (col & 7)));
+                                            if (!(fabsf(v) < INFINITY)) o[nr][c][2 * h + e] += p * v;
+                                        }
+                                }
+                        }
                     }
                 }
+            };
+            if constexpr (T == GDN_KV_I8) {
+                // two copies of the code, so that the plain tiles do without the tests (for the
+                // other types, whose edge tiles look for values that are not finite, two copies spill)
+                if (edge_tile)
+                    finish(Flag<true>{});
+                else
+                    finish(Flag<false>{});
+            } else {
+                finish(edge_tile);
             }
             __syncwarp();
             if (2 * i + 1 + L::NS < 2 * mine) issue(2 * i + 1 + L::NS, slot, page_b);

@@ -69,9 +69,10 @@ struct AtSmem {
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
     static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
-    // Q in; S, P and P V by buffer; decisions by group and 32 rows; images and raw tiles, full and empty
-    static constexpr int QF = 0, SF = 1, PF = 3, PV = 5, FIN = 7, DR = 8, KF = 16, KE = KF + ST, VF = KE + ST, VE = VF + ST,
-                         RF = VE + ST, RE = RF + RS, NBAR = RE + RS;
+    // Q in; P by buffer; decisions by group and 32 rows; per image slot: K and V full, S and P V done (which also
+    // empties the slot); raw tiles, full and empty
+    static constexpr int QF = 0, PF = 1, FIN = 3, DR = 4, KF = 12, VF = KF + ST, SF = VF + ST, PV = SF + ST, RF = PV + ST,
+                         RE = RF + RS, NBAR = RE + RS;
     static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite
     static constexpr int BYTES = MISC + 16;
     // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
@@ -134,7 +135,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             int n = 1;
             if (i == L::QF) n = AT_SM_WARPS;
             if (i == L::PF || i == L::PF + 1) n = AT_SM_WARPS / 2;
-            if (Q8 && ((i >= L::KF && i < L::KE) || (i >= L::VF && i < L::VE) || i >= L::RE)) n = 4;   // the converting warps
+            if (Q8 && ((i >= L::KF && i < L::SF) || i >= L::RE)) n = 4;   // the converting warps
             mbar_init_cta(bars + i, n);
         }
         mbar_init_fence();
@@ -198,7 +199,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 } else {
                     const bool v = warp == 10;
                     const uint32_t sl = n % ST;
-                    if (n >= ST) ok = __all_sync(0xffffffffu, at_wait(bars + (v ? L::VE : L::KE) + sl, (n / ST - 1) & 1, abort));
+                    if (n >= ST) ok = __all_sync(0xffffffffu, at_wait(bars + (v ? L::PV : L::SF) + sl, (n / ST - 1) & 1, abort));
                     if (ok) load(v ? &mv : &mk, bars + (v ? L::VF : L::KF) + sl, (v ? L::V0 : L::K0) + sl * L::TILE, L::TILE, j, page);
                 }
                 page = ahead;
@@ -214,7 +215,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 for (int v = 0; ok && v < 2; ++v) {
                     const uint32_t m = 2 * n + v, sl = m % RS;
                     ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort);
-                    if (ok && n >= ST) ok = at_wait(bars + (v ? L::VE : L::KE) + n % ST, (n / ST - 1) & 1, abort);
+                    if (ok && n >= ST) ok = at_wait(bars + (v ? L::PV : L::SF) + n % ST, (n / ST - 1) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const unsigned char* src = base + L::R0 + sl * L::RAW;
@@ -251,59 +252,84 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // S of a tile needs its K image and its buffer (P V two tiles before has
-        // read P there); P V needs P and the V image.  One thread polls both and
-        // issues what is ready; a stall past 2 s sets the error word.
-        if (lane == 0) {
-            constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
-            constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
-            bool ok = true;
-            uint32_t piece = 0;
-            while (ok && next()) {
-                ok = at_wait(bars + L::QF, piece & 1, abort);
-                ++piece;
-                int ns = 0, np = 0, spins = 0;
-                uint64_t t_last = 0;
-                while (ok && np < nb) {
-                    const uint32_t is = n + ns, ip = n + np;
-                    if (ns < nb && ns < np + 2 && (ns < 2 || at_ready(bars + L::PV + (is & 1), ((is - 2) >> 1) & 1)) &&
-                        at_ready(bars + L::KF + is % ST, (is / ST) & 1)) {
-                        t5::fence_after();
-                        const uint32_t kt = sbase + L::K0 + (is % ST) * L::TILE;
+        // read P there); P V needs P and the V image.  The warp polls both and one
+        // lane issues what is ready; a stall past 2 s sets the error word.  All
+        // lanes run the loop, on values that are uniform to the compiler (votes and
+        // reductions): a single thread's loop took longer to issue the products
+        // than they run.
+        constexpr uint32_t FULL = 0xffffffffu;
+        constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
+        constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
+        const uint32_t one = lane == 0, tm = __reduce_max_sync(FULL, tmem);
+        const uint64_t kd0 = t5::desc_sw128(sbase + L::K0), vd0 = t5::desc_sw128_mn(sbase + L::V0, BN * 128);
+        bool ok = true;
+        uint32_t piece = 0;
+        uint32_t si = 0, sslot = 0, sphase = 0;    // tile, image slot and its phase of the next S
+        uint32_t bslot = 0, bphase = 0;            // slot and phase of P V two tiles before it
+        uint32_t pi = 0, pslot = 0, pphase = 0;    // of the next P V
+        while (ok && next()) {
+            ok = __all_sync(FULL, at_wait(bars + L::QF, piece & 1, abort));
+            ++piece;
+            const int tiles = static_cast<int>(__reduce_max_sync(FULL, static_cast<uint32_t>(nb)));
+            int ns = 0, np = 0, spins = 0;
+            uint64_t t_last = 0;
+            while (ok && np < tiles) {
+                // all four tests under one latency; what is ready of both is issued without another look
+                const bool k = at_ready(bars + L::KF + sslot, sphase), b = at_ready(bars + L::PV + bslot, bphase);
+                const bool p = at_ready(bars + L::PF + (pi & 1), (pi >> 1) & 1), v = at_ready(bars + L::VF + pslot, pphase);
+                const bool s_on = __all_sync(FULL, ns < tiles && ns < np + 2 && k && (ns < 2 || b));
+                const bool p_on = __all_sync(FULL, np < ns && p && v);
+                if (s_on) {
+                    t5::fence_after();
+                    const uint64_t kd = kd0 + sslot * (L::TILE / 16);
+                    const uint32_t to = tm + (si & 1) * BN;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            t5::mma_f16_ts(tmem + (is & 1) * BN, tmem + L::QCOL + kk * 8,
-                                           t5::desc_sw128(kt + (kk >> 2) * (BN * 128) + (kk & 3) * 32), IDS, kk > 0 ? 1u : 0u);
-                        t5::commit(bars + L::SF + (is & 1));
-                        t5::commit(bars + L::KE + is % ST);
-                        ++ns;
-                        spins = 0;
-                    } else if (np < ns && at_ready(bars + L::PF + (ip & 1), (ip >> 1) & 1) &&
-                               at_ready(bars + L::VF + ip % ST, (ip / ST) & 1)) {
-                        t5::fence_after();
-                        const uint32_t vt = sbase + L::V0 + (ip % ST) * L::TILE;
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            t5::mma_f16_ts(tmem + L::OCOL, tmem + (ip & 1) * BN + kk * 8, t5::desc_sw128_mn(vt + kk * 2048, BN * 128),
-                                           IDO, (np > 0 || kk > 0) ? 1u : 0u);
-                        t5::commit(bars + L::PV + (ip & 1));
-                        t5::commit(bars + L::VE + ip % ST);
-                        ++np;
-                        spins = 0;
-                    } else if (++spins >= 1024) {
-                        if (spins == 1024) t_last = globaltimer_ns();
-                        if (*abort || globaltimer_ns() - t_last > 2000000000ull) {
-                            if (!*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
-                            *abort = 1;
-                            ok = false;
-                        }
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        t5::mma_f16_ts_on(one, to, tm + L::QCOL + kk * 8, kd + ((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16, IDS,
+                                          kk > 0 ? 1u : 0u);
+                    t5::commit_on(one, bars + L::SF + sslot);
+                    ++ns;
+                    if (++sslot == ST) {
+                        sslot = 0;
+                        sphase ^= 1;
+                    }
+                    if (++si > 2 && ++bslot == ST) {
+                        bslot = 0;
+                        bphase ^= 1;
                     }
                 }
-                n += nb;
+                if (p_on) {
+                    t5::fence_after();
+                    const uint64_t vd = vd0 + pslot * (L::TILE / 16);
+                    const uint32_t from = tm + (pi & 1) * BN;
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        t5::mma_f16_ts_on(one, tm + L::OCOL, from + kk * 8, vd + kk * (2048 / 16), IDO, (np > 0 || kk > 0) ? 1u : 0u);
+                    t5::commit_on(one, bars + L::PV + pslot);
+                    ++np;
+                    ++pi;
+                    if (++pslot == ST) {
+                        pslot = 0;
+                        pphase ^= 1;
+                    }
+                }
+                if (s_on || p_on) {
+                    spins = 0;
+                } else if (++spins >= 1024) {
+                    const uint64_t now = globaltimer_ns();
+                    if (spins == 1024) t_last = now;
+                    if (__any_sync(FULL, *abort || now - t_last > 2000000000ull)) {
+                        if (lane == 0 && !*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
+                        __syncwarp();
+                        *abort = 1;
+                        ok = false;
+                    }
+                }
             }
-            // every product issued has completed before TMEM is released
-            t5::commit(bars + L::FIN);
-            mbar_wait_bounded(bars + L::FIN, 0, nullptr, 0, 200000000ull);
         }
+        // every product issued has completed before TMEM is released
+        t5::commit_on(one, bars + L::FIN);
+        mbar_wait_bounded(bars + L::FIN, 0, nullptr, 0, 200000000ull);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
@@ -431,7 +457,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     scales_of(j + 2);
                 }
 
-                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + (i & 1), (i >> 1) & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + i % ST, (i / ST) & 1, abort));
                 // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
                 float xs[KEEP][32];
                 auto scores = [&](int ch, float (&x)[32]) {
@@ -481,7 +507,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     }
                     if (ok && __any_sync(0xffffffffu, bm > m + AC_MARGIN)) {
                         // O is rescaled once P V of tile i - 1 has finished
-                        ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort));
+                        ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + (i - 1) % ST, ((i - 1) / ST) & 1, abort));
                         if (ok) {
                             const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
                             m = mn;
@@ -590,8 +616,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             // ---- the piece's rows out
             const uint32_t i1 = n - 1;
             // the last S first: the phase of P V before the last one, of the same barrier, is then over
-            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + (i1 & 1), (i1 >> 1) & 1, abort) &&
-                                             at_wait(bars + L::PV + (i1 & 1), (i1 >> 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + i1 % ST, (i1 / ST) & 1, abort) &&
+                                             at_wait(bars + L::PV + i1 % ST, (i1 / ST) & 1, abort));
             // the last decision, for the group that did not take it
             at_bar_softmax();
             const float mo = row_max[r];
