@@ -36,7 +36,8 @@ struct AttCacheArgs {
     int start;          // blocks that each pair counts more than it has
     int box;            // keys of one copy
     float sl2;          // scale * log2(e)
-    float* part;        // [runs * ranks][2][rows][D + 2] partials
+    float* part;        // partial accumulators [runs * ranks][2][rows][D]
+    float2* part_ml;    // and their maxima and sums [runs * ranks][2][rows]
 };
 
 // A sequence as the kernels see it, its device-held numbers forced into range.

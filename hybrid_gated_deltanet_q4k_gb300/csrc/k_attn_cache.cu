@@ -638,7 +638,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         }
         __syncthreads();
         const bool whole = b0 == 0 && b1 == pc.blocks;
-        float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (b0 > 0 ? 0 : 1)) * L::ROWS * (D + 2);
+        const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (b0 > 0 ? 0 : 1)) * L::ROWS;
         for (int e = tid; e < rows * (D / 2); e += L::THREADS) {
             const int r = e / (D / 2), c = (e % (D / 2)) * 2;
             float mx = -INFINITY;
@@ -660,8 +660,8 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     *reinterpret_cast<uint32_t*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + c) =
                         bf16x2(x * inv, z * inv);
             } else {
-                *reinterpret_cast<float2*>(part + r * (D + 2) + 2 + c) = make_float2(x, z);
-                if (c == 0) *reinterpret_cast<float2*>(part + r * (D + 2)) = make_float2(mx, lt);
+                *reinterpret_cast<float2*>(a.part + (part0 + r) * D + c) = make_float2(x, z);
+                if (c == 0) a.part_ml[part0 + r] = make_float2(mx, lt);
             }
         }
         fence_proxy_async_smem();   // the ring was written here; copies come next
@@ -674,19 +674,18 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     }
 }
 
-// Joins the partials of the pairs that lie in more than one run: a block per
-// pair and row (every gridDim.y-th row), D/4 threads across a row and the runs
-// dealt over the others, since one row's chain of loads would take longer than
-// its bytes.
+// Joins the partials of the pairs that lie in more than one run.  blockIdx.x is
+// the pair.  Few partials: a warp per row, no barrier.  Many (one long
+// sequence): a block per row, the partials dealt over its warps, since one
+// row's chain of loads would take longer than its bytes.
 template <int D>
 __global__ void __launch_bounds__(AC_JOIN_THREADS)
 attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
-    constexpr int W = D / 4, G = AC_JOIN_THREADS / W;
-    __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[AC_JOIN_THREADS / 32];
+    constexpr int WARPS = AC_JOIN_THREADS / 32, E = D / 32;   // each lane E columns, 2 at a time
+    __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[WARPS];
     __shared__ AcSeq seq[GDN_MAX_SEQS];
-    __shared__ float2 ml[AC_MAX_RUNS];
-    __shared__ float4 acc[G][W];
-    const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    __shared__ float2 acc[WARPS][D / 2];
+    const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ac_prefix(a, pre, seq, wsum, false);     // inputs of the call: complete before the kernel that is waited for began
     pdl_wait();
     const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total), counted = pre[s + 1] - pre[s];
@@ -695,47 +694,65 @@ attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
     if (counted == 0 || first / per == last / per) return;   // written by its one run
     const AcSeq q = seq[s];
     const int c0 = static_cast<int>(first / per), n = static_cast<int>(last / per) - c0 + 1;
-    const int c = threadIdx.x % W, grp = threadIdx.x / W;
-    for (int rr = blockIdx.y; rr < q.nq * a.ratio; rr += gridDim.y) {
-        const int rank = rr / rank_rows, r = rr % rank_rows;
+    const bool many = n > 8;
+    const int rows = q.nq * a.ratio;
+    for (int rr = many ? blockIdx.y : blockIdx.y * WARPS + warp; rr < rows; rr += many ? gridDim.y : gridDim.y * WARPS) {
+        const int rank = rr / rank_rows, r = rr - rank * rank_rows;
         auto piece = [&](int k) {
-            const int run = c0 + k, which = run * per > first ? 0 : 1;
-            return a.part + ((static_cast<int64_t>(run) * a.ranks + rank) * 2 + which) * rank_rows * (D + 2) + r * (D + 2);
+            return ((static_cast<int64_t>(c0 + k) * a.ranks + rank) * 2 + (k > 0 ? 0 : 1)) * rank_rows + r;
         };
-        if (threadIdx.x < n) ml[threadIdx.x] = *reinterpret_cast<const float2*>(piece(threadIdx.x));
-        __syncthreads();
+        // maximum over all partials; each lane's weight and share of the sum (partials lane, lane + 32, ..)
         float mx = -INFINITY;
-        for (int k = 0; k < n; ++k) mx = fmaxf_nan(mx, ml[k].x);
+        for (int k = lane; k < n; k += 32) mx = fmaxf_nan(mx, a.part_ml[piece(k)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         float lt = 0.0f;
-        for (int k = 0; k < n; ++k) lt = fmaf(ml[k].x == -INFINITY ? 0.0f : ex2_ftz(ml[k].x - mx), ml[k].y, lt);
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = grp; k < n; k += G) {
-            const float f = ml[k].x == -INFINITY ? 0.0f : ex2_ftz(ml[k].x - mx);
-            const float2* p = reinterpret_cast<const float2*>(piece(k) + 2 + 4 * c);
-            const float2 u = p[0], v = p[1];
-            x.x = fmaf(f, u.x, x.x);
-            x.y = fmaf(f, u.y, x.y);
-            x.z = fmaf(f, v.x, x.z);
-            x.w = fmaf(f, v.y, x.w);
-        }
-        acc[grp][c] = x;
-        __syncthreads();
-        if (grp == 0) {
-            for (int k = 1; k < G; ++k) {
-                const float4 v = acc[k][c];
-                x.x += v.x;
-                x.y += v.y;
-                x.z += v.z;
-                x.w += v.w;
+        float2 x[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) x[e] = make_float2(0.0f, 0.0f);
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float w = 0.0f;
+            if (k0 + lane < n) {
+                const float2 v = a.part_ml[piece(k0 + lane)];
+                // weight 0, not left out: a NaN (of a score, or 0 times an infinite value) stays
+                w = v.x == -INFINITY ? 0.0f : ex2_ftz(v.x - mx);
+                lt = fmaf(w, v.y, lt);
             }
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-            const int i = rr / a.ratio;
-            if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
-                *reinterpret_cast<uint2*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + 4 * c) =
-                    make_uint2(bf16x2(x.x * inv, x.y * inv), bf16x2(x.z * inv, x.w * inv));
+#pragma unroll 4
+            for (int k = many ? warp : 0; k < min(n - k0, 32); k += many ? WARPS : 1) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+                const float2* p = reinterpret_cast<const float2*>(a.part + piece(k0 + k) * D) + lane;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const float2 v = p[32 * e];
+                    x[e].x = fmaf(f, v.x, x[e].x);
+                    x[e].y = fmaf(f, v.y, x[e].y);
+                }
+            }
         }
-        __syncthreads();
+        lt = warp_sum(lt);
+        if (many) {
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) acc[warp][lane + 32 * e] = x[e];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e)
+                    for (int w = 1; w < WARPS; ++w) {
+                        x[e].x += acc[w][lane + 32 * e].x;
+                        x[e].y += acc[w][lane + 32 * e].y;
+                    }
+            }
+            __syncthreads();
+            if (warp > 0) continue;
+        }
+        const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+        const int i = rr / a.ratio;
+        if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq)) {
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D) + lane;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) out[32 * e] = bf16x2(x[e].x * inv, x[e].y * inv);
+        }
     }
 }
 
@@ -751,7 +768,7 @@ constexpr int AC_TREE_ROWS = 33;
 size_t attn_cache_workspace_bytes(const gdn_kv_cache& c, int64_t n_tokens, int hq) {
     // partials of the rows of one CTA: 4096 / D at most in the kernel for few rows
     const int rows = n_tokens * (hq / c.n_kv_heads) >= AC_TREE_ROWS ? AC_TREE_TILE : 4096 / c.head_dim;
-    return static_cast<size_t>(AC_MAX_RUNS) * 2 * rows * (c.head_dim + 2) * 4;
+    return static_cast<size_t>(AC_MAX_RUNS) * 2 * rows * (c.head_dim * 4 + 8);
 }
 
 template <int D>
@@ -818,8 +835,11 @@ cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t 
     a.max_q = max_q < n_tokens ? max_q : static_cast<int>(n_tokens);
     a.max_blocks = max_blocks;
     a.sl2 = scale * LOG2E;
-    a.part = static_cast<float*>(workspace);
+    a.part_ml = static_cast<float2*>(workspace);
     const int rows = a.max_q * a.ratio;
+    // maxima and sums first, then the accumulators
+    const int part_rows = rows >= AC_TREE_ROWS ? AC_TREE_TILE : 4096 / c.head_dim;
+    a.part = static_cast<float*>(workspace) + static_cast<int64_t>(AC_MAX_RUNS) * 2 * part_rows * 2;
     if (rows >= AC_TREE_ROWS) {
         const cudaError_t e = launch_attn_tree(c, a, st);
         if (e != cudaSuccess) return e;

@@ -58,14 +58,15 @@ struct AtSmem {
     static constexpr int TILE = BN * D * 2;                 // a K or V image
     // images of K (and of V) held at once, raw tiles in flight
     static constexpr int ST = Q8 ? 2 : D == 256 ? 3 : 6;
-    static constexpr int RS = !Q8 ? 1 : D == 256 ? 5 : 10;
+    static constexpr int RS = !Q8 ? 1 : D == 256 ? 4 : 8;
     static constexpr int K0 = 0;
     static constexpr int V0 = K0 + ST * TILE;
     static constexpr int R0 = V0 + ST * TILE;
     static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN]
     static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 2 * BN * 4 : 0);   // maximum of each row; masks of zero weights [2][128]
     static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each group
-    static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
+    static constexpr int E0 = L0 + 2 * AT_ROWS * 4;         // 16 columns on their way out: [softmax warp][32 rows][17]
+    static constexpr int P0 = E0 + AT_SM_WARPS * 32 * 17 * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
     static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
@@ -358,7 +359,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 float up = 1.0f;
                 if constexpr (Q8) {
                     float amax = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = 0; c < D / 16; ++c) {
                         const uint4 w = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
                         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -373,7 +374,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                     factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
                 }
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < D / 16; c += 4) {
                     uint32_t u[16];
 #pragma unroll
@@ -633,25 +634,28 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const float lt = lsum[r] + lsum[AT_ROWS + r];
             if (ok) {
                 t5::fence_after();
+                // Half of the columns, 16 at a time, through this warp's piece of shared
+                // memory: a thread holds a row, and memory wants whole sectors of one.
                 const bool whole = pc.b0 == 0 && pc.b1 == pc.blocks;
                 const float inv = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
-                const bool store = on && GDN_IN_RANGE(g_attn_cache_error, q.tok + tok < a.n_tokens && hq < a.hq);
-                uint16_t* orow = a.o + (q.tok + tok) * a.ld_o + hq * D;
-                float* part = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (pc.b0 > 0 ? 0 : 1)) * AT_ROWS + r) * (D + 2);
+                float* stage = reinterpret_cast<float*>(base + L::E0) + (warp - 2) * (32 * 17);
+                const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (pc.b0 > 0 ? 0 : 1)) * AT_ROWS + 32 * quad;
 #pragma unroll 1
-                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
-                    float ov[32];
-                    t5::ld32(trow + L::OCOL + c0, ov);
-                    if (odd_keys && store) {
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
+                    float ov[16];
+                    t5::ld16(trow + L::OCOL + c0, ov);
+                    if (odd_keys) {
                         // values that are not finite: infinite or NaN whatever their (positive) weight is
 #pragma unroll 1
                         for (int d = 0; d < 64; ++d) {
                             if (!((odd_keys >> d) & 1)) continue;
-                            const int key = ctx + d, pg = table[min(key >> a.page_shift, a.max_blocks - 1)];
-                            if (key < 0 || key < pc.b0 * AC_BLOCK || key >= pc.b1 * AC_BLOCK || pg < 0 || pg >= a.n_pages) continue;
+                            const int key = ctx + d;
+                            if (key < 0 || key < pc.b0 * AC_BLOCK || key >= pc.b1 * AC_BLOCK) continue;
+                            const int pg = page_at(key);
+                            if (pg < 0 || pg >= a.n_pages) continue;
                             const int64_t vr = ((static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key & (a.page - 1))) * D + c0;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
+                            for (int e = 0; e < 16; ++e) {
                                 float v;
                                 if constexpr (Q8)
                                     v = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(a.v)[vr + e], __NV_E4M3)));
@@ -661,24 +665,32 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             }
                         }
                     }
-                    if (!store) continue;
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) stage[lane * 17 + e] = ov[e] * inv;
+                    __syncwarp();
                     if (whole) {
+                        // four rows of 32 bytes at a time
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(ov[e + 2 * h] * inv, ov[e + 2 * h + 1] * inv);
-                                u[h] = *reinterpret_cast<const uint32_t*>(&b2);
+                        for (int y = 0; y < 32; y += 4) {
+                            const int rl = y + (lane >> 3), c = 2 * (lane & 7), orow = row0 + 32 * quad + rl, ot = orow / a.ratio;
+                            if (32 * quad + rl < rows &&
+                                GDN_IN_RANGE(g_attn_cache_error, q.tok + ot < a.n_tokens && pc.head * a.ratio + orow - ot * a.ratio < a.hq)) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(stage[rl * 17 + c], stage[rl * 17 + c + 1]);
+                                *reinterpret_cast<uint32_t*>(a.o + (q.tok + ot) * a.ld_o + (pc.head * a.ratio + orow - ot * a.ratio) * D + c0 + c) =
+                                    *reinterpret_cast<const uint32_t*>(&b2);
                             }
-                            *reinterpret_cast<uint4*>(orow + c0 + e) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     } else {
+                        // two rows of 64 bytes at a time
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2*>(part + 2 + c0 + e) = make_float2(ov[e], ov[e + 1]);
+                        for (int y = 0; y < 32; y += 2) {
+                            const int rl = y + (lane >> 4), c = lane & 15;
+                            if (32 * quad + rl < rows) a.part[(part0 + rl) * D + c0 + c] = stage[rl * 17 + c];
+                        }
                     }
                 }
-                if (!whole && on && half == 0) *reinterpret_cast<float2*>(part) = make_float2(m, lt);
+                if (!whole && on && half == 0) a.part_ml[part0 + lane] = make_float2(m, lt);
                 t5::fence_before();
             }
             at_bar_softmax();           // every row has read what the others left it
@@ -709,7 +721,7 @@ static cudaError_t at_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
         return cudaErrorInvalidDevice;
     CUtensorMap mk, mv;
     a.box = c.page_tokens < L::BN ? c.page_tokens : L::BN;
-    a.start = 768 / L::ROW > 0 ? 768 / L::ROW : 1;
+    a.start = 4;   // starting and ending a piece take about as long as four blocks
     if (!ac_map(&mk, c.k, c, a.box, 1) || !ac_map(&mv, c.v, c, a.box, 1)) return cudaErrorInvalidValue;
     a.ranks = (a.max_q * a.ratio + AT_ROWS - 1) / AT_ROWS;
     a.runs = AC_MAX_RUNS / a.ranks;
