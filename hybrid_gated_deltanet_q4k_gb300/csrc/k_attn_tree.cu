@@ -74,8 +74,8 @@ struct AtSmem {
     // empties the slot); raw tiles, full and empty
     static constexpr int QF = 0, PF = 1, FIN = 3, DR = 4, KF = 12, VF = KF + ST, SF = VF + ST, PV = SF + ST, RF = PV + ST,
                          RE = RF + RS, NBAR = RE + RS;
-    static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite
-    static constexpr int BYTES = MISC + 16;
+    static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite, tiles of the piece
+    static constexpr int BYTES = MISC + 32;
     // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
     static constexpr int DYN = BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024;
     static_assert(DYN <= 227 * 1024, "shared memory of a CTA");
@@ -84,11 +84,31 @@ struct AtSmem {
     static_assert(OCOL + D <= 512, "TMEM columns");
 };
 
+// Waits for a phase, asleep for up to 20 us at a time: warps that poll take
+// issue slots and shared-memory cycles from the one that issues the products.
+// Gives up after 2 s with the error word set, and at once after any wait of the
+// CTA has.
 __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_test(bar, parity)) return true;
-    if (*abort) return false;
-    if (mbar_wait_bounded(bar, parity, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) return true;
-    *abort = 1;
+    auto sleep = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        return ok != 0;
+    };
+    if (sleep()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!*abort) {
+        if (sleep()) return true;
+        if (globaltimer_ns() - t0 > 2000000000ull) {
+            atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
+            *abort = 1;
+        }
+    }
     return false;
 }
 __device__ __forceinline__ bool at_ready(uint64_t* bar, uint32_t parity) {
@@ -128,6 +148,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     uint32_t* tslot = reinterpret_cast<uint32_t*>(base + L::MISC);
     volatile int* abort = reinterpret_cast<volatile int*>(base + L::MISC + 4);
     unsigned long long* odd = reinterpret_cast<unsigned long long*>(base + L::MISC + 8);
+    volatile int* piece_tiles = reinterpret_cast<volatile int*>(base + L::MISC + 16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t sbase = smem_addr(base);
 
@@ -268,10 +289,12 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         uint32_t si = 0, sslot = 0, sphase = 0;    // tile, image slot and its phase of the next S
         uint32_t bslot = 0, bphase = 0;            // slot and phase of P V two tiles before it
         uint32_t pi = 0, pslot = 0, pphase = 0;    // of the next P V
-        while (ok && next()) {
+        while (true) {
+            // the softmax says how many tiles the piece has (0: no more pieces)
             ok = __all_sync(FULL, at_wait(bars + L::QF, piece & 1, abort));
+            const int tiles = static_cast<int>(__reduce_max_sync(FULL, static_cast<uint32_t>(*piece_tiles)));
+            if (!ok || tiles == 0) break;
             ++piece;
-            const int tiles = static_cast<int>(__reduce_max_sync(FULL, static_cast<uint32_t>(nb)));
             int ns = 0, np = 0, spins = 0;
             uint64_t t_last = 0;
             while (ok && np < tiles) {
@@ -393,6 +416,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     t5::st16u(trow + L::QCOL + half * (D / 4) + 4 * c, u);
                 }
                 t5::fence_before();
+                if (warp == 2 && lane == 0) *piece_tiles = nb;
                 at_arrive_warp(bars + L::QF, lane);
             }
 
@@ -696,6 +720,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             at_bar_softmax();           // every row has read what the others left it
             if (st == 0) *odd = 0;
         }
+        if (warp == 2 && lane == 0) *piece_tiles = 0;
+        at_arrive_warp(bars + L::QF, lane);
     }
 
     if (*abort && tid == 0) {
