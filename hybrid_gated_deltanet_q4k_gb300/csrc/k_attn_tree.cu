@@ -10,18 +10,17 @@
 // same run of blocks; they walk it at the same time, so the cache comes from L2
 // for all but one.
 //
-// Per tile of 64 keys (row r = TMEM lane r):
-//   S = Q K^T      M = 128, N = 64, K = D; Q in TMEM (from shared memory its
-//                  reads alone would take three times the product), K shared;
-//                  two S buffers
-//   softmax        a thread per row; two groups of four warps take the tiles in
-//                  turn, so that one's exponentials run beside the other's
-//                  waits; P goes over its own S
-//   O += P V       M = 128, N = D, K = 64; P from TMEM, V [key][d] as the
+// Per tile of 128 keys (row r = TMEM lane r):
+//   S = Q K^T      M = 128, N = 128, K = D; Q in TMEM, K from shared memory; two
+//                  S buffers (one for heads of 256, where TMEM has no more)
+//   softmax        two threads per row, 64 scores each; P goes over the
+//                  thread's own scores.  The running maximum is raised only
+//                  past a margin: the two threads swap their maxima when one of
+//                  their 32 rows asks for it, a vote in the barrier between them
+//   O += P V       M = 128, N = D, K = 128; P from TMEM, V [key][d] as the
 //                  MN-major operand, the image that the copy writes: no transpose
-// The running maximum is raised only past a margin; the groups hand it on: a
-// warp waits for the decision of the tile before (not for its exponentials)
-// before it takes its own.
+// The products are as wide as they go, for an instruction takes 65 cycles to
+// issue here however little it multiplies (tiles of 64 keys were bound by that).
 // The pages are bf16: TMA writes the operand images (128-byte swizzle).  8-bit
 // codes go through a ring of raw tiles that four warps turn into fp16 images
 // (exact); the row scales stay out of the products, as in the other kernel: a
@@ -29,9 +28,8 @@
 // probabilities are p' 2^11, exact to 2^-11 down to 2^-25 of the largest and
 // zero below 2^-36 of it.
 //
-// Warps: 0 copies the keys (8-bit: both), 1 allocates TMEM and issues the
-// products (S of a tile two ahead of its P V), 2-5 and 6-9 softmax, 10 copies
-// the values (8-bit: 10-13 convert).  Every wait is bounded; after one runs out the
+// Warps: 0 copies, 1 allocates TMEM and issues the products, 2-9 softmax, and
+// for 8-bit caches 10-13 convert.  Every wait is bounded; after one runs out the
 // CTA stops issuing, lets copies and products finish and returns with the error
 // word set.
 #include "attn_cache.cuh"
@@ -48,39 +46,38 @@ constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
 template <int D, int T>
 struct AtSmem {
     static constexpr bool Q8 = T != GDN_KV_BF16;
-    static constexpr int BN = 64;
-    static constexpr int THREADS = 32 * (2 + AT_SM_WARPS + (Q8 ? 4 : 1));
+    static constexpr int BN = 128;
+    static constexpr int THREADS = 32 * (2 + AT_SM_WARPS + (Q8 ? 4 : 0));
     static constexpr int ROW = D * (Q8 ? 1 : 2);
     static constexpr int SLAB = ROW < 128 ? ROW : 128;      // bytes of a cached row in one slab of the copies
     static constexpr int NSLAB = ROW / SLAB;
     static constexpr int RAW = BN * ROW;                    // a tile as cached
     static constexpr int S16 = D / 64;                      // slabs of an operand image: [rows][64 x 16 bit]
     static constexpr int TILE = BN * D * 2;                 // a K or V image
-    // images of K (and of V) held at once, raw tiles in flight
-    static constexpr int ST = Q8 ? 2 : D == 256 ? 3 : 6;
-    static constexpr int RS = !Q8 ? 1 : D == 256 ? 4 : 8;
-    static constexpr int K0 = 0;
-    static constexpr int V0 = K0 + ST * TILE;
-    static constexpr int R0 = V0 + ST * TILE;
-    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN]
-    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 2 * BN * 4 : 0);   // maximum of each row; masks of zero weights [2][128]
-    static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each group
+    // S buffers in TMEM; images held at once (K and V of the tiles in turn); raw tiles in flight.  An odd
+    // number of images needs the single S buffer (see the waits on ID).
+    static constexpr int SB = D == 256 ? 1 : 2;
+    static constexpr int NI = Q8 ? (D == 256 ? 2 : 4) : D == 256 ? 3 : D == 128 ? 6 : 8;
+    static constexpr int RS = !Q8 ? 1 : D == 256 ? 2 : D == 128 ? 4 : 8;
+    static constexpr int I0 = 0;
+    static constexpr int R0 = I0 + NI * TILE;
+    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN / 2]
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
+    static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
     static constexpr int E0 = L0 + 2 * AT_ROWS * 4;         // 16 columns on their way out: [softmax warp][32 rows][17]
     static constexpr int P0 = E0 + AT_SM_WARPS * 32 * 17 * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
     static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
-    // Q in; P by buffer; decisions by group and 32 rows; per image slot: K and V full, S and P V done (which also
-    // empties the slot); raw tiles, full and empty
-    static constexpr int QF = 0, PF = 1, FIN = 3, DR = 4, KF = 12, VF = KF + ST, SF = VF + ST, PV = SF + ST, RF = PV + ST,
-                         RE = RF + RS, NBAR = RE + RS;
+    // Q in; P in, alternating; per image: full, and done (the product that reads it); raw tiles, full and empty
+    static constexpr int QF = 0, PF = 1, FIN = 3, IF = 4, ID = IF + NI, RF = ID + NI, RE = RF + RS, NBAR = RE + RS;
     static constexpr int MISC = B0 + 8 * NBAR;              // TMEM base, abort flag, keys with values that are not finite, tiles of the piece
     static constexpr int BYTES = MISC + 32;
     // at least 120 KB, so that one CTA holds an SM (it allocates all TMEM columns)
     static constexpr int DYN = BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024;
     static_assert(DYN <= 227 * 1024, "shared memory of a CTA");
-    // TMEM columns: two buffers of S (BN columns) with P over their first BN / 2, Q, O
-    static constexpr uint32_t QCOL = 2 * BN, OCOL = 2 * BN + D / 2;
+    // TMEM columns: S (BN each; the P of either half over the first half of its scores), Q, O
+    static constexpr uint32_t QCOL = SB * BN, OCOL = QCOL + D / 2;
     static_assert(OCOL + D <= 512, "TMEM columns");
 };
 
@@ -130,15 +127,28 @@ __device__ __forceinline__ void at_arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) at_arrive(bar);
 }
-// All softmax threads.
+// All softmax threads; the two warps that share 32 rows (barriers 2 .. 5), as they are and with a vote.
 __device__ __forceinline__ void at_bar_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(AT_SM_THREADS) : "memory"); }
+__device__ __forceinline__ void at_bar_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory"); }
+__device__ __forceinline__ bool at_vote_rows(int quad, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.or.pred p, %1, 64, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r)
+        : "r"(2 + quad), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
 
 template <int D, int T>
 __global__ void __launch_bounds__(AtSmem<D, T>::THREADS, 1)
 attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttCacheArgs a) {
     using L = AtSmem<D, T>;
-    constexpr int BN = L::BN, ST = L::ST, RS = L::RS;
+    constexpr int BN = L::BN, HN = BN / 2, SB = L::SB, NI = L::NI, RS = L::RS;
     constexpr bool Q8 = L::Q8;
     extern __shared__ __align__(1024) unsigned char smb[];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smb) + 1023) & ~uintptr_t(1023));
@@ -155,9 +165,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
             int n = 1;
-            if (i == L::QF) n = AT_SM_WARPS;
-            if (i == L::PF || i == L::PF + 1) n = AT_SM_WARPS / 2;
-            if (Q8 && ((i >= L::KF && i < L::SF) || i >= L::RE)) n = 4;   // the converting warps
+            if (i == L::QF || i == L::PF || i == L::PF + 1) n = AT_SM_WARPS;
+            if (Q8 && ((i >= L::IF && i < L::ID) || i >= L::RE)) n = 4;   // the converting warps
             mbar_init_cta(bars + i, n);
         }
         mbar_init_fence();
@@ -193,7 +202,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int copies = BN / a.box;
     uint32_t n = 0;   // tiles so far, over all pieces
 
-    if (warp == 0 || (!Q8 && warp == 10)) {
+    if (warp == 0) {
         // ------------------------------------------------------------ TMA
         const int p = lane / L::NSLAB, slab = lane % L::NSLAB;
         const bool on = lane < copies * L::NSLAB;
@@ -211,18 +220,17 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             int page = page_of(0);
             for (int j = 0; ok && j < nb; ++j) {
                 const int ahead = page_of(min(j + 1, nb - 1));
-                if constexpr (Q8) {
-                    // raw tiles: keys, then values
-                    for (int v = 0; ok && v < 2; ++v) {
-                        const uint32_t m = 2 * n + v, sl = m % RS;
+                for (int v = 0; ok && v < 2; ++v) {      // keys, then values
+                    const uint32_t m = 2 * n + v;
+                    if constexpr (Q8) {
+                        const uint32_t sl = m % RS;
                         if (m >= RS) ok = __all_sync(0xffffffffu, at_wait(bars + L::RE + sl, (m / RS - 1) & 1, abort));
                         if (ok) load(v ? &mv : &mk, bars + L::RF + sl, L::R0 + sl * L::RAW, L::RAW, j, page);
+                    } else {
+                        const uint32_t sl = m % NI;
+                        if (m >= NI) ok = __all_sync(0xffffffffu, at_wait(bars + L::ID + sl, (m / NI - 1) & 1, abort));
+                        if (ok) load(v ? &mv : &mk, bars + L::IF + sl, L::I0 + sl * L::TILE, L::TILE, j, page);
                     }
-                } else {
-                    const bool v = warp == 10;
-                    const uint32_t sl = n % ST;
-                    if (n >= ST) ok = __all_sync(0xffffffffu, at_wait(bars + (v ? L::PV : L::SF) + sl, (n / ST - 1) & 1, abort));
-                    if (ok) load(v ? &mv : &mk, bars + (v ? L::VF : L::KF) + sl, (v ? L::V0 : L::K0) + sl * L::TILE, L::TILE, j, page);
                 }
                 page = ahead;
                 ++n;
@@ -235,13 +243,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         while (ok && next()) {
             for (int j = 0; ok && j < nb; ++j) {
                 for (int v = 0; ok && v < 2; ++v) {
-                    const uint32_t m = 2 * n + v, sl = m % RS;
+                    const uint32_t m = 2 * n + v, sl = m % RS, im = m % NI;
                     ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort);
-                    if (ok && n >= ST) ok = at_wait(bars + (v ? L::PV : L::SF) + n % ST, (n / ST - 1) & 1, abort);
+                    if (ok && m >= NI) ok = at_wait(bars + L::ID + im, (m / NI - 1) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const unsigned char* src = base + L::R0 + sl * L::RAW;
-                    unsigned char* dst = base + (v ? L::V0 : L::K0) + (n % ST) * L::TILE;
+                    unsigned char* dst = base + L::I0 + im * L::TILE;
                     // 16 codes per step; consecutive threads take consecutive keys
 #pragma unroll 4
                     for (int e = ct; e < BN * (D / 16); e += 128) {
@@ -265,7 +273,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             make_uint4(codes_f16<T, 0, 1>(w.z), codes_f16<T, 2, 3>(w.z), codes_f16<T, 0, 1>(w.w), codes_f16<T, 2, 3>(w.w));
                     }
                     fence_proxy_async_smem();
-                    at_arrive_warp(bars + (v ? L::VF : L::KF) + n % ST, lane);
+                    at_arrive_warp(bars + L::IF + im, lane);
                     at_arrive_warp(bars + L::RE + sl, lane);
                 }
                 ++n;
@@ -273,22 +281,26 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        // S of a tile needs its K image and its buffer (P V two tiles before has
-        // read P there); P V needs P and the V image.  The warp polls both and one
-        // lane issues what is ready; a stall past 2 s sets the error word.  All
-        // lanes run the loop, on values that are uniform to the compiler (votes and
-        // reductions): a single thread's loop took longer to issue the products
-        // than they run.
+        // S of a tile needs its K image and its buffer (P V of the tile SB before
+        // has read P there); P V needs P and the V image.  The warp polls both and
+        // one lane issues what is ready; a stall past 2 s sets the error word.
         constexpr uint32_t FULL = 0xffffffffu;
         constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
         constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
         const uint32_t one = lane == 0, tm = __reduce_max_sync(FULL, tmem);
-        const uint64_t kd0 = t5::desc_sw128(sbase + L::K0), vd0 = t5::desc_sw128_mn(sbase + L::V0, BN * 128);
+        const uint64_t kd0 = t5::desc_sw128(sbase + L::I0), vd0 = t5::desc_sw128_mn(sbase + L::I0, BN * 128);
         bool ok = true;
         uint32_t piece = 0;
-        uint32_t si = 0, sslot = 0, sphase = 0;    // tile, image slot and its phase of the next S
-        uint32_t bslot = 0, bphase = 0;            // slot and phase of P V two tiles before it
-        uint32_t pi = 0, pslot = 0, pphase = 0;    // of the next P V
+        uint32_t si = 0, sslot = 0, sphase = 0;    // tile, image and its phase of the next S
+        uint32_t bslot = 1, bphase = 0;            // image and phase of P V of the tile SB before it
+        uint32_t pi = 0, pslot = 1, pphase = 0;    // of the next P V
+        auto two_on = [](uint32_t& slot, uint32_t& phase) {    // the image of the next tile
+            slot += 2;
+            if (slot >= NI) {
+                slot -= NI;
+                phase ^= 1;
+            }
+        };
         while (true) {
             // the softmax says how many tiles the piece has (0: no more pieces)
             ok = __all_sync(FULL, at_wait(bars + L::QF, piece & 1, abort));
@@ -299,43 +311,35 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             uint64_t t_last = 0;
             while (ok && np < tiles) {
                 // all four tests under one latency; what is ready of both is issued without another look
-                const bool k = at_ready(bars + L::KF + sslot, sphase), b = at_ready(bars + L::PV + bslot, bphase);
-                const bool p = at_ready(bars + L::PF + (pi & 1), (pi >> 1) & 1), v = at_ready(bars + L::VF + pslot, pphase);
-                const bool s_on = __all_sync(FULL, ns < tiles && ns < np + 2 && k && (ns < 2 || b));
+                const bool k = at_ready(bars + L::IF + sslot, sphase), b = at_ready(bars + L::ID + bslot, bphase);
+                const bool p = at_ready(bars + L::PF + (pi & 1), (pi >> 1) & 1), v = at_ready(bars + L::IF + pslot, pphase);
+                const bool s_on = __all_sync(FULL, ns < tiles && ns < np + SB && k && (ns < SB || b));
                 const bool p_on = __all_sync(FULL, np < ns && p && v);
                 if (s_on) {
                     t5::fence_after();
                     const uint64_t kd = kd0 + sslot * (L::TILE / 16);
-                    const uint32_t to = tm + (si & 1) * BN;
+                    const uint32_t to = tm + (SB == 2 ? (si & 1) * BN : 0);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         t5::mma_f16_ts_on(one, to, tm + L::QCOL + kk * 8, kd + ((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16, IDS,
                                           kk > 0 ? 1u : 0u);
-                    t5::commit_on(one, bars + L::SF + sslot);
+                    t5::commit_on(one, bars + L::ID + sslot);
                     ++ns;
-                    if (++sslot == ST) {
-                        sslot = 0;
-                        sphase ^= 1;
-                    }
-                    if (++si > 2 && ++bslot == ST) {
-                        bslot = 0;
-                        bphase ^= 1;
-                    }
+                    two_on(sslot, sphase);
+                    if (++si > SB) two_on(bslot, bphase);
                 }
                 if (p_on) {
                     t5::fence_after();
                     const uint64_t vd = vd0 + pslot * (L::TILE / 16);
-                    const uint32_t from = tm + (pi & 1) * BN;
+                    const uint32_t from = tm + (SB == 2 ? (pi & 1) * BN : 0);
 #pragma unroll
                     for (int kk = 0; kk < BN / 16; ++kk)
-                        t5::mma_f16_ts_on(one, tm + L::OCOL, from + kk * 8, vd + kk * (2048 / 16), IDO, (np > 0 || kk > 0) ? 1u : 0u);
-                    t5::commit_on(one, bars + L::PV + pslot);
+                        t5::mma_f16_ts_on(one, tm + L::OCOL, from + (kk >> 2) * HN + (kk & 3) * 8, vd + kk * (2048 / 16), IDO,
+                                          (np > 0 || kk > 0) ? 1u : 0u);
+                    t5::commit_on(one, bars + L::ID + pslot);
                     ++np;
                     ++pi;
-                    if (++pslot == ST) {
-                        pslot = 0;
-                        pphase ^= 1;
-                    }
+                    two_on(pslot, pphase);
                 }
                 if (s_on || p_on) {
                     spins = 0;
@@ -357,14 +361,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        // group `half` takes the tiles of its parity (and half of the columns of q and o)
-        const int quad = warp & 3, half = (warp - 2) >> 2, r = 32 * quad + lane, st = (tid - 64) & 127;
+        // thread half `half` of a row: half of the keys of each tile, and of the columns of q and o
+        const int quad = warp & 3, half = (warp - 2) >> 2, r = 32 * quad + lane, st = tid - 64;
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-        float* row_max = reinterpret_cast<float*>(base + L::X0);
+        float* xmax = reinterpret_cast<float*>(base + L::X0);
         float* lsum = reinterpret_cast<float*>(base + L::L0);
-        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * 2 * BN;   // this warp's: BN key factors, BN log2 value scales
-        float* vlog = kfac + BN;
-        constexpr int CH = BN / 32;                       // 32 scores at a time
+        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * BN;   // this warp's: HN key factors, HN log2 value scales
+        float* vlog = kfac + HN;
+        constexpr int CH = HN / 32;                       // 32 scores at a time
         bool ok = true;
         while (next()) {
             const AcSeq q = pc.q;
@@ -433,11 +437,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             auto page_at = [&](int key) { return table[min(key >> a.page_shift, a.max_blocks - 1)]; };
 
-            // ---- 8-bit: the scales of the tile's keys (by lane), read one of this group's tiles ahead, their pages two
-            constexpr int KL = BN / 32;     // keys per lane
+            // ---- 8-bit: the scales of this half's keys (by lane), read a tile ahead, their pages two
+            constexpr int KL = HN / 32;     // keys per lane
             float ksn[KL], vsn[KL];
             int pgn[KL];
-            auto key_of = [&](int j, int x) { return (t0 + min(j, nb - 1)) * BN + 32 * x + lane; };
+            auto key_of = [&](int j, int x) { return (t0 + min(j, nb - 1)) * BN + half * HN + 32 * x + lane; };
             auto scales_of = [&](int j) {
 #pragma unroll
                 for (int x = 0; x < KL; ++x) {
@@ -445,14 +449,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     const int64_t row = (static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key_of(j, x) & (a.page - 1));
                     ksn[x] = a.sk[row];
                     vsn[x] = a.sv[row];
-                    pgn[x] = page_at(key_of(j + 2, x));
+                    pgn[x] = page_at(key_of(j + 1, x));
                 }
             };
-            const int j0 = (n & 1) == static_cast<uint32_t>(half) ? 0 : 1;    // this group's first tile
             if constexpr (Q8) {
 #pragma unroll
-                for (int x = 0; x < KL; ++x) pgn[x] = page_at(key_of(j0, x));
-                scales_of(j0);
+                for (int x = 0; x < KL; ++x) pgn[x] = page_at(key_of(0, x));
+                scales_of(0);
             }
 
             float m = -INFINITY, l = 0.0f;
@@ -461,10 +464,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             // the tests inside its loops would cost the plain tiles five times their exponentials.
             auto tile = [&](int j, auto edge_tag) {
                 constexpr bool edge = decltype(edge_tag)::value;
-                constexpr int KEEP = edge || Q8 ? 1 : CH;   // scores in registers (fewer: the others are read twice)
+                constexpr int KEEP = edge || Q8 ? 1 : CH;   // chunks of scores in registers (fewer: read twice)
                 const uint32_t i = n + j;
                 const int key0 = (t0 + j) * BN;
-                const uint32_t sbuf = trow + (i & 1) * BN;
+                const uint32_t sbuf = trow + (SB == 2 ? (i & 1) * BN : 0) + half * HN;   // this half's scores
                 auto exists = [&](int key) {
                     if (key0 + key >= q.len) return false;
                     if (all_in) return true;
@@ -479,10 +482,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         vlog[32 * x + lane] = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
                     }
                     __syncwarp();
-                    scales_of(j + 2);
+                    scales_of(j + 1);
                 }
 
-                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + i % ST, (i / ST) & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + 2 * i % NI, (2 * i / NI) & 1, abort));
                 // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
                 float xs[KEEP][32];
                 auto scores = [&](int ch, float (&x)[32]) {
@@ -500,7 +503,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     if constexpr (edge) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const int key = 32 * ch + c, d = key0 + key - ctx;
+                            const int key = half * HN + 32 * ch + c, d = key0 + key - ctx;
                             if (!exists(key) || (d >= 0 && !((seen >> (d & 63)) & 1))) x[c] = -INFINITY;
                         }
                     }
@@ -522,25 +525,24 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     }
                     if constexpr (!Q8) bm *= factor;
                 }
-                // ---- the maximum after the tile before (the other group's), then this tile's
-                if (j > 0) {
-                    ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::DR + 4 * (half ^ 1) + quad, ((i - 1) >> 1) & 1, abort));
-                    const float mo = row_max[r];
-                    if (__any_sync(0xffffffffu, mo != m)) {
-                        l *= m == -INFINITY ? 0.0f : ex2_ftz(m - mo);
-                        m = mo;
-                    }
-                    if (ok && __any_sync(0xffffffffu, bm > m + AC_MARGIN)) {
+                if (at_vote_rows(quad, j == 0 || bm > m + AC_MARGIN)) {
+                    // the row's maximum over both halves
+                    xmax[half * AT_ROWS + r] = bm;
+                    at_bar_rows(quad);
+                    bm = fmaxf(bm, xmax[(half ^ 1) * AT_ROWS + r]);
+                    at_bar_rows(quad);
+                    if (j == 0) {
+                        m = bm;
+                    } else {
                         // O is rescaled once P V of tile i - 1 has finished
-                        ok = __all_sync(0xffffffffu, at_wait(bars + L::PV + (i - 1) % ST, ((i - 1) / ST) & 1, abort));
+                        ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i - 1) % NI, ((2 * i - 1) / NI) & 1, abort));
                         if (ok) {
                             const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
                             m = mn;
                             l *= f;
-                            row_max[r] = m;
                             t5::fence_after();
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
+                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                                 float ov[32];
                                 t5::ld32(trow + L::OCOL + c0, ov);
 #pragma unroll
@@ -549,11 +551,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             }
                         }
                     }
-                } else {
-                    m = bm;
-                    row_max[r] = m;
                 }
-                at_arrive_warp(bars + L::DR + 4 * half + quad, lane);
                 if (ok) {
                     const float mm = m == -INFINITY ? 0.0f : Q8 ? m - AC_LIFT : m;
                     const F2 nm = f2(-mm, -mm), ff = f2(factor, factor);
@@ -588,7 +586,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             if constexpr (edge) {
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const int d = key0 + 32 * ch + c + e - ctx;
+                                    const int d = key0 + half * HN + 32 * ch + c + e - ctx;
                                     if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
                                 }
                             }
@@ -601,11 +599,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     if constexpr (edge) {
                         // values of keys that do not exist become zero, and so do those of
                         // new keys that are not finite: the rows that see them add them at the end
-                        ok = __all_sync(0xffffffffu, at_wait(bars + L::VF + i % ST, (i / ST) & 1, abort));
-                        unsigned char* vt = base + L::V0 + (i % ST) * L::TILE;
+                        ok = __all_sync(0xffffffffu, at_wait(bars + L::IF + (2 * i + 1) % NI, ((2 * i + 1) / NI) & 1, abort));
+                        unsigned char* vt = base + L::I0 + (2 * i + 1) % NI * L::TILE;
                         if (ok)
 #pragma unroll 1
-                            for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS / 2) {
+                            for (int e = st; e < BN * (D / 8); e += AT_SM_THREADS) {
                                 const int key = e % BN, c = e / BN, d = key0 + key - ctx;
                                 uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * (BN * 128) + key * 128 + (((c ^ key) & 7) << 4));
                                 if (!exists(key)) {
@@ -630,7 +628,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 t5::fence_before();
                 at_arrive_warp(bars + L::PF + (i & 1), lane);
             };
-            for (int j = j0; j < nb; j += 2) {
+            for (int j = 0; j < nb; ++j) {
                 if ((t0 + j + 1) * BN > ctx || !all_in)
                     tile(j, std::true_type{});
                 else
@@ -640,17 +638,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
             // ---- the piece's rows out
             const uint32_t i1 = n - 1;
-            // the last S first: the phase of P V before the last one, of the same barrier, is then over
-            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::SF + i1 % ST, (i1 / ST) & 1, abort) &&
-                                             at_wait(bars + L::PV + i1 % ST, (i1 / ST) & 1, abort));
-            // the last decision, for the group that did not take it
-            at_bar_softmax();
-            const float mo = row_max[r];
-            l *= m == -INFINITY ? 0.0f : ex2_ftz(m - mo);
-            m = mo;
+            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i1 + 1) % NI, ((2 * i1 + 1) / NI) & 1, abort));
             lsum[half * AT_ROWS + r] = l;
-            at_bar_softmax();
-            uint64_t* none_of = reinterpret_cast<uint64_t*>(row_max);   // the maxima have been read
+            uint64_t* none_of = reinterpret_cast<uint64_t*>(xmax);   // the maxima have been read: every P is in
             none_of[half * AT_ROWS + r] = none;
             at_bar_softmax();
             const uint64_t odd_keys = *odd & seen;
@@ -726,7 +716,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
     if (*abort && tid == 0) {
         // a wait ran out: let copies already issued land (bounded) before the shared memory is released
-        for (int i = L::KF; i < L::NBAR; ++i)
+        for (int i = L::IF; i < L::NBAR; ++i)
             for (uint32_t par = 0; par < 2; ++par) mbar_wait_bounded(bars + i, par, nullptr, 0, 20000000ull);
     }
     t5::fence_before();
