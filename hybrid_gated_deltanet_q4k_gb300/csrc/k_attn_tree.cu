@@ -61,8 +61,8 @@ struct AtSmem {
     static constexpr int RS = !Q8 ? 1 : D == 256 ? 2 : D == 128 ? 4 : 8;
     static constexpr int I0 = 0;
     static constexpr int R0 = I0 + NI * TILE;
-    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors and log2 value scales: [softmax warp][2][BN / 2]
-    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * BN * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
+    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors, log2 value scales, their inverses: [softmax warp][3][BN / 2]
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 3 * BN / 2 * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
     static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
     static constexpr int E0 = L0 + 2 * AT_ROWS * 4;         // 16 columns on their way out: [softmax warp][32 rows][17]
     static constexpr int P0 = E0 + AT_SM_WARPS * 32 * 17 * 4;         // blocks before each sequence
@@ -366,8 +366,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
         float* xmax = reinterpret_cast<float*>(base + L::X0);
         float* lsum = reinterpret_cast<float*>(base + L::L0);
-        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * BN;   // this warp's: HN key factors, HN log2 value scales
-        float* vlog = kfac + HN;
+        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * 3 * HN;   // this warp's: HN key factors,
+        float* vlog = kfac + HN;                          // log2 value scales, and the scales' inverses
+        float* vinv = vlog + HN;
         constexpr int CH = HN / 32;                       // 32 scores at a time
         bool ok = true;
         while (next()) {
@@ -467,6 +468,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 constexpr int KEEP = edge || Q8 ? 1 : CH;   // chunks of scores in registers (fewer: read twice)
                 const uint32_t i = n + j;
                 const int key0 = (t0 + j) * BN;
+                bool wide = false;      // a value scale so far from 1 that its inverse will not do
                 const uint32_t sbuf = trow + (SB == 2 ? (i & 1) * BN : 0) + half * HN;   // this half's scores
                 auto exists = [&](int key) {
                     if (key0 + key >= q.len) return false;
@@ -478,10 +480,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < KL; ++x) {
+                        const float lv = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
                         kfac[32 * x + lane] = ksn[x];
-                        vlog[32 * x + lane] = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
+                        vlog[32 * x + lane] = lv;
+                        vinv[32 * x + lane] = ex2_ftz(-lv);
+                        wide |= !(fabsf(lv) <= 60.0f);
                     }
-                    __syncwarp();
+                    wide = __any_sync(0xffffffffu, wide);
                     scales_of(j + 1);
                 }
 
@@ -556,43 +561,58 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     const float mm = m == -INFINITY ? 0.0f : Q8 ? m - AC_LIFT : m;
                     const F2 nm = f2(-mm, -mm), ff = f2(factor, factor);
                     F2 l2 = f2(0.0f, 0.0f);
+                    // P over this half's scores, and the row's sum: of 2^(x - m), which is p' times the inverse
+                    // of the value's scale, or for scales far from 1 a power of its own
+                    auto probabilities = [&](auto wide_tag) {
+                        constexpr bool far = decltype(wide_tag)::value;
 #pragma unroll
-                    for (int ch = 0; ch < CH; ++ch) {
-                        float(&x)[32] = xs[KEEP == CH ? ch : 0];
-                        if (KEEP < CH) scores(ch, x);
-                        uint32_t pk[16];
+                        for (int ch = 0; ch < CH; ++ch) {
+                            float(&x)[32] = xs[KEEP == CH ? ch : 0];
+                            if (KEEP < CH) scores(ch, x);
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float y0, y1;
-                            f2_split(Q8 ? f2_add(f2(x[c], x[c + 1]), nm) : f2_fma(f2(x[c], x[c + 1]), ff, nm), y0, y1);
-                            const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
-                            if constexpr (Q8) {
-                                const float2 lv = *reinterpret_cast<const float2*>(vlog + 32 * ch + c);
-                                float e0, e1;
-                                f2_split(f2_sub(f2(y0, y1), f2(lv.x, lv.y)), e0, e1);
-                                e0 = ex2_ftz(e0);
-                                e1 = ex2_ftz(e1);
-                                if constexpr (edge) {     // a scale that is no number reaches only the rows that see its key
-                                    if (y0 == -INFINITY) e0 = 0.0f;
-                                    if (y1 == -INFINITY) e1 = 0.0f;
+                            for (int c = 0; c < 32; c += 2) {
+                                float y0, y1;
+                                f2_split(Q8 ? f2_add(f2(x[c], x[c + 1]), nm) : f2_fma(f2(x[c], x[c + 1]), ff, nm), y0, y1);
+                                const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+                                if constexpr (Q8 && far) {
+                                    const float2 lv = *reinterpret_cast<const float2*>(vlog + 32 * ch + c);
+                                    float e0, e1;
+                                    f2_split(f2_sub(f2(y0, y1), f2(lv.x, lv.y)), e0, e1);
+                                    e0 = ex2_ftz(e0);
+                                    e1 = ex2_ftz(e1);
+                                    if constexpr (edge) {     // a scale that is no number reaches only the rows that see its key
+                                        if (y0 == -INFINITY) e0 = 0.0f;
+                                        if (y1 == -INFINITY) e1 = 0.0f;
+                                    }
+                                    l2 = f2_add(l2, f2(e0, e1));
+                                } else if constexpr (Q8) {
+                                    const float2 iv = *reinterpret_cast<const float2*>(vinv + 32 * ch + c);
+                                    l2 = f2_fma(f2(p0, p1), f2(iv.x, iv.y), l2);
+                                } else {
+                                    l2 = f2_add(l2, f2(p0, p1));
                                 }
-                                l2 = f2_add(l2, f2(e0, e1));
-                                pk[c / 2] = f16x2_bits(p0, p1);
-                            } else {
-                                l2 = f2_add(l2, f2(p0, p1));
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                                pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                            }
-                            if constexpr (edge) {
+                                if constexpr (Q8) {
+                                    pk[c / 2] = f16x2_bits(p0, p1);
+                                } else {
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                                    pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
+                                if constexpr (edge) {
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int d = key0 + half * HN + 32 * ch + c + e - ctx;
-                                    if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int d = key0 + half * HN + 32 * ch + c + e - ctx;
+                                        if (d >= 0 && d < 64 && (e ? p1 : p0) == 0.0f) none |= 1ull << d;
+                                    }
                                 }
                             }
+                            t5::st16u(sbuf + 16 * ch, pk);   // over scores that have been read
                         }
-                        t5::st16u(sbuf + 16 * ch, pk);   // over scores that have been read
-                    }
+                    };
+                    if (Q8 && wide)
+                        probabilities(std::true_type{});
+                    else
+                        probabilities(std::false_type{});
                     float s0, s1;
                     f2_split(l2, s0, s1);
                     l += s0 + s1;
