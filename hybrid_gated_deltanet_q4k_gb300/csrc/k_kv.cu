@@ -13,6 +13,7 @@ static __device__ int g_kv_error;   // a row or slot out of range
 
 struct KvArgs {
     int heads, page, page_shift;
+    uint32_t heads_inv;  // floor(2^32 / heads) + 1, or 0 for one head
     int64_t n_slots;     // n_pages * page
     void *ck, *cv;
     float *sk, *sv;
@@ -26,26 +27,38 @@ struct KvArgs {
 constexpr int KV_THREADS = 256;
 constexpr int KV_ITER = 4;   // rows a thread has in flight
 
-// Eight bf16 values at p: one 16-byte access, or eight where the caller's rows
-// are not 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ uint4 load8(const uint16_t* p) {
-    if constexpr (VEC) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = p[2 * e] | (static_cast<uint32_t>(p[2 * e + 1]) << 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(uint16_t* p, uint4 v) {
-    if constexpr (VEC) {
-        *reinterpret_cast<uint4*>(p) = v;
+// Sixteen bf16 values.  Rows that start on 32 bytes move in one access a thread,
+// which keeps a warp's accesses to whole sectors; on 16 bytes in two; any others
+// value by value.
+struct KvVals {
+    uint32_t w[8];
+};
+template <int BYTES>
+__device__ __forceinline__ KvVals load16(const uint16_t* p) {
+    KvVals r;
+    if constexpr (BYTES == 32) {
+        load32(p, r.w);
+    } else if constexpr (BYTES == 16) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
+        r = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
     } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            p[2 * e] = static_cast<uint16_t>(w[e]);
-            p[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
+        for (int e = 0; e < 8; ++e) r.w[e] = p[2 * e] | (static_cast<uint32_t>(p[2 * e + 1]) << 16);
+    }
+    return r;
+}
+template <int BYTES>
+__device__ __forceinline__ void store16(uint16_t* p, const KvVals& r) {
+    if constexpr (BYTES == 32) {
+        store32(p, r.w);
+    } else if constexpr (BYTES == 16) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        *reinterpret_cast<uint4*>(p + 8) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[2 * e] = static_cast<uint16_t>(r.w[e]);
+            p[2 * e + 1] = static_cast<uint16_t>(r.w[e] >> 16);
         }
     }
 }
@@ -61,28 +74,65 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Eight e4m3 codes of x / s (the IEEE quotient, rounded to nearest even; scale
-// 0 or a NaN quotient: 0).  As the int8 quantiser does, the quotient is first
-// taken as x * fl(1/s), within 3 units of the last place of fl(x/s): the two
-// can round apart only next to a border, where the 20 bits that e4m3 drops are
-// about one half, or below the smallest normal code; then all eight divide.
-__device__ __forceinline__ uint2 e4m3_codes8(const float (&x)[8], const QScale& q) {
+// The row's scale and what the quotients need of it.
+struct KvScale {
+    float s, rs;
+};
+
+// Eight codes of x / s: int8, or e4m3 rounded to nearest even (scale 0 or a NaN
+// quotient: 0).  The quotient is x * fl(1/s) corrected once by its residual
+// (P. Markstein, 1990): y = fl(y0 + fl(x - y0 s) fl(1/s)) is within 2^-22 of a
+// unit of the last place of x / s, rounded once.  That rounds to the same code
+// as fl(x/s) does: between them lies the middle m of two codes only where x / s
+// comes within 2^-22 ulp of m +- ulp/2.  With x = X 2^i (bf16, 8 bits) and
+// s = S 2^j (24 bits) that asks for S within 8 of a multiple of 2^20 (e4m3, m of
+// 5 bits) or of 2^17 (int8, 8 bits), but S is an 8-bit number over 7 or 127
+// rounded, whose digits repeat with a period of 3 or 7 and so hold no run of
+// that many zeros or ones, or it is such a multiple itself and x / s is not that
+// near without being there.  No step underflows for s >= 2^-60, which is 2^-71
+// for the smallest x with a code other than 0.  Otherwise, and where x holds a
+// NaN, all eight divide.
+template <int T>
+__device__ __forceinline__ uint2 kv_codes8(const float (&x)[8], KvScale q) {
+    const F2 rs = f2(q.rs, q.rs), ns = f2(-q.s, -q.s);
     float y[8];
-    bool redo = !q.fast;
+    F2 sum;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        y[e] = __fmul_rn(x[e], q.rs);
-        const uint32_t b = __float_as_uint(y[e]) & 0x7fffffffu;
-        redo |= (((b + 8u) ^ 0x80000u) & 0xfffffu) <= 16u || (b < 0x3c800000u && b != 0u) || b >= 0x7f800000u;
+    for (int e = 0; e < 8; e += 2) {
+        const F2 x2 = f2(x[e], x[e + 1]), y0 = f2_mul(x2, rs);
+        F2 y2 = f2_fma(f2_fma(y0, ns, x2), rs, y0);
+        sum = e == 0 ? y2 : f2_add(sum, y2);
+        if constexpr (T == GDN_KV_I8) y2 = f2_add(y2, f2(QCODE_MAGIC, QCODE_MAGIC));
+        f2_split(y2, y[e], y[e + 1]);
     }
-    if (redo) {
+    float a, b;
+    f2_split(sum, a, b);
+    a += b;
+    if (!(q.s >= 0x1p-60f && q.s <= 1e30f) || a != a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = q.s == 0.0f ? 0.0f : __fdiv_rn(x[e], q.s);
-            y[e] = d != d ? 0.0f : d;
+            float d = q.s == 0.0f ? 0.0f : __fdiv_rn(x[e], q.s);
+            d = d != d ? 0.0f : d;
+            y[e] = T == GDN_KV_I8 ? __fadd_rn(fminf(fmaxf(d, -127.0f), 127.0f), QCODE_MAGIC) : d;
         }
     }
+    if constexpr (T == GDN_KV_I8)
+        return make_uint2(codes_to_i8x4(y[0], y[1], y[2], y[3]), codes_to_i8x4(y[4], y[5], y[6], y[7]));
     return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
+// The largest |x| of each of two rows' sixteen bf16, side by side.
+__device__ __forceinline__ __nv_bfloat162 kv_amax2(const KvVals& u, const KvVals& v) {
+    const auto row = [](const KvVals& a) {
+        __nv_bfloat162 m = as_bf162(a.w[0] & 0x7fff7fffu);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) m = __hmax2(m, as_bf162(a.w[e] & 0x7fff7fffu));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    const uint32_t a = row(u), b = row(v);
+    return __hmax2(as_bf162(__byte_perm(a, b, 0x5410)), as_bf162(__byte_perm(a, b, 0x7632)));
 }
 
 __device__ __forceinline__ void e4m3_pair(uint32_t w, float& lo, float& hi) {
@@ -93,136 +143,176 @@ __device__ __forceinline__ void e4m3_pair(uint32_t w, float& lo, float& hi) {
     hi = f.y;
 }
 
-// D/8 threads per row, each eight of its elements; blockIdx.y is the side (keys
-// or values).  A thread takes KV_ITER rows a block's width apart, all loads
-// before the first use.
-template <int D, int T, bool VEC>
-__global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const __grid_constant__ KvArgs a) {
-    constexpr int G = D / 8, RB = KV_THREADS / G;
+// D/16 threads per row, each sixteen of its elements; blockIdx.y is the side
+// (keys or values).  A thread takes KV_ITER rows a block's width apart, all
+// indices before the first row's load, all loads before the first use.  The
+// block's first token is divided out once; from there a row is a small number
+// (under 256 heads + 256 rows), whose product with heads_inv has the quotient in
+// its upper word.
+template <int D>
+struct KvRows {
+    static constexpr int G = D / 16, RB = KV_THREADS / G;
+    int64_t tok0, left;   // first token, rows from its first head to the end
+    uint32_t r0;
+    int h;
+    __device__ __forceinline__ explicit KvRows(const KvArgs& a) {
+        const int64_t base = static_cast<int64_t>(blockIdx.x) * (RB * KV_ITER);
+        tok0 = base / a.heads;
+        left = (a.n - tok0) * a.heads;
+        r0 = static_cast<uint32_t>(base - tok0 * a.heads) + threadIdx.x / G;
+    }
+    // row i's token, or false past the end; sets its head
+    __device__ __forceinline__ bool token(const KvArgs& a, int i, int64_t& tok) {
+        const uint32_t r = r0 + i * RB, t = a.heads_inv ? __umulhi(r, a.heads_inv) : r;
+        h = static_cast<int>(r - t * a.heads);
+        tok = tok0 + t;
+        return r < left;
+    }
+};
+
+template <int D, int T, int BYTES>
+__global__ void __launch_bounds__(KV_THREADS, 4) kv_write_kernel(const __grid_constant__ KvArgs a) {
+    using R = KvRows<D>;
     pdl_wait();
     pdl_trigger();
-    const int sub = threadIdx.x % G, side = blockIdx.y;
-    const uint16_t* src = side ? a.v : a.k;
-    const int64_t ld = side ? a.ld_v : a.ld_k, n_rows = a.n * a.heads;
+    const int sub = threadIdx.x % R::G, side = blockIdx.y;
+    const uint16_t* src = (side ? a.v : a.k) + 16 * sub;
+    const int64_t ld = side ? a.ld_v : a.ld_k;
     void* codes = side ? a.cv : a.ck;
-    uint4 w[KV_ITER];
-    int64_t to[KV_ITER];     // cache row, -1: none
+    KvVals w[KV_ITER];
+    int64_t to[KV_ITER], row[KV_ITER];     // slot, then cache row, -1: none; the caller's row
+    int head[KV_ITER];
+    R rows(a);
 #pragma unroll
     for (int i = 0; i < KV_ITER; ++i) {
-        const int64_t r = static_cast<int64_t>(blockIdx.x) * (RB * KV_ITER) + i * RB + threadIdx.x / G;
-        to[i] = -1;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (r >= n_rows) continue;
-        const int64_t tok = r / a.heads;
-        const int h = static_cast<int>(r - tok * a.heads);
-        const int64_t row = a.rows ? a.rows[tok] : tok, slot = a.slots[tok];
-        if (slot < 0) continue;
-        if (row < 0 || row >= a.n_rows || slot >= a.n_slots) {
-            if (sub == 0) atomicCAS(&g_kv_error, 0, static_cast<int>(ERR_INDEX));
-            continue;
-        }
-        to[i] = ((slot >> a.page_shift) * a.heads + h) * a.page + (slot & (a.page - 1));
-        w[i] = load8<VEC>(src + row * ld + h * D + 8 * sub);
+        int64_t tok;
+        const bool in = rows.token(a, i, tok);
+        head[i] = rows.h;
+        to[i] = in ? a.slots[tok] : -1;
+        row[i] = !in ? -1 : a.rows ? a.rows[tok] : tok;
     }
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < KV_ITER; ++i) {
-        if constexpr (T == GDN_KV_BF16) {
-            if (to[i] >= 0) store8<true>(static_cast<uint16_t*>(codes) + to[i] * D + 8 * sub, w[i]);
-        } else {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            float x[8], amax = 0.0f;
+        const bool ok = row[i] >= 0 && row[i] < a.n_rows;
+        w[i] = KvVals{};
+        if (ok) w[i] = load16<BYTES>(src + row[i] * ld + head[i] * D);   // does not wait for the slot
+        bad |= to[i] >= 0 && (!ok || to[i] >= a.n_slots);
+        to[i] = ok && to[i] >= 0 && to[i] < a.n_slots ? ((to[i] >> a.page_shift) * a.heads + head[i]) * a.page + (to[i] & (a.page - 1)) : -1;
+    }
+    if (bad) atomicCAS(&g_kv_error, 0, static_cast<int>(ERR_INDEX));
+    if constexpr (T == GDN_KV_BF16) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = __uint_as_float(u[e] << 16);
-                x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-                amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-            }
+        for (int i = 0; i < KV_ITER; ++i)
+            if (to[i] >= 0) store16<32>(static_cast<uint16_t*>(codes) + to[i] * D + 16 * sub, w[i]);
+    } else {
+        // the four maxima, two to a register; then lane i of a row's threads
+        // divides for row i, and the others take its results
+        static_assert(KV_ITER == 4 && R::G >= KV_ITER);
+        __nv_bfloat162 m[2] = {kv_amax2(w[0], w[1]), kv_amax2(w[2], w[3])};
 #pragma unroll
-            for (int s = G / 2; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-            QScale q = make_qscale(amax);
-            if constexpr (T == GDN_KV_E4M3) {
-                q.s = __fdiv_rn(amax, 448.0f);
-                q.rs = __frcp_rn(q.s);
-                q.fast = q.s >= 1e-30f && q.s <= 1e30f;
-            }
-            uint2 c;
-            if constexpr (T == GDN_KV_I8) {
-                float t[8];
-                quantise8(x, q, t);
-                c = make_uint2(codes_to_i8x4(t[0], t[1], t[2], t[3]), codes_to_i8x4(t[4], t[5], t[6], t[7]));
-            } else {
-                c = e4m3_codes8(x, q);
+        for (int s = R::G / 2; s > 0; s >>= 1)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m[j] = __hmax2(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
+        const float2 m01 = __bfloat1622float2(m[0]), m23 = __bfloat1622float2(m[1]);
+        const float mine = sub & 2 ? (sub & 1 ? m23.y : m23.x) : (sub & 1 ? m01.y : m01.x);
+        const float s = __fdiv_rn(fmaxf(mine, 0.0f), T == GDN_KV_I8 ? 127.0f : 448.0f), rs = __frcp_rn(s);   // a row of NaN: 0
+#pragma unroll
+        for (int i = 0; i < KV_ITER; ++i) {
+            const KvScale q = {__shfl_sync(0xffffffffu, s, i, R::G), __shfl_sync(0xffffffffu, rs, i, R::G)};
+            uint2 c[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(w[i].w[4 * p + e] << 16);
+                    x[2 * e + 1] = __uint_as_float(w[i].w[4 * p + e] & 0xffff0000u);
+                }
+                c[p] = kv_codes8<T>(x, q);
             }
             if (to[i] >= 0) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + to[i] * D + 8 * sub) = c;
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + to[i] * D + 16 * sub) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
                 if (sub == 0) (side ? a.sv : a.sk)[to[i]] = q.s;
             }
         }
     }
 }
 
-template <int D, int T, bool VEC>
+template <int D, int T, int BYTES>
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const __grid_constant__ KvArgs a) {
-    constexpr int G = D / 8, RB = KV_THREADS / G;
+    using R = KvRows<D>;
     pdl_wait();
     pdl_trigger();
-    const int sub = threadIdx.x % G, side = blockIdx.y;
+    const int sub = threadIdx.x % R::G, side = blockIdx.y;
     const void* codes = side ? a.cv : a.ck;
     const float* scales = side ? a.sv : a.sk;
-    const int64_t ld = side ? a.ld_v : a.ld_k, n_rows = a.n * a.heads;
-    uint4 w[KV_ITER];
+    const int64_t ld = side ? a.ld_v : a.ld_k;
+    uint16_t* out = (side ? a.v : a.k) + 16 * sub;
+    KvVals w[KV_ITER];
     float s[KV_ITER];
-    uint16_t* dst[KV_ITER];
+    int64_t from[KV_ITER], dst[KV_ITER];
+    int head[KV_ITER];
+    R rows(a);
 #pragma unroll
     for (int i = 0; i < KV_ITER; ++i) {
-        const int64_t r = static_cast<int64_t>(blockIdx.x) * (RB * KV_ITER) + i * RB + threadIdx.x / G;
-        dst[i] = nullptr;
-        w[i] = make_uint4(0, 0, 0, 0);
+        int64_t tok;
+        const bool in = rows.token(a, i, tok);
+        head[i] = rows.h;
+        from[i] = in ? a.slots[tok] : -1;
+        dst[i] = in ? tok * ld + rows.h * D : -1;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < KV_ITER; ++i) {
+        w[i] = KvVals{};   // zeros where there is no slot
         s[i] = 0.0f;
-        if (r >= n_rows) continue;
-        const int64_t tok = r / a.heads;
-        const int h = static_cast<int>(r - tok * a.heads);
-        dst[i] = (side ? a.v : a.k) + tok * ld + h * D + 8 * sub;
-        const int64_t slot = a.slots[tok];
-        if (slot < 0 || slot >= a.n_slots) {   // zeros
-            if (slot >= 0 && sub == 0) atomicCAS(&g_kv_error, 0, static_cast<int>(ERR_INDEX));
-            continue;
-        }
-        const int64_t from = ((slot >> a.page_shift) * a.heads + h) * a.page + (slot & (a.page - 1));
+        bad |= from[i] >= a.n_slots;
+        if (from[i] < 0 || from[i] >= a.n_slots) continue;
+        const int64_t c = ((from[i] >> a.page_shift) * a.heads + head[i]) * a.page + (from[i] & (a.page - 1));
         if constexpr (T == GDN_KV_BF16) {
-            w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(codes) + from * D + 8 * sub);
+            w[i] = load16<32>(static_cast<const uint16_t*>(codes) + c * D + 16 * sub);
         } else {
-            const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(codes) + from * D + 8 * sub);
-            w[i].x = c.x;
-            w[i].y = c.y;
-            s[i] = scales[from];
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + c * D + 16 * sub);
+            w[i].w[0] = v.x;
+            w[i].w[1] = v.y;
+            w[i].w[2] = v.z;
+            w[i].w[3] = v.w;
+            s[i] = scales[c];
         }
     }
+    if (bad) atomicCAS(&g_kv_error, 0, static_cast<int>(ERR_INDEX));
 #pragma unroll
     for (int i = 0; i < KV_ITER; ++i) {
-        if (!dst[i]) continue;
         if constexpr (T != GDN_KV_BF16) {
-            const uint32_t u[2] = {w[i].x, w[i].y};
-            float x[8];
+            const F2 s2 = f2(s[i], s[i]);
+            KvVals r;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t c = u[e >> 2] >> (8 * (e & 3));
-                if constexpr (T == GDN_KV_I8)
-                    x[e] = static_cast<float>(static_cast<int8_t>(c));
-                else if (e % 2 == 0)
-                    e4m3_pair(c & 0xffffu, x[e], x[e + 1]);
+                const uint32_t u = w[i].w[e >> 1];
+                float lo, hi;
+                if constexpr (T == GDN_KV_I8) {
+                    // the code's offset byte in the low byte of 2^23, which is then taken off again
+                    const uint32_t b = u ^ 0x80808080u;
+                    lo = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 | (2 * e & 3)));
+                    hi = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 | (2 * e + 1 & 3)));
+                    f2_split(f2_mul(f2_sub(f2(lo, hi), f2(8388736.0f, 8388736.0f)), s2), lo, hi);
+                } else {
+                    e4m3_pair((u >> (16 * (e & 1))) & 0xffffu, lo, hi);
+                    f2_split(f2_mul(f2(lo, hi), s2), lo, hi);
+                }
+                r.w[e] = bf16_pair(lo, hi);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], s[i]);
-            w[i] = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+            w[i] = r;
         }
-        store8<VEC>(dst[i], w[i]);
+        if (dst[i] >= 0) store16<BYTES>(out + dst[i], w[i]);
     }
 }
 
 static KvArgs kv_args(const gdn_kv_cache& c, const int64_t* slots, int64_t n) {
     KvArgs a{};
     a.heads = c.n_kv_heads;
+    a.heads_inv = c.n_kv_heads == 1 ? 0u : 0xffffffffu / c.n_kv_heads + 1u;
     a.page = c.page_tokens;
     a.page_shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
     a.n_slots = c.n_pages * c.page_tokens;
@@ -237,12 +327,14 @@ static KvArgs kv_args(const gdn_kv_cache& c, const int64_t* slots, int64_t n) {
 
 template <int D, int T>
 static cudaError_t kv_launch(bool write, const KvArgs& a, cudaStream_t st) {
-    constexpr int ROWS = KV_THREADS / (D / 8) * KV_ITER;
-    const dim3 grid(static_cast<unsigned>((a.n * a.heads + ROWS - 1) / ROWS), 2);
-    const bool vec = a.ld_k % 8 == 0 && a.ld_v % 8 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.v) % 16 == 0;
-    auto kernel = write ? (vec ? kv_write_kernel<D, T, true> : kv_write_kernel<D, T, false>)
-                        : (vec ? kv_read_kernel<D, T, true> : kv_read_kernel<D, T, false>);
+    constexpr int ROWS = KvRows<D>::RB * KV_ITER;
+    const int64_t blocks = (a.n * a.heads + ROWS - 1) / ROWS;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;   // more rows than any memory holds
+    const dim3 grid(static_cast<unsigned>(blocks), 2);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) | static_cast<uintptr_t>(2 * (a.ld_k | a.ld_v));
+    auto kernel = at % 32 == 0   ? (write ? kv_write_kernel<D, T, 32> : kv_read_kernel<D, T, 32>)
+                  : at % 16 == 0 ? (write ? kv_write_kernel<D, T, 16> : kv_read_kernel<D, T, 16>)
+                                 : (write ? kv_write_kernel<D, T, 2> : kv_read_kernel<D, T, 2>);
     return launch_dependent(kernel, grid, dim3(KV_THREADS), 0, st, a);
 }
 

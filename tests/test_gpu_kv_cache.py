@@ -154,6 +154,27 @@ def test_rows_that_are_not_finite(L, kind):
     assert bool(torch.isnan(ko[1]).all()) and bool(torch.isfinite(ko[[0, 2]]).all())
 
 
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("size", [-40, 0, 55])
+def test_every_quotient_of_two_mantissas(L, kind, size):
+    """Rows whose largest element has each of the 128 mantissas, over elements of every mantissa and of 18 exponents
+    from the largest one down: every quotient that a row of bf16 can have, but for powers of two."""
+    big = np.arange(128, 256, dtype=np.float64)
+    x = np.zeros((128, 18, 256), np.float64)
+    x[:, :, :128] = np.minimum(np.arange(128, 256) * np.exp2(-np.arange(18.0))[:, None], big[:, None, None])
+    x[:, :, 128:] = -x[:, :, :128]
+    x[:, :, 0] = big[:, None]
+    x = torch.from_numpy((x * 2.0 ** size).reshape(-1, 2, 256).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    n = x.shape[0]
+    cache = api.KvCache.new(kind, n // 16, 2, 16, 256)
+    cache.write(x, x, torch.arange(n, device=DEV))
+    sync(L)
+    codes, scale = _expected(x, kind)
+    for side in "kv":
+        got, s = _values(cache, side)
+        assert np.array_equal(s, scale) and np.array_equal(got, codes)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_indices_out_of_range_are_skipped_and_reported(L, kind):
     heads, page, d, n = 2, 16, 128, 4
