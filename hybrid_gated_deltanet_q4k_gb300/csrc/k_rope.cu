@@ -43,56 +43,67 @@ __device__ __forceinline__ void rope_pair(uint16_t a, uint16_t b, float2 cs, uin
     y = float_to_bf16_bits(fa * cs.y + fb * cs.x);
 }
 
+// Where pair p of a token has its sine and cosine in the table: eight threads
+// read sixteen bytes each of pairs 8c + 2e, 64 bytes apart, which the exchange
+// of e puts into different banks.
+__device__ __forceinline__ int rope_at(int c, int e) { return 8 * c + 2 * (e ^ ((c >> 1) & 3)); }
+
 // Rows whose parts are whole 16-byte pieces: a unit is 16 elements of a row,
 // eight pairs (half layout: 8 elements at 8c and 8 at rot/2 + 8c; interleaved:
 // 16 together) or 16 that pass through.  blockDim = (units of a row, rows);
-// each thread takes K rows, all loads first.
-template <int K>
-__global__ void __launch_bounds__(ROPE_THREADS)
+// each thread takes K rows, all loads first.  WIDE: every row starts on 32
+// bytes, and 16 elements that lie together move in one access.
+template <int K, bool WIDE>
+__global__ void __launch_bounds__(ROPE_THREADS, 4)
 rope_vec_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant__ RopeArgs a) {
     extern __shared__ float2 table[];   // [tokens of the run][rot / 2]
     pdl_wait();
     pdl_trigger();
     const int half = t.rot / 2, heads = a.hq + a.hk, c = threadIdx.x;
     const int64_t rows = a.n * heads, r0 = static_cast<int64_t>(blockIdx.x) * (blockDim.y * K);
-    const int64_t t0 = r0 / heads, r1 = min(r0 + static_cast<int64_t>(blockDim.y) * K, rows);
-    const int toks = static_cast<int>((r1 - 1) / heads - t0) + 1;
+    const int64_t t0 = r0 / heads;
+    const int first = static_cast<int>(r0 - t0 * heads), n_rows = static_cast<int>(min(static_cast<int64_t>(blockDim.y) * K, rows - r0));
+    const int toks = (first + n_rows - 1) / heads + 1;
     const bool turns = c < t.rot / 16, split = turns && t.layout == GDN_ROPE_HALF;
     const int ea = split ? 8 * c : 16 * c, eb = split ? half + 8 * c : ea + 8;
-    uint4 va[K], vb[K];
-    uint16_t* dst[K];
-    int tk[K];
+    uint32_t v[K][8];
+    int tk[K], hd[K];   // the row's token in the run (-1: nothing to do) and head
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t r = r0 + k * blockDim.y + threadIdx.y;
-        dst[k] = nullptr;
-        if (r >= rows) continue;
-        tk[k] = (static_cast<int>(r - t0 * heads)) / heads;
-        const int64_t tok = t0 + tk[k];
-        const int h = static_cast<int>(r - tok * heads);
+        const int i = k * blockDim.y + threadIdx.y;
+        tk[k] = -1;
+        if (i >= n_rows) continue;
+        const int r = first + i, tl = r / heads, h = r - tl * heads;
         const bool is_q = h < a.hq;
         if (!turns && !(is_q ? a.q_copy : a.k_copy)) continue;
+        const int64_t tok = t0 + tl;
         if (!GDN_IN_RANGE(g_rope_error, tok < a.n && ea + 8 <= a.d && eb + 8 <= a.d)) continue;
+        tk[k] = tl;
+        hd[k] = h;
         const uint16_t* src = is_q ? a.q + tok * a.ld_q + h * a.d : a.k + tok * a.ld_k + (h - a.hq) * a.d;
-        dst[k] = is_q ? a.qo + tok * a.ld_qo + h * a.d : a.ko + tok * a.ld_ko + (h - a.hq) * a.d;
-        va[k] = *reinterpret_cast<const uint4*>(src + ea);
-        vb[k] = *reinterpret_cast<const uint4*>(src + eb);
+        if (WIDE && !split) {
+            load32(src + ea, v[k]);
+        } else {
+            const uint4 va = *reinterpret_cast<const uint4*>(src + ea), vb = *reinterpret_cast<const uint4*>(src + eb);
+            v[k][0] = va.x, v[k][1] = va.y, v[k][2] = va.z, v[k][3] = va.w;
+            v[k][4] = vb.x, v[k][5] = vb.y, v[k][6] = vb.z, v[k][7] = vb.w;
+        }
     }
     for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < toks * half; i += blockDim.x * blockDim.y) {
         const int tok = i / half, p = i - tok * half;
-        table[i] = rope_cs(t.step[p], a.pos[t0 + tok], t.amp);
+        table[tok * half + rope_at(p / 8, p % 8 / 2) + p % 2] = rope_cs(t.step[p], a.pos[t0 + tok], t.amp);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (!dst[k]) continue;
+        if (tk[k] < 0) continue;
+        uint32_t(&x)[8] = v[k];
         if (turns) {
-            const float4* cs = reinterpret_cast<const float4*>(table + tk[k] * half + 8 * c);
-            uint32_t x[8] = {va[k].x, va[k].y, va[k].z, va[k].w, vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+            const float2* cs = table + tk[k] * half;
             if (split) {   // x[e] and x[4 + e] hold pairs 2e, 2e + 1
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float4 w = cs[e];
+                    const float4 w = *reinterpret_cast<const float4*>(cs + rope_at(c, e));
                     uint16_t a0, a1, b0, b1;
                     rope_pair(static_cast<uint16_t>(x[e]), static_cast<uint16_t>(x[4 + e]), make_float2(w.x, w.y), a0, b0);
                     rope_pair(static_cast<uint16_t>(x[e] >> 16), static_cast<uint16_t>(x[4 + e] >> 16), make_float2(w.z, w.w), a1, b1);
@@ -102,7 +113,7 @@ rope_vec_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant_
             } else {       // x[e] is pair e
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    const float4 w = cs[e / 2];
+                    const float4 w = *reinterpret_cast<const float4*>(cs + rope_at(c, e / 2));
                     uint16_t a0, b0;
                     rope_pair(static_cast<uint16_t>(x[e]), static_cast<uint16_t>(x[e] >> 16), make_float2(w.x, w.y), a0, b0);
                     x[e] = a0 | (static_cast<uint32_t>(b0) << 16);
@@ -110,11 +121,16 @@ rope_vec_kernel(const __grid_constant__ gdn_rope_table t, const __grid_constant_
                     x[e + 1] = a0 | (static_cast<uint32_t>(b0) << 16);
                 }
             }
-            va[k] = make_uint4(x[0], x[1], x[2], x[3]);
-            vb[k] = make_uint4(x[4], x[5], x[6], x[7]);
         }
-        *reinterpret_cast<uint4*>(dst[k] + ea) = va[k];
-        *reinterpret_cast<uint4*>(dst[k] + eb) = vb[k];
+        const int64_t tok = t0 + tk[k];
+        const int h = hd[k];
+        uint16_t* dst = h < a.hq ? a.qo + tok * a.ld_qo + h * a.d : a.ko + tok * a.ld_ko + (h - a.hq) * a.d;
+        if (WIDE && !split) {
+            store32(dst + ea, x);
+        } else {
+            *reinterpret_cast<uint4*>(dst + ea) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(dst + eb) = make_uint4(x[4], x[5], x[6], x[7]);
+        }
     }
 }
 
@@ -152,20 +168,23 @@ cudaError_t launch_rope(const gdn_rope_table& t, const int32_t* pos, int64_t n, 
                         int hq, uint16_t* qo, int64_t ld_qo, const uint16_t* k, int64_t ld_k, int hk, uint16_t* ko,
                         int64_t ld_ko, cudaStream_t st) {
     const RopeArgs a{pos, n, d, hq, hk, q, qo, k, ko, ld_q, ld_qo, ld_k, ld_ko, q != qo, k != ko};
-    auto pieces = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
+    uintptr_t at = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(qo) | static_cast<uintptr_t>(2 * (ld_q | ld_qo));
+    if (hk) at |= reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(ko) | static_cast<uintptr_t>(2 * (ld_k | ld_ko));
     const int units = d / 16;
-    if (t.rot % 16 || d % 16 || !pieces(q, ld_q) || !pieces(qo, ld_qo) || !pieces(k, ld_k) || !pieces(ko, ld_ko)) {
+    if (t.rot % 16 || d % 16 || at % 16) {
         return launch_dependent(rope_kernel, dim3(static_cast<unsigned>(n)), dim3(ROPE_THREADS), 0, st, t, a);
     }
     const dim3 block(static_cast<unsigned>(units), static_cast<unsigned>(ROPE_THREADS / units));
     const int64_t rows = n * (hq + hk);
     auto smem = [&](int kk) { return ((block.y * kk - 1) / (hq + hk) + 2) * (t.rot / 2) * sizeof(float2); };
     auto grid = [&](int kk) { return static_cast<unsigned>((rows + block.y * kk - 1) / (block.y * kk)); };
-    if (smem(4) <= 40960 && grid(4) >= 608)
-        return launch_dependent(rope_vec_kernel<4>, dim3(grid(4)), block, smem(4), st, t, a);
-    if (smem(2) <= 40960 && grid(2) >= 608)
-        return launch_dependent(rope_vec_kernel<2>, dim3(grid(2)), block, smem(2), st, t, a);
-    return launch_dependent(rope_vec_kernel<1>, dim3(grid(1)), block, smem(1), st, t, a);
+    const bool wide = at % 32 == 0;
+    const auto launch = [&](void (*kernel)(const gdn_rope_table, const RopeArgs), int kk) {
+        return launch_dependent(kernel, dim3(grid(kk)), block, smem(kk), st, t, a);
+    };
+    if (smem(4) <= 40960 && grid(4) >= 608) return launch(wide ? rope_vec_kernel<4, true> : rope_vec_kernel<4, false>, 4);
+    if (smem(2) <= 40960 && grid(2) >= 608) return launch(wide ? rope_vec_kernel<2, true> : rope_vec_kernel<2, false>, 2);
+    return launch(wide ? rope_vec_kernel<1, true> : rope_vec_kernel<1, false>, 1);
 }
 
 int read_and_clear_rope_error() {
