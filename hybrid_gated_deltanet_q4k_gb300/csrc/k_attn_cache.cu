@@ -76,6 +76,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 // ------------------------------------------------------------ shared memory
 
+// A run's place, the piece it is at and that piece's rows.
+struct AcRun {
+    int64_t at, end;
+    AcPiece pc;
+    int s, rows;
+};
+
 // A row of a tile is cut into slabs of 128 bytes (one of 64 for 8-bit heads of
 // 64), each slab [keys][128 bytes] with the TMA's 128-byte (64-byte) swizzle,
 // so that eight keys' 16-byte pieces fall into different banks.
@@ -96,7 +103,8 @@ struct AcSmem {
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int NS = AC_RING / WARPS / HALF < 8 ? AC_RING / WARPS / HALF : 8;   // half tiles in flight per warp
     static constexpr int ROWS = 8 * NR;
-    static constexpr int OLD = D + 8;                       // padded rows of the joined accumulators
+    static constexpr int OLD = D + 4;                       // padded rows of the joined accumulators: a warp's pieces in different banks
+    static constexpr int QR = (ROWS + WARPS - 1) / WARPS;   // rows of q that a warp prepares
     static constexpr int R0 = 0;                            // ring [warp][slot]; the accumulators at the end of a pair
     static constexpr int S0 = AC_RING;                      // row scales of the half tiles: [warp][slot][keys]
     static constexpr int M0 = S0 + WARPS * NS * KEYS * 4;        // maxima and sums: [warp][rows][2]
@@ -106,7 +114,9 @@ struct AcSmem {
     static constexpr int F0 = W0 + WARPS * 8;                    // pages in range, a bit per copy: [warp][slot]
     static constexpr int N0 = F0 + WARPS * NS * 4;               // mask word of each row
     static constexpr int X0 = N0 + ROWS * 8;                     // score factor of each row
-    static constexpr int Q0 = (X0 + ROWS * 4 + 15) & ~15;        // q fragments [row tile][step][lane] x 8 bytes
+    static constexpr int J0 = (X0 + ROWS * 4 + 7) & ~7;          // maximum and sum of each row
+    static constexpr int H0 = J0 + ROWS * 8;                     // where the run stands while a piece's tiles pass
+    static constexpr int Q0 = (H0 + static_cast<int>(sizeof(AcRun)) + 15) & ~15;        // q fragments [row tile][step][lane] x 8 bytes
     static constexpr int B0 = Q0 + NR * (D / 16) * 256;          // mbarriers [warp][slot]
     static constexpr int BYTES = B0 + WARPS * NS * 8;
     static_assert(WARPS * ROWS * OLD * 4 <= AC_RING, "the joined accumulators fit the ring");
@@ -149,6 +159,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     float2* ml = reinterpret_cast<float2*>(base + L::M0);
     uint64_t* seen = reinterpret_cast<uint64_t*>(base + L::N0);
     float* row_factor = reinterpret_cast<float*>(base + L::X0);
+    float2* total_ml = reinterpret_cast<float2*>(base + L::J0);
     uint2* qsm = reinterpret_cast<uint2*>(base + L::Q0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::B0) + warp * L::NS;
     unsigned char* ring = base + L::R0 + warp * L::NS * L::HALF;
@@ -164,11 +175,13 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const int run = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
     ac_prefix(a, pre, seq, reinterpret_cast<int64_t*>(base + L::W0), blockIdx.x == 0);
     const int64_t total = pre[a.n_seqs] * a.heads, per = ac_run_blocks(a, total);
-    int64_t at = run * per;
-    const int64_t end = at + per < total ? at + per : total;
-    if (at >= end) return;
-
-    int s = ac_seq_of(a, pre, at);
+    // in registers only between the tile loops, which have none to spare
+    AcRun at{};
+    at.at = run * per;
+    at.end = at.at + per < total ? at.at + per : total;
+    if (at.at >= at.end) return;
+    at.s = ac_seq_of(a, pre, at.at);
+    volatile AcRun* kept = reinterpret_cast<volatile AcRun*>(base + L::H0);
     int slot = 0;               // the next half tile of this warp's ring and its phase
     uint32_t par = 0;
     bool dead = false;          // a wait ran out
@@ -181,24 +194,73 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const uint32_t koff = ac_piece<L>(kr, kc), voff = ac_piece<L>(vr, vc);
     auto piece_at = [](uint32_t b, int c) { return (b ^ ((c & 7) << 4)) + (c >> 3) * (L::KEYS * 128); };
 
-    AcPiece pc;
-    while (ac_next(a, pre, seq, at, end, s, pc)) {
-        const AcSeq q = pc.q;
-        const int head = pc.head, b0 = pc.b0, b1 = pc.b1;
-        const int row0 = rank * L::ROWS, rows = min(q.nq * a.ratio - row0, L::ROWS);
-        if (rows <= 0) continue;
-        const int t0 = b0 * L::TILES, t1 = min(b1 * L::TILES, q.len == 0 ? 1 : (q.len - 1) / L::KEYS + 1);   // tiles
+    // The run's next piece that has rows of this rank, its first pages and its
+    // rows of q (lane's share of rows warp, warp + WARPS, ..): asked for before
+    // the piece before it is joined, so that its copies start without a wait.
+    constexpr int QE = D / 32;            // elements of a row of q in a lane
+    constexpr int PG = (L::NS + 1) / 2;   // tiles whose keys the ring takes
+    const int row0 = rank * L::ROWS;
+    const int copies = L::KEYS / a.box, mycopy = lane < copies ? lane * a.box : 0;
+    int pg[PG];
+    uint32_t qw[L::QR][QE / 2];
+    auto last_tile = [](const AcPiece& p) { return min(p.b1 * L::TILES, p.q.len == 0 ? 1 : (p.q.len - 1) / L::KEYS + 1); };
+    auto tiles_of_warp = [&](int t0, int t1) { return t1 - t0 - warp > 0 ? (t1 - t0 - warp + L::WARPS - 1) / L::WARPS : 0; };
+    auto page_of = [&](const int32_t* table, int t0, int i) {
+        return table[min(((t0 + warp + i * L::WARPS) * L::KEYS + mycopy) >> a.page_shift, a.max_blocks - 1)];
+    };
+    auto next = [&] {
+        do {
+            if (!ac_next(a, pre, seq, at.at, at.end, at.s, at.pc)) return false;
+            at.rows = min(at.pc.q.nq * a.ratio - row0, L::ROWS);
+        } while (at.rows <= 0);
+        const int t0 = at.pc.b0 * L::TILES, n = tiles_of_warp(t0, last_tile(at.pc));
+#pragma unroll
+        for (int i = 0; i < PG; ++i) pg[i] = page_of(a.table + at.pc.s * a.ld_table, t0, min(i, max(n - 1, 0)));
+#pragma unroll
+        for (int x = 0; x < L::QR; ++x) {
+            const int r = warp + x * L::WARPS, rr = row0 + r, i = rr / a.ratio;
+#pragma unroll
+            for (int e = 0; e < QE / 2; ++e) qw[x][e] = 0;
+            if (r < at.rows) {
+                const uint16_t* src = a.q + static_cast<int64_t>(at.pc.q.tok + i) * a.ld_q +
+                                      (at.pc.head * a.ratio + rr - i * a.ratio) * D + lane * QE;
+                if constexpr (QE == 8) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    qw[x][0] = v.x, qw[x][1] = v.y, qw[x][2] = v.z, qw[x][3] = v.w;
+                } else if constexpr (QE == 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    qw[x][0] = v.x, qw[x][1] = v.y;
+                } else {
+                    qw[x][0] = *reinterpret_cast<const uint32_t*>(src);
+                }
+            }
+        }
+        return true;
+    };
+
+    bool more = next();
+    while (more) {
+        const AcSeq q = at.pc.q;
+        const int head = at.pc.head, t0 = at.pc.b0 * L::TILES;
+        const int mine = tiles_of_warp(t0, last_tile(at.pc));   // tiles of this warp
         const int ctx = q.len - q.nq;      // keys every row sees
-        const int32_t* table = a.table + pc.s * a.ld_table;
+        const int32_t* table = a.table + at.pc.s * a.ld_table;
+        if (tid == 0) {
+            kept->at = at.at;
+            kept->end = at.end;
+            kept->s = at.s;
+            kept->rows = at.rows;
+            kept->pc.s = at.pc.s;
+            kept->pc.b0 = at.pc.b0;
+            kept->pc.b1 = at.pc.b1;
+            kept->pc.blocks = at.pc.blocks;
+            kept->pc.q.tok = q.tok;
+            kept->pc.q.len = q.len;
+        }
 
         // ---- copies: half tile j (keys of tile j / 2, then its values)
         // follows j - NS in its slot.  A tile may lie in several pages: lane p
         // copies the rows of the p-th.
-        const int mine = t1 - t0 - warp > 0 ? (t1 - t0 - warp + L::WARPS - 1) / L::WARPS : 0;   // tiles of this warp
-        const int copies = L::KEYS / a.box, mycopy = lane < copies ? lane * a.box : 0;
-        auto page_of = [&](int i) {
-            return table[min(((t0 + warp + i * L::WARPS) * L::KEYS + mycopy) >> a.page_shift, a.max_blocks - 1)];
-        };
         auto issue = [&](int j, int sl, int page) {   // whole warp
             const int row = ((t0 + warp + (j >> 1) * L::WARPS) * L::KEYS + mycopy) & (a.page - 1);
             const bool in = page >= 0 && page < a.n_pages, val = j & 1;
@@ -216,9 +278,6 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
         };
         if (!dead) {
-            int pg[(L::NS + 1) / 2];     // all pages before the first copy: one latency
-#pragma unroll
-            for (int i = 0; i < (L::NS + 1) / 2; ++i) pg[i] = page_of(min(i, max(mine - 1, 0)));
             int sl = slot;
 #pragma unroll
             for (int j = 0; j < L::NS; ++j)
@@ -228,49 +287,41 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 }
         }
         // pages of the tiles whose keys (a) and values (b) the next two free slots take
-        int page_a = page_of(min(L::NS / 2, max(mine - 1, 0))), page_b = page_of(min((L::NS + 1) / 2, max(mine - 1, 0)));
+        int page_a = page_of(table, t0, min(L::NS / 2, max(mine - 1, 0))), page_b = page_of(table, t0, min((L::NS + 1) / 2, max(mine - 1, 0)));
 
-        // ---- q fragments: row 8 nr + g, the same for every warp, in shared
-        // memory.  The d elements a thread holds at step kt are those its key
-        // fragments hold.
+        // ---- q fragments, the same for every warp, in shared memory: a thread's
+        // d elements at step kt are those its key fragments hold (row 8 nr + g:
+        // elements 4t .. 4t + 3 of 16, or 2t, 2t + 1, 2t + 8, 2t + 9 of bf16)
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            const int r = 8 * nr + g, rr = row0 + r, i = rr / a.ratio;
-            const bool on = r < rows;
-            const uint16_t* src = a.q + static_cast<int64_t>(q.tok + (on ? i : 0)) * a.ld_q +
-                                  (head * a.ratio + (on ? rr - i * a.ratio : 0)) * D;
+        for (int x = 0; x < L::QR; ++x) {
+            const int r = warp + x * L::WARPS;
+            if (r >= L::ROWS) break;
             float factor = a.sl2;
+            unsigned char* dst = reinterpret_cast<unsigned char*>(qsm + ((r >> 3) * KT + lane * QE / 16) * 32 + 4 * (r & 7));
+            const int e0 = lane * QE & 15;
             if constexpr (!Q8) {
-                for (int kt = warp; kt < KT; kt += L::WARPS)
-                    qsm[(nr * KT + kt) * 32 + lane] =
-                        on ? make_uint2(*reinterpret_cast<const uint32_t*>(src + 16 * kt + 2 * t),
-                                        *reinterpret_cast<const uint32_t*>(src + 16 * kt + 8 + 2 * t))
-                           : make_uint2(0u, 0u);
+#pragma unroll
+                for (int e = 0; e < QE / 2; ++e)
+                    *reinterpret_cast<uint32_t*>(dst + ((e0 & 7) + 2 * e) / 2 * 8 + (e0 >> 3) * 4) = qw[x][e];
             } else {
                 float amax = 0.0f;
-                uint2 w[KT];
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    w[kt] = on ? *reinterpret_cast<const uint2*>(src + 16 * kt + 4 * t) : make_uint2(0u, 0u);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[kt].x << 16)), fabsf(__uint_as_float(w[kt].x & 0xffff0000u))),
-                                             fmaxf(fabsf(__uint_as_float(w[kt].y << 16)), fabsf(__uint_as_float(w[kt].y & 0xffff0000u)))));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                for (int e = 0; e < QE / 2; ++e)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qw[x][e] << 16)), fabsf(__uint_as_float(qw[x][e] & 0xffff0000u))));
+                amax = warp_max(amax);
                 // 2^e with amax 2^e in [2^14, 2^15): exact both ways within the exponents that keep 2^e finite
                 const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                 factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-                    if (kt % L::WARPS == warp)
-                        qsm[(nr * KT + kt) * 32 + lane] =
-                            make_uint2(f16x2_bits(__uint_as_float(w[kt].x << 16) * up, __uint_as_float(w[kt].x & 0xffff0000u) * up),
-                                       f16x2_bits(__uint_as_float(w[kt].y << 16) * up, __uint_as_float(w[kt].y & 0xffff0000u) * up));
+                for (int e = 0; e < QE / 2; ++e)
+                    *reinterpret_cast<uint32_t*>(dst + (e0 + 2 * e) * 2) =
+                        f16x2_bits(__uint_as_float(qw[x][e] << 16) * up, __uint_as_float(qw[x][e] & 0xffff0000u) * up);
             }
-            if (warp == 0 && t == 0) {
+            if (lane == 0) {
+                const int i = (row0 + r) / a.ratio;
                 row_factor[r] = factor;
-                seen[r] = !on ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
+                seen[r] = r >= at.rows ? 0 : a.tree ? a.tree[q.tok + i] : i >= 63 ? ~0ull : (1ull << (i + 1)) - 1;
             }
         }
         __syncthreads();
@@ -600,9 +651,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 slot = 0;
                 par ^= 1;
             }
-            const int next = page_of(min(i + 1 + (L::NS + 1) / 2, mine - 1));
-            page_a = L::NS % 2 ? page_b : next;
-            page_b = next;
+            const int page = page_of(table, t0, min(i + 1 + (L::NS + 1) / 2, mine - 1));
+            page_a = L::NS % 2 ? page_b : page;
+            page_b = page;
         }
 
         // ---- join the warps
@@ -616,7 +667,29 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 if (g == 0) ml[warp * L::ROWS + 8 * nr + 2 * t + e] = make_float2(m[nr][e], l[nr][e]);
             }
         __syncthreads();   // every warp is done with its ring
-        const int live = min(t1 - t0, L::WARPS);
+        at.at = kept->at;
+        at.end = kept->end;
+        at.s = kept->s;
+        at.pc.b0 = kept->pc.b0;
+        at.pc.b1 = kept->pc.b1;
+        at.pc.q.len = kept->pc.q.len;
+        const int b0 = at.pc.b0, live = min(last_tile(at.pc) - b0 * L::TILES, L::WARPS), rows = kept->rows, tok = kept->pc.q.tok;
+        const bool whole = b0 == 0 && at.pc.b1 == kept->pc.blocks;
+        // a thread per row and warp: what the warp's accumulator counts for, and the row's maximum and sum
+        if (tid < L::ROWS * L::WARPS) {
+            const int w = tid % L::WARPS, r = tid / L::WARPS;
+            const float2 v = w < live ? ml[w * L::ROWS + r] : make_float2(-INFINITY, 0.0f);
+            float mx = v.x;
+#pragma unroll
+            for (int x = L::WARPS / 2; x > 0; x >>= 1) mx = fmaxf_nan(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            // weight 0, not left out: a NaN (of a score, or 0 times an infinite value) stays
+            const float f = v.x == -INFINITY ? 0.0f : ex2_ftz(v.x - mx);
+            float lt = f * v.y;
+#pragma unroll
+            for (int x = L::WARPS / 2; x > 0; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+            ml[w * L::ROWS + r].x = f;
+            if (w == 0) total_ml[r] = make_float2(mx, lt);
+        }
         if (warp < live) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -636,32 +709,32 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     }
                 }
         }
+        more = next();     // its loads fly while this piece is joined
         __syncthreads();
-        const bool whole = b0 == 0 && b1 == pc.blocks;
         const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (b0 > 0 ? 0 : 1)) * L::ROWS;
-        for (int e = tid; e < rows * (D / 2); e += L::THREADS) {
-            const int r = e / (D / 2), c = (e % (D / 2)) * 2;
-            float mx = -INFINITY;
-            for (int w = 0; w < live; ++w) mx = fmaxf_nan(mx, ml[w * L::ROWS + r].x);
-            float lt = 0.0f, x = 0.0f, z = 0.0f;
+        for (int e = tid; e < rows * (D / 4); e += L::THREADS) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+            const float* from = join + r * L::OLD + c;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
             for (int w = 0; w < live; ++w) {
-                const float2 v = ml[w * L::ROWS + r];
-                // weight 0, not left out: a NaN (of a score, or 0 times an infinite value) stays
-                const float f = v.x == -INFINITY ? 0.0f : ex2_ftz(v.x - mx);
-                const float2 ov = *reinterpret_cast<const float2*>(join + (w * L::ROWS + r) * L::OLD + c);
-                lt = fmaf(f, v.y, lt);
-                x = fmaf(f, ov.x, x);
-                z = fmaf(f, ov.y, z);
+                const float f = ml[w * L::ROWS + r].x;
+                const float4 v = *reinterpret_cast<const float4*>(from + w * (L::ROWS * L::OLD));
+                x.x = fmaf(f, v.x, x.x);
+                x.y = fmaf(f, v.y, x.y);
+                x.z = fmaf(f, v.z, x.z);
+                x.w = fmaf(f, v.w, x.w);
             }
+            const float2 tot = total_ml[r];
             if (whole) {
-                const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+                const float inv = tot.y == 0.0f ? 0.0f : 1.0f / tot.y;
                 const int rr = row0 + r, i = rr / a.ratio;
-                if (GDN_IN_RANGE(g_attn_cache_error, q.tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
-                    *reinterpret_cast<uint32_t*>(a.o + (q.tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + c) =
-                        bf16x2(x * inv, z * inv);
+                if (GDN_IN_RANGE(g_attn_cache_error, tok + i < a.n_tokens && head * a.ratio + rr - i * a.ratio < a.hq))
+                    *reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(tok + i) * a.ld_o + (head * a.ratio + rr - i * a.ratio) * D + c) =
+                        make_uint2(bf16x2(x.x * inv, x.y * inv), bf16x2(x.z * inv, x.w * inv));
             } else {
-                *reinterpret_cast<float2*>(a.part + (part0 + r) * D + c) = make_float2(x, z);
-                if (c == 0) a.part_ml[part0 + r] = make_float2(mx, lt);
+                *reinterpret_cast<float4*>(a.part + (part0 + r) * D + c) = x;
+                if (c == 0) a.part_ml[part0 + r] = tot;
             }
         }
         fence_proxy_async_smem();   // the ring was written here; copies come next
