@@ -96,10 +96,14 @@ struct AcSmem {
     static constexpr int KEYS = 16 * SUB;                   // tile's waits and copies are worth their instructions
     static constexpr int HALF = KEYS * ROW;                 // the keys, or the values, of a tile
     static constexpr int TILES = AC_BLOCK / KEYS;           // tiles of a block
-    static constexpr int START = 768 / ROW > 0 ? 768 / ROW : 1;   // blocks' worth of starting a pair: 4 us of 45 GB/s
-    // 16 warps where a thread's accumulators are at most 64 registers and a
-    // warp's share of the ring holds a tile and a half
-    static constexpr int WARPS = D * NR <= 256 && NR <= 2 && 16 * 3 * HALF <= AC_RING ? 16 : 8;
+    // blocks' worth of starting and joining a pair: 48 sequences of 1 .. 16384 keys, 8-bit heads of 256, take 155 us
+    // counted as 512 / ROW blocks, 145 as 768, 135 as 1152 and 138 as 2304; 16 chains of heads of 128 72, 70, 69 and 77
+    static constexpr int START = 1152 / ROW;
+    // 16 warps where 128 registers hold the accumulators (one row tile, two of
+    // heads of 64) and a warp's share of the ring a tile and a half.  Two row
+    // tiles of heads of 64, e4m3: 49 us for six sequences of up to 24000 keys,
+    // with 8 warps 59; of heads of 128, int8: 82 us, with 8 warps 65
+    static constexpr int WARPS = (NR == 1 || D * NR <= 128) && 16 * 3 * HALF <= AC_RING ? 16 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int NS = AC_RING / WARPS / HALF < 8 ? AC_RING / WARPS / HALF : 8;   // half tiles in flight per warp
     static constexpr int ROWS = 8 * NR;
