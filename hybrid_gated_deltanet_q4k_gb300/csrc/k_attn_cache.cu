@@ -42,6 +42,8 @@
 // element in [2^14, 2^15): elements below 2^-38 of it are lost.
 #include "attn_cache.cuh"
 
+#include <algorithm>
+
 namespace gdn {
 
 constexpr int AC_RING = 192 * 1024;     // bytes of tiles in flight per CTA
@@ -756,7 +758,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 // sequence): a block per row, the partials dealt over its warps, since one
 // row's chain of loads would take longer than its bytes.
 template <int D>
-__global__ void __launch_bounds__(AC_JOIN_THREADS)
+__global__ void __launch_bounds__(AC_JOIN_THREADS, D == 256 ? 3 : 4)
 attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
     constexpr int WARPS = AC_JOIN_THREADS / 32, E = D / 32;   // each lane E columns, 2 at a time
     __shared__ int64_t pre[GDN_MAX_SEQS + 2], wsum[WARPS];
@@ -778,6 +780,17 @@ attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
         auto piece = [&](int k) {
             return ((static_cast<int64_t>(c0 + k) * a.ranks + rank) * 2 + (k > 0 ? 0 : 1)) * rank_rows + r;
         };
+        // the first accumulators are asked for before the maxima that weigh them
+        const int k_first = many ? warp : 0, k_step = many ? WARPS : 1;
+        float2 ahead[4][E / 2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = k_first + j * k_step;
+            if (k >= n) continue;
+            const float2* p = reinterpret_cast<const float2*>(a.part + piece(k) * D) + lane;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) ahead[j][e] = p[32 * e];
+        }
         // maximum over all partials; each lane's weight and share of the sum (partials lane, lane + 32, ..)
         float mx = -INFINITY;
         for (int k = lane; k < n; k += 32) mx = fmaxf_nan(mx, a.part_ml[piece(k)].x);
@@ -795,8 +808,21 @@ attn_cache_join_kernel(const __grid_constant__ AttCacheArgs a, int rank_rows) {
                 w = v.x == -INFINITY ? 0.0f : ex2_ftz(v.x - mx);
                 lt = fmaf(w, v.y, lt);
             }
-#pragma unroll 4
-            for (int k = many ? warp : 0; k < min(n - k0, 32); k += many ? WARPS : 1) {
+            if (k0 == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k_first + j * k_step;
+                    const float f = __shfl_sync(0xffffffffu, w, k & 31);
+                    if (k >= n) continue;
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        x[e].x = fmaf(f, ahead[j][e].x, x[e].x);
+                        x[e].y = fmaf(f, ahead[j][e].y, x[e].y);
+                    }
+                }
+            }
+#pragma unroll 2
+            for (int k = k_first + (k0 == 0 ? 4 * k_step : 0); k < min(n - k0, 32); k += k_step) {
                 const float f = __shfl_sync(0xffffffffu, w, k);
                 const float2* p = reinterpret_cast<const float2*>(a.part + piece(k0 + k) * D) + lane;
 #pragma unroll
@@ -850,9 +876,9 @@ size_t attn_cache_workspace_bytes(const gdn_kv_cache& c, int64_t n_tokens, int h
 
 template <int D>
 static cudaError_t ac_join(const AttCacheArgs& a, int rank_rows, cudaStream_t st) {
-    // a row per block, up to a few blocks per SM
+    // a warp per row, and up to a block per row while that is two blocks per SM
     const int rows = a.max_q * a.ratio, pairs = a.n_seqs * a.heads;
-    const int y = pairs >= 8 * AC_MAX_RUNS ? 1 : 8 * AC_MAX_RUNS / pairs < rows ? 8 * AC_MAX_RUNS / pairs : rows;
+    const int y = std::max((rows + AC_JOIN_THREADS / 32 - 1) / (AC_JOIN_THREADS / 32), std::min(rows, 2 * AC_MAX_RUNS / pairs));
     return launch_dependent(attn_cache_join_kernel<D>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(y)),
                             dim3(AC_JOIN_THREADS), 0, st, a, rank_rows);
 }
