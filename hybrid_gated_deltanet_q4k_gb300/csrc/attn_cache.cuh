@@ -35,6 +35,7 @@ struct AttCacheArgs {
     int runs, ranks;    // runs of blocks, and row tiles of a pair (a CTA per run and rank of rows)
     int start;          // blocks that each pair counts more than it has
     int box;            // keys of one copy
+    int wide;           // rows of q and o start on 32 bytes (kernel for many rows)
     float sl2;          // scale * log2(e)
     float* part;        // partial accumulators [runs * ranks][2][rows][D]
     float2* part_ml;    // and their maxima and sums [runs * ranks][2][rows]

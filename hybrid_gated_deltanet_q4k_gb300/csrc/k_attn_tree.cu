@@ -64,8 +64,7 @@ struct AtSmem {
     static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors, log2 value scales, their inverses: [softmax warp][3][BN / 2]
     static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 3 * BN / 2 * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
     static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
-    static constexpr int E0 = L0 + 2 * AT_ROWS * 4;         // 16 columns on their way out: [softmax warp][32 rows][17]
-    static constexpr int P0 = E0 + AT_SM_WARPS * 32 * 17 * 4;         // blocks before each sequence
+    static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
     static constexpr int W0 = T0 + GDN_MAX_SEQS * 12;
     static constexpr int B0 = W0 + 16 * 8;                  // mbarriers
@@ -382,17 +381,27 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             // ---- Q to TMEM: this thread half a row.  The last piece's products have read theirs.
             float factor = a.sl2;
             {
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(q.tok + (on ? tok : 0)) * a.ld_q +
-                                                                  (on ? hq : 0) * D + half * (D / 2));
+                const uint16_t* src = a.q + static_cast<int64_t>(q.tok + (on ? tok : 0)) * a.ld_q + (on ? hq : 0) * D + half * (D / 2);
+                auto load = [&](int c, uint32_t (&w)[8]) {     // elements 16 c .. 16 c + 15
+                    if (a.wide) {
+                        load32(src + 16 * c, w);
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4*>(src + 16 * c), y = *reinterpret_cast<const uint4*>(src + 16 * c + 8);
+                        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+                        w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = on ? w[e] : 0u;
+                };
                 float up = 1.0f;
                 if constexpr (Q8) {
                     float amax = 0.0f;
-#pragma unroll 8
-                    for (int c = 0; c < D / 16; ++c) {
-                        const uint4 w = on ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 4
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t u[8];
+                        load(c, u);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
                     }
                     lsum[half * AT_ROWS + r] = amax;
@@ -403,22 +412,18 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
                 }
 #pragma unroll
-                for (int c = 0; c < D / 16; c += 4) {
-                    uint32_t u[16];
+                for (int c = 0; c < D / 32; c += 2) {
+                    uint32_t v[2][8], u[16];
+                    load(c, v[0]);
+                    load(c + 1, v[1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 w = on ? src[c + e] : make_uint4(0u, 0u, 0u, 0u);
-                        u[4 * e] = w.x;
-                        u[4 * e + 1] = w.y;
-                        u[4 * e + 2] = w.z;
-                        u[4 * e + 3] = w.w;
-                    }
+                    for (int e = 0; e < 16; ++e) u[e] = v[e >> 3][e & 7];
                     if constexpr (Q8) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             u[e] = f16x2_bits(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
                     }
-                    t5::st16u(trow + L::QCOL + half * (D / 4) + 4 * c, u);
+                    t5::st16u(trow + L::QCOL + half * (D / 4) + 8 * c, u);
                 }
                 t5::fence_before();
                 if (warp == 2 && lane == 0) *piece_tiles = nb;
@@ -668,16 +673,15 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const float lt = lsum[r] + lsum[AT_ROWS + r];
             if (ok) {
                 t5::fence_after();
-                // Half of the columns, 16 at a time, through this warp's piece of shared
-                // memory: a thread holds a row, and memory wants whole sectors of one.
+                // half of the columns, 32 at a time, in whole sectors: 32 bytes a thread
                 const bool whole = pc.b0 == 0 && pc.b1 == pc.blocks;
                 const float inv = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
-                float* stage = reinterpret_cast<float*>(base + L::E0) + (warp - 2) * (32 * 17);
-                const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (pc.b0 > 0 ? 0 : 1)) * AT_ROWS + 32 * quad;
+                const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (pc.b0 > 0 ? 0 : 1)) * AT_ROWS + r;
+                const bool out = on && GDN_IN_RANGE(g_attn_cache_error, q.tok + tok < a.n_tokens && hq < a.hq);
 #pragma unroll 1
-                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
-                    float ov[16];
-                    t5::ld16(trow + L::OCOL + c0, ov);
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                    float ov[32];
+                    t5::ld32(trow + L::OCOL + c0, ov);
                     if (odd_keys) {
                         // values that are not finite: infinite or NaN whatever their (positive) weight is
 #pragma unroll 1
@@ -689,7 +693,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             if (pg < 0 || pg >= a.n_pages) continue;
                             const int64_t vr = ((static_cast<int64_t>(pg) * a.heads + pc.head) * a.page + (key & (a.page - 1))) * D + c0;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 32; ++e) {
                                 float v;
                                 if constexpr (Q8)
                                     v = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(a.v)[vr + e], __NV_E4M3)));
@@ -699,32 +703,31 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             }
                         }
                     }
-                    __syncwarp();
+                    if (whole && out) {
+                        uint16_t* dst = a.o + static_cast<int64_t>(q.tok + tok) * a.ld_o + static_cast<int64_t>(hq) * D + c0;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) stage[lane * 17 + e] = ov[e] * inv;
-                    __syncwarp();
-                    if (whole) {
-                        // four rows of 32 bytes at a time
+                        for (int y = 0; y < 32; y += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int y = 0; y < 32; y += 4) {
-                            const int rl = y + (lane >> 3), c = 2 * (lane & 7), orow = row0 + 32 * quad + rl, ot = orow / a.ratio;
-                            if (32 * quad + rl < rows &&
-                                GDN_IN_RANGE(g_attn_cache_error, q.tok + ot < a.n_tokens && pc.head * a.ratio + orow - ot * a.ratio < a.hq)) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(stage[rl * 17 + c], stage[rl * 17 + c + 1]);
-                                *reinterpret_cast<uint32_t*>(a.o + (q.tok + ot) * a.ld_o + (pc.head * a.ratio + orow - ot * a.ratio) * D + c0 + c) =
-                                    *reinterpret_cast<const uint32_t*>(&b2);
+                            for (int e = 0; e < 8; ++e) w[e] = bf16x2(ov[y + 2 * e] * inv, ov[y + 2 * e + 1] * inv);
+                            if (a.wide) {
+                                store32(dst + y, w);
+                            } else {
+                                *reinterpret_cast<uint4*>(dst + y) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4*>(dst + y + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                             }
                         }
-                    } else {
-                        // two rows of 64 bytes at a time
+                    } else if (!whole && on) {
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            const int rl = y + (lane >> 4), c = lane & 15;
-                            if (32 * quad + rl < rows) a.part[(part0 + rl) * D + c0 + c] = stage[rl * 17 + c];
+                        for (int y = 0; y < 32; y += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[y + e]);
+                            store32(a.part + part0 * D + c0 + y, w);
                         }
                     }
                 }
-                if (!whole && on && half == 0) a.part_ml[part0 + lane] = make_float2(m, lt);
+                if (!whole && on && half == 0) a.part_ml[part0] = make_float2(m, lt);
                 t5::fence_before();
             }
             at_bar_softmax();           // every row has read what the others left it
@@ -763,6 +766,7 @@ static cudaError_t at_launch(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
     if (!ac_map(&mk, c.k, c, a.box, 1) || !ac_map(&mv, c.v, c, a.box, 1)) return cudaErrorInvalidValue;
     a.ranks = (a.max_q * a.ratio + AT_ROWS - 1) / AT_ROWS;
     a.runs = AC_MAX_RUNS / a.ranks;
+    a.wide = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.o) | static_cast<uintptr_t>(2 * (a.ld_q | a.ld_o))) & 31) == 0;
     return launch_dependent(attn_tree_kernel<D, T>, dim3(static_cast<unsigned>(a.runs * a.ranks)), dim3(L::THREADS), L::DYN, st,
                             mk, mv, a);
 }
