@@ -42,8 +42,7 @@
 // element in [2^14, 2^15): elements below 2^-38 of it are lost.
 //
 // Measured (us; bytes of the cache over the time): one token over 131072 int8
-// keys, 16 over 4 heads of 256: 54, 5.0 TB/s, of which the join is 6 and the
-// start of a run 4; 48 sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by
+// keys, 16 over 4 heads of 256: 54, 5.0 TB/s, of which the join is 5; 48 sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by
 // memory; 16 chains of up to four tokens over 300 to 12000 int8 keys, 32 over 8
 // heads of 128: 65, 3.0 TB/s, bound by the 16 rows' conversions and products (one
 // token each, eight rows: 48).  777 bf16 keys of one sequence: 9, the latencies of
@@ -874,10 +873,11 @@ constexpr int AC_TREE_TILE = 128;       // its rows per CTA
 
 // The kernel for many rows from this many rows of a pair on (max_q times the
 // heads of a key/value head).  Six sequences of 4000 to 24000 keys, this kernel
-// and the other: 32 rows of bf16 heads of 256 81 and 106 us, of 128 99 and 101,
-// of 64 58 and 65; of int8 heads of 256 81 and 122, of 128 93 and 160, of 64 56
-// and 125.  Past 32 rows this one would read the cache once more per 32 (16 for
-// heads of 256), and the other not until 129.
+// and the other, us, heads of 256 / 128 / 64: 32 rows bf16 80 and 82 / 99 and 86
+// / 56 and 59, int8 80 and 106 / 92 and 154 / 57 and 109; 48 rows bf16 112 and 86
+// / 174 and 92 / 93 and 59, int8 111 and 108 / 163 and 153 / 94 and 110.  Up to 32
+// rows this kernel reads the cache once (twice for heads of 256), the other up to
+// 128.
 constexpr int AC_TREE_ROWS = 33;
 
 size_t attn_cache_workspace_bytes(const gdn_kv_cache& c, int64_t n_tokens, int hq) {
