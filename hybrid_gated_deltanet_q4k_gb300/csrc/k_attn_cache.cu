@@ -38,12 +38,13 @@
 // loses bits (2^-25 of the largest), matter only to elements that are zero in
 // every more probable row; a tile that has one multiplies the rounding errors
 // p' - fp16(p') in bf16, whose exponents reach as far as fp32's, in a second
-// pass, and leaves out the first where fp16 holds nothing.  q goes to fp16 times a power of two per row that puts its largest
-// element in [2^14, 2^15): elements below 2^-38 of it are lost.
+// pass, and leaves out the first where fp16 holds nothing.  q goes to fp16 times
+// a power of two per row that puts its largest element in [2^14, 2^15): elements
+// below 2^-38 of it are lost.
 //
 // Measured (us; bytes of the cache over the time): one token over 131072 int8
-// keys, 16 over 4 heads of 256: 54, 5.0 TB/s, of which the join is 5; 48 sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by
-// memory; 16 chains of up to four tokens over 300 to 12000 int8 keys, 32 over 8
+// keys, 16 over 4 heads of 256: 54, 5.0 TB/s, of which the join is 5; 48
+// sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by memory; 16 chains of up to four tokens over 300 to 12000 int8 keys, 32 over 8
 // heads of 128: 65, 3.0 TB/s, bound by the 16 rows' conversions and products (one
 // token each, eight rows: 48).  777 bf16 keys of one sequence: 9, the latencies of
 // two kernels.
