@@ -500,6 +500,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         wide |= !(fabsf(lv) <= 60.0f);
                     }
                     wide = __any_sync(0xffffffffu, wide);
+                    __syncwarp();     // the tables are read by all lanes (a vote does not order memory)
                     scales_of(j + 1);
                 }
 
