@@ -39,6 +39,8 @@ struct AttCacheArgs {
     float sl2;          // scale * log2(e)
     float* part;        // partial accumulators [runs * ranks][2][rows][D]
     float2* part_ml;    // and their maxima and sums [runs * ranks][2][rows]
+    uint64_t wait_ns;   // the limit of a wait
+    int withhold;       // test: the first copy of a CTA is never issued, so that a wait for it runs out
 };
 
 // A sequence as the kernels see it, its device-held numbers forced into range.

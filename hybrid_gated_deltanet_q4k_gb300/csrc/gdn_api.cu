@@ -66,7 +66,7 @@ cudaError_t launch_kv_read(const gdn_kv_cache&, const int64_t*, int64_t, uint16_
                            cudaStream_t);
 cudaError_t launch_attn_cache(const gdn_kv_cache&, const uint16_t*, int64_t, const int32_t*, int64_t, int, const uint64_t*,
                               const int32_t*, int64_t, int, const int32_t*, int, int, float, uint16_t*, int64_t, void*,
-                              cudaStream_t);
+                              cudaStream_t, uint64_t);
 size_t attn_cache_workspace_bytes(const gdn_kv_cache&, int64_t, int);
 int read_and_clear_rope_error();
 int read_and_clear_kv_error();
@@ -1087,10 +1087,11 @@ size_t gdn_attn_cache_workspace_size(const gdn_kv_cache* cache, int64_t n_tokens
     return attn_cache_workspace_bytes(*cache, n_tokens, n_q_heads);
 }
 
-int gdn_attn_cache(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, const int32_t* cu_q, int64_t n_tokens,
-                   int max_q, const uint64_t* tree, const int32_t* block_table, int64_t ld_table, int max_blocks,
-                   const int32_t* lens, int n_seqs, int n_q_heads, float scale, uint16_t* o, int64_t ld_o, void* workspace,
-                   size_t ws_bytes, void* stream) {
+// fault_wait_ns: 0, or the wait limit of gdn_test_attn_cache_wait_timeout
+static int attn_cache_impl(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, const int32_t* cu_q, int64_t n_tokens,
+                           int max_q, const uint64_t* tree, const int32_t* block_table, int64_t ld_table, int max_blocks,
+                           const int32_t* lens, int n_seqs, int n_q_heads, float scale, uint16_t* o, int64_t ld_o,
+                           void* workspace, size_t ws_bytes, uint64_t fault_wait_ns, void* stream) {
     int r = check_cache(cache, "gdn_attn_cache");
     if (r) return r;
     if (n_seqs < 1 || n_seqs > GDN_MAX_SEQS)
@@ -1117,10 +1118,30 @@ int gdn_attn_cache(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, c
     if (ws_bytes < need) return fail(GDN_ENOMEM, "gdn_attn_cache: workspace %zu B < %zu B", ws_bytes, need);
     const float sc = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
     const cudaError_t e = launch_attn_cache(*cache, q, ld_q, cu_q, n_tokens, max_q, tree, block_table, ld_table, max_blocks, lens,
-                                            n_seqs, n_q_heads, sc, o, ld_o, workspace, static_cast<cudaStream_t>(stream));
+                                            n_seqs, n_q_heads, sc, o, ld_o, workspace, static_cast<cudaStream_t>(stream),
+                                            fault_wait_ns);
     if (e == cudaErrorInvalidValue) return fail(GDN_EINVAL, "gdn_attn_cache: tensor map rejected");
     if (e != cudaSuccess) return cuda_fail(e, "gdn_attn_cache");
     return GDN_OK;
+}
+
+int gdn_attn_cache(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, const int32_t* cu_q, int64_t n_tokens,
+                   int max_q, const uint64_t* tree, const int32_t* block_table, int64_t ld_table, int max_blocks,
+                   const int32_t* lens, int n_seqs, int n_q_heads, float scale, uint16_t* o, int64_t ld_o, void* workspace,
+                   size_t ws_bytes, void* stream) {
+    return attn_cache_impl(cache, q, ld_q, cu_q, n_tokens, max_q, tree, block_table, ld_table, max_blocks, lens, n_seqs,
+                           n_q_heads, scale, o, ld_o, workspace, ws_bytes, 0, stream);
+}
+
+int gdn_test_attn_cache_wait_timeout(const gdn_kv_cache* cache, const uint16_t* q, int64_t ld_q, const int32_t* cu_q,
+                                     int64_t n_tokens, int max_q, const uint64_t* tree, const int32_t* block_table,
+                                     int64_t ld_table, int max_blocks, const int32_t* lens, int n_seqs, int n_q_heads,
+                                     float scale, uint16_t* o, int64_t ld_o, void* workspace, size_t ws_bytes,
+                                     uint64_t wait_ns, void* stream) {
+    if (wait_ns < 1000 || wait_ns > 100000000ull)
+        return fail(GDN_EINVAL, "gdn_test_attn_cache_wait_timeout: wait_ns in [1 us, 100 ms] required");
+    return attn_cache_impl(cache, q, ld_q, cu_q, n_tokens, max_q, tree, block_table, ld_table, max_blocks, lens, n_seqs,
+                           n_q_heads, scale, o, ld_o, workspace, ws_bytes, wait_ns, stream);
 }
 
 int gdn_sync_status(void* stream) {

@@ -296,7 +296,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
             for (int j = 0; j < L::NS; ++j)
                 if (j < 2 * mine) {
-                    issue(j, sl, pg[j >> 1]);
+                    if (!(a.withhold && warp == 0 && j == 0)) issue(j, sl, pg[j >> 1]);
                     sl = sl + 1 == L::NS ? 0 : sl + 1;
                 }
         }
@@ -357,7 +357,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const int key0 = (t0 + warp + i * L::WARPS) * L::KEYS;
             const uint32_t kb = smem_addr(ring + slot * L::HALF) + koff;
 
-            if (!dead && !mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
+            if (!dead && !mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT, a.wait_ns)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             const uint32_t ok = page_in[slot] | (~0u << copies);
@@ -422,7 +422,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             const uint32_t vb = smem_addr(ring + slot * L::HALF) + voff;
 
-            if (!mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT)) dead = true;
+            if (!mbar_wait_bounded(bars + slot, par, &g_attn_cache_error, ERR_WAIT_TIMEOUT, a.wait_ns)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
 
@@ -926,8 +926,10 @@ static cudaError_t ac_launch_t(const gdn_kv_cache& c, AttCacheArgs& a, cudaStrea
 cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t ld_q, const int32_t* cu, int64_t n_tokens,
                               int max_q, const uint64_t* tree, const int32_t* table, int64_t ld_table, int max_blocks,
                               const int32_t* lens, int n_seqs, int hq, float scale, uint16_t* o, int64_t ld_o,
-                              void* workspace, cudaStream_t st) {
+                              void* workspace, cudaStream_t st, uint64_t fault_wait_ns) {
     AttCacheArgs a{};
+    a.wait_ns = fault_wait_ns ? fault_wait_ns : 2000000000ull;
+    a.withhold = fault_wait_ns != 0;
     a.n_pages = c.n_pages;
     a.heads = c.n_kv_heads;
     a.page = c.page_tokens;

@@ -90,9 +90,9 @@ struct AtSmem {
 
 // Waits for a phase, asleep for up to 20 us at a time: warps that poll take
 // issue slots and shared-memory cycles from the one that issues the products.
-// Gives up after 2 s with the error word set, and at once after any wait of the
-// CTA has.
-__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// Gives up after limit_ns with the error word set, and at once after any wait of
+// the CTA has.
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     auto sleep = [&]() {
         uint32_t ok;
         asm volatile(
@@ -108,7 +108,7 @@ __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile
     const uint64_t t0 = globaltimer_ns();
     while (!*abort) {
         if (sleep()) return true;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
+        if (globaltimer_ns() - t0 > limit_ns) {
             atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
             *abort = 1;
         }
@@ -231,12 +231,12 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     const uint32_t m = 2 * n + v;
                     if constexpr (Q8) {
                         const uint32_t sl = m % RS;
-                        if (m >= RS) ok = __all_sync(0xffffffffu, at_wait(bars + L::RE + sl, (m / RS - 1) & 1, abort));
-                        if (ok) load(v ? &mv : &mk, bars + L::RF + sl, L::R0 + sl * L::RAW, L::RAW, j, page);
+                        if (m >= RS) ok = __all_sync(0xffffffffu, at_wait(bars + L::RE + sl, (m / RS - 1) & 1, abort, a.wait_ns));
+                        if (ok && !(a.withhold && m == 0)) load(v ? &mv : &mk, bars + L::RF + sl, L::R0 + sl * L::RAW, L::RAW, j, page);
                     } else {
                         const uint32_t sl = m % NI;
-                        if (m >= NI) ok = __all_sync(0xffffffffu, at_wait(bars + L::ID + sl, (m / NI - 1) & 1, abort));
-                        if (ok) load(v ? &mv : &mk, bars + L::IF + sl, L::I0 + sl * L::TILE, L::TILE, j, page);
+                        if (m >= NI) ok = __all_sync(0xffffffffu, at_wait(bars + L::ID + sl, (m / NI - 1) & 1, abort, a.wait_ns));
+                        if (ok && !(a.withhold && m == 0)) load(v ? &mv : &mk, bars + L::IF + sl, L::I0 + sl * L::TILE, L::TILE, j, page);
                     }
                 }
                 page = ahead;
@@ -251,8 +251,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int j = 0; ok && j < nb; ++j) {
                 for (int v = 0; ok && v < 2; ++v) {
                     const uint32_t m = 2 * n + v, sl = m % RS, im = m % NI;
-                    ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort);
-                    if (ok && m >= NI) ok = at_wait(bars + L::ID + im, (m / NI - 1) & 1, abort);
+                    ok = at_wait(bars + L::RF + sl, (m / RS) & 1, abort, a.wait_ns);
+                    if (ok && m >= NI) ok = at_wait(bars + L::ID + im, (m / NI - 1) & 1, abort, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const unsigned char* src = base + L::R0 + sl * L::RAW;
@@ -290,7 +290,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // ------------------------------------------------------------ MMA issuer
         // S of a tile needs its K image and its buffer (P V of the tile SB before
         // has read P there); P V needs P and the V image.  The warp polls both and
-        // one lane issues what is ready; a stall past 2 s sets the error word.
+        // one lane issues what is ready; a stall past the limit sets the error word.
         constexpr uint32_t FULL = 0xffffffffu;
         constexpr uint32_t IDS = Q8 ? t5::idesc_f16(AT_ROWS, BN) : t5::idesc_bf16(AT_ROWS, BN);
         constexpr uint32_t IDO = (Q8 ? t5::idesc_f16(AT_ROWS, D) : t5::idesc_bf16(AT_ROWS, D)) | (1u << 16);   // B MN-major
@@ -310,7 +310,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         };
         while (true) {
             // the softmax says how many tiles the piece has (0: no more pieces)
-            ok = __all_sync(FULL, at_wait(bars + L::QF, piece & 1, abort));
+            ok = __all_sync(FULL, at_wait(bars + L::QF, piece & 1, abort, a.wait_ns));
             const int tiles = static_cast<int>(__reduce_max_sync(FULL, static_cast<uint32_t>(*piece_tiles)));
             if (!ok || tiles == 0) break;
             ++piece;
@@ -353,7 +353,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 } else if (++spins >= 1024) {
                     const uint64_t now = globaltimer_ns();
                     if (spins == 1024) t_last = now;
-                    if (__any_sync(FULL, *abort || now - t_last > 2000000000ull)) {
+                    if (__any_sync(FULL, *abort || now - t_last > a.wait_ns)) {
                         if (lane == 0 && !*abort) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_WAIT_TIMEOUT));
                         __syncwarp();
                         *abort = 1;
@@ -504,7 +504,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     scales_of(j + 1);
                 }
 
-                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + 2 * i % NI, (2 * i / NI) & 1, abort));
+                ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + 2 * i % NI, (2 * i / NI) & 1, abort, a.wait_ns));
                 // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
                 float xs[KEEP][32];
                 auto scores = [&](int ch, float (&x)[32]) {
@@ -554,7 +554,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         m = bm;
                     } else {
                         // O is rescaled once P V of tile i - 1 has finished
-                        ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i - 1) % NI, ((2 * i - 1) / NI) & 1, abort));
+                        ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i - 1) % NI, ((2 * i - 1) / NI) & 1, abort, a.wait_ns));
                         if (ok) {
                             const float mn = fmaxf(m, bm), f = m == -INFINITY ? 0.0f : ex2_ftz(m - mn);
                             m = mn;
@@ -633,7 +633,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     if constexpr (edge) {
                         // values of keys that do not exist become zero, and so do those of
                         // new keys that are not finite: the rows that see them add them at the end
-                        ok = __all_sync(0xffffffffu, at_wait(bars + L::IF + (2 * i + 1) % NI, ((2 * i + 1) / NI) & 1, abort));
+                        ok = __all_sync(0xffffffffu, at_wait(bars + L::IF + (2 * i + 1) % NI, ((2 * i + 1) / NI) & 1, abort, a.wait_ns));
                         unsigned char* vt = base + L::I0 + (2 * i + 1) % NI * L::TILE;
                         if (ok)
 #pragma unroll 1
@@ -672,7 +672,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
             // ---- the piece's rows out
             const uint32_t i1 = n - 1;
-            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i1 + 1) % NI, ((2 * i1 + 1) / NI) & 1, abort));
+            ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + (2 * i1 + 1) % NI, ((2 * i1 + 1) / NI) & 1, abort, a.wait_ns));
             lsum[half * AT_ROWS + r] = l;
             uint64_t* none_of = reinterpret_cast<uint64_t*>(xmax);   // the maxima have been read: every P is in
             none_of[half * AT_ROWS + r] = none;
@@ -746,9 +746,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         at_arrive_warp(bars + L::QF, lane);
     }
 
+    __syncthreads();   // the copies' warp may be through long before another one's wait runs out
     if (*abort && tid == 0) {
         // a wait ran out: let copies already issued land (bounded) before the shared memory is released
-        for (int i = L::IF; i < L::NBAR; ++i)
+        constexpr int FIRST = Q8 ? L::RF : L::IF, N = Q8 ? RS : NI;
+        for (int i = FIRST; i < FIRST + N; ++i)
             for (uint32_t par = 0; par < 2; ++par) mbar_wait_bounded(bars + i, par, nullptr, 0, 20000000ull);
     }
     t5::fence_before();

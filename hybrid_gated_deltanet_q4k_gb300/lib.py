@@ -79,6 +79,8 @@ _SIGNATURES = {
     "gdn_attn_cache_workspace_size": (c_size_t, [_P, c_int64, c_int32]),
     "gdn_attn_cache": (c_int32, [_P, _P, c_int64, _P, c_int64, c_int32, _P, _P, c_int64, c_int32, _P, c_int32, c_int32, c_float, _P,
                                  c_int64, _P, c_size_t, _P]),
+    "gdn_test_attn_cache_wait_timeout": (c_int32, [_P, _P, c_int64, _P, c_int64, c_int32, _P, _P, c_int64, c_int32, _P, c_int32,
+                                                   c_int32, c_float, _P, c_int64, _P, c_size_t, ctypes.c_uint64, _P]),
     "gdn_sync_status": (c_int32, [_P]),
     "gdn_last_error": (ctypes.c_char_p, []),
     "gdn_set_stage_events": (c_int32, [ctypes.POINTER(c_void_p), c_int32]),

@@ -496,6 +496,21 @@ int gdn_attn_cache(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, c
                    void *stream);
 
 /*
+ * gdn_test_attn_cache_wait_timeout -- gdn_attn_cache with the first copy of
+ * every CTA never issued, so that the wait for it runs out after wait_ns
+ * nanoseconds (1 us .. 100 ms).  The kernel records the timeout, waits (again
+ * with a limit) for its other copies and its products, frees its tensor memory
+ * and returns; nothing faults and the context stays usable.  gdn_sync_status
+ * then reports GDN_ETIMEOUT once and the next call runs normally.  What it
+ * leaves in o (its rows) and in the workspace means nothing.
+ */
+int gdn_test_attn_cache_wait_timeout(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, const int32_t *cu_q,
+                                     int64_t n_tokens, int max_q, const uint64_t *tree, const int32_t *block_table,
+                                     int64_t ld_table, int max_blocks, const int32_t *lens, int n_seqs, int n_q_heads,
+                                     float scale, uint16_t *o, int64_t ld_o, void *workspace, size_t ws_bytes,
+                                     uint64_t wait_ns, void *stream);
+
+/*
  * gdn_sync_status -- wait for `stream`, then report (and clear) the device
  * error words the kernels set: GDN_OK, GDN_ETIMEOUT (a bounded wait ran out),
  * GDN_ERANGE (a value beyond the fp16 operand range of the recurrence: the
