@@ -150,12 +150,18 @@ class DeviceLayer:
                                          gl.stream_handle(stream), check=check)
 
 
-def _heads(t: torch.Tensor, name: str, width=None) -> int:
+def _on_device(t: torch.Tensor, name: str, device: int):
+    if t.get_device() != device:      # -1: host memory, which a kernel must not be given
+        raise ValueError(f"{name}: a tensor on device cuda:{device} is required")
+
+
+def _heads(t: torch.Tensor, name: str, device: int, width=None) -> int:
     """Elements between the tokens of a bf16 tensor [tokens][heads][head_dim] whose heads are contiguous (and
     whose heads and head_dim are ``width``, if given)."""
     shape = t.shape
     if t.dtype is not torch.bfloat16 or len(shape) != 3 or not t.is_cuda:
         raise ValueError(f"{name}: a bf16 device tensor [tokens][heads][head_dim] is required")
+    _on_device(t, name, device)
     n, h, d = shape
     if width is not None and (h, d) != width:
         raise ValueError(f"{name}: [tokens][{width[0]}][{width[1]}] is required")
@@ -165,9 +171,9 @@ def _heads(t: torch.Tensor, name: str, width=None) -> int:
     return sn if n > 1 else h * d
 
 
-def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str):
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: {n} contiguous {dtype} on the device are required")
+def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str, device: int):
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: {n} contiguous {dtype} on device cuda:{device} are required")
 
 
 class RopeTable:
@@ -196,14 +202,15 @@ class RopeTable:
         positions int32 [n]; into q_out and k_out, or in place without them."""
         n, hq, d = q.shape
         q_out = q if q_out is None else q_out
-        _vector(positions, torch.int32, n, "positions")
-        ld_q, ld_qo = _heads(q, "q"), _heads(q_out, "q_out")
+        dev = q.get_device()
+        ld_q, ld_qo = _heads(q, "q", dev), _heads(q_out, "q_out", dev)
+        _vector(positions, torch.int32, n, "positions", dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out: the shape of q is required")
         hk = ld_k = ld_ko = 0
         if k is not None:
             k_out = k if k_out is None else k_out
-            ld_k, ld_ko, hk = _heads(k, "k"), _heads(k_out, "k_out"), k.shape[1]
+            ld_k, ld_ko, hk = _heads(k, "k", dev), _heads(k_out, "k_out", dev), k.shape[1]
             if k.shape[0] != n or k.shape[2] != d or k_out.shape != k.shape:
                 raise ValueError("k and k_out: as many tokens of the same head size as q are required")
         return self.lib.gdn_rope(self._ref, gl.ptr(positions), n, d, gl.ptr(q), ld_q, hq, gl.ptr(q_out), ld_qo, gl.ptr(k),
@@ -234,6 +241,9 @@ class KvCache:
                 raise ValueError("a bf16 cache has no scales")
         elif any(s is None or s.shape != k.shape[:3] or s.dtype != torch.float32 or not s.is_contiguous() for s in scales):
             raise ValueError("k_scale and v_scale: contiguous fp32 [n_pages][n_kv_heads][page_tokens] are required")
+        self._device = k.get_device()
+        if self._device < 0 or any(t is not None and t.get_device() != self._device for t in (v, *scales)):
+            raise ValueError("the pages and their scales: memory of one CUDA device is required")
         self.lib = gl.load(debug=debug)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = k.shape
@@ -265,21 +275,21 @@ class KvCache:
               check=True) -> int:
         """Enqueue gdn_kv_write: rows of k and v (bf16 [n][n_kv_heads][head_dim]) into slots (int64); with
         rows (int32), token t is row rows[t]: the accepted tokens of a drafted tree."""
-        ld_k, ld_v = _heads(k, "k", self._width), _heads(v, "v", self._width)
+        ld_k, ld_v = _heads(k, "k", self._device, self._width), _heads(v, "v", self._device, self._width)
         n = slots.numel()
-        _vector(slots, torch.int64, n, "slots")
+        _vector(slots, torch.int64, n, "slots", self._device)
         if v.shape[0] != k.shape[0]:
             raise ValueError("k and v: the same number of rows is required")
         if rows is not None:
-            _vector(rows, torch.int32, n, "rows")
+            _vector(rows, torch.int32, n, "rows", self._device)
         return self.lib.gdn_kv_write(self._ref, gl.ptr(k), ld_k, gl.ptr(v), ld_v, k.shape[0], gl.ptr(rows), gl.ptr(slots), n,
                                      gl.stream_handle(stream), check=check)
 
     def read(self, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None, check=True) -> int:
         """Enqueue gdn_kv_read: the values of the slots (int64) into k and v (bf16 [n][n_kv_heads][head_dim])."""
-        ld_k, ld_v = _heads(k, "k", self._width), _heads(v, "v", self._width)
+        ld_k, ld_v = _heads(k, "k", self._device, self._width), _heads(v, "v", self._device, self._width)
         n = slots.numel()
-        _vector(slots, torch.int64, n, "slots")
+        _vector(slots, torch.int64, n, "slots", self._device)
         if k.shape[0] != n or v.shape[0] != n:
             raise ValueError(f"k and v: {n} rows are required")
         return self.lib.gdn_kv_read(self._ref, gl.ptr(slots), n, gl.ptr(k), ld_k, gl.ptr(v), ld_v, gl.stream_handle(stream),
@@ -298,19 +308,23 @@ class KvCache:
         tokens.  lens int32 [n_seqs] counts the cached tokens, the new ones (already written) among them;
         block_table int32 [n_seqs][blocks]; cu_q int32 [n_seqs + 1] the new tokens' offsets (None: max_q
         each); tree int64 [T] mask words (None: a chain)."""
-        ld_q, ld_o = _heads(q, "q"), _heads(o, "o")
+        ld_q, ld_o = _heads(q, "q", self._device), _heads(o, "o", self._device)
         n, hq, d = q.shape
         if o.shape != q.shape or d != self.head_dim:
             raise ValueError(f"q and o: [tokens][heads][{self.head_dim}] of one shape are required")
         s = lens.numel()
-        _vector(lens, torch.int32, s, "lens")
+        _vector(lens, torch.int32, s, "lens", self._device)
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s or (
                 block_table.shape[1] > 1 and block_table.stride(1) != 1) or (s > 1 and block_table.stride(0) < block_table.shape[1]):
             raise ValueError(f"block_table: int32 [{s}][blocks] is required")
+        _on_device(block_table, "block_table", self._device)
+        _on_device(workspace, "workspace", self._device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous memory is required")
         if cu_q is not None:
-            _vector(cu_q, torch.int32, s + 1, "cu_q")
+            _vector(cu_q, torch.int32, s + 1, "cu_q", self._device)
         if tree is not None:
-            _vector(tree, torch.int64, n, "tree")
+            _vector(tree, torch.int64, n, "tree", self._device)
         ld_table = block_table.stride(0) if s > 1 else block_table.shape[1]
         return self.lib.gdn_attn_cache(self._ref, gl.ptr(q), ld_q, gl.ptr(cu_q), n, max_q, gl.ptr(tree), gl.ptr(block_table),
                                        ld_table, block_table.shape[1], gl.ptr(lens), s, hq, scale, gl.ptr(o), ld_o, gl.ptr(workspace),
