@@ -268,6 +268,8 @@ class KvCache:
 
     def slots(self, pages: torch.Tensor, first: int, n: int) -> torch.Tensor:
         """Slots (int64) of tokens first .. first + n - 1 of a sequence whose block table row is ``pages``."""
+        if first < 0 or n < 0 or first + n > pages.numel() * self.page_tokens:
+            raise ValueError(f"tokens {first} .. {first + n - 1} lie outside the {pages.numel()} pages")
         t = torch.arange(first, first + n, device=pages.device)
         return pages[t // self.page_tokens].long() * self.page_tokens + t % self.page_tokens
 

@@ -95,3 +95,20 @@ def test_rope_takes_the_device_s_tensors_alone(fake):
         for device in ("cpu", "cuda:1"):
             with pytest.raises(ValueError):
                 r.apply(**{**ok, name: _new(tuple(t.shape), t.dtype, device)})
+
+
+@pytest.mark.parametrize("first,n", [(-1, 1), (-16, 4), (0, 81), (80, 1), (70, 11), (3, -1)])
+def test_slots_outside_the_pages_are_refused(fake, first, n):
+    """An index past the table would be a failed assertion on the device, and one below zero another token's slot."""
+    c = _cache()
+    with pytest.raises(ValueError, match="pages"):
+        c.slots(_new((5,), torch.int32), first, n)
+
+
+@pytest.mark.parametrize("first,n", [(0, 0), (80, 0), (0, 80), (15, 18), (79, 1)])
+def test_slots_inside_the_pages(first, n):
+    c = object.__new__(api.KvCache)
+    c.page_tokens = 16
+    pages = torch.tensor([7, 2, -1, 0, 9], dtype=torch.int32)
+    want = [int(pages[t // 16]) * 16 + t % 16 for t in range(first, first + n)]
+    assert c.slots(pages, first, n).tolist() == want and c.slots(pages, first, n).dtype is torch.int64
