@@ -11,8 +11,10 @@
 
 namespace gdn {
 
-// A wait that ran out, or an index out of range; one word per translation unit.
-static __device__ int g_attn_cache_error;
+// Of each translation unit: a wait that ran out (or an index check of the debug
+// build), and an index held in device memory that was out of range.  Two words,
+// so that a skipped index does not hide that the results are not valid.
+static __device__ int g_attn_cache_error, g_attn_cache_skipped;
 
 constexpr int AC_BLOCK = 128;           // keys of a block
 constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
@@ -56,7 +58,7 @@ __device__ __forceinline__ AcSeq ac_seq(const AttCacheArgs& a, int s, bool repor
     r.tok = ok ? lo : 0;
     r.nq = ok ? hi - lo : 0;
     r.len = len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
-    if (report && (!ok || r.len != len)) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+    if (report && (!ok || r.len != len)) atomicExch(&g_attn_cache_skipped, static_cast<int>(ERR_INDEX));
     return r;
 }
 // Blocks of each of its pairs (at least one where there is a row to write), and as they count.

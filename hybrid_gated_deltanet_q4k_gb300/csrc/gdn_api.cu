@@ -72,6 +72,8 @@ int read_and_clear_rope_error();
 int read_and_clear_kv_error();
 int read_and_clear_attn_cache_error();
 int read_and_clear_attn_tree_error();
+int read_and_clear_attn_cache_skipped();
+int read_and_clear_attn_tree_skipped();
 int read_and_clear_gemm_error();
 int read_and_clear_delta_error();
 int read_and_clear_q4k_error();
@@ -1159,27 +1161,40 @@ int gdn_sync_status(void* stream) {
     const int pcode = read_and_clear_rope_error();
     const int kcode = read_and_clear_kv_error();
     const int fcode = read_and_clear_attn_cache_error(), tcode = read_and_clear_attn_tree_error();
-    const int xcode = fcode ? fcode : tcode;
-    if (kcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped");
-    if (xcode == ERR_INDEX) return fail(GDN_EINDEX, "gdn_attn_cache: an offset, length or page out of range was skipped");
+    const int fskip = read_and_clear_attn_cache_skipped(), tskip = read_and_clear_attn_tree_skipped();
     const int words[] = {read_and_clear_q4k_error(), read_and_clear_q6k_error(), read_and_clear_quant_error(),
-                         gcode, ccode, dcode, ncode, rcode, acode, pcode};
+                         gcode, ccode, dcode, ncode, rcode, acode, pcode, fcode, tcode};
     const char* units[] = {"Q4_K decode", "Q6_K decode", "activation quantisation", "projection", "conv",
-                           "delta-rule", "gated-norm", "decode-step", "attention", "rotary"};
+                           "delta-rule", "gated-norm", "decode-step", "attention", "rotary", "cache attention",
+                           "cache attention"};
+    // An index of the caller's that a kernel skipped comes last: beside a wait that ran out or a value out of range,
+    // whose results are not valid, it is only named.
+    const char* skipped = kcode && (fskip || tskip)
+                              ? "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped; gdn_attn_cache: an offset, "
+                                "length or page out of range was skipped"
+                          : kcode          ? "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped"
+                          : fskip || tskip ? "gdn_attn_cache: an offset, length or page out of range was skipped"
+                                           : "";
+    const char* also = *skipped ? "; " : "";
     for (int i = 0; i < static_cast<int>(sizeof(words) / sizeof(words[0])); ++i)
         if (words[i] == ERR_INDEX)
             return fail(GDN_EINDEX, "an index check of the %s kernel failed (the store was skipped; debug library)",
                         units[i]);
-    if (gcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the projection kernel ran out");
-    if (acode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the attention kernel ran out");
-    if (xcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the cache attention kernel ran out");
-    if (ncode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the gated-norm kernel ran out");
-    if (dcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in the delta-rule kernel ran out");
-    if (rcode == ERR_WAIT_TIMEOUT) return fail(GDN_ETIMEOUT, "a bounded wait in a decode-step kernel ran out");
-    if (rcode == ERR_RANGE) return fail(GDN_ERANGE, "a decode-step output o exceeded the fp16 range (|x| > 65504)");
+    const auto timeout = [&](const char* unit) {
+        return fail(GDN_ETIMEOUT, "a bounded wait in %s kernel ran out%s%s", unit, also, skipped);
+    };
+    if (gcode == ERR_WAIT_TIMEOUT) return timeout("the projection");
+    if (acode == ERR_WAIT_TIMEOUT) return timeout("the attention");
+    if (fcode == ERR_WAIT_TIMEOUT || tcode == ERR_WAIT_TIMEOUT) return timeout("the cache attention");
+    if (ncode == ERR_WAIT_TIMEOUT) return timeout("the gated-norm");
+    if (dcode == ERR_WAIT_TIMEOUT) return timeout("the delta-rule");
+    if (rcode == ERR_WAIT_TIMEOUT) return timeout("a decode-step");
+    if (rcode == ERR_RANGE)
+        return fail(GDN_ERANGE, "a decode-step output o exceeded the fp16 range (|x| > 65504)%s%s", also, skipped);
     if (ccode == ERR_RANGE || dcode == ERR_RANGE)
-        return fail(GDN_ERANGE, "a %s value exceeded the fp16 operand range (|x| > 65504)",
-                    ccode == ERR_RANGE ? "q, k or v" : "delta-rule intermediate (T, A T, S, R or Delta)");
+        return fail(GDN_ERANGE, "a %s value exceeded the fp16 operand range (|x| > 65504)%s%s",
+                    ccode == ERR_RANGE ? "q, k or v" : "delta-rule intermediate (T, A T, S, R or Delta)", also, skipped);
+    if (*skipped) return fail(GDN_EINDEX, "%s", skipped);
     return GDN_OK;
 }
 

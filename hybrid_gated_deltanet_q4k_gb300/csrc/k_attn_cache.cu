@@ -363,7 +363,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const uint32_t ok = page_in[slot] | (~0u << copies);
             const bool edge_tile = key0 + L::KEYS > ctx || ok != ~0u;
             if (ok != ~0u && lane < copies && !((ok >> lane) & 1) && key0 + mycopy < q.len)
-                atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+                atomicExch(&g_attn_cache_skipped, static_cast<int>(ERR_INDEX));
             // keys of 16-key step u below limit(u) exist; those of an unseen page do not
             auto limit = [&](int u) {
                 return (ok >> (16 * u / a.box)) & 1 ? q.len - key0 - 16 * u : 0;
@@ -973,6 +973,13 @@ int read_and_clear_attn_cache_error() {
     int v = 0, z = 0;
     cudaMemcpyFromSymbol(&v, g_attn_cache_error, sizeof(int));
     if (v) cudaMemcpyToSymbol(g_attn_cache_error, &z, sizeof(int));
+    return v;
+}
+
+int read_and_clear_attn_cache_skipped() {
+    int v = 0, z = 0;
+    cudaMemcpyFromSymbol(&v, g_attn_cache_skipped, sizeof(int));
+    if (v) cudaMemcpyToSymbol(g_attn_cache_skipped, &z, sizeof(int));
     return v;
 }
 

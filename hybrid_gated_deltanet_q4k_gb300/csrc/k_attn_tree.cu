@@ -447,7 +447,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     all_in &= pg >= 0 && pg < a.n_pages;
                 }
                 all_in = __all_sync(0xffffffffu, all_in);
-                if (!all_in && warp == 2 && lane == 0) atomicCAS(&g_attn_cache_error, 0, static_cast<int>(ERR_INDEX));
+                if (!all_in && warp == 2 && lane == 0) atomicExch(&g_attn_cache_skipped, static_cast<int>(ERR_INDEX));
             }
             auto page_at = [&](int key) { return table[min(key >> a.page_shift, a.max_blocks - 1)]; };
 
@@ -800,6 +800,13 @@ int read_and_clear_attn_tree_error() {
     int v = 0, z = 0;
     cudaMemcpyFromSymbol(&v, g_attn_cache_error, sizeof(int));
     if (v) cudaMemcpyToSymbol(g_attn_cache_error, &z, sizeof(int));
+    return v;
+}
+
+int read_and_clear_attn_tree_skipped() {
+    int v = 0, z = 0;
+    cudaMemcpyFromSymbol(&v, g_attn_cache_skipped, sizeof(int));
+    if (v) cudaMemcpyToSymbol(g_attn_cache_skipped, &z, sizeof(int));
     return v;
 }
 

@@ -515,7 +515,10 @@ int gdn_test_attn_cache_wait_timeout(const gdn_kv_cache *cache, const uint16_t *
  * error words the kernels set: GDN_OK, GDN_ETIMEOUT (a bounded wait ran out),
  * GDN_ERANGE (a value beyond the fp16 operand range of the recurrence: the
  * results of that call are not valid), GDN_EINDEX (an index that a kernel
- * skipped) or GDN_ECUDA (a CUDA error from the stream).
+ * skipped) or GDN_ECUDA (a CUDA error from the stream).  Where several are set
+ * the first of this order is returned (in the debug library an index check of
+ * a kernel's own comes before them), and gdn_last_error names the skipped
+ * index beside it.
  */
 int gdn_sync_status(void *stream);
 
