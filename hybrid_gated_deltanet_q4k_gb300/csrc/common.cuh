@@ -32,7 +32,7 @@ struct PerDeviceOnce {
 // Kernels whose waits are bounded keep an error word in their own translation
 // unit (`static __device__ int`, no relocatable device code): when a wait runs
 // out they record a code there and return early; gdn_sync_status() reads and
-// clears every such word through the unit's host accessor.
+// clears every such word, whose address the unit's host accessor gives.
 enum : int { ERR_NONE = 0, ERR_WAIT_TIMEOUT = 1, ERR_RANGE = 2, ERR_INDEX = 3 };
 
 // Index checks of the debug build (compiled with GDN_DEBUG): a global store

@@ -467,11 +467,9 @@ cudaError_t launch_attn(const uint16_t* q, const uint16_t* k, const uint16_t* v,
     return launch_attn_d<256>(q, k, vt, nq, nk, hq, hkv, scale, o, st);
 }
 
-int read_and_clear_attn_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_attn_error, &z, sizeof(int));
-    return v;
+int* attn_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_attn_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

@@ -969,18 +969,14 @@ cudaError_t launch_attn_cache(const gdn_kv_cache& c, const uint16_t* q, int64_t 
     return rows <= 8 ? ac_launch_t<64, 1>(c, a, st) : rows <= 16 ? ac_launch_t<64, 2>(c, a, st) : ac_launch_t<64, 4>(c, a, st);
 }
 
-int read_and_clear_attn_cache_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_attn_cache_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_attn_cache_error, &z, sizeof(int));
-    return v;
+int* attn_cache_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_attn_cache_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
-int read_and_clear_attn_cache_skipped() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_attn_cache_skipped, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_attn_cache_skipped, &z, sizeof(int));
-    return v;
+int* attn_cache_skipped_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_attn_cache_skipped) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

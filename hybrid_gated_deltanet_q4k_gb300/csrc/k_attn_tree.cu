@@ -796,18 +796,14 @@ cudaError_t launch_attn_tree(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
     return at_launch_t<256>(c, a, st);
 }
 
-int read_and_clear_attn_tree_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_attn_cache_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_attn_cache_error, &z, sizeof(int));
-    return v;
+int* attn_tree_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_attn_cache_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
-int read_and_clear_attn_tree_skipped() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_attn_cache_skipped, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_attn_cache_skipped, &z, sizeof(int));
-    return v;
+int* attn_tree_skipped_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_attn_cache_skipped) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

@@ -304,11 +304,9 @@ cudaError_t launch_conv_ckpt(const gdn_layer& L, const uint16_t* qkvz, int64_t l
     return cudaGetLastError();
 }
 
-int read_and_clear_conv_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_conv_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_conv_error, &z, sizeof(int));
-    return v;
+int* conv_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_conv_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

@@ -1368,11 +1368,9 @@ cudaError_t launch_decode_mid(const gdn_layer& L, const uint16_t* qkvz, int64_t 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-int read_and_clear_decode_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_decode_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_decode_error, &z, sizeof(int));
-    return v;
+int* decode_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_decode_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

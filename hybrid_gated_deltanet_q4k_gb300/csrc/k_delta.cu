@@ -985,11 +985,9 @@ static bool make_qkv_map(CUtensorMap* map, const uint16_t* qkv, int64_t n, int c
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int read_and_clear_delta_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_delta_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_delta_error, &z, sizeof(int));
-    return v;
+int* delta_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_delta_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 // Token segments of DELTA_SEG_CHUNKS chunks of every sequence (twice that

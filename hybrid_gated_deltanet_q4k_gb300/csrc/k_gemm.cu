@@ -566,11 +566,9 @@ cudaError_t launch_gemm_codes(const uint16_t* a, const float* sa, const uint16_t
     return cudaGetLastError();
 }
 
-int read_and_clear_gemm_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_gemm_error, &z, sizeof(int));
-    return v;
+int* gemm_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_gemm_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 // ------------------------------------------------------------ fp32 projection

@@ -375,11 +375,9 @@ cudaError_t launch_kv_read(const gdn_kv_cache& c, const int64_t* slots, int64_t 
     return kv_launch_d(c, false, a, st);
 }
 
-int read_and_clear_kv_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_kv_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_kv_error, &z, sizeof(int));
-    return v;
+int* kv_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_kv_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

@@ -251,11 +251,9 @@ static bool launch_norm_staged(const gdn_layer& L, const uint16_t* o, const uint
     return true;
 }
 
-int read_and_clear_norm_error() {
-    int v = 0, zr = 0;
-    cudaMemcpyFromSymbol(&v, g_norm_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_norm_error, &zr, sizeof(int));
-    return v;
+int* norm_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_norm_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 template <int CPL, bool QUANT>

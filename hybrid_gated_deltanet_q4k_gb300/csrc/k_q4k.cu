@@ -101,11 +101,9 @@ cudaError_t launch_q4k_deq_codes2(const void* b0, int64_t rows0, int64_t cols0, 
     return launch_deq<uint16_t>(j0, j1, st);
 }
 
-int read_and_clear_q4k_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_q4k_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_q4k_error, &z, sizeof(int));
-    return v;
+int* q4k_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_q4k_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

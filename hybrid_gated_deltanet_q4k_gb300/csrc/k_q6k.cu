@@ -81,11 +81,9 @@ cudaError_t launch_q6k_deq_codes(const void* blocks, int64_t rows, int64_t cols,
     return launch_q6k<uint16_t>(blocks, rows, cols, q, s, st);
 }
 
-int read_and_clear_q6k_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_q6k_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_q6k_error, &z, sizeof(int));
-    return v;
+int* q6k_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_q6k_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

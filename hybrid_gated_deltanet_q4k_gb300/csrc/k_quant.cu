@@ -78,11 +78,9 @@ cudaError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, uin
     return cudaGetLastError();
 }
 
-int read_and_clear_quant_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_quant_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_quant_error, &z, sizeof(int));
-    return v;
+int* quant_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_quant_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

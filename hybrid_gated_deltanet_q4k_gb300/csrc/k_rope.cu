@@ -190,11 +190,9 @@ cudaError_t launch_rope(const gdn_rope_table& t, const int32_t* pos, int64_t n, 
     return launch(wide ? rope_vec_kernel<1, true> : rope_vec_kernel<1, false>, 1);
 }
 
-int read_and_clear_rope_error() {
-    int v = 0, z = 0;
-    cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(int));
-    if (v) cudaMemcpyToSymbol(g_rope_error, &z, sizeof(int));
-    return v;
+int* rope_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_rope_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdn

@@ -1,6 +1,7 @@
 """gdn_sync_status where several error words are set: a result that is not valid is reported before an index that
 was skipped."""
 import ctypes
+import time
 
 import numpy as np
 import pytest
@@ -94,3 +95,19 @@ def test_a_wait_that_ran_out_is_reported_before_a_length_of_the_same_launch(L, n
     assert L.gdn_sync_status(stream(), check=False) == gl.GDN_OK
     L.gdn_attn_cache(*args, stream())
     assert L.gdn_sync_status(stream(), check=False) == gl.GDN_EINDEX
+
+
+def test_the_words_are_read_in_one_go(L):
+    """gdn_sync_status is called after every step, and a copy for each word made it as long as fifteen of them: a launch
+    and a copy take as long as two or three."""
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    at = stream()
+    call, copy = [], []
+    for _ in range(300):
+        t = time.perf_counter()
+        L.gdn_sync_status(at)
+        call.append(time.perf_counter() - t)
+        t = time.perf_counter()
+        word.cpu()
+        copy.append(time.perf_counter() - t)
+    assert np.median(call) < 6 * np.median(copy)
