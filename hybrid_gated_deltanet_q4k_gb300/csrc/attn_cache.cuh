@@ -21,6 +21,12 @@ constexpr int AC_MAX_RUNS = 152;        // one CTA per SM
 constexpr int AC_JOIN_THREADS = 256;
 constexpr float AC_MARGIN = 4.0f;
 constexpr float AC_LIFT = 11.0f;        // fp16 probabilities times 2^11
+// The least log2 of a value's scale that the running maximum knows: a smaller
+// scale (a row of zeros has 0) counts as 2^-80 there, and as it is in the
+// probability.  A key adds 2^(x - m) to the sum, and while only such keys have
+// been seen m is as low as x - 80: up to 2^(4 + 11 + 80), which 2^30 keys do not
+// bring past fp32.  AC_VS_FLOOR keeps the logarithm of a scale of 0 finite.
+constexpr float AC_VS_MIN = -80.0f, AC_VS_TINY = 0x1p-80f, AC_VS_FLOOR = 1e-44f;
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct AttCacheArgs {

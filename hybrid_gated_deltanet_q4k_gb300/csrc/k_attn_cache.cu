@@ -434,8 +434,10 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)   // a scale below 2^-110 counts as that (a row of zeros has scale 0 and codes 0)
-                        lv[u][h] = Q8 ? lg2(fmaxf_nan(scales[slot * L::KEYS + 16 * u + 8 * h + g], 7.7e-34f)) : 0.0f;
+                    for (int h = 0; h < 2; ++h) {   // a row of zeros has scale 0 and codes 0
+                        lv[u][h] = Q8 ? lg2(fmaxf_nan(scales[slot * L::KEYS + 16 * u + 8 * h + g], AC_VS_FLOOR)) : 0.0f;
+                        up |= lv[u][h] < AC_VS_MIN;
+                    }
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) {
                         const float2 qs = *reinterpret_cast<const float2*>(row_factor + 8 * nr + 2 * t);
@@ -466,9 +468,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float bm = fmaxf(y[0][nr][e], y[0][nr][2 + e]);
+                            float bm = -INFINITY;
 #pragma unroll
-                            for (int u = 1; u < SUB; ++u) bm = fmaxf(bm, fmaxf(y[u][nr][e], y[u][nr][2 + e]));
+                            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)   // a scale counts as 2^AC_VS_MIN at least
+                                    bm = fmaxf(bm, Q8 ? y[u][nr][2 * h + e] + fmaxf(AC_VS_MIN - lv[u][h], 0.0f) : y[u][nr][2 * h + e]);
                             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
                             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
                             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));

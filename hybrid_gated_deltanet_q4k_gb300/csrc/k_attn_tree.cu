@@ -69,8 +69,8 @@ struct AtSmem {
     static constexpr int RS = !Q8 ? 1 : D == 256 ? 2 : D == 128 ? 4 : 8;
     static constexpr int I0 = 0;
     static constexpr int R0 = I0 + NI * TILE;
-    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors, log2 value scales, their inverses: [softmax warp][3][BN / 2]
-    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 3 * BN / 2 * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
+    static constexpr int F0 = R0 + (Q8 ? RS * RAW : 0);     // key factors, log2 value scales, their inverses: [softmax warp][4][BN / 2]
+    static constexpr int X0 = F0 + (Q8 ? AT_SM_WARPS * 4 * BN / 2 * 4 : 0);   // maxima of the halves; masks of zero weights [2][128]
     static constexpr int L0 = X0 + 2 * AT_ROWS * 8;         // row sums of each half
     static constexpr int P0 = L0 + 2 * AT_ROWS * 4;         // blocks before each sequence
     static constexpr int T0 = P0 + (GDN_MAX_SEQS + 2) * 8;  // the sequences
@@ -373,9 +373,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
         float* xmax = reinterpret_cast<float*>(base + L::X0);
         float* lsum = reinterpret_cast<float*>(base + L::L0);
-        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * 3 * HN;   // this warp's: HN key factors,
+        float* kfac = reinterpret_cast<float*>(base + L::F0) + (warp - 2) * 4 * HN;   // this warp's: HN key factors,
         float* vlog = kfac + HN;                          // log2 value scales, and the scales' inverses
         float* vinv = vlog + HN;
+        float* vraw = vinv + HN;
         constexpr int CH = HN / 32;                       // 32 scores at a time
         bool ok = true;
         while (next()) {
@@ -493,10 +494,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < KL; ++x) {
-                        const float lv = lg2(fmaxf_nan(vsn[x], 7.7e-34f));
+                        const float lv = lg2(fmaxf_nan(vsn[x], AC_VS_TINY));
                         kfac[32 * x + lane] = ksn[x];
                         vlog[32 * x + lane] = lv;
                         vinv[32 * x + lane] = ex2_ftz(-lv);
+                        vraw[32 * x + lane] = lg2(fmaxf_nan(vsn[x], AC_VS_FLOOR));
                         wide |= !(fabsf(lv) <= 60.0f);
                     }
                     wide = __any_sync(0xffffffffu, wide);
@@ -507,14 +509,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 ok = __all_sync(0xffffffffu, ok && at_wait(bars + L::ID + 2 * i % NI, (2 * i / NI) & 1, abort, a.wait_ns));
                 // 32 scores: raw for a bf16 cache (their factor is positive), else y = x + log2 of the value's scale
                 float xs[KEEP][32];
-                auto scores = [&](int ch, float (&x)[32]) {
+                auto scores = [&](int ch, float (&x)[32], const float* vs) {
                     t5::ld32(sbuf + 32 * ch, x);
                     if constexpr (Q8) {
                         const F2 f = f2(factor, factor);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 k4 = *reinterpret_cast<const float4*>(kfac + 32 * ch + c);
-                            const float4 v4 = *reinterpret_cast<const float4*>(vlog + 32 * ch + c);
+                            const float4 v4 = *reinterpret_cast<const float4*>(vs + 32 * ch + c);
                             f2_split(f2_fma(f2(x[c], x[c + 1]), f2_mul(f, f2(k4.x, k4.y)), f2(v4.x, v4.y)), x[c], x[c + 1]);
                             f2_split(f2_fma(f2(x[c + 2], x[c + 3]), f2_mul(f, f2(k4.z, k4.w)), f2(v4.z, v4.w)), x[c + 2], x[c + 3]);
                         }
@@ -533,7 +535,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch) {
                         float(&x)[32] = xs[KEEP == CH ? ch : 0];
-                        scores(ch, x);
+                        scores(ch, x, vlog);
                         float b0 = fmaxf(x[0], x[1]), b1 = fmaxf(x[2], x[3]);
 #pragma unroll
                         for (int c = 4; c < 32; c += 4) {
@@ -582,7 +584,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
                         for (int ch = 0; ch < CH; ++ch) {
                             float(&x)[32] = xs[KEEP == CH ? ch : 0];
-                            if (KEEP < CH) scores(ch, x);
+                            if (KEEP < CH) scores(ch, x, far ? vraw : vlog);
                             uint32_t pk[16];
 #pragma unroll
                             for (int c = 0; c < 32; c += 2) {
@@ -590,7 +592,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                                 f2_split(Q8 ? f2_add(f2(x[c], x[c + 1]), nm) : f2_fma(f2(x[c], x[c + 1]), ff, nm), y0, y1);
                                 const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
                                 if constexpr (Q8 && far) {
-                                    const float2 lv = *reinterpret_cast<const float2*>(vlog + 32 * ch + c);
+                                    const float2 lv = *reinterpret_cast<const float2*>(vraw + 32 * ch + c);
                                     float e0, e1;
                                     f2_split(f2_sub(f2(y0, y1), f2(lv.x, lv.y)), e0, e1);
                                     e0 = ex2_ftz(e0);

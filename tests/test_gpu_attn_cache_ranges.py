@@ -76,3 +76,70 @@ def test_scales_of_every_key_reach_their_own_scores(L, kind, d, nq):
     _check(c, o, scores=8 * 3e-4)          # keys up to 2^3 times as large: their scores' errors too
     assert torch.equal(o, c.run(L))
     sync(L)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq", [FEW, MANY])
+@pytest.mark.parametrize("zeros,n,hkv", [(256, 1300, 1), (2048, 2500, 1), (20000, 20700, 1), (2048, 2300, 160), (300, 300, 2)])
+def test_values_of_zero_ahead_of_others(L, kind, nq, zeros, n, hkv):
+    """Tokens whose values (and keys) are zero, more than a tile of them, ahead of ordinary ones: within one piece of a
+    run (160 heads: a run takes whole pairs) and over many runs."""
+    c = Case(kind, 64, 64, hkv, 1, [n], [nq], seed=zeros + nq)
+    k, v = (c.rng.standard_normal((n, hkv, 64)) for _ in "kv")
+    k[:zeros] = v[:zeros] = 0.0
+    _store(c, 0, _bf16(k), _bf16(v + 0.5 * (v != 0)))
+    o = c.run(L)
+    sync(L)
+    _check(c, o)
+    assert bool(o.any()) == (n > zeros)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq", [FEW, MANY])
+@pytest.mark.parametrize("score", [25.0, 45.0])
+@pytest.mark.parametrize("where", ["first", "amid", "last"])
+def test_values_of_zero_that_score_above_all_others(L, kind, nq, score, where):
+    """Tokens whose values are zero and whose scores are 25 and 45 above the others': the sum is theirs, the result is what
+    little the others have of it."""
+    n, zeros, d = 2600, 1000, 64
+    c = Case(kind, d, 64, 1, 1, [n], [nq], seed=int(score))
+    k, v = (c.rng.standard_normal((n, 1, d)) for _ in "kv")
+    k[..., 0] = 0.0                          # the first element carries the difference alone
+    at = {"first": 0, "amid": 777, "last": n - nq - zeros}[where]
+    k[at:at + zeros], v[at:at + zeros] = 0.0, 0.0
+    k[at:at + zeros, 0, 0] = score * d ** 0.5
+    c.q[..., 0] = 1.0
+    _store(c, 0, _bf16(k), _bf16(v))
+    o = c.run(L)
+    sync(L)
+    _check(c, o)
+    assert bool(o.any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq", [FEW, MANY])
+def test_rows_of_every_size(L, kind, d, nq):
+    """Values from 1e-30 to 1e30 in one sequence, small ones alone, and every value near 2^-100."""
+    n = 400
+    c = Case(kind, d, 16, 1, 2, [n], [nq], seed=19)
+    x = c.rng.standard_normal((n, 1, d))
+    v = x * 10.0 ** c.rng.integers(-30, 30, (n, 1, 1))
+    v[5], v[11] = 0, 1e-38
+    for y in (v, v * 1e-36, x * 2.0 ** 60, x * 2.0 ** -60, x * 2.0 ** -70):
+        _store(c, 0, v=_bf16(y))
+        o = c.run(L)
+        sync(L)
+        _check(c, o)
+    # a scale below 2^-80 counts as that for the running maximum: at 2^-85 the largest product may be 2^-14 of what it is
+    # otherwise (amax / 448 > 2^-94), at 2^-100 2^-29
+    _store(c, 0, v=_bf16(x * 2.0 ** -85))
+    o = c.run(L)
+    sync(L)
+    _check(c, o, lost=2.0 ** -22)
+    _store(c, 0, v=_bf16(x * 2.0 ** -100))
+    o = c.run(L)
+    sync(L)
+    # (the kernel for few rows multiplies what fp16 loses in bf16)
+    _check(c, o, lost=2.0 ** -36 if nq == FEW else 2.0 ** -7, weights=2.0 ** -8)
+    assert bool(o.any())
