@@ -27,6 +27,9 @@ constexpr float AC_LIFT = 11.0f;        // fp16 probabilities times 2^11
 // been seen m is as low as x - 80: up to 2^(4 + 11 + 80), which 2^30 keys do not
 // bring past fp32.  AC_VS_FLOOR keeps the logarithm of a scale of 0 finite.
 constexpr float AC_VS_MIN = -80.0f, AC_VS_TINY = 0x1p-80f, AC_VS_FLOOR = 1e-44f;
+// The least exponent of a row of q that its power of two still lifts to 2^14: 2^(14 +
+// 112) and its inverse are normal numbers, and so are 2^(14 - 127) and its inverse.
+constexpr int AC_Q_MIN = -112;
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct AttCacheArgs {

@@ -323,8 +323,8 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 for (int e = 0; e < QE / 2; ++e)
                     amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qw[x][e] << 16)), fabsf(__uint_as_float(qw[x][e] & 0xffff0000u))));
                 amax = warp_max(amax);
-                // 2^e with amax 2^e in [2^14, 2^15): exact both ways within the exponents that keep 2^e finite
-                const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
+                // 2^e with amax 2^e in [2^14, 2^15): exact both ways (below 2^AC_Q_MIN 2^e is that of 2^AC_Q_MIN)
+                const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, AC_Q_MIN), 127);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                 factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
 #pragma unroll

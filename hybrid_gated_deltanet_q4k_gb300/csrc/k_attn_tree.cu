@@ -416,7 +416,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     lsum[half * AT_ROWS + r] = amax;
                     at_bar_softmax();
                     amax = fmaxf(amax, lsum[(half ^ 1) * AT_ROWS + r]);
-                    const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, -100), 100);
+                    const int ex = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255) - 127, AC_Q_MIN), 127);
                     up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
                     factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
                 }

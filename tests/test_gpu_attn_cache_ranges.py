@@ -143,3 +143,18 @@ def test_rows_of_every_size(L, kind, d, nq):
     # (the kernel for few rows multiplies what fp16 loses in bf16)
     _check(c, o, lost=2.0 ** -36 if nq == FEW else 2.0 ** -7, weights=2.0 ** -8)
     assert bool(o.any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq", [FEW, MANY])
+@pytest.mark.parametrize("power", [-118, -60, 60, 110, 118])
+def test_queries_of_every_size(L, kind, nq, power):
+    """Queries of 2^power over keys of 2^-power: the scores are those of ordinary rows."""
+    c = Case(kind, 128, 32, 2, 2, [300], [nq], seed=20)
+    plain = c.q.clone()
+    k = c.rng.standard_normal((300, 2, 128))
+    _store(c, 0, k=_bf16(k * 2.0 ** -power))
+    c.q = (plain.double() * 2.0 ** power).to(torch.bfloat16)
+    o = c.run(L)
+    sync(L)
+    _check(c, o)
