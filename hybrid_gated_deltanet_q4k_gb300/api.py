@@ -275,8 +275,9 @@ class KvCache:
 
     def write(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor | None = None, stream=None,
               check=True) -> int:
-        """Enqueue gdn_kv_write: rows of k and v (bf16 [n][n_kv_heads][head_dim]) into slots (int64); with
-        rows (int32), token t is row rows[t]: the accepted tokens of a drafted tree."""
+        """Enqueue gdn_kv_write: rows of k and v (bf16 [n][n_kv_heads][head_dim]) into slots (int64, no slot
+        twice, a negative one for a token that is not stored); with rows (int32), token t is row rows[t]: the
+        accepted tokens of a drafted tree."""
         ld_k, ld_v = _heads(k, "k", self._device, self._width), _heads(v, "v", self._device, self._width)
         n = slots.numel()
         _vector(slots, torch.int64, n, "slots", self._device)

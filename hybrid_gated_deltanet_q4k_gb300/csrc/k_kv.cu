@@ -146,7 +146,8 @@ __device__ __forceinline__ void e4m3_pair(uint32_t w, float& lo, float& hi) {
 }
 
 // D/16 threads per row, each sixteen of its elements; blockIdx.y is the side
-// (keys or values).  A thread takes KV_ITER rows a block's width apart, all
+// (keys or values).  Nothing orders two rows of one slot, which the contract
+// excludes: one winner would take a word per slot and two more launches.  A thread takes KV_ITER rows a block's width apart, all
 // indices before the first row's load, all loads before the first use.  The
 // block's first token is divided out once; from there a row is a small number
 // (under 256 heads + 256 rows), whose product with heads_inv has the quotient in

@@ -443,7 +443,9 @@ typedef struct gdn_kv_cache {
  *   rows    device int32 [n_tokens] or NULL: token t is row rows[t] (NULL: row
  *           t; n_tokens <= n_rows)
  *   slots   device int64 [n_tokens]: where token t goes; negative: nowhere.
- *           Slots given twice hold one of the tokens.
+ *           The slots of a call that are not negative must differ: nothing
+ *           orders the writers, so a slot given twice may hold pieces of
+ *           several tokens (and every other slot what it should).
  * A row outside [0, n_rows) or a slot past the cache is skipped and reported
  * as GDN_EINDEX by gdn_sync_status.  n_tokens = 0 does nothing.
  */

@@ -112,3 +112,13 @@ def test_slots_inside_the_pages(first, n):
     pages = torch.tensor([7, 2, -1, 0, 9], dtype=torch.int32)
     want = [int(pages[t // 16]) * 16 + t % 16 for t in range(first, first + n)]
     assert c.slots(pages, first, n).tolist() == want and c.slots(pages, first, n).dtype is torch.int64
+
+
+def test_the_contract_asks_for_distinct_slots():
+    """Nothing orders two writers of one slot, so no text may promise that one of them wins."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    header = " ".join(open(os.path.join(root, "include", "gdn.h")).read().replace(" * ", " ").split())
+    assert "hold one of the tokens" not in header
+    assert "The slots of a call that are not negative must differ" in header
+    assert "no slot twice" in " ".join(api.KvCache.write.__doc__.split())
