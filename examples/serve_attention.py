@@ -81,6 +81,11 @@ def difference(a, b):
     return float((a - b).norm() / b.norm())
 
 
+def worse(a, b):
+    """The larger difference; one that is no number stays (max() would drop it)."""
+    return a if b <= a or a != a else b
+
+
 def serve(kind="e4m3", prompts=(1000, 77, 333), rounds=3, nodes=12, extension=40, seed=0, **layer):
     """Relative differences: of accepted tokens against single decoding, and of the extension."""
     rng = np.random.default_rng(seed)
@@ -119,7 +124,7 @@ def serve(kind="e4m3", prompts=(1000, 77, 333), rounds=3, nodes=12, extension=40
                 q1, k1, v1 = lay.project(ids[s][r:r + 1], [lens[s] + j])
                 lay.cache.write(k1, v1, lay.cache.slots(check[s], lens[s] + j, 1))
                 one = lay.attend(q1, [lens[s] + j + 1], check[s:s + 1])
-                worst_tree = max(worst_tree, difference(o[int(cu[s]) + r], one[0]))
+                worst_tree = worse(worst_tree, difference(o[int(cu[s]) + r], one[0]))
             lens[s] += len(path)
 
     # the first sequence comes back from the cache and is extended
