@@ -86,8 +86,9 @@ def worse(a, b):
     return a if b <= a or a != a else b
 
 
-def serve(kind="e4m3", prompts=(1000, 77, 333), rounds=3, nodes=12, extension=40, seed=0, **layer):
-    """Relative differences: of accepted tokens against single decoding, and of the extension."""
+def serve(kind="e4m3", prompts=(1000, 77, 333), rounds=3, nodes=12, extension=40, seed=0, least=1, **layer):
+    """Relative differences: of accepted tokens against single decoding, and of the extension.  Trees have from
+    ``least`` to ``nodes`` tokens."""
     rng = np.random.default_rng(seed)
     page = layer.get("page", 64)
     blocks = -(-(max(prompts) + rounds * nodes + extension + nodes) // page)
@@ -106,7 +107,7 @@ def serve(kind="e4m3", prompts=(1000, 77, 333), rounds=3, nodes=12, extension=40
 
     worst_tree = 0.0
     for _ in range(rounds):
-        trees = [draft(rng, int(rng.integers(1, nodes + 1))) for _ in lens]
+        trees = [draft(rng, int(rng.integers(least, nodes + 1))) for _ in lens]
         ids = [rng.integers(0, vocab, len(t[0])) for t in trees]
         cu = np.concatenate([[0], np.cumsum([len(i) for i in ids])])
         q, k, v = lay.project(np.concatenate(ids), np.concatenate([n + t[1] for n, t in zip(lens, trees)]))
