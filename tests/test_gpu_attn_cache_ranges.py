@@ -158,3 +158,52 @@ def test_queries_of_every_size(L, kind, nq, power):
     o = c.run(L)
     sync(L)
     _check(c, o)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,n,nq", [(64, 900, 50), (128, 2100, 64), (256, 1300, 41)])
+def test_peaked_rows_of_many_tokens(L, kind, d, n, nq):
+    """The running maximum rises often, by more than its margin, and the accumulator is scaled again each time."""
+    c = Case(kind, d, 32, 1, 4, [n], [nq], tree=_tree(np.random.default_rng(5), [nq]), seed=21, gain=30.0)
+    k = c.rng.standard_normal((n, 1, d)) * np.linspace(0.2, 1.0, n)[:, None, None]      # later keys count for more
+    _store(c, 0, k=_bf16(k))
+    o = c.run(L)
+    sync(L)
+    _check(c, o, scores=1e-2)              # scores up to some hundreds: their fp32 error is 2e-5 of them
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,ratio,hkv,n", [(1, 8, 16, 40000), (4, 4, 8, 9001), (64, 2, 1, 40000), (64, 2, 1, 16500)])
+def test_every_key_counts_once(L, kind, nq, ratio, hkv, n):
+    """Each row has two keys that take all of its weight, one of them at or beside a border of blocks and runs: a tile
+    that is left out, or counted twice, changes the row by a sixth of the values or more."""
+    d = 128
+    rows = nq * ratio                       # of a key/value head; row r looks along its own axis r % 128
+    assert rows <= d
+    c = Case(kind, d, 64, hkv, ratio, [n], [nq], tree=[1 << i for i in range(nq)], seed=22)
+    ctx = n - nq
+    edges = np.unique(np.clip(np.concatenate([np.arange(0, n, 128) + e for e in (-1, 0, 1, 15, 16, 63, 64)]), 0, ctx - 2))
+    places = c.rng.permutation(edges)[:hkv * rows].reshape(hkv, -1) if len(edges) >= hkv * rows else None
+    assert places is not None
+    other = ctx - 1                          # the second key of every row
+    k = np.zeros((n, hkv, d))
+    k[other] = 64.0
+    for h in range(hkv):
+        for r in range(rows):
+            k[places[h, r], h, r] += 64.0
+    v = c.rng.choice([-1.0, 1.0], size=(n, hkv, d)) * c.rng.uniform(0.5, 1.0, (n, hkv, d))
+    q = np.zeros((nq, hkv * ratio, d), np.float32)
+    for h in range(hkv):
+        for r in range(rows):
+            q[r // ratio, h * ratio + r % ratio, r] = 8.0      # a score of 8 * 64 / sqrt(128) = 45; the others 0
+    _store(c, 0, _bf16(k), _bf16(v))
+    c.q = _bf16(q)
+    o = c.run(L)
+    sync(L)
+    got = o.double().cpu().numpy()
+    for h in range(hkv):
+        for r in range(rows):
+            want = (c.v[0][places[h, r], h] + c.v[0][other, h]) / 2
+            err = np.abs(got[r // ratio, h * ratio + r % ratio] - want)
+            # the rest: 40000 e^-45 of weight; the output's and the probabilities' rounding
+            assert np.all(err <= 2.0 ** -8 * np.abs(want) + 2.0 ** -8), (h, r, places[h, r], err.max())
