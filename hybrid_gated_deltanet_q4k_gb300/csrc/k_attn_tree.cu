@@ -180,11 +180,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         *abort = 0;
         *odd = 0;
     }
-    if (warp == 1) t5::alloc(tslot, 512);
+    // TMEM is taken when the kernel before this one is through, and the next one may start when it is taken: a CTA that
+    // held it while it waited could keep it from the kernel it waits for
     pdl_wait();
-    pdl_trigger();
+    if (warp == 1) t5::alloc(tslot, 512);
     t5::fence_before();
     ac_prefix(a, pre, seq, reinterpret_cast<int64_t*>(base + L::W0), blockIdx.x == 0);   // ends with a barrier
+    pdl_trigger();
     t5::fence_after();
     const uint32_t tmem = *tslot;
     const int run = blockIdx.x / a.ranks, row0 = (blockIdx.x % a.ranks) * AT_ROWS;
