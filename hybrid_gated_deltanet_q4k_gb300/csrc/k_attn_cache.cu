@@ -40,14 +40,17 @@
 // p' - fp16(p') in bf16, whose exponents reach as far as fp32's, in a second
 // pass, and leaves out the first where fp16 holds nothing.  q goes to fp16 times
 // a power of two per row that puts its largest element in [2^14, 2^15): elements
-// below 2^-38 of it are lost.
+// below 2^-38 of it are lost.  A scale counts as 2^-80 at least where the maximum
+// is raised (AC_VS_MIN).
 //
 // Measured (us; bytes of the cache over the time): one token over 131072 int8
 // keys, 16 over 4 heads of 256: 54, 5.0 TB/s, of which the join is 5; 48
-// sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by memory; 16 chains of up to four tokens over 300 to 12000 int8 keys, 32 over 8
-// heads of 128: 65, 3.0 TB/s, bound by the 16 rows' conversions and products (one
-// token each, eight rows: 48).  777 bf16 keys of one sequence: 9, the latencies of
-// two kernels.
+// sequences of 1 to 16384 e4m3 keys: 134, 6.0 TB/s, bound by memory; 16 chains of
+// up to four tokens over 300 to 12000 int8 keys, 32 over 8 heads of 128: 66, 3.0
+// TB/s, where nothing is saturated (issue slots 43 %, tensor pipe 20 %): 16 rows'
+// accumulators leave registers for two warps a scheduler, too few for the latency
+// of loads, conversions and products in turn (one token each, eight rows: 48).
+// 777 bf16 keys of one sequence: 10, the latencies of two kernels.
 #include "attn_cache.cuh"
 
 #include <algorithm>
@@ -878,10 +881,13 @@ cudaError_t launch_attn_tree(const gdn_kv_cache& c, AttCacheArgs& a, cudaStream_
 constexpr int AC_TREE_TILE = 128;       // its rows per CTA
 
 // The kernel for many rows from this many rows of a pair on (max_q times the
-// heads of a key/value head).  Six sequences of 4000 to 24000 keys, this kernel
-// and the other, us, heads of 256 / 128 / 64: 32 rows bf16 80 and 82 / 99 and 86
-// / 56 and 59, int8 80 and 106 / 92 and 154 / 57 and 109; 48 rows bf16 112 and 86
-// / 174 and 92 / 93 and 59, int8 111 and 108 / 163 and 153 / 94 and 110.  Up to 32
+// heads of a key/value head), for every type and head size.  Six sequences of
+// 4000 to 24000 keys, this kernel and the other, us, heads of 256 / 128 / 64: 32
+// rows bf16 81 and 82 / 99 and 90 / 57 and 59, int8 81 and 104 / 93 and 150 / 57
+// and 110, e4m3 93 and 109 / 125 and 152 / 85 and 110; 48 rows bf16 113 and 86 /
+// 173 and 92 / 93 and 59, int8 113 and 107 / 163 and 149 / 92 and 112, e4m3 131
+// and 111 / 226 and 152 / 142 and 112.  So one threshold costs bf16 heads of 128 a
+// tenth from 20 to 32 rows and int8 heads of 64 a fifth from 33 to 64.  Up to 32
 // rows this kernel reads the cache once (twice for heads of 256), the other up to
 // 128.
 constexpr int AC_TREE_ROWS = 33;

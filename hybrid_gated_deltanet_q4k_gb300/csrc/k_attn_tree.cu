@@ -26,7 +26,9 @@
 // (exact); the row scales stay out of the products, as in the other kernel: a
 // key's multiplies its scores, a value's goes into the exponent of p'.  fp16
 // probabilities are p' 2^11, exact to 2^-11 down to 2^-25 of the largest and
-// zero below 2^-36 of it.
+// zero below 2^-36 of it.  The scales' logarithms are held twice: at least -80
+// (AC_VS_MIN) for the maximum, and as they are for the probabilities where a tile
+// has one far from 1.
 //
 // Warps: 0 copies, 1 allocates TMEM and issues the products, 2-9 softmax, and
 // for 8-bit caches 10-13 convert.  Every wait is bounded; after one runs out the
@@ -34,11 +36,13 @@
 // word set.
 //
 // Measured: six trees of 28 to 63 tokens over 11674 to 24000 keys, 16 over 4
-// heads of 256: bf16 139 us (585 TFLOP/s, 3.3 TB/s of cache), int8 222.  S, the
-// softmax and P V of a tile of heads of 256 follow each other, because TMEM holds
-// one S beside Q and O: of a tile's 4400 cycles the softmax waits 2800 for S.
-// 8-bit tiles are bound by the conversion of the codes, which shares its issue
-// slots with the softmax.  A piece's start and end
+// heads of 256: bf16 139 us (585 TFLOP/s, 3.3 TB/s of cache), int8 222, e4m3 224.
+// S, the softmax and P V of a tile of heads of 256 follow each other, because TMEM
+// holds one S beside Q and O: of a tile's 4400 cycles the softmax waits 2800 for S
+// (tensor pipe 41 %, issue slots 19 %).  8-bit tiles of heads of 256 add the
+// conversion to that chain, for shared memory holds two images; those of 128 and
+// 64 (32 over 8 heads: 250 and 193) wait for their four converting warps, one a
+// scheduler (tensor pipe 18 and 11 %, issue slots 48 %).  A piece's start and end
 // take 8 us of the 139, the join 9.
 #include "attn_cache.cuh"
 #include "tcgen05.cuh"

@@ -385,7 +385,8 @@ int gdn_attn_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, in
  * where g = clamp((r - slow) / (fast - slow), 0, 1) and r = orig_len f_i / 2 pi
  * is the number of turns pair i makes over the original context (the
  * published "NTK by parts" interpolation, whose usual bounds are slow = 1,
- * fast = 32).  amp multiplies both outputs; 0 means 1, and for GDN_ROPE_PARTS
+ * fast = 32; its ramp is linear in the turns r, not in the pair index i, as
+ * checkpoints with a ramp over the index want it).  amp multiplies both outputs; 0 means 1, and for GDN_ROPE_PARTS
  * the published 0.1 ln(factor) + 1.
  * step[i] = f_i / 2 pi as a fraction of 2^64, so pos * step[i] mod 2^64 is the
  * angle in turns, exactly reduced, for any 32-bit position.
@@ -488,8 +489,20 @@ int gdn_kv_read(const gdn_kv_cache *cache, const int64_t *slots, int64_t n_token
  * Nothing is read back to the host, so a captured graph may be replayed with
  * other lengths, pages and masks.  A length out of range is clamped to it, a
  * sequence whose offsets are out of range is left out, and the tokens of a
- * page outside the cache count as not seen; each is reported as GDN_EINDEX.  Scores, maxima, sums and the result are fp32 until the one
- * rounding to bf16.  1 <= n_seqs <= GDN_MAX_SEQS.
+ * page outside the cache count as not seen; each is reported as GDN_EINDEX.
+ * 1 <= n_seqs <= GDN_MAX_SEQS.
+ * Scores, maxima, sums and accumulators are fp32 and the result is rounded to
+ * bf16 once.  The probabilities enter the product with the values rounded to
+ * its operand type: bf16 over a bf16 cache (2^-8 of each at most), fp16 over
+ * codes (2^-11), there multiplied by the value row's scale.  Calls of up to 32
+ * rows (max_q times the query heads of a key/value head) multiply again in bf16
+ * what fp16 loses of such a product; calls of more rows round one below 2^-25
+ * of the row's largest to 2^-36 of it, which shows in elements that are zero in
+ * every row of more weight.  Over codes q is fp16 times a power of two: elements
+ * below 2^-38 of the row's largest are lost.  A value scale below 2^-80 counts as
+ * 2^-80 where the largest product is sought, and as it is elsewhere: where all of
+ * a sequence's scales are s < 2^-80, the 2^-25 and 2^-36 are 2^-80 / s times as
+ * large.
  */
 size_t gdn_attn_cache_workspace_size(const gdn_kv_cache *cache, int64_t n_tokens, int n_q_heads);
 int gdn_attn_cache(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, const int32_t *cu_q, int64_t n_tokens,
