@@ -150,18 +150,12 @@ class DeviceLayer:
                                          gl.stream_handle(stream), check=check)
 
 
-def _on_device(t: torch.Tensor, name: str, device: int):
-    if t.get_device() != device:      # -1: host memory, which a kernel must not be given
-        raise ValueError(f"{name}: a tensor on device cuda:{device} is required")
-
-
 def _heads(t: torch.Tensor, name: str, device: int, width=None) -> int:
-    """Elements between the tokens of a bf16 tensor [tokens][heads][head_dim] whose heads are contiguous (and
-    whose heads and head_dim are ``width``, if given)."""
+    """Elements between the tokens of a bf16 tensor [tokens][heads][head_dim] on ``device`` (-1: host memory, which
+    a kernel must not be given) whose heads are contiguous (and whose heads and head_dim are ``width``, if given)."""
     shape = t.shape
-    if t.dtype is not torch.bfloat16 or len(shape) != 3 or not t.is_cuda:
-        raise ValueError(f"{name}: a bf16 device tensor [tokens][heads][head_dim] is required")
-    _on_device(t, name, device)
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or device < 0 or t.get_device() != device:
+        raise ValueError(f"{name}: a bf16 tensor [tokens][heads][head_dim] on the device of the others is required")
     n, h, d = shape
     if width is not None and (h, d) != width:
         raise ValueError(f"{name}: [tokens][{width[0]}][{width[1]}] is required")
@@ -317,13 +311,12 @@ class KvCache:
             raise ValueError(f"q and o: [tokens][heads][{self.head_dim}] of one shape are required")
         s = lens.numel()
         _vector(lens, torch.int32, s, "lens", self._device)
-        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s or (
+        if block_table.dtype != torch.int32 or block_table.get_device() != self._device or block_table.dim() != 2 or \
+                block_table.shape[0] != s or (
                 block_table.shape[1] > 1 and block_table.stride(1) != 1) or (s > 1 and block_table.stride(0) < block_table.shape[1]):
-            raise ValueError(f"block_table: int32 [{s}][blocks] is required")
-        _on_device(block_table, "block_table", self._device)
-        _on_device(workspace, "workspace", self._device)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: contiguous memory is required")
+            raise ValueError(f"block_table: int32 [{s}][blocks] on the cache's device is required")
+        if workspace.get_device() != self._device or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous memory of the cache's device is required")
         if cu_q is not None:
             _vector(cu_q, torch.int32, s + 1, "cu_q", self._device)
         if tree is not None:
