@@ -209,7 +209,7 @@ def _inputs(case, seed):
         stack = np.full(n_pages, -1, np.int32)
         stack[:free] = order[at:at + free]
         st.update(lens=ints(lens), n_new=ints(n), table=ints(table), n_blocks=ints(had), stack=ints(stack), n_free=ints([free]),
-                  room=t + t // 7 + 3, pages=n_pages)
+                  room=t if case["tree"] else t + t // 7 + 3, pages=n_pages)
     return st
 
 
@@ -438,7 +438,7 @@ def _plain_plan(case, st):
     slot = table[seq, (pos // page).clamp(max=wide - 1)].long() * page + pos % page
     if st["tree"] is not None:
         depth = _depth(st)
-        pos = lens[seq] + torch.cat([depth, torch.zeros(st["room"] - st["total"], dtype=torch.long, device=DEV)])
+        pos = lens[seq] + depth
     live = tok < cu[-1]
     return {"lens": torch.where(got, lens + new, lens).to(torch.int32), "cu": cu.to(torch.int32),
             "positions": torch.where(live, pos, 0).to(torch.int32), "slots": torch.where(live & got[seq], slot, -1),
