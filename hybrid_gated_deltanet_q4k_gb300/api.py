@@ -1,5 +1,6 @@
-"""User-facing wrappers: a GDN layer resident on the GPU, prefilled through the C ABI, and the
-rotary table and paged key/value cache that serve the full-attention layers.
+"""User-facing wrappers: a GDN layer resident on the GPU, prefilled through the C ABI, the rotary
+table, the paged key/value cache and its pages that serve the full-attention layers, and the
+operators that decide drafted tokens.
 
 Weights are encoded to Q4_K on the host by the library's ``q4k_pack`` (or kept
 fp32 for an F32 layer) and uploaded once; ``prefill`` enqueues one
@@ -54,12 +55,19 @@ class DeviceLayer:
         for k in ("conv_w", "A_log", "dt_bias", "norm_w"):
             self.dev[k] = t(params[k].astype(np.float32))
         self.eps_l2, self.eps_rms = eps_l2, eps_rms
+        self._struct = None
         self.q_scale = spec.dk ** -0.5 if q_scale is None else q_scale
 
     def struct(self, gate_log_a=None, gate_b=None) -> gl.GdnLayer:
         L = gl.make_layer_struct(self.spec, self.dev, self.eps_l2, self.eps_rms, self.q_scale, gate_log_a, gate_b)
         L.q6k_mask = self.q6k_mask
         return L
+
+    def _ref(self):
+        """The layer's struct without drawn gates, made once."""
+        if self._struct is None:
+            self._struct = self.struct()
+        return ctypes.byref(self._struct)
 
     def workspace_bytes(self, ubatch_tokens: int) -> int:
         s = self.struct()
@@ -148,6 +156,95 @@ class DeviceLayer:
                                          gl.ptr(conv_state), gl.ptr(y), int(ckpt_every), gl.ptr(ckpt_state),
                                          gl.ptr(ckpt_conv), gl.ptr(workspace), workspace.numel(),
                                          gl.stream_handle(stream), check=check)
+
+    def _drafts(self, n_seqs: int, n_tokens: int, cu, max_new: int, tree, device: int):
+        """The common arguments of the calls over drafted tokens, checked."""
+        if device < 0:
+            raise ValueError("memory of a CUDA device is required")
+        if cu is not None:
+            _vector(cu, torch.int32, n_seqs + 1, "cu", device)
+        if tree is not None:
+            _vector(tree, torch.int64, n_tokens, "tree", device)
+        return gl.ptr(cu), n_tokens, max_new, gl.ptr(tree), n_seqs
+
+    def conv_tree(self, qkvz: torch.Tensor, ba: torch.Tensor | None, conv_state: torch.Tensor, qkv: torch.Tensor,
+                  log_a: torch.Tensor | None = None, b: torch.Tensor | None = None, cu: torch.Tensor | None = None, max_new: int = 1,
+                  tree: torch.Tensor | None = None, stream=None, check=True) -> int:
+        """Enqueue gdn_conv_tree: the conv over each sequence's drafted tokens.  qkvz bf16 [T][at least C_conv] and
+        ba fp32 [T][2 Hv] are the projection's rows, conv_state fp32 [n_seqs][C_conv][3] is only read; qkv fp16
+        [T][C_conv], log_a and b fp32 [T][Hv] are written.  cu int32 [n_seqs + 1] (None: max_new tokens each),
+        tree int64 [T] mask words (None: chains)."""
+        sp, dev, t = self.spec, conv_state.get_device(), qkvz.shape[0]
+        ld = _matrix(qkvz, torch.bfloat16, (t, sp.c_conv), "qkvz", dev, wider=True)
+        _block(conv_state, torch.float32, (conv_state.shape[0], sp.c_conv, 3), "conv_state", dev)
+        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
+        if ba is None or log_a is None or b is None:
+            raise ValueError("ba, log_a and b are required")
+        ld_ba = _matrix(ba, torch.float32, (t, 2 * sp.n_v_heads), "ba", dev, wider=True)
+        _block(log_a, torch.float32, (t, sp.n_v_heads), "log_a", dev)
+        _block(b, torch.float32, (t, sp.n_v_heads), "b", dev)
+        return self.lib.gdn_conv_tree(self._ref(), gl.ptr(qkvz), ld, gl.ptr(ba), ld_ba, gl.ptr(conv_state),
+                                      *self._drafts(conv_state.shape[0], t, cu, max_new, tree, dev), gl.ptr(qkv), gl.ptr(log_a),
+                                      gl.ptr(b), gl.stream_handle(stream), check=check)
+
+    def delta_tree(self, qkv: torch.Tensor, log_a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
+                   delta: torch.Tensor, cu: torch.Tensor | None = None, max_new: int = 1, tree: torch.Tensor | None = None, stream=None,
+                   check=True) -> int:
+        """Enqueue gdn_delta_tree: the delta rule over each sequence's drafted tokens from its held state fp32
+        [n_seqs][Hv][dv][dk], which stays.  qkv fp16 [T][C_conv], log_a and b fp32 [T][Hv] as conv_tree writes them;
+        o fp16 [T][Hv][dv] and delta fp32 [T][Hv][dv] (for delta_commit) are written."""
+        sp, dev, t = self.spec, state.get_device(), qkv.shape[0]
+        _block(state, torch.float32, (state.shape[0], sp.n_v_heads, sp.dv, sp.dk), "state", dev)
+        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
+        for name, x in (("log_a", log_a), ("b", b)):
+            _block(x, torch.float32, (t, sp.n_v_heads), name, dev)
+        for name, x, dtype in (("o", o, torch.float16), ("delta", delta, torch.float32)):
+            _block(x, dtype, (t, sp.n_v_heads, sp.dv), name, dev)
+        return self.lib.gdn_delta_tree(self._ref(), gl.ptr(qkv), gl.ptr(log_a), gl.ptr(b), gl.ptr(state),
+                                       *self._drafts(state.shape[0], t, cu, max_new, tree, dev), gl.ptr(o), gl.ptr(delta),
+                                       gl.stream_handle(stream), check=check)
+
+    def delta_commit(self, qkv: torch.Tensor, log_a: torch.Tensor, delta: torch.Tensor, node: torch.Tensor, state_in: torch.Tensor,
+                     state_out: torch.Tensor, qkvz: torch.Tensor | None = None, conv_in: torch.Tensor | None = None,
+                     conv_out: torch.Tensor | None = None, cu: torch.Tensor | None = None, max_new: int = 1,
+                     tree: torch.Tensor | None = None, stream=None, check=True) -> int:
+        """Enqueue gdn_delta_commit: the state (and, with qkvz, the conv state) after token node[s] (int32 [n_seqs], -1:
+        unchanged) of each sequence, from what conv_tree and delta_tree were given and left.  The outputs may be
+        the inputs."""
+        sp, dev, t, s = self.spec, state_in.get_device(), qkv.shape[0], state_in.shape[0]
+        for name, x in (("state_in", state_in), ("state_out", state_out)):
+            _block(x, torch.float32, (s, sp.n_v_heads, sp.dv, sp.dk), name, dev)
+        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
+        _block(log_a, torch.float32, (t, sp.n_v_heads), "log_a", dev)
+        _block(delta, torch.float32, (t, sp.n_v_heads, sp.dv), "delta", dev)
+        _vector(node, torch.int32, s, "node", dev)
+        ld = 0
+        if qkvz is not None:
+            ld = _matrix(qkvz, torch.bfloat16, (t, sp.c_conv), "qkvz", dev, wider=True)
+            if conv_in is None or conv_out is None:
+                raise ValueError("conv_in and conv_out are required with qkvz")
+            for name, x in (("conv_in", conv_in), ("conv_out", conv_out)):
+                _block(x, torch.float32, (s, sp.c_conv, 3), name, dev)
+        elif conv_in is not None or conv_out is not None:
+            raise ValueError("conv_in and conv_out need qkvz")
+        return self.lib.gdn_delta_commit(self._ref(), gl.ptr(qkv), gl.ptr(log_a), gl.ptr(delta),
+                                         *self._drafts(s, t, cu, max_new, tree, dev), gl.ptr(node), gl.ptr(state_in), gl.ptr(state_out),
+                                         gl.ptr(qkvz), ld, gl.ptr(conv_in), gl.ptr(conv_out), gl.stream_handle(stream), check=check)
+
+
+def _block(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: int):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on device cuda:{device} are required")
+
+
+def _matrix(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: int, wider: bool = False) -> int:
+    """Elements between the rows of a matrix (whose rows may have more columns, if ``wider``)."""
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != shape[0] or t.get_device() != device or device < 0 or (
+            t.shape[1] < shape[1] if wider else t.shape[1] != shape[1]):
+        raise ValueError(f"{name}: {dtype} {list(shape)} on device cuda:{device} are required")
+    if shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if shape[0] > 1 else t.shape[1]
 
 
 def _heads(t: torch.Tensor, name: str, device: int, width=None) -> int:
@@ -325,3 +422,86 @@ class KvCache:
         return self.lib.gdn_attn_cache(self._ref, gl.ptr(q), ld_q, gl.ptr(cu_q), n, max_q, gl.ptr(tree), gl.ptr(block_table),
                                        ld_table, block_table.shape[1], gl.ptr(lens), s, hq, scale, gl.ptr(o), ld_o, gl.ptr(workspace),
                                        workspace.numel(), gl.stream_handle(stream), check=check)
+
+
+class KvPages:
+    """The pages of a cache's sequences on the GPU: block table, pages held, and a stack of free ones.
+
+    block_table int32 [n_seqs][max_blocks], n_blocks int32 [n_seqs], free_pages int32 [n_pages] (the stack, its top at
+    n_free - 1), n_free int32 [1]; ``KvPages.new`` makes them with every page free."""
+
+    def __init__(self, page_tokens: int, block_table: torch.Tensor, n_blocks: torch.Tensor, free_pages: torch.Tensor,
+                 n_free: torch.Tensor, debug: bool = False):
+        self._device = block_table.get_device()
+        if block_table.dtype is not torch.int32 or block_table.dim() != 2 or self._device < 0:
+            raise ValueError("block_table: int32 [n_seqs][max_blocks] on a CUDA device is required")
+        self.n_seqs = block_table.shape[0]
+        ld = _matrix(block_table, torch.int32, tuple(block_table.shape), "block_table", self._device)
+        _vector(n_blocks, torch.int32, self.n_seqs, "n_blocks", self._device)
+        _vector(free_pages, torch.int32, free_pages.numel(), "free_pages", self._device)
+        _vector(n_free, torch.int32, 1, "n_free", self._device)
+        self.lib = gl.load(debug=debug)
+        self.page_tokens, self.block_table, self.n_blocks, self.free_pages, self.n_free = (page_tokens, block_table, n_blocks,
+                                                                                           free_pages, n_free)
+        self.struct = gl.GdnKvPages(page_tokens, block_table.shape[1], free_pages.numel(), gl.ptr(block_table), ld,
+                                    gl.ptr(n_blocks), gl.ptr(free_pages), gl.ptr(n_free))
+        self._ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def new(cls, n_seqs: int, max_blocks: int, n_pages: int, page_tokens: int, device: str = "cuda", debug: bool = False) -> "KvPages":
+        ints = lambda shape, x: torch.full(shape, x, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(page_tokens, ints((n_seqs, max_blocks), -1), ints((n_seqs,), 0),
+                   torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device), ints((1,), n_pages), debug=debug)
+
+    def extend(self, lens: torch.Tensor, n_new: torch.Tensor, lens_out: torch.Tensor, cu: torch.Tensor, positions: torch.Tensor,
+               slots: torch.Tensor, tree: torch.Tensor | None = None, stream=None, check=True) -> int:
+        """Enqueue gdn_kv_extend: pages for n_new int32 [n_seqs] tokens after the lens int32 [n_seqs] held ones; lens_out
+        (may be lens), cu int32 [n_seqs + 1], positions int32 [T] and slots int64 [T] are written, T at least the
+        number of new tokens.  A sequence that found no pages keeps its length and has slots -1."""
+        n, t = self.n_seqs, positions.numel()
+        for name, x, size in (("lens", lens, n), ("n_new", n_new, n), ("lens_out", lens_out, n), ("cu", cu, n + 1),
+                              ("positions", positions, t)):
+            _vector(x, torch.int32, size, name, self._device)
+        _vector(slots, torch.int64, t, "slots", self._device)
+        if tree is not None:
+            _vector(tree, torch.int64, t, "tree", self._device)
+        return self.lib.gdn_kv_extend(self._ref, gl.ptr(lens), gl.ptr(n_new), n, gl.ptr(tree), t, gl.ptr(lens_out),
+                                      gl.ptr(cu), gl.ptr(positions), gl.ptr(slots), gl.stream_handle(stream), check=check)
+
+    def trim(self, keep: torch.Tensor, stream=None, check=True) -> int:
+        """Enqueue gdn_kv_trim: the pages past the first keep int32 [n_seqs] tokens of each sequence become free."""
+        _vector(keep, torch.int32, self.n_seqs, "keep", self._device)
+        return self.lib.gdn_kv_trim(self._ref, gl.ptr(keep), self.n_seqs, gl.stream_handle(stream), check=check)
+
+
+def verify(p: torch.Tensor, tokens: torch.Tensor, rows: torch.Tensor, ids: torch.Tensor, count: torch.Tensor, node: torch.Tensor,
+           next: torch.Tensor, u: torch.Tensor | None = None, u_next: torch.Tensor | None = None, q: torch.Tensor | None = None,
+           cu: torch.Tensor | None = None, max_new: int = 1, tree: torch.Tensor | None = None, stream=None, check=True,
+           debug: bool = False) -> int:
+    """Enqueue gdn_verify: which drafted tokens stay.  p [T][vocab] (fp32 or bf16) the target's probabilities after each
+    token, q (the same type) the draft's or None, tokens int32 [T], u fp32 [T] and u_next fp32 [n_seqs] random numbers
+    in [0, 1); without them p holds scores and the largest is the choice.  rows and ids int32 [T], count, node and
+    next int32 [n_seqs] are written."""
+    dev, s = p.get_device(), count.numel()
+    if p.dtype not in (torch.float32, torch.bfloat16) or p.dim() != 2:
+        raise ValueError("p: fp32 or bf16 [tokens][vocab] is required")
+    t, vocab = p.shape
+    ld_p = _matrix(p, p.dtype, (t, vocab), "p", dev)
+    ld_q = 0 if q is None else _matrix(q, p.dtype, (t, vocab), "q", dev)
+    for name, x in (("tokens", tokens), ("rows", rows), ("ids", ids)):
+        _vector(x, torch.int32, t, name, dev)
+    for name, x in (("count", count), ("node", node), ("next", next)):
+        _vector(x, torch.int32, s, name, dev)
+    if (u is None) != (u_next is None):
+        raise ValueError("u and u_next: both or neither")
+    if u is not None:
+        _vector(u, torch.float32, t, "u", dev)
+        _vector(u_next, torch.float32, s, "u_next", dev)
+    if cu is not None:
+        _vector(cu, torch.int32, s + 1, "cu", dev)
+    if tree is not None:
+        _vector(tree, torch.int64, t, "tree", dev)
+    code = gl.GDN_P_F32 if p.dtype is torch.float32 else gl.GDN_P_BF16
+    return gl.load(debug=debug).gdn_verify(code, gl.ptr(p), ld_p, gl.ptr(q), ld_q, vocab, gl.ptr(tokens), gl.ptr(cu), t, max_new,
+                                           gl.ptr(tree), s, gl.ptr(u), gl.ptr(u_next), gl.ptr(rows), gl.ptr(ids), gl.ptr(count),
+                                           gl.ptr(node), gl.ptr(next), gl.stream_handle(stream), check=check)

@@ -26,7 +26,7 @@ DEBUG_DIR = os.path.join(OUT_DIR, "debug")
 DEBUG_LIB = os.path.join(OUT_DIR, "libgdn_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-CU_SOURCES = ["k_q4k.cu", "k_q6k.cu", "k_quant.cu", "k_gemm.cu", "k_conv.cu", "k_delta.cu", "k_norm.cu", "k_decode.cu", "k_attn.cu", "k_rope.cu", "k_kv.cu", "k_attn_cache.cu", "k_attn_tree.cu", "streams.cu", "gdn_api.cu"]
+CU_SOURCES = ["k_q4k.cu", "k_q6k.cu", "k_quant.cu", "k_gemm.cu", "k_conv.cu", "k_delta.cu", "k_norm.cu", "k_decode.cu", "k_attn.cu", "k_rope.cu", "k_kv.cu", "k_attn_cache.cu", "k_attn_tree.cu", "k_draft.cu", "k_verify.cu", "k_pages.cu", "streams.cu", "gdn_api.cu"]
 CPP_SOURCES = ["kquant_pack.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

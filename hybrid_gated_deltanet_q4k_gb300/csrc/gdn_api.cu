@@ -9,7 +9,7 @@
 // every unsupported input returns a negative status, and the workspace is
 // sized per ubatch of tokens: when it holds fewer than N tokens the call runs
 // in passes, each an exact extend of the previous one.
-#include "common.cuh"
+#include "drafts.cuh"
 #include "streams.h"
 
 #include <cmath>
@@ -68,6 +68,22 @@ cudaError_t launch_attn_cache(const gdn_kv_cache&, const uint16_t*, int64_t, con
                               const int32_t*, int64_t, int, const int32_t*, int, int, float, uint16_t*, int64_t, void*,
                               cudaStream_t, uint64_t);
 size_t attn_cache_workspace_bytes(const gdn_kv_cache&, int64_t, int);
+cudaError_t launch_conv_tree(const gdn_layer&, const DraftTokens&, const uint16_t*, int64_t, const float*, int64_t, const float*,
+                             uint16_t*, float*, float*, cudaStream_t);
+cudaError_t launch_delta_tree(const gdn_layer&, const DraftTokens&, const uint16_t*, const float*, const float*, const float*,
+                              uint16_t*, float*, cudaStream_t);
+cudaError_t launch_delta_commit(const gdn_layer&, const DraftTokens&, const uint16_t*, const float*, const float*, const int32_t*,
+                                const float*, float*, const uint16_t*, int64_t, const float*, float*, cudaStream_t);
+cudaError_t launch_verify(const DraftTokens&, bool, const void*, int64_t, const void*, int64_t, int64_t, const int32_t*, const float*,
+                          const float*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, cudaStream_t);
+cudaError_t launch_kv_extend(const gdn_kv_pages&, const int32_t*, const int32_t*, int, const uint64_t*, int64_t, int32_t*, int32_t*,
+                             int32_t*, int64_t*, cudaStream_t);
+cudaError_t launch_kv_trim(const gdn_kv_pages&, const int32_t*, int, cudaStream_t);
+int* draft_error_word();
+int* draft_skipped_word();
+int* verify_error_word();
+int* verify_skipped_word();
+int* pages_skipped_word();
 int* rope_error_word();
 int* kv_error_word();
 int* attn_cache_error_word();
@@ -120,7 +136,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 // The units' error words, and a kernel that takes them (an exchange each, so that
 // a code set meanwhile stays for the next call).
 struct ErrorWords {
-    static constexpr int N = 15;
+    static constexpr int N = 20;
     int* at[N];
 };
 __device__ int g_taken[ErrorWords::N];
@@ -1170,18 +1186,151 @@ int gdn_test_attn_cache_wait_timeout(const gdn_kv_cache* cache, const uint16_t* 
                            n_q_heads, scale, o, ld_o, workspace, ws_bytes, wait_ns, stream);
 }
 
+// The tokens of a call over drafted tokens.
+static int check_drafts(const char* who, const int32_t* cu, int64_t n_tokens, int max_new, const uint64_t* tree, int n_seqs,
+                        DraftTokens* d) {
+    if (n_seqs < 1 || n_seqs > GDN_MAX_SEQS)
+        return fail(GDN_EINVAL, "%s: 1 <= n_seqs <= %d required (got %d)", who, GDN_MAX_SEQS, n_seqs);
+    if (max_new < 1 || max_new > GDN_MAX_NEW)
+        return fail(GDN_EINVAL, "%s: 1 <= max_new <= %d required (got %d)", who, GDN_MAX_NEW, max_new);
+    const int64_t most = static_cast<int64_t>(n_seqs) * max_new;
+    if (n_tokens < 0 || n_tokens > most || (!cu && n_tokens != most))
+        return fail(GDN_EINVAL, "%s: n_tokens %lld of %d sequences of at most %d", who, (long long)n_tokens, n_seqs, max_new);
+    if (!aligned(cu, 4) || !aligned(tree, 8)) return fail(GDN_EINVAL, "%s: cu or tree misaligned", who);
+    *d = DraftTokens{cu, tree, static_cast<int>(n_tokens), max_new, n_seqs};
+    return GDN_OK;
+}
+
+int gdn_conv_tree(const gdn_layer* layer, const uint16_t* qkvz, int64_t ld_qkvz, const float* ba, int64_t ld_ba,
+                  const float* conv_state, const int32_t* cu, int64_t n_tokens, int max_new, const uint64_t* tree, int n_seqs,
+                  uint16_t* qkv, float* log_a, float* b, void* stream) {
+    Sizes s;
+    int r = check_layer(layer, &s);
+    DraftTokens d;
+    if (r || (r = check_drafts("gdn_conv_tree", cu, n_tokens, max_new, tree, n_seqs, &d))) return r;
+    if (n_tokens == 0) return GDN_OK;
+    if (!conv_state || !aligned(conv_state, 4)) return fail(GDN_EINVAL, "gdn_conv_tree: conv_state");
+    if (!rows_ok(qkvz, ld_qkvz, s.c_conv) || !aligned(qkvz, 8) || ld_qkvz % 4 || !qkv || !aligned(qkv, 16))
+        return fail(GDN_EINVAL, "gdn_conv_tree: qkvz of rows of at least %lld (a multiple of 4 apart, 8-byte aligned) and qkv (16-byte "
+                    "aligned) required", (long long)s.c_conv);
+    if (!layer->gate_log_a && (!ba || ld_ba < 2 * s.hv || !log_a || !b || !aligned(ba, 4) || !aligned(log_a, 4) || !aligned(b, 4)))
+        return fail(GDN_EINVAL, "gdn_conv_tree: ba, log_a and b");
+    GDN_LAUNCH(launch_conv_tree(*layer, d, qkvz, ld_qkvz, ba, ld_ba, conv_state, qkv, log_a, b, static_cast<cudaStream_t>(stream)),
+               "gdn_conv_tree");
+    return GDN_OK;
+}
+
+int gdn_delta_tree(const gdn_layer* layer, const uint16_t* qkv, const float* log_a, const float* b, const float* state,
+                   const int32_t* cu, int64_t n_tokens, int max_new, const uint64_t* tree, int n_seqs, uint16_t* o, float* delta,
+                   void* stream) {
+    Sizes s;
+    int r = check_layer(layer, &s);
+    DraftTokens d;
+    if (r || (r = check_drafts("gdn_delta_tree", cu, n_tokens, max_new, tree, n_seqs, &d))) return r;
+    if (n_tokens == 0) return GDN_OK;
+    if (!qkv || !log_a || !b || !state || !o || !delta) return fail(GDN_EINVAL, "gdn_delta_tree: NULL pointer");
+    if (!aligned(qkv, 16) || !aligned(state, 16) || !aligned(o, 16) || !aligned(delta, 16) || !aligned(log_a, 4) || !aligned(b, 4))
+        return fail(GDN_EINVAL, "gdn_delta_tree: qkv, state, o and delta 16-byte alignment required");
+    GDN_LAUNCH(launch_delta_tree(*layer, d, qkv, log_a, b, state, o, delta, static_cast<cudaStream_t>(stream)), "gdn_delta_tree");
+    return GDN_OK;
+}
+
+int gdn_delta_commit(const gdn_layer* layer, const uint16_t* qkv, const float* log_a, const float* delta, const int32_t* cu,
+                     int64_t n_tokens, int max_new, const uint64_t* tree, int n_seqs, const int32_t* node, const float* state_in,
+                     float* state_out, const uint16_t* qkvz, int64_t ld_qkvz, const float* conv_in, float* conv_out, void* stream) {
+    Sizes s;
+    int r = check_layer(layer, &s);
+    DraftTokens d;
+    if (r || (r = check_drafts("gdn_delta_commit", cu, n_tokens, max_new, tree, n_seqs, &d))) return r;
+    if (!node || !state_in || !state_out || !aligned(node, 4) || !aligned(state_in, 16) || !aligned(state_out, 16))
+        return fail(GDN_EINVAL, "gdn_delta_commit: node, state_in and state_out (16-byte aligned) required");
+    if (n_tokens && (!qkv || !log_a || !delta || !aligned(qkv, 16) || !aligned(delta, 16) || !aligned(log_a, 4)))
+        return fail(GDN_EINVAL, "gdn_delta_commit: qkv, log_a and delta (16-byte aligned) required");
+    if (qkvz && (!rows_ok(qkvz, ld_qkvz, s.c_conv) || !conv_in || !conv_out || !aligned(conv_in, 4) || !aligned(conv_out, 4)))
+        return fail(GDN_EINVAL, "gdn_delta_commit: qkvz rows of at least %lld and conv_in, conv_out required", (long long)s.c_conv);
+    if (!qkvz && (conv_in || conv_out)) return fail(GDN_EINVAL, "gdn_delta_commit: a conv state needs qkvz");
+    GDN_LAUNCH(launch_delta_commit(*layer, d, qkv, log_a, delta, node, state_in, state_out, qkvz, ld_qkvz, conv_in, conv_out,
+                                   static_cast<cudaStream_t>(stream)),
+               "gdn_delta_commit");
+    return GDN_OK;
+}
+
+int gdn_verify(int dtype, const void* p, int64_t ld_p, const void* q, int64_t ld_q, int64_t vocab, const int32_t* tokens,
+               const int32_t* cu, int64_t n_tokens, int max_new, const uint64_t* tree, int n_seqs, const float* u, const float* u_next,
+               int32_t* rows, int32_t* ids, int32_t* count, int32_t* node, int32_t* next, void* stream) {
+    DraftTokens d;
+    int r = check_drafts("gdn_verify", cu, n_tokens, max_new, tree, n_seqs, &d);
+    if (r) return r;
+    if (dtype != GDN_P_F32 && dtype != GDN_P_BF16) return fail(GDN_EINVAL, "gdn_verify: unknown dtype %d", dtype);
+    if (vocab < 1 || vocab >= 0x20000000) return fail(GDN_EINVAL, "gdn_verify: 1 <= vocab < 2^29 required (got %lld)", (long long)vocab);
+    if ((u == nullptr) != (u_next == nullptr)) return fail(GDN_EINVAL, "gdn_verify: u and u_next: both or neither");
+    if (!u && q) return fail(GDN_EINVAL, "gdn_verify: the greedy choice takes no q");
+    if (!count || !node || !next || !aligned(count, 4) || !aligned(node, 4) || !aligned(next, 4))
+        return fail(GDN_EINVAL, "gdn_verify: count, node and next required");
+    const size_t size = dtype == GDN_P_F32 ? 4 : 2;
+    if (n_tokens && (!p || !aligned(p, size) || ld_p < vocab || !aligned(q, size) || (q && ld_q < vocab)))
+        return fail(GDN_EINVAL, "gdn_verify: p and q rows of %lld required", (long long)vocab);
+    if (n_tokens && (!tokens || !rows || !ids || !aligned(tokens, 4) || !aligned(rows, 4) || !aligned(ids, 4) || !aligned(u, 4) || !aligned(u_next, 4)))
+        return fail(GDN_EINVAL, "gdn_verify: tokens, rows and ids required");
+    GDN_LAUNCH(launch_verify(d, dtype == GDN_P_BF16, p, ld_p, q, ld_q, vocab, tokens, u, u_next, rows, ids, count, node, next,
+                             static_cast<cudaStream_t>(stream)),
+               "gdn_verify");
+    return GDN_OK;
+}
+
+static int check_pages(const char* who, const gdn_kv_pages* p, int n_seqs) {
+    if (!p) return fail(GDN_EINVAL, "%s: pages is NULL", who);
+    if (n_seqs < 1 || n_seqs > GDN_MAX_SEQS)
+        return fail(GDN_EINVAL, "%s: 1 <= n_seqs <= %d required (got %d)", who, GDN_MAX_SEQS, n_seqs);
+    if (p->page_tokens != 16 && p->page_tokens != 32 && p->page_tokens != 64 && p->page_tokens != 128)
+        return fail(GDN_EINVAL, "%s: page_tokens must be 16, 32, 64 or 128 (got %d)", who, p->page_tokens);
+    if (p->max_blocks < 1 || p->max_blocks > (1 << 30) / p->page_tokens || p->ld_table < p->max_blocks)
+        return fail(GDN_EINVAL, "%s: max_blocks >= 1, max_blocks * page_tokens <= 2^30 and ld_table >= max_blocks required", who);
+    if (p->n_pages < 1 || p->n_pages > 0x7fffffff) return fail(GDN_EINVAL, "%s: 1 <= n_pages < 2^31 required", who);
+    if (!p->block_table || !p->n_blocks || !p->free_pages || !p->n_free || !aligned(p->block_table, 4) || !aligned(p->n_blocks, 4) ||
+        !aligned(p->free_pages, 4) || !aligned(p->n_free, 4))
+        return fail(GDN_EINVAL, "%s: block_table, n_blocks, free_pages and n_free required", who);
+    return GDN_OK;
+}
+
+int gdn_kv_extend(const gdn_kv_pages* pages, const int32_t* lens, const int32_t* n_new, int n_seqs, const uint64_t* tree,
+                  int64_t max_tokens, int32_t* lens_out, int32_t* cu, int32_t* positions, int64_t* slots, void* stream) {
+    int r = check_pages("gdn_kv_extend", pages, n_seqs);
+    if (r) return r;
+    if (max_tokens < 0 || max_tokens > 0x7fffffff) return fail(GDN_EINVAL, "gdn_kv_extend: 0 <= max_tokens < 2^31 required");
+    if (!lens || !n_new || !lens_out || !cu || !aligned(lens, 4) || !aligned(n_new, 4) || !aligned(lens_out, 4) || !aligned(cu, 4))
+        return fail(GDN_EINVAL, "gdn_kv_extend: lens, n_new, lens_out and cu required");
+    if (max_tokens && (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 8)))
+        return fail(GDN_EINVAL, "gdn_kv_extend: positions and slots required");
+    if (!aligned(tree, 8)) return fail(GDN_EINVAL, "gdn_kv_extend: tree misaligned");
+    GDN_LAUNCH(launch_kv_extend(*pages, lens, n_new, n_seqs, tree, max_tokens, lens_out, cu, positions, slots,
+                                static_cast<cudaStream_t>(stream)),
+               "gdn_kv_extend");
+    return GDN_OK;
+}
+
+int gdn_kv_trim(const gdn_kv_pages* pages, const int32_t* keep, int n_seqs, void* stream) {
+    int r = check_pages("gdn_kv_trim", pages, n_seqs);
+    if (r) return r;
+    if (!keep || !aligned(keep, 4)) return fail(GDN_EINVAL, "gdn_kv_trim: keep required");
+    GDN_LAUNCH(launch_kv_trim(*pages, keep, n_seqs, static_cast<cudaStream_t>(stream)), "gdn_kv_trim");
+    return GDN_OK;
+}
+
 int gdn_sync_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
     // every unit's error word is read and cleared, all in one go
-    enum { GEMM, ATTN, DELTA, DECODE, CONV, NORM, ROPE, Q4K, Q6K, QUANT, FEW, MANY, KV, FEW_SKIP, MANY_SKIP, N_WORDS };
+    enum { GEMM, ATTN, DELTA, DECODE, CONV, NORM, ROPE, Q4K, Q6K, QUANT, FEW, MANY, KV, FEW_SKIP, MANY_SKIP, DRAFT, DRAFT_SKIP, VERIFY, VERIFY_SKIP,
+           PAGES_SKIP, N_WORDS };
     static_assert(N_WORDS == ErrorWords::N);
     const ErrorWords at = {{gemm_error_word(), attn_error_word(), delta_error_word(), decode_error_word(), conv_error_word(),
                             norm_error_word(), rope_error_word(), q4k_error_word(), q6k_error_word(), quant_error_word(),
                             attn_cache_error_word(), attn_tree_error_word(), kv_error_word(), attn_cache_skipped_word(),
-                            attn_tree_skipped_word()}};
+                            attn_tree_skipped_word(), draft_error_word(), draft_skipped_word(), verify_error_word(),
+                            verify_skipped_word(), pages_skipped_word()}};
     int w[N_WORDS];
     e = read_and_clear(at, w);
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
@@ -1190,16 +1339,20 @@ int gdn_sync_status(void* stream) {
         const char* unit;
     } checks[] = {{Q4K, "Q4_K decode"}, {Q6K, "Q6_K decode"}, {QUANT, "activation quantisation"}, {GEMM, "projection"},
                   {CONV, "conv"}, {DELTA, "delta-rule"}, {NORM, "gated-norm"}, {DECODE, "decode-step"},
-                  {ATTN, "attention"}, {ROPE, "rotary"}, {FEW, "cache attention"}, {MANY, "cache attention"}};
+                  {ATTN, "attention"}, {ROPE, "rotary"}, {FEW, "cache attention"}, {MANY, "cache attention"},
+                  {DRAFT, "drafted tokens'"}, {VERIFY, "verification"}};
     // An index of the caller's that a kernel skipped comes last: beside a wait that ran out or a value out of range,
     // whose results are not valid, it is only named.
-    const bool kv = w[KV] != 0, attn = w[FEW_SKIP] || w[MANY_SKIP];
-    const char* skipped = kv && attn
-                              ? "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped; gdn_attn_cache: an offset, "
-                                "length or page out of range was skipped"
-                          : kv   ? "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped"
-                          : attn ? "gdn_attn_cache: an offset, length or page out of range was skipped"
-                                 : "";
+    std::string named;
+    const auto name = [&](bool set, const char* what) {
+        if (set) named += (named.empty() ? "" : "; ") + std::string(what);
+    };
+    name(w[KV] != 0, "gdn_kv_write or gdn_kv_read: a row or slot out of range was skipped");
+    name(w[FEW_SKIP] || w[MANY_SKIP], "gdn_attn_cache: an offset, length or page out of range was skipped");
+    name(w[DRAFT_SKIP] != 0, "gdn_conv_tree, gdn_delta_tree or gdn_delta_commit: an offset or node out of range was skipped");
+    name(w[VERIFY_SKIP] != 0, "gdn_verify: an offset or token out of range was skipped");
+    name(w[PAGES_SKIP] != 0, "gdn_kv_extend or gdn_kv_trim: a length, number or page out of range was skipped");
+    const char* skipped = named.c_str();
     const char* also = *skipped ? "; " : "";
     for (const auto& c : checks)
         if (w[c.word] == ERR_INDEX)
@@ -1215,6 +1368,8 @@ int gdn_sync_status(void* stream) {
     if (w[DECODE] == ERR_WAIT_TIMEOUT) return timeout("a decode-step");
     if (w[DECODE] == ERR_RANGE)
         return fail(GDN_ERANGE, "a decode-step output o exceeded the fp16 range (|x| > 65504)%s%s", also, skipped);
+    if (w[DRAFT] == ERR_RANGE)
+        return fail(GDN_ERANGE, "a q, k, v or o of drafted tokens exceeded the fp16 range (|x| > 65504)%s%s", also, skipped);
     if (w[CONV] == ERR_RANGE || w[DELTA] == ERR_RANGE)
         return fail(GDN_ERANGE, "a %s value exceeded the fp16 operand range (|x| > 65504)%s%s",
                     w[CONV] == ERR_RANGE ? "q, k or v" : "delta-rule intermediate (T, A T, S, R or Delta)", also, skipped);

@@ -25,6 +25,7 @@ GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_PARTS = 0, 1, 2
 GDN_ROPE_MAX_PAIRS = 128
 GDN_KV_BF16, GDN_KV_I8, GDN_KV_E4M3 = 0, 1, 2
 GDN_MAX_NEW = 64
+GDN_P_F32, GDN_P_BF16 = 0, 1
 GDN_NOALLOC_SCRATCH_BYTES = 48 << 20
 STAGE_NAMES = ["dequant", "act_quant", "in_proj", "conv", "delta_rule", "gated_norm", "out_proj"]
 
@@ -50,6 +51,12 @@ class GdnKvCache(ctypes.Structure):
     """Mirror of ``struct gdn_kv_cache``."""
     _fields_ = [("dtype", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_tokens", c_int32),
                 ("n_pages", c_int64), ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class GdnKvPages(ctypes.Structure):
+    """Mirror of ``struct gdn_kv_pages``."""
+    _fields_ = [("page_tokens", c_int32), ("max_blocks", c_int32), ("n_pages", c_int64), ("block_table", c_void_p),
+                ("ld_table", c_int64), ("n_blocks", c_void_p), ("free_pages", c_void_p), ("n_free", c_void_p)]
 
 
 _P = c_void_p
@@ -81,6 +88,13 @@ _SIGNATURES = {
                                  c_int64, _P, c_size_t, _P]),
     "gdn_test_attn_cache_wait_timeout": (c_int32, [_P, _P, c_int64, _P, c_int64, c_int32, _P, _P, c_int64, c_int32, _P, c_int32,
                                                    c_int32, c_float, _P, c_int64, _P, c_size_t, ctypes.c_uint64, _P]),
+    "gdn_conv_tree": (c_int32, [_P, _P, c_int64, _P, c_int64, _P, _P, c_int64, c_int32, _P, c_int32, _P, _P, _P, _P]),
+    "gdn_delta_tree": (c_int32, [_P, _P, _P, _P, _P, _P, c_int64, c_int32, _P, c_int32, _P, _P, _P]),
+    "gdn_delta_commit": (c_int32, [_P, _P, _P, _P, _P, c_int64, c_int32, _P, c_int32, _P, _P, _P, _P, c_int64, _P, _P, _P]),
+    "gdn_verify": (c_int32, [c_int32, _P, c_int64, _P, c_int64, c_int64, _P, _P, c_int64, c_int32, _P, c_int32, _P, _P, _P, _P, _P, _P,
+                             _P, _P]),
+    "gdn_kv_extend": (c_int32, [_P, _P, _P, c_int32, _P, c_int64, _P, _P, _P, _P, _P]),
+    "gdn_kv_trim": (c_int32, [_P, _P, c_int32, _P]),
     "gdn_sync_status": (c_int32, [_P]),
     "gdn_last_error": (ctypes.c_char_p, []),
     "gdn_set_stage_events": (c_int32, [ctypes.POINTER(c_void_p), c_int32]),

@@ -511,6 +511,173 @@ int gdn_attn_cache(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, c
                    void *stream);
 
 /*
+ * Drafted tokens of the hybrid model, decided on the device.  A step of
+ * several sequences, each with 1 to GDN_MAX_NEW new tokens (the last token that
+ * is certain and the drafts after it, a chain or a tree): gdn_kv_extend gives
+ * them pages, slots and positions; the full-attention layers run gdn_rope,
+ * gdn_kv_write and gdn_attn_cache; the GDN layers run gdn_conv_tree and
+ * gdn_delta_tree, which leave the held state as it is; gdn_verify decides which
+ * drafts stay; gdn_delta_commit moves the state to the last of them, and
+ * gdn_kv_trim gives the other pages back.  Nothing is read back to the host, so
+ * a captured graph of the step may be replayed.
+ *
+ * Shared by gdn_conv_tree, gdn_delta_tree, gdn_delta_commit and gdn_verify:
+ *   cu        device int32 [n_seqs + 1]: sequence s holds the token rows
+ *             [cu[s], cu[s+1]) of the n_tokens rows, at most max_new (it may be
+ *             empty); NULL: max_new each, n_tokens = n_seqs * max_new.  Rows
+ *             outside every sequence are neither read nor written.
+ *   tree      device uint64 [n_tokens] mask words as gdn_attn_cache takes them:
+ *             bit j < i of token i's word is set if token j of the sequence is
+ *             an ancestor of i (its other bits do not matter), so its parent
+ *             is its highest such bit; NULL: a chain.
+ *   1 <= n_seqs <= GDN_MAX_SEQS, 1 <= max_new <= GDN_MAX_NEW, n_tokens <=
+ *   n_seqs * max_new.  A sequence whose offsets are out of range counts as
+ *   empty and is reported as GDN_EINDEX by gdn_sync_status.
+ */
+
+/*
+ * gdn_conv_tree -- gdn_conv over drafted tokens: the conv's taps on a token are
+ * the token, its parent, grandparent and great-grandparent; before the
+ * sequence's first token, its conv state.
+ *   qkvz, ba   the projection's rows as in gdn_conv (ld_qkvz, ld_ba elements
+ *              between rows); ba NULL and log_a, b unused where the layer's
+ *              gates are drawn
+ *   conv_state fp32 [n_seqs][C_conv][3], read only
+ *   qkv        fp16 [n_tokens][C_conv]; log_a, b fp32 [n_tokens][Hv]
+ * fp32 arithmetic, one rounding to fp16; a value beyond fp16's range is
+ * reported as GDN_ERANGE.
+ */
+int gdn_conv_tree(const gdn_layer *layer, const uint16_t *qkvz, int64_t ld_qkvz, const float *ba, int64_t ld_ba,
+                  const float *conv_state, const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree,
+                  int n_seqs, uint16_t *qkv, float *log_a, float *b, void *stream);
+
+/*
+ * gdn_delta_tree -- gdn_delta_rule over drafted tokens.  With S the state along
+ * a token's path (its parent's; at the root the held one):
+ *     u = b (v - a S k),   S' = a S + u k^T,   o = S' q
+ *   qkv    fp16 [n_tokens][C_conv] (16-byte aligned); log_a, b fp32
+ *          [n_tokens][Hv]
+ *   state  fp32 [n_seqs][Hv][dv][dk] (16-byte aligned), read only
+ *   o      fp16 [n_tokens][C_v] (16-byte aligned)
+ *   delta  fp32 [n_tokens][Hv][dv] (16-byte aligned): u, for gdn_delta_commit
+ * In fp32 (products with the state from operands of 22 bits and more); o is
+ * rounded once, and a value of it beyond fp16's range is reported as
+ * GDN_ERANGE.  log_a = -inf (a = 0) is allowed.  A token depends on its ancestors
+ * alone, whatever the others hold.
+ */
+int gdn_delta_tree(const gdn_layer *layer, const uint16_t *qkv, const float *log_a, const float *b, const float *state,
+                   const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree, int n_seqs, uint16_t *o,
+                   float *delta, void *stream);
+
+/*
+ * gdn_delta_commit -- the state after token node[s] of each sequence.
+ *   qkv, log_a, cu, tree   of the gdn_delta_tree call, and delta as it left it
+ *   node        device int32 [n_seqs], the token's number within its sequence;
+ *               -1: the state stays.  One outside the sequence counts as -1 and
+ *               is reported as GDN_EINDEX.
+ *   state_in, state_out  fp32 [n_seqs][Hv][dv][dk] (16-byte aligned); may be the
+ *               same
+ *   qkvz        the rows of gdn_conv_tree, or NULL: no conv state
+ *   conv_in, conv_out    fp32 [n_seqs][C_conv][3], the conv state before and
+ *               after the token; may be the same
+ */
+int gdn_delta_commit(const gdn_layer *layer, const uint16_t *qkv, const float *log_a, const float *delta,
+                     const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree, int n_seqs,
+                     const int32_t *node, const float *state_in, float *state_out, const uint16_t *qkvz,
+                     int64_t ld_qkvz, const float *conv_in, float *conv_out, void *stream);
+
+/*
+ * gdn_verify -- which drafted tokens stay, and the token after them.  The first
+ * token of a sequence is certain.  At the last token that stays, c, its
+ * children are tried in order: child x is accepted with probability
+ * min(1, r(x) / q(x)), r = p to begin with, p and q the target's and the draft's
+ * probabilities after c (row c); on a rejection r becomes max(0, r - q) divided
+ * by its sum.  When no child is accepted the next token is drawn from r.  So
+ * the tokens follow the target's distribution if siblings are independent
+ * draws from q.  Without q the drafts are certain proposals (siblings differ):
+ * child x is accepted with probability r(x), and r loses x when it is rejected.
+ * Without u and u_next (both NULL) the choice is greedy: p holds scores, and a
+ * child is accepted if it is the row's largest (the lowest of equal ones).
+ *   dtype    GDN_P_F32 or GDN_P_BF16, of p and q
+ *   p, q     device [n_tokens][vocab], ld_p / ld_q elements between rows; q NULL:
+ *            certain drafts.  Probabilities: negative ones and NaN count as 0,
+ *            ones above 1 as 1, and a row's sum is to stay below 8.  Scores:
+ *            any; NaN is never the largest.
+ *   tokens   device int32 [n_tokens]; a draft outside [0, vocab) is rejected and
+ *            reported as GDN_EINDEX
+ *   u        device fp32 [n_tokens] in [0, 1): child x is accepted if
+ *            u_x q(x) < r(x); u_next [n_seqs]: the next token is the first whose
+ *            running sum of r passes u_next times the whole sum
+ *   rows     device int32 [n_tokens]: rows[cu[s] + d] is the token row (of all
+ *            n_tokens) of the d-th accepted token, as gdn_kv_write takes it, -1
+ *            past the last
+ *   ids      device int32 [n_tokens]: ids[cu[s] + d] is the token that follows
+ *            it: the count[s] new tokens of the sequence, -1 past them
+ *   count    device int32 [n_seqs]: accepted tokens, the first one among them
+ *   node     device int32 [n_seqs]: the last accepted one within its sequence
+ *   next     device int32 [n_seqs]: the token after it, ids' last
+ * An empty sequence has count 0, node and next -1.  Where nothing is left of r
+ * the next token is drawn from p; where p has nothing either it is -1.
+ * Comparisons are made in 64 bits: a product u q exactly, sums in multiples of
+ * 2^-60, so results do not depend on the order of summation.
+ * 1 <= vocab < 2^31 / 4.
+ */
+#define GDN_P_F32 0
+#define GDN_P_BF16 1
+int gdn_verify(int dtype, const void *p, int64_t ld_p, const void *q, int64_t ld_q, int64_t vocab, const int32_t *tokens,
+               const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree, int n_seqs, const float *u,
+               const float *u_next, int32_t *rows, int32_t *ids, int32_t *count, int32_t *node, int32_t *next,
+               void *stream);
+
+/*
+ * The pages of the sequences of a cache, kept on the device: the block table of
+ * gdn_attn_cache and a stack of free pages.  The memory is the caller's.
+ */
+typedef struct gdn_kv_pages {
+    int32_t page_tokens;  /* 16, 32, 64 or 128 */
+    int32_t max_blocks;   /* columns of the block table; max_blocks * page_tokens <= 2^30 */
+    int64_t n_pages;      /* of the cache, < 2^31 */
+    int32_t *block_table; /* [n_seqs] rows, ld_table apart */
+    int64_t ld_table;
+    int32_t *n_blocks;    /* [n_seqs]: pages each sequence holds */
+    int32_t *free_pages;  /* [n_pages]: the stack, its top at n_free - 1 */
+    int32_t *n_free;      /* [1] */
+} gdn_kv_pages;
+
+/*
+ * gdn_kv_extend -- pages, slots and positions of new tokens.  Sequence s holds
+ * lens[s] tokens and gets n_new[s] more; where its pages do not reach for them it
+ * takes pages from the top of the stack, sequences and blocks in order.  The
+ * first sequence for which the stack does not reach, and those after it that
+ * need a page, get none: their length stays and their tokens get slot -1.
+ *   lens, n_new  device int32 [n_seqs], not negative
+ *   tree         device uint64 [max_tokens] mask words, or NULL: a token's
+ *                position is lens[s] plus the number of its ancestors (NULL: of
+ *                the new tokens before it); only with n_new <= 64
+ *   max_tokens   rows of positions and slots; the new tokens of all sequences
+ *                come first, in order, and the rows behind them get position 0
+ *                and slot -1
+ *   lens_out     device int32 [n_seqs]: lens + n_new; may equal lens
+ *   cu           device int32 [n_seqs + 1]: offsets of the new tokens
+ *   positions    device int32 [max_tokens]; slots device int64 [max_tokens]
+ * 1 <= n_seqs <= GDN_MAX_SEQS, 0 <= max_tokens < 2^31.  Out of range and
+ * reported as GDN_EINDEX: negative numbers (taken as 0), n_blocks and n_free
+ * (held to their ranges), a sequence that would pass its row of the block table
+ * or max_tokens (it gets nothing; cu stays within max_tokens), a page outside
+ * the cache (its tokens get slot -1).
+ */
+int gdn_kv_extend(const gdn_kv_pages *pages, const int32_t *lens, const int32_t *n_new, int n_seqs, const uint64_t *tree,
+                  int64_t max_tokens, int32_t *lens_out, int32_t *cu, int32_t *positions, int64_t *slots, void *stream);
+
+/*
+ * gdn_kv_trim -- each sequence keeps the pages of its first keep[s] tokens (0:
+ * none); the others go back onto the stack, the first of them on top, so that a
+ * trim after an extension leaves the stack as it was.  What the block table
+ * holds past n_blocks means nothing.
+ */
+int gdn_kv_trim(const gdn_kv_pages *pages, const int32_t *keep, int n_seqs, void *stream);
+
+/*
  * gdn_test_attn_cache_wait_timeout -- gdn_attn_cache with the first copy of
  * every CTA never issued, so that the wait for it runs out after wait_ns
  * nanoseconds (1 us .. 100 ms).  The kernel records the timeout, waits (again
