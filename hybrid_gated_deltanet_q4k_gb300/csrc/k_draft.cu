@@ -146,95 +146,311 @@ struct DeltaTreeArgs {
 
 __device__ __forceinline__ float clamp_log_a(float la) { return la < LOG_A_MIN ? LOG_A_MIN : la; }
 
+// Sums of log a along paths of up to 64 tokens, whose differences enter an
+// exponential: two floats each, so a difference keeps fp32's relative accuracy
+// where the sums themselves are large.
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 sum2(Sum2 a, Sum2 b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Shared memory of delta_tree_kernel for np tokens (a multiple of 8) and a
+// number of warps: byte offsets.
+constexpr int DT_STAGE = 336;               // floats per warp, see the kernel
 template <int D>
 struct DeltaTreeSmem {
-    float k[GDN_MAX_NEW][D], q[GDN_MAX_NEW][D], u[GDN_MAX_NEW][D], o[GDN_MAX_NEW][D];
-    float kk[GDN_MAX_NEW][GDN_MAX_NEW], qk[GDN_MAX_NEW][GDN_MAX_NEW];
-    double g[GDN_MAX_NEW];
-    uint64_t anc[GDN_MAX_NEW];
-    float la[GDN_MAX_NEW], b[GDN_MAX_NEW];
+    int k, q, kk, qk, u, stage, anc, uni, g, up, eg, b, end;
+    __host__ __device__ DeltaTreeSmem(int np, int warps) {
+        k = 0;                              // fp16 rows in units of 16 bytes, unit x of row r at x ^ 4 (r & 1)
+        q = k + np * D * 2;
+        kk = q + np * D * 2;                // [j][i]: -e^{g_i - g_j} k_j . k_i, 0 where j is no ancestor of i
+        qk = kk + np * np * 4;              // [j][i]: e^{g_i - g_j} k_j . q_i, where j is one or i itself
+        u = qk + np * np * 4;               // per warp [token][16 rows]: v, then u
+        stage = u + warps * np * 64;        // per warp: S_0 k and S_0 q of 8 tokens
+        anc = stage + warps * DT_STAGE * 4;
+        uni = anc + np * 8;                 // per block of 8 tokens: their ancestors before the block
+        g = uni + 64;
+        up = g + np * 8;
+        eg = up + np * 4;
+        b = eg + np * 4;
+        end = b + np * 4;
+    }
 };
 
-// One CTA per (value head, sequence), a thread per state row.
+// A warp holds 16 rows of S_0 for the whole kernel; the rows of u and o follow
+// from them alone, so the CTA's warps meet only for what all rows share, the
+// decayed products of keys and queries.  S_0 is read once, 32 bytes a thread
+// and row at a time, straight into operands of the tensor cores (the k index is
+// permuted alike in both operands: thread t of a quad holds columns 8t .. 8t+7
+// of each 32): each row times a power of two, split into two fp16 numbers, the
+// second taken 2^11 times as large, so that 22 bits of it and more count.  Keys
+// and queries are fp16 as they come.
+//
+// Tokens go in blocks of 8: the products with S_0 by mma, then what the block's
+// ancestors before it add (one pass over the union of their bits), then the
+// block itself, token by token.  Lane r and lane 16 + r work on row r, the
+// first for u, the second for o.  A u that is not finite is kept out of the
+// sums (0 times it would reach tokens that do not descend from it) and marks
+// its descendants.
 template <int D>
-__global__ void __launch_bounds__(D) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
+__global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
+    constexpr int KB = D / 32;              // blocks of 32 columns
+    constexpr int UNITS = D / 8;            // 16-byte units of a row of keys
     extern __shared__ __align__(16) unsigned char raw[];
-    DeltaTreeSmem<D>& sm = *reinterpret_cast<DeltaTreeSmem<D>*>(raw);
-    const int h = blockIdx.x, s = blockIdx.y, hk = h / a.ratio, tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int warps = blockDim.x >> 5, parts = D / (16 * warps);
+    const int h = blockIdx.x / parts, part = blockIdx.x % parts, s = blockIdx.y, hk = h / a.ratio;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     int first;
     const int n = draft_range(a.d, s, first, g_draft_skipped);
     if (n == 0) return;
-    for (int e = tid; e < n; e += D) {
-        sm.anc[e] = draft_ancestors(a.d, first, e);
-        sm.la[e] = clamp_log_a(a.log_a[static_cast<int64_t>(first + e) * a.hv + h]);
-        sm.b[e] = a.b[static_cast<int64_t>(first + e) * a.hv + h];
-    }
-    for (int i = 0; i < n; ++i) {
-        const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv;
-        sm.q[i][tid] = __half2float(__ushort_as_half(row[hk * D + tid]));
-        sm.k[i][tid] = __half2float(__ushort_as_half(row[a.c_qk + hk * D + tid]));
-        sm.u[i][tid] = __half2float(__ushort_as_half(row[2 * a.c_qk + h * D + tid]));
-    }
-    __syncthreads();
-    for (int i = tid; i < n; i += D) {
-        double g = sm.la[i];
-        for (uint64_t m = sm.anc[i]; m; m &= m - 1) g += sm.la[__ffsll(static_cast<long long>(m)) - 1];
-        sm.g[i] = g;
-    }
-    __syncthreads();
-    for (int e = tid; e < n * n; e += D) {
-        const int i = e / n, j = e % n;
-        if (j != i && !(sm.anc[i] >> j & 1)) continue;
-        float kk = 0.0f, qk = 0.0f;
-        for (int c = 0; c < D; ++c) {
-            kk = fmaf(sm.k[j][c], sm.k[i][c], kk);
-            qk = fmaf(sm.k[j][c], sm.q[i][c], qk);
+    const int np = (n + 7) & ~7;
+    const DeltaTreeSmem<D> at(np, warps);
+    const int r0 = (part * warps + warp) * 16;              // the warp's rows
+    uint32_t w0[KB][8], w1[KB][8];                          // rows g and g + 8
+    {
+        const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + r0 + g) * D + 8 * t;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            load32(S + 32 * b, w0[b]);
+            load32(S + 8 * D + 32 * b, w1[b]);
         }
-        const float w = expf(static_cast<float>(sm.g[i] - sm.g[j]));
-        sm.kk[i][j] = w * kk;
-        sm.qk[i][j] = w * qk;
     }
-    const float* row = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + tid) * D;
-    for (int i = 0; i < n; ++i) {
-        float sk = 0.0f, sq = 0.0f;
-        for (int c = 0; c < D; ++c) {
-            sk = fmaf(row[c], sm.k[i][c], sk);
-            sq = fmaf(row[c], sm.q[i][c], sq);
+    uint4* ks = reinterpret_cast<uint4*>(raw + at.k);
+    uint4* qs = reinterpret_cast<uint4*>(raw + at.q);
+    float* kk = reinterpret_cast<float*>(raw + at.kk);
+    float* qk = reinterpret_cast<float*>(raw + at.qk);
+    float* us = reinterpret_cast<float*>(raw + at.u) + warp * np * 16;
+    float* stage = reinterpret_cast<float*>(raw + at.stage) + warp * DT_STAGE;
+    uint64_t* anc = reinterpret_cast<uint64_t*>(raw + at.anc);
+    uint64_t* uni = reinterpret_cast<uint64_t*>(raw + at.uni);
+    Sum2* gs = reinterpret_cast<Sum2*>(raw + at.g);
+    int* ups = reinterpret_cast<int*>(raw + at.up);
+    float* eg = reinterpret_cast<float*>(raw + at.eg);
+    float* bs = reinterpret_cast<float*>(raw + at.b);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int e = tid; e < np * UNITS; e += blockDim.x) {
+        const int i = e / UNITS, x = e % UNITS;
+        const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv + hk * D + 8 * x;
+        const int to = i * UNITS + (x ^ (4 * (i & 1)));
+        qs[to] = i < n ? *reinterpret_cast<const uint4*>(row) : zero;
+        ks[to] = i < n ? *reinterpret_cast<const uint4*>(row + a.c_qk) : zero;
+    }
+    for (int e = lane; e < 2 * np; e += 32) {               // v of the warp's rows, 8 at a time
+        const int i = e >> 1, r = 8 * (e & 1);
+        const uint4 v = i < n ? *reinterpret_cast<const uint4*>(a.qkv + static_cast<int64_t>(first + i) * a.c_conv + 2 * a.c_qk + h * D + r0 + r)
+                              : zero;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[m]));
+            us[i * 16 + r + 2 * m] = f.x;
+            us[i * 16 + r + 2 * m + 1] = f.y;
         }
-        const float w = expf(static_cast<float>(sm.g[i]));
-        sm.u[i][tid] -= w * sk;
-        sm.o[i][tid] = w * sq;
+    }
+    if (warp == 0) {
+        // sums along the paths by doubling: after a round that looked 2^m tokens
+        // back, a token holds the sum of the nearest 2^(m + 1) of its path
+        Sum2 sum[2];
+        int up[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int i = lane + 32 * m;
+            const bool in = i < n;
+            const uint64_t x = in ? draft_ancestors(a.d, first, i) : 0ull;
+            sum[m] = {in ? clamp_log_a(a.log_a[static_cast<int64_t>(first + i) * a.hv + h]) : 0.0f, 0.0f};
+            up[m] = draft_parent(x);
+            if (i < np) {
+                anc[i] = x;
+                bs[i] = in ? a.b[static_cast<int64_t>(first + i) * a.hv + h] : 0.0f;
+                gs[i] = sum[m];
+                ups[i] = up[m];
+            }
+        }
+        __syncwarp();
+        for (int step = 1; step < n; step <<= 1) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (up[m] >= 0) {
+                    sum[m] = sum2(sum[m], gs[up[m]]);
+                    up[m] = ups[up[m]];
+                }
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (lane + 32 * m < np) {
+                    gs[lane + 32 * m] = sum[m];
+                    ups[lane + 32 * m] = up[m];
+                }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (lane + 32 * m < np) eg[lane + 32 * m] = expf(sum[m].hi + sum[m].lo);
+        if (lane < np / 8) {
+            uint64_t x = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x |= anc[8 * lane + c];
+            uni[lane] = x & ((1ull << 8 * lane) - 1);
+        }
     }
     __syncthreads();
+    const int sw = t ^ (4 * (g & 1));       // the unit of columns 8t .. 8t+7 in rows of g's parity
+    const int nb = np / 8;
+    // products of the tokens, 16 tokens j by 8 tokens i, with keys and with queries
+    for (int x = warp; x < ((np + 15) / 16) * nb * 2; x += warps) {
+        const int side = x & 1, bi = (x >> 1) % nb, jt = (x >> 1) / nb;
+        if (16 * jt > 8 * bi + 7) continue;
+        float c[4] = {};
+        const uint4* other = side ? qs : ks;
+        const int j0 = 16 * jt + g;
+        const bool second = 16 * jt + 8 < np;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            const int unit = (4 * b) ^ sw;
+            const uint4 x0 = ks[j0 * UNITS + unit], x1 = second ? ks[(j0 + 8) * UNITS + unit] : zero;
+            const uint4 y = other[(8 * bi + g) * UNITS + unit];
+            mma_f16(c, x0.x, x1.x, x0.y, x1.y, y.x, y.y);
+            mma_f16(c, x0.z, x1.z, x0.w, x1.w, y.z, y.w);
+        }
+        float* out = side ? qk : kk;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int j = j0 + 8 * (m >> 1), i = 8 * bi + 2 * t + (m & 1);
+            if (j >= np) continue;
+            const bool on = (anc[i] >> j & 1) || (side && i == j);
+            const float w = expf((gs[i].hi - gs[j].hi) + (gs[i].lo - gs[j].lo));
+            out[j * np + i] = on ? (side ? w : -w) * c[m] : 0.0f;
+        }
+    }
+    // S_0's operands: row maxima to [2^13, 2^14), then high and low parts
+    uint32_t h0[KB][4], h1[KB][4], l0[KB][4], l1[KB][4];
+    float back[2];
+    {
+        const auto split = [&](const uint32_t (&w)[KB][8], uint32_t (&hi)[KB][4], uint32_t (&lo)[KB][4], float& undo) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, w[b][e] & 0x7fffffffu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t e8 = min(max(top >> 23, 14u), 254u);
+            const float scale = __uint_as_float((267u - e8) << 23);
+            undo = __uint_as_float((e8 - 13u) << 23);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = __uint_as_float(w[b][2 * e]) * scale, y = __uint_as_float(w[b][2 * e + 1]) * scale;
+                    const __half2 hh = __floats2half2_rn(x, y);
+                    const float2 f = __half22float2(hh);
+                    hi[b][e] = *reinterpret_cast<const uint32_t*>(&hh);
+                    lo[b][e] = f16x2_bits((x - f.x) * 2048.0f, (y - f.y) * 2048.0f);
+                }
+        };
+        split(w0, h0, l0, back[0]);
+        split(w1, h1, l1, back[1]);
+    }
+    __syncthreads();
+    const int row = lane & 15, side = lane >> 4;
+    const float* coef = side ? qk : kk;
+    uint64_t bad = 0;                       // tokens whose u in this row is not finite
     bool over = false;
-    for (int i = 0; i < n; ++i) {
-        float u = sm.u[i][tid], o = sm.o[i][tid];
-        for (uint64_t m = sm.anc[i]; m; m &= m - 1) {
+    float* du = a.delta + (static_cast<int64_t>(first) * a.hv + h) * D + r0 + row;
+    uint16_t* dof = a.o + (static_cast<int64_t>(first) * a.hv + h) * D + r0 + row;
+    for (int bi = 0; bi < nb; ++bi) {
+#pragma unroll
+        for (int sd = 0; sd < 2; ++sd) {
+            float c[4] = {}, d[4] = {};
+            const uint4* other = sd ? qs : ks;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                const uint4 y = other[(8 * bi + g) * UNITS + ((4 * b) ^ sw)];
+                mma_f16(c, h0[b][0], h1[b][0], h0[b][1], h1[b][1], y.x, y.y);
+                mma_f16(d, l0[b][0], l1[b][0], l0[b][1], l1[b][1], y.x, y.y);
+                mma_f16(c, h0[b][2], h1[b][2], h0[b][3], h1[b][3], y.z, y.w);
+                mma_f16(d, l0[b][2], l1[b][2], l0[b][3], l1[b][3], y.z, y.w);
+            }
+            // token c of the block at 20 c: the writers' banks differ, and so do the two halves of the readers'
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                stage[176 * sd + 20 * (2 * t + (m & 1)) + g + 8 * (m >> 1)] = fmaf(d[m], 0x1p-11f, c[m]) * back[m >> 1];
+        }
+        __syncwarp();
+        float acc[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float x = stage[176 * side + 20 * c + row] * eg[8 * bi + c];
+            acc[c] = side ? x : us[(8 * bi + c) * 16 + row] - x;
+        }
+        for (uint64_t m = uni[bi]; m; m &= m - 1) {
             const int j = __ffsll(static_cast<long long>(m)) - 1;
-            u = fmaf(-sm.kk[i][j], sm.u[j][tid], u);
-            o = fmaf(sm.qk[i][j], sm.u[j][tid], o);
+            const float u = us[j * 16 + row];
+            const float4 x = *reinterpret_cast<const float4*>(coef + j * np + 8 * bi);
+            const float4 y = *reinterpret_cast<const float4*>(coef + j * np + 8 * bi + 4);
+            acc[0] = fmaf(x.x, u, acc[0]);
+            acc[1] = fmaf(x.y, u, acc[1]);
+            acc[2] = fmaf(x.z, u, acc[2]);
+            acc[3] = fmaf(x.w, u, acc[3]);
+            acc[4] = fmaf(y.x, u, acc[4]);
+            acc[5] = fmaf(y.y, u, acc[5]);
+            acc[6] = fmaf(y.z, u, acc[6]);
+            acc[7] = fmaf(y.w, u, acc[7]);
         }
-        u *= sm.b[i];
-        o = fmaf(sm.qk[i][i], u, o);
-        sm.u[i][tid] = u;
-        over |= !(fabsf(o) <= 65504.0f);
-        const int64_t at = (static_cast<int64_t>(first + i) * a.hv + h) * D + tid;
-        if (GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens)) {
-            a.delta[at] = u;
-            a.o[at] = __half_as_ushort(__float2half_rn(o));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int i = 8 * bi + c;
+            float u = acc[c] * bs[i];
+            if (bad & anc[i]) u = __uint_as_float(0x7fffffffu);
+            u = __shfl_sync(0xffffffffu, u, row);
+            const bool fine = fabsf(u) <= 3.402823466e38f;
+            const float v = fine ? u : 0.0f;
+            if (!fine) bad |= 1ull << i;
+            const float* cr = coef + i * np + 8 * bi;
+#pragma unroll
+            for (int e = c; e < 8; ++e) acc[e] = fmaf(cr[e], v, acc[e]);
+            if (side == 0) us[i * 16 + row] = v;
+            if (i < n && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens)) {
+                const int64_t to = static_cast<int64_t>(i) * a.hv * D;
+                if (side == 0) {
+                    du[to] = u;
+                } else {
+                    const float o = bad & (anc[i] | 1ull << i) ? __uint_as_float(0x7fffffffu) : acc[c];
+                    over |= !(fabsf(o) <= 65504.0f);
+                    dof[to] = __half_as_ushort(__float2half_rn(o));
+                }
+            }
         }
+        __syncwarp();
     }
     if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
 
 template <int D>
 static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
+    const int np = (a.d.max_new + 7) & ~7;
     static PerDeviceOnce once;
     once.run([](int) {
-        cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DeltaTreeSmem<D>));
+        cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, 8).end);
     });
-    delta_tree_kernel<D><<<dim3(a.hv, a.d.n_seqs), D, sizeof(DeltaTreeSmem<D>), st>>>(a);
-    return cudaGetLastError();
+    // the whole head in a CTA, or its rows in several where that leaves SMs without one
+    int warps = D / 16;
+    while (warps > 2 && a.hv * a.d.n_seqs * (D / 16 / warps) < 152) warps >>= 1;
+    return launch_dependent(delta_tree_kernel<D>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
+                            static_cast<size_t>(DeltaTreeSmem<D>(np, warps).end), st, a);
 }
 
 cudaError_t launch_delta_tree(const gdn_layer& L, const DraftTokens& d, const uint16_t* qkv, const float* log_a, const float* b,
