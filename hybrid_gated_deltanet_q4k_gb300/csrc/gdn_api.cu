@@ -83,6 +83,7 @@ int* draft_error_word();
 int* draft_skipped_word();
 int* verify_error_word();
 int* verify_skipped_word();
+int* pages_error_word();
 int* pages_skipped_word();
 int* rope_error_word();
 int* kv_error_word();
@@ -136,7 +137,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 // The units' error words, and a kernel that takes them (an exchange each, so that
 // a code set meanwhile stays for the next call).
 struct ErrorWords {
-    static constexpr int N = 20;
+    static constexpr int N = 21;
     int* at[N];
 };
 __device__ int g_taken[ErrorWords::N];
@@ -1324,13 +1325,13 @@ int gdn_sync_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
     // every unit's error word is read and cleared, all in one go
     enum { GEMM, ATTN, DELTA, DECODE, CONV, NORM, ROPE, Q4K, Q6K, QUANT, FEW, MANY, KV, FEW_SKIP, MANY_SKIP, DRAFT, DRAFT_SKIP, VERIFY, VERIFY_SKIP,
-           PAGES_SKIP, N_WORDS };
+           PAGES, PAGES_SKIP, N_WORDS };
     static_assert(N_WORDS == ErrorWords::N);
     const ErrorWords at = {{gemm_error_word(), attn_error_word(), delta_error_word(), decode_error_word(), conv_error_word(),
                             norm_error_word(), rope_error_word(), q4k_error_word(), q6k_error_word(), quant_error_word(),
                             attn_cache_error_word(), attn_tree_error_word(), kv_error_word(), attn_cache_skipped_word(),
                             attn_tree_skipped_word(), draft_error_word(), draft_skipped_word(), verify_error_word(),
-                            verify_skipped_word(), pages_skipped_word()}};
+                            verify_skipped_word(), pages_error_word(), pages_skipped_word()}};
     int w[N_WORDS];
     e = read_and_clear(at, w);
     if (e != cudaSuccess) return cuda_fail(e, "gdn_sync_status");
@@ -1340,7 +1341,7 @@ int gdn_sync_status(void* stream) {
     } checks[] = {{Q4K, "Q4_K decode"}, {Q6K, "Q6_K decode"}, {QUANT, "activation quantisation"}, {GEMM, "projection"},
                   {CONV, "conv"}, {DELTA, "delta-rule"}, {NORM, "gated-norm"}, {DECODE, "decode-step"},
                   {ATTN, "attention"}, {ROPE, "rotary"}, {FEW, "cache attention"}, {MANY, "cache attention"},
-                  {DRAFT, "drafted tokens'"}, {VERIFY, "verification"}};
+                  {DRAFT, "drafted tokens'"}, {VERIFY, "verification"}, {PAGES, "block-table"}};
     // An index of the caller's that a kernel skipped comes last: beside a wait that ran out or a value out of range,
     // whose results are not valid, it is only named.
     std::string named;

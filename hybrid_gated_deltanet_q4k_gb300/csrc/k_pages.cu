@@ -1,10 +1,20 @@
 // Block tables and slots of a paged cache, kept on the device: pages for the
 // new tokens of every sequence from a stack of free ones, each token's slot and
 // position, and the pages past a sequence's length back onto the stack.
+//
+// Who gets which page follows from sums over the sequences (at most
+// GDN_MAX_SEQS), which every CTA takes for itself: a thread per sequence and
+// two scans.  From there tokens and pages are independent: each finds its
+// sequence by bisection of the sums in shared memory.  What is read by all
+// (lengths, pages held, the stack's height) is written last: by the one CTA, or
+// after a cluster's barrier, or by a second launch that waits for the first.
 #include "common.cuh"
+
+#include <cooperative_groups.h>
 
 namespace gdn {
 
+static __device__ int g_pages_error;      // debug: a store's index
 static __device__ int g_pages_skipped;    // a length, page or number of the caller's, out of range
 
 struct PagesArgs {
@@ -13,6 +23,7 @@ struct PagesArgs {
     const int32_t* n_new;
     const uint64_t* tree;
     int n_seqs;
+    int page_shift;
     int max_tokens;
     int32_t* lens_out;
     int32_t* cu;
@@ -20,7 +31,8 @@ struct PagesArgs {
     int64_t* slots;
 };
 
-constexpr int PG_THREADS = GDN_MAX_SEQS;   // a thread per sequence where the tables change
+constexpr int PG_THREADS = 512;
+static_assert(PG_THREADS >= GDN_MAX_SEQS, "a thread per sequence");
 
 __device__ __forceinline__ void pages_bad() { atomicCAS(&g_pages_skipped, 0, static_cast<int>(ERR_INDEX)); }
 
@@ -31,126 +43,205 @@ __device__ __forceinline__ int pages_held(int x, int lo, int hi) {
     return x < lo ? lo : hi;
 }
 
-// Inclusive sums over the block's threads.
-__device__ __forceinline__ int64_t pages_scan(int64_t x) {
-    __shared__ int64_t warp_total[PG_THREADS / 32];
+// Inclusive sums of x over the first GDN_MAX_SEQS threads.
+__device__ __forceinline__ int64_t pages_scan(int64_t x, int64_t* warp_total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
+    if (lane == 31 && w < GDN_MAX_SEQS / 32) warp_total[w] = x;
     __syncthreads();
-    if (lane == 31) warp_total[w] = x;
-    __syncthreads();
-    for (int i = 0; i < w; ++i) x += warp_total[i];
+#pragma unroll
+    for (int i = 0; i < GDN_MAX_SEQS / 32; ++i) x += i < w ? warp_total[i] : 0;
     return x;
 }
 
-__global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(const __grid_constant__ PagesArgs a) {
-    const int s = threadIdx.x;
+// The last i < n with first[i] <= x.
+__device__ __forceinline__ int pages_find(const int* first, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+struct ExtendSums {
+    int first[GDN_MAX_SEQS];   // token rows of the sequences, within max_tokens
+    int page[GDN_MAX_SEQS];    // pages asked for by the sequences before
+    int len[GDN_MAX_SEQS];
+    int had[GDN_MAX_SEQS];     // pages held; negative: the sequence gets nothing
+    int64_t warp_total[2][GDN_MAX_SEQS / 32];
+    int used, total;
+};
+
+// tokens: this launch writes slots, positions and the block table; last: it
+// ends with what the other CTAs read.
+__global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(const __grid_constant__ PagesArgs a, bool tokens, bool last) {
+    __shared__ ExtendSums sm;
+    pdl_wait();
+    pdl_trigger();
+    const int s = threadIdx.x, shift = a.page_shift;
     const bool in = s < a.n_seqs;
-    const int64_t room = static_cast<int64_t>(a.p.max_blocks) * a.p.page_tokens;
+    const int64_t room = static_cast<int64_t>(a.p.max_blocks) << shift;
     const int len = in ? pages_held(a.lens[s], 0, 0x7fffffff) : 0;
     const int n = in ? pages_held(a.n_new[s], 0, 0x7fffffff) : 0;
     const int had = in ? pages_held(a.p.n_blocks[s], 0, a.p.max_blocks) : 0;
     const int free = pages_held(*a.p.n_free, 0, static_cast<int>(a.p.n_pages));
-    const int64_t end = pages_scan(n), total = static_cast<int64_t>(len) + n;
-    const int64_t lo = end - n < a.max_tokens ? end - n : a.max_tokens, hi = end < a.max_tokens ? end : a.max_tokens;
-    bool fits = total <= room && end <= a.max_tokens;
+    if (s == 0) sm.used = 0;
+    const int64_t end = pages_scan(n, sm.warp_total[0]), total = static_cast<int64_t>(len) + n;
+    const int lo = static_cast<int>(end - n < a.max_tokens ? end - n : a.max_tokens);
+    const int hi = static_cast<int>(end < a.max_tokens ? end : a.max_tokens);
+    const bool fits = total <= room && end <= a.max_tokens;
     if (in && !fits) pages_bad();
-    int64_t need = fits ? (total + a.p.page_tokens - 1) / a.p.page_tokens - had : 0;
+    int64_t need = fits ? ((total + (1 << shift) - 1) >> shift) - had : 0;
     if (need < 0) need = 0;
-    const int64_t upto = pages_scan(need);
+    const int64_t upto = pages_scan(need, sm.warp_total[1]);
+    // once the stack did not reach, it does not reach for any later one that asks
     const bool got = fits && (need == 0 || upto <= free);
-    if (!got) need = 0;
-    const int64_t used = pages_scan(need);
     if (in) {
-        int32_t* row = a.p.block_table + s * a.p.ld_table;
-        const int64_t top = free - 1 - (upto - need);          // of the stack, when it is this sequence's turn
-        for (int64_t b = 0; b < need; ++b) row[had + b] = a.p.free_pages[top - b];
-        a.p.n_blocks[s] = had + static_cast<int>(need);
-        a.lens_out[s] = got ? static_cast<int>(total) : len;
-        if (s == 0) a.cu[0] = 0;
-        a.cu[s + 1] = static_cast<int>(hi);
+        sm.first[s] = lo;
+        sm.page[s] = static_cast<int>(upto - need < 0x7fffffff ? upto - need : 0x7fffffff);
+        sm.len[s] = len;
+        sm.had[s] = got ? had : -1;
+        if (got && need) atomicMax(&sm.used, static_cast<int>(upto));
+        if (s == a.n_seqs - 1) sm.total = hi;
     }
     __syncthreads();
-    if (threadIdx.x == a.n_seqs - 1) *a.p.n_free = free - static_cast<int>(used);
-    if (!in) return;
-    for (int64_t t = lo; t < hi; ++t) {
-        const int64_t i = t - lo, at = len + i;
-        int64_t slot = -1;
-        if (got) {
-            const int page = a.p.block_table[s * a.p.ld_table + at / a.p.page_tokens];
-            if (page >= 0 && page < a.p.n_pages) slot = static_cast<int64_t>(page) * a.p.page_tokens + at % a.p.page_tokens;
-            else pages_bad();
+    const int used = sm.used;
+    if (tokens) {
+        const int step = gridDim.x * PG_THREADS;
+        for (int k = blockIdx.x * PG_THREADS + s; k < used; k += step) {
+            const int q = pages_find(sm.page, a.n_seqs, k);
+            const int64_t to = q * a.p.ld_table + sm.had[q] + (k - sm.page[q]);
+            if (GDN_IN_RANGE(g_pages_error, sm.had[q] >= 0 && sm.had[q] + (k - sm.page[q]) < a.p.max_blocks))
+                a.p.block_table[to] = a.p.free_pages[free - 1 - k];
         }
-        int64_t pos = at;
-        if (a.tree && i < 64) pos = len + __popcll(a.tree[t] & ((1ull << i) - 1));
-        if (a.tree && i >= 64) pages_bad();
-        a.slots[t] = slot;
-        a.positions[t] = static_cast<int>(pos);
+        for (int t = blockIdx.x * PG_THREADS + s; t < a.max_tokens; t += step) {
+            int64_t slot = -1;
+            int pos = 0;
+            if (t < sm.total) {
+                const int q = pages_find(sm.first, a.n_seqs, t), i = t - sm.first[q], h = sm.had[q];
+                const int64_t at = static_cast<int64_t>(sm.len[q]) + i;
+                if (h >= 0) {
+                    // a new block's page is where the loop above takes it from
+                    const int b = static_cast<int>(at >> shift);
+                    const int page = b < h ? a.p.block_table[q * a.p.ld_table + b] : a.p.free_pages[free - 1 - (sm.page[q] + b - h)];
+                    if (page >= 0 && page < a.p.n_pages) slot = (static_cast<int64_t>(page) << shift) + (at & ((1 << shift) - 1));
+                    else pages_bad();
+                }
+                pos = static_cast<int>(at);
+                if (a.tree) {
+                    if (i < 64) pos = sm.len[q] + __popcll(a.tree[t] & ((1ull << i) - 1));
+                    else pages_bad();
+                }
+            }
+            a.slots[t] = slot;
+            a.positions[t] = pos;
+        }
     }
-}
-
-// The rows behind the last sequence's.
-__global__ void pages_rest_kernel(const __grid_constant__ PagesArgs a) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (t >= a.cu[a.n_seqs] && t < a.max_tokens) {
-        a.slots[t] = -1;
-        a.positions[t] = 0;
+    if (!last) return;
+    __syncthreads();
+    if (in) {
+        a.p.n_blocks[s] = had + (got ? static_cast<int>(need) : 0);
+        a.lens_out[s] = got ? static_cast<int>(total) : len;
+        if (s == 0) {
+            a.cu[0] = 0;
+            *a.p.n_free = free - used;
+        }
+        a.cu[s + 1] = hi;
     }
 }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_trim_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ int first[GDN_MAX_SEQS], held[GDN_MAX_SEQS];
+    __shared__ int64_t warp_total[GDN_MAX_SEQS / 32];
+    __shared__ int64_t sum;
+    pdl_wait();
+    pdl_trigger();
     const int s = threadIdx.x;
     const bool in = s < a.n_seqs;
     const int len = in ? pages_held(a.lens[s], 0, 0x7fffffff) : 0;
     const int had = in ? pages_held(a.p.n_blocks[s], 0, a.p.max_blocks) : 0;
     const int free = pages_held(*a.p.n_free, 0, static_cast<int>(a.p.n_pages));
-    const int64_t want = (static_cast<int64_t>(len) + a.p.page_tokens - 1) / a.p.page_tokens;
+    const int64_t want = (static_cast<int64_t>(len) + (1 << a.page_shift) - 1) >> a.page_shift;
     const int keep = want < had ? static_cast<int>(want) : had;
-    const int64_t upto = pages_scan(had - keep);
-    __shared__ int64_t total;
-    if (s == PG_THREADS - 1) total = upto;
-    __syncthreads();
-    const int64_t after = free + total;
+    const int64_t upto = pages_scan(had - keep, warp_total);
     if (in) {
-        for (int b = keep; b < had; ++b) {
-            const int64_t at = after - 1 - (upto - (had - keep)) - (b - keep);
-            if (at < a.p.n_pages) a.p.free_pages[at] = a.p.block_table[s * a.p.ld_table + b];
-            else pages_bad();
-        }
-        a.p.n_blocks[s] = keep;
+        first[s] = static_cast<int>(upto - (had - keep) < 0x7fffffff ? upto - (had - keep) : 0x7fffffff);
+        held[s] = keep;
+        if (s == a.n_seqs - 1) sum = upto;
     }
+    __syncthreads();
+    // more than the cache has pages is a mistake of the caller's; the stack ends there
+    const int64_t after = free + sum;
+    if (after > a.p.n_pages) pages_bad();
+    const int back = static_cast<int>(sum < 0x7fffffff ? sum : 0x7fffffff);
+    for (int64_t k = blockIdx.x * PG_THREADS + s; k < back; k += gridDim.x * PG_THREADS) {
+        const int64_t to = after - 1 - k;
+        if (to >= a.p.n_pages) continue;
+        const int q = pages_find(first, a.n_seqs, static_cast<int>(k));
+        a.p.free_pages[to] = a.p.block_table[q * a.p.ld_table + held[q] + (k - first[q])];
+    }
+    if (gridDim.x > 1) cooperative_groups::this_cluster().sync();
+    else __syncthreads();
+    if (blockIdx.x) return;
+    if (in) a.p.n_blocks[s] = keep;
     if (s == 0) *a.p.n_free = static_cast<int>(after < a.p.n_pages ? after : a.p.n_pages);
+}
+
+static PagesArgs pages_args(const gdn_kv_pages& p, const int32_t* lens, int n_seqs) {
+    PagesArgs a{};
+    a.p = p;
+    a.lens = lens;
+    a.n_seqs = n_seqs;
+    a.page_shift = p.page_tokens == 16 ? 4 : p.page_tokens == 32 ? 5 : p.page_tokens == 64 ? 6 : 7;
+    return a;
 }
 
 cudaError_t launch_kv_extend(const gdn_kv_pages& p, const int32_t* lens, const int32_t* n_new, int n_seqs, const uint64_t* tree,
                              int64_t max_tokens, int32_t* lens_out, int32_t* cu, int32_t* positions, int64_t* slots, cudaStream_t st) {
-    PagesArgs a{};
-    a.p = p;
-    a.lens = lens;
+    PagesArgs a = pages_args(p, lens, n_seqs);
     a.n_new = n_new;
     a.tree = tree;
-    a.n_seqs = n_seqs;
     a.max_tokens = static_cast<int>(max_tokens);
     a.lens_out = lens_out;
     a.cu = cu;
     a.positions = positions;
     a.slots = slots;
-    pages_extend_kernel<<<1, PG_THREADS, 0, st>>>(a);
-    if (max_tokens) pages_rest_kernel<<<static_cast<unsigned>((max_tokens + 255) / 256), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    // one CTA where its threads have a few tokens each, else all SMs and a second launch for what they read
+    constexpr int FEW = 4 * PG_THREADS;
+    if (max_tokens <= FEW) return launch_dependent(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, true, true);
+    const int64_t want = (max_tokens + 2 * PG_THREADS - 1) / (2 * PG_THREADS);
+    const cudaError_t e = launch_dependent(pages_extend_kernel, dim3(static_cast<unsigned>(want < 304 ? want : 304)), dim3(PG_THREADS), 0, st,
+                                           a, true, false);
+    return e != cudaSuccess ? e : launch_dependent(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, false, true);
 }
 
 cudaError_t launch_kv_trim(const gdn_kv_pages& p, const int32_t* keep, int n_seqs, cudaStream_t st) {
-    PagesArgs a{};
-    a.p = p;
-    a.lens = keep;
-    a.n_seqs = n_seqs;
-    pages_trim_kernel<<<1, PG_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    const PagesArgs a = pages_args(p, keep, n_seqs);
+    // a cluster where there may be many pages
+    const unsigned ctas = static_cast<int64_t>(n_seqs) * p.max_blocks > 16 * PG_THREADS ? 8 : 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(PG_THREADS);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, pages_trim_kernel, a);
+}
+
+int* pages_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_pages_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 int* pages_skipped_word() {
