@@ -11,7 +11,7 @@
 // the path, which is drawn from the last r.  Without q a draft was certain:
 // accepted with probability r(x), and r loses x when it is rejected.
 //
-// Sums are taken in integers, multiples of 2^-60: their order changes nothing,
+// Sums are taken in integers, multiples of 2^-44: their order changes nothing,
 // so the token drawn does not depend on how a row was split.
 #include "drafts.cuh"
 
@@ -46,13 +46,31 @@ __device__ __forceinline__ float vf_value(const float* p) { return *p; }
 __device__ __forceinline__ float vf_value(const uint16_t* p) { return bf16_bits_to_float(*p); }
 
 // A probability: what is negative or no number counts as 0, what is above 1 as 1.
-__device__ __forceinline__ float vf_prob(float x) { return x > 0.0f ? fminf(x, 1.0f) : 0.0f; }
+__device__ __forceinline__ float vf_prob(float x) { return __saturatef(x); }
 
-// x in [0, 1] as a multiple of 2^-60 (what is below is cut off).
-__device__ __forceinline__ uint64_t vf_fixed(float x) {
-    const uint32_t b = __float_as_uint(x), e = b >> 23;
-    const uint64_t m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
-    return e >= 90 ? m << (e - 90) : e > 66 ? m >> (90 - e) : 0ull;
+// x + e, x in [0, 1] and |e| <= 2^-23, as a multiple of 2^-44, in two parts: hi
+// multiples of 2^-22 and lo.  Adding 3 (1.5 times 2^-21) rounds to the last place
+// of numbers of that size, which then stands in the low bits.
+struct Fixed {
+    uint32_t hi;
+    int32_t lo;
+    __device__ __forceinline__ int64_t all() const { return (static_cast<int64_t>(hi) << 22) + lo; }
+};
+__device__ __forceinline__ Fixed vf_fixed(float x, float e) {
+    const float t = __fadd_rn(x, 3.0f);
+    const float r = __fadd_rn(__fsub_rn(x, __fsub_rn(t, 3.0f)), e);      // the difference is exact
+    const float v = __fadd_rn(r, 0x1.8p-21f);
+    return {__float_as_uint(t) - 0x40400000u, static_cast<int32_t>(__float_as_uint(v) - 0x35400000u)};
+}
+
+// max(0, p - c q), c = ch + cl: the product's and the difference's roundings go
+// into a second number, so that together they are good to 2^-47.
+__device__ __forceinline__ Fixed vf_residual(float p, float q, float ch, float cl) {
+    const float m = __fmul_rn(ch, q), d = __fsub_rn(p, m);
+    const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), m), __fmaf_rn(cl, q, __fmaf_rn(ch, q, -m)));
+    const bool some = __fadd_rn(d, e) > 0.0f;
+    const Fixed f = vf_fixed(d, e);
+    return {some ? f.hi : 0u, some ? f.lo : 0};
 }
 
 // x in [0, 1) as a multiple of 2^-64.
@@ -70,7 +88,7 @@ __device__ __forceinline__ uint32_t vf_order(float x) {
     return x != x ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint64_t vf_warp_sum(uint64_t x) {
+__device__ __forceinline__ int64_t vf_warp_sum(int64_t x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
@@ -84,99 +102,250 @@ __device__ __forceinline__ uint64_t vf_warp_max(uint64_t x) {
     return x;
 }
 
-struct VerifySmem {
-    // what the first CTA of the cluster read, in all of them: the same to the bit, so that they take the same turns
-    int first, n;
-    int parent[GDN_MAX_NEW], token[GDN_MAX_NEW];
+// What the decisions need but the sums of rows: read by the first CTA of the
+// cluster and taken from it by the others, the same to the bit, so that all take
+// the same turns.
+struct VerifyNodes {
+    uint64_t children[GDN_MAX_NEW];
+    int token[GDN_MAX_NEW];
     float u[GDN_MAX_NEW], p[GDN_MAX_NEW], q[GDN_MAX_NEW];    // p and q of the token in its parent's row
     float u_next;
+    int first, n, pad;
+};
+
+struct VerifySmem {
+    VerifyNodes node;
     uint64_t total[2][VF_MOST];           // the CTAs' sums (or largest scores), by the parity of the row's turn
     uint64_t warp_sum[VF_WARPS];
-    int gone[GDN_MAX_NEW];
+    int gone[GDN_MAX_NEW];                // rejected certain drafts
     int found;
 };
 
-// A cluster per sequence, each of whose warps has a run of the vocabulary.  The
-// first CTA gathers all that the decisions need but the sums of rows and gives it
-// to the others; from there each CTA takes the same decisions, and they meet
-// (one barrier, their sums sent around before it) once per row that is read.
+// A row in runs of whole 16-byte vectors, one per warp of the cluster; the
+// elements before the first vector go with the first run, those after the last
+// one with the last.
 template <class T>
-__global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
+struct VerifyRow {
+    static constexpr int VEC = 16 / sizeof(T);
+    const T *p, *q;
+    int head, vecs, per, runs, vocab;
+    bool q_aligned;
+    __device__ __forceinline__ VerifyRow(const T* p_, const T* q_, int vocab_, int runs_) : p(p_), q(q_), runs(runs_), vocab(vocab_) {
+        head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / static_cast<int>(sizeof(T)), vocab);
+        vecs = (vocab - head) / VEC;
+        per = (vecs + runs - 1) / runs;
+        q_aligned = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    }
+    __device__ __forceinline__ int vec(int r) const { return min(r * per, vecs); }
+    __device__ __forceinline__ int begin(int r) const { return r == 0 ? 0 : head + vec(r) * VEC; }
+    __device__ __forceinline__ int end(int r) const { return r == runs - 1 ? vocab : head + vec(r + 1) * VEC; }
+    __device__ __forceinline__ int run_of(int j) const {
+        if (j < head || vecs == 0) return j < head ? 0 : runs - 1;
+        const int v = (j - head) / VEC;
+        return v < vecs ? v / per : runs - 1;
+    }
+    // the elements of vector v
+    static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[VEC]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (VEC == 4) {
+                x[e] = __uint_as_float(u[e]);
+            } else {
+                x[2 * e] = __uint_as_float(u[e] << 16);
+                x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ uint4 load_p(int v) const { return *reinterpret_cast<const uint4*>(p + head + v * VEC); }
+    __device__ __forceinline__ uint4 load_q(int v) const {
+        const T* at = q + head + v * VEC;
+        if (q_aligned) return *reinterpret_cast<const uint4*>(at);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (VEC == 4) w[e] = __float_as_uint(at[e]);
+            else w[e] = at[2 * e] | static_cast<uint32_t>(at[2 * e + 1]) << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// A lane's share of the weights of vectors v, v + 32, ... below v1: max(0, p - c q)
+// (REST) or p.  Functions of their own, a copy each: unrolled into every place
+// that reads a row they do not fit the instruction cache.
+template <class T, bool REST>
+__device__ __noinline__ int64_t vf_sum_vectors(const VerifyRow<T> row, int v, int v1, float ch, float cl) {
+    using Row = VerifyRow<T>;
+    constexpr int BATCH = 16 / Row::VEC;  // vectors that a thread has in flight
+    int64_t w = 0;
+#pragma unroll 1
+    for (; v < v1; v += 32 * BATCH) {
+        uint4 x[BATCH], y[BATCH];         // past the run: zeros
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            x[k] = v + 32 * k < v1 ? row.load_p(v + 32 * k) : make_uint4(0, 0, 0, 0);
+            if (REST) y[k] = v + 32 * k < v1 ? row.load_q(v + 32 * k) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t hi = 0;
+        int32_t lo = 0;                   // 16 times 2^22 at most
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            float xe[Row::VEC], ye[Row::VEC];
+            Row::unpack(x[k], xe);
+            if (REST) Row::unpack(y[k], ye);
+#pragma unroll
+            for (int e = 0; e < Row::VEC; ++e) {
+                const Fixed f = REST ? vf_residual(vf_prob(xe[e]), vf_prob(ye[e]), ch, cl) : vf_fixed(vf_prob(xe[e]), 0.0f);
+                hi += f.hi;
+                lo += f.lo;
+            }
+        }
+        w += (static_cast<int64_t>(hi) << 22) + lo;
+    }
+    return w;
+}
+
+// The key of a score: the larger the score, and of equal ones the lower the
+// place, the larger the key.
+__device__ __forceinline__ uint64_t vf_key(float x, int j) { return static_cast<uint64_t>(vf_order(x)) << 32 | (0xffffffffu - j); }
+
+// The key of a lane's largest score above -inf among its vectors, 0 if there is
+// none.  A vector is looked at element by element only where its largest one is
+// a new record of the lane's, which its first few mostly are.
+template <class T>
+__device__ __noinline__ uint64_t vf_top_vectors(const VerifyRow<T> row, int v, int v1) {
+    using Row = VerifyRow<T>;
+    constexpr int BATCH = 4;
+    float top = __uint_as_float(0xff800000u);
+    int at = -1;
+#pragma unroll 1
+    for (; v < v1; v += 32 * BATCH) {
+        uint4 x[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) x[k] = row.load_p(min(v + 32 * k, v1 - 1));   // the last one again changes nothing
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            float xe[Row::VEC];
+            Row::unpack(x[k], xe);
+            float m = xe[0];
+#pragma unroll
+            for (int e = 1; e < Row::VEC; ++e) m = fmaxf(m, xe[e]);
+            if (m > top) {
+                top = m;
+#pragma unroll
+                for (int e = Row::VEC - 1; e >= 0; --e)
+                    if (xe[e] == m) at = row.head + min(v + 32 * k, v1 - 1) * Row::VEC + e;
+            }
+        }
+    }
+    return at < 0 ? 0 : vf_key(top, at);
+}
+
+// An integer of up to 50 bits times 2^-44 as two floats.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair vf_pair(int64_t x) {
+    const float a = static_cast<float>(static_cast<uint32_t>(x >> 26)) * 0x1p-18f;
+    const float b = static_cast<float>(static_cast<uint32_t>(x) & 0x3ffffffu) * 0x1p-44f;
+    const float s = a + b;                // a is 0 or more than b
+    return {s, b - (s - a)};
+}
+
+// (c0 + u z) q < p, in pairs of floats: sm_103a has next to no units for 64 bits,
+// and every warp decides for itself.  With c0 = 0 and z = 1 it is exact.
+__device__ __forceinline__ bool vf_accepted(Pair c0, float u, Pair z, float q, float p) {
+    const float m = __fmul_rn(u, z.hi), me = __fmaf_rn(u, z.lo, __fmaf_rn(u, z.hi, -m));      // u z
+    const float s = __fadd_rn(c0.hi, m), t = __fsub_rn(s, c0.hi);                             // c0 + u z
+    const float se = __fadd_rn(__fadd_rn(__fsub_rn(c0.hi, __fsub_rn(s, t)), __fsub_rn(m, t)), __fadd_rn(c0.lo, me));
+    const float x = __fmul_rn(s, q), xe = __fmaf_rn(se, q, __fmaf_rn(s, q, -x));              // times q
+    const float d = __fsub_rn(p, x);      // exact where p and x are near each other
+    return __fadd_rn(d, -xe) > 0.0f;
+}
+
+// A cluster per sequence, each of whose warps has a run of the vocabulary.  The
+// CTAs meet once at the start and once per row that is read, their sums sent
+// around before the barrier.
+template <class T>
+__global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     namespace cg = cooperative_groups;
-    __shared__ VerifySmem sm;
+    using Row = VerifyRow<T>;
+    constexpr int VEC = Row::VEC;
+    __shared__ __align__(16) VerifySmem sm;
     const cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     const int s = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const T* P = static_cast<const T*>(a.p);
     const T* Q = static_cast<const T*>(a.q);
     const bool greedy = !a.u;
+    if (tid == 0) sm.found = -1;
     pdl_wait();
     pdl_trigger();
-    cluster.sync();                       // every CTA is there: their memory may be written
-    if (rank == 0 && tid < GDN_MAX_NEW) {
+    if (rank == 0) {
+        if (tid < GDN_MAX_NEW) sm.node.children[tid] = 0;
+        __syncthreads();
         int first;
         const int n = draft_range(a.d, s, first, g_verify_skipped);
-        int parent = -2, token = -1;
-        float u = 0.0f, p = 0.0f, q = 0.0f;
+        if (tid == 0) {
+            sm.node.first = first;
+            sm.node.n = n;
+            sm.node.u_next = n && !greedy ? a.u_next[s] : 0.0f;
+        }
         if (tid < n) {
-            parent = draft_parent(draft_ancestors(a.d, first, tid));
-            token = a.tokens[first + tid];
+            const int parent = draft_parent(draft_ancestors(a.d, first, tid));
+            int token = a.tokens[first + tid];
+            float u = greedy ? 0.0f : a.u[first + tid], p = 0.0f, q = 0.0f;
             if (tid > 0 && (token < 0 || token >= a.vocab)) {
                 atomicCAS(&g_verify_skipped, 0, static_cast<int>(ERR_INDEX));
                 token = -1;
             }
-            if (!greedy) {
-                u = a.u[first + tid];
-                if (parent >= 0 && token >= 0) {
-                    p = vf_prob(vf_value(P + (first + parent) * a.ld_p + token));
-                    if (Q) q = vf_prob(vf_value(Q + (first + parent) * a.ld_q + token));
-                }
+            if (!greedy && parent >= 0 && token >= 0) {
+                p = vf_prob(vf_value(P + (first + parent) * a.ld_p + token));
+                if (Q) q = vf_prob(vf_value(Q + (first + parent) * a.ld_q + token));
             }
-        }
-        for (int c = 0; c < ctas; ++c) {
-            VerifySmem* to = cluster.map_shared_rank(&sm, c);
-            to->parent[tid] = parent;
-            to->token[tid] = token;
-            to->u[tid] = u;
-            to->p[tid] = p;
-            to->q[tid] = q;
-            if (tid == 0) {
-                to->first = first;
-                to->n = n;
-                to->u_next = n && !greedy ? a.u_next[s] : 0.0f;
-            }
+            if (parent >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&sm.node.children[parent]), 1ull << tid);
+            sm.node.token[tid] = token;
+            sm.node.u[tid] = u;
+            sm.node.p[tid] = p;
+            sm.node.q[tid] = q;
         }
     }
-    cluster.sync();
-    const int n = sm.n, first = sm.first;
+    cluster.sync();                       // the first CTA has its nodes, and all are there
+    if (rank) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(cluster.map_shared_rank(&sm.node, 0));
+        for (int e = tid; e < static_cast<int>(sizeof(VerifyNodes) / 4); e += VF_THREADS) reinterpret_cast<uint32_t*>(&sm.node)[e] = from[e];
+    }
+    __syncthreads();
+    const int n = sm.node.n, first = sm.node.first;
     if (n == 0) {
         if (rank == 0 && tid == 0) {
             a.count[s] = 0;
             a.node[s] = a.next[s] = -1;
         }
+        cluster.sync();                   // the first CTA's memory is read until here
         return;
     }
-    const int run = (a.vocab + ctas * VF_THREADS - 1) / (ctas * VF_THREADS) * 32;      // a warp's part of a row
-    const int j0 = min((rank * VF_WARPS + warp) * run, a.vocab), j1 = min(j0 + run, a.vocab);
+    const int mine = rank * VF_WARPS + warp, runs = ctas * VF_WARPS;
     int cur = 0, depth = 0, n_gone = 0, turn = 0;
-    uint64_t C = 0, Z = 1ull << 60;       // c0 in multiples of 2^-50; the sum of the residual
-    bool summed = false;                  // Z is the sum of this row
+    int64_t C = 0, Z = 1ll << 44;         // c0 and the sum of the residual, in multiples of 2^-44
+    Pair c0 = {0.0f, 0.0f};
+    bool summed = false;                  // the CTAs' and warps' sums are those of this residual
     int best = -1;
-    const T* p = P + static_cast<int64_t>(first) * a.ld_p;
-    const T* q = Q ? Q + static_cast<int64_t>(first) * a.ld_q : nullptr;
-    const auto weight = [&](int j) -> uint64_t {
-        const uint64_t x = vf_fixed(vf_prob(vf_value(p + j)));
-        if (!C) return x;
-        const uint64_t y = vf_fixed(vf_prob(vf_value(q + j)));
-        const uint64_t c = C == 1ull << 50 ? y : (__umul64hi(y, C) << 14) | (y * C >> 50);
-        return x > c ? x - c : 0ull;
+    const auto row_of = [&](int i) {
+        return Row(P + static_cast<int64_t>(first + i) * a.ld_p, Q ? Q + static_cast<int64_t>(first + i) * a.ld_q : nullptr, a.vocab, runs);
+    };
+    Row row = row_of(0);
+    const auto weight = [&](int j) -> int64_t {
+        const float x = vf_prob(vf_value(row.p + j));
+        return (C ? vf_residual(x, vf_prob(vf_value(row.q + j)), c0.hi, c0.lo) : vf_fixed(x, 0.0f)).all();
     };
     const auto is_gone = [&](int x) {
         for (int g = 0; g < n_gone; ++g)
             if (sm.gone[g] == x) return true;
         return false;
     };
-    // the CTAs' numbers, each put together with a CTA's others, in every CTA
+    // the CTAs' numbers in every CTA
     const auto spread = [&](uint64_t x) {
         uint64_t* all = sm.total[turn & 1];
         ++turn;
@@ -184,12 +353,13 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
         cluster.sync();
         return all;
     };
+    // the row's sum (of what C says is left; rejected certain drafts are still in it)
     const auto sum_row = [&]() {
-        uint64_t w = 0;
-#pragma unroll 4
-        for (int j = j0 + lane; j < j1; j += 32) w += weight(j);
-        if (lane < n_gone && sm.gone[lane] >= j0 && sm.gone[lane] < j1) w -= weight(sm.gone[lane]);
-        if (lane + 32 < n_gone && sm.gone[lane + 32] >= j0 && sm.gone[lane + 32] < j1) w -= weight(sm.gone[lane + 32]);
+        int64_t w = 0;
+        if (mine == 0 && lane < row.head) w += weight(lane);
+        if (mine == runs - 1 && row.head + row.vecs * VEC + lane < a.vocab) w += weight(row.head + row.vecs * VEC + lane);
+        const int v0 = row.vec(mine) + lane, v1 = row.vec(mine + 1);
+        w += C ? vf_sum_vectors<T, true>(row, v0, v1, c0.hi, c0.lo) : vf_sum_vectors<T, false>(row, v0, v1, 0.0f, 0.0f);
         w = vf_warp_sum(w);
         if (lane == 0) sm.warp_sum[warp] = w;
         __syncthreads();
@@ -201,13 +371,8 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
         for (int c = 0; c < ctas; ++c) Z += all[c];
         summed = true;
     };
-    const auto find_best = [&]() {
-        uint64_t top = 0;
-#pragma unroll 4
-        for (int j = j0 + lane; j < j1; j += 32) {
-            const uint64_t v = static_cast<uint64_t>(vf_order(vf_value(p + j))) << 32 | (0xffffffffu - j);
-            top = v > top ? v : top;
-        }
+    // the CTAs' and the block's largest key
+    const auto top_of_all = [&](uint64_t top) {
         top = vf_warp_max(top);
         if (lane == 0) sm.warp_sum[warp] = top;
         __syncthreads();
@@ -216,20 +381,66 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
         for (int i = 0; i < VF_WARPS; ++i) top = sm.warp_sum[i] > top ? sm.warp_sum[i] : top;
         const uint64_t* all = spread(top);
         for (int c = 0; c < ctas; ++c) top = all[c] > top ? all[c] : top;
+        return top;
+    };
+    const auto find_best = [&]() {
+        uint64_t top = vf_top_vectors<T>(row, row.vec(mine) + lane, row.vec(mine + 1));
+        const auto take = [&](int j) {
+            const float x = vf_value(row.p + j);
+            const uint64_t k = x > __uint_as_float(0xff800000u) ? vf_key(x, j) : 0;
+            top = k > top ? k : top;
+        };
+        const int tail = row.head + row.vecs * VEC + lane;
+        if (mine == 0 && lane < row.head) take(lane);
+        if (mine == runs - 1 && tail < a.vocab) take(tail);
+        top = top_of_all(top);
+        if (top == 0) {                   // nothing above -inf: its first place, or the row's where there is none
+            for (int j = row.begin(mine) + lane; j < row.end(mine); j += 32) {
+                const uint64_t k = vf_key(vf_value(row.p + j), j);
+                top = k > top ? k : top;
+            }
+            top = top_of_all(top);
+        }
         best = static_cast<int>(0xffffffffu - static_cast<uint32_t>(top));
     };
     int path = 0, id = -1;                // thread d: the path's token d and the one after it
-    if (greedy) find_best();
-    for (int i = 1; i < n; ++i) {
-        if (sm.parent[i] != cur) continue;
-        const int x = sm.token[i];
+    uint64_t left = sm.node.children[0];  // children still to be tried
+    bool read = greedy, over = false;     // the row is to be read; the target's own row takes a residual's place
+    int drop = -1;                        // a rejected certain draft, to be taken off the row's sum
+    for (;;) {
+        if (read) {
+            if (greedy) find_best();
+            else sum_row();
+            read = false;
+        }
+        if (drop >= 0) {
+            const int x = sm.node.token[drop];
+            if (x >= 0 && !is_gone(x)) {
+                Z -= vf_fixed(sm.node.p[drop], 0.0f).all();
+                __syncthreads();
+                if (tid == 0) sm.gone[n_gone] = x;
+                __syncthreads();
+                ++n_gone;
+            }
+            drop = -1;
+        }
+        if (!left) {
+            if (greedy || (summed && (Z != 0 || over))) break;
+            if (summed) {                 // nothing is left of the residual
+                C = 0;
+                n_gone = 0;
+                over = true;
+            }
+            read = true;
+            continue;
+        }
+        const int i = __ffsll(static_cast<long long>(left)) - 1, x = sm.node.token[i];
         bool ok;
         if (greedy) {
             ok = x == best;
         } else {
-            const double z = static_cast<double>(Z) * 0x1p-60, c0 = static_cast<double>(C) * 0x1p-50;
-            const double px = sm.p[i], qx = sm.q[i], u = sm.u[i];
-            ok = x >= 0 && (Q ? (c0 + u * z) * qx < px : !is_gone(x) && u * z < px);
+            // a certain draft's q is 1, and what it was taken off the row shows in z alone
+            ok = x >= 0 && vf_accepted(c0, sm.node.u[i], vf_pair(Z), Q ? sm.node.q[i] : 1.0f, sm.node.p[i]) && !is_gone(x);
         }
         if (ok) {
             if (tid == depth) {
@@ -238,36 +449,42 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
             }
             cur = i;
             ++depth;
+            left = sm.node.children[i];
             n_gone = 0;
             C = 0;
-            Z = 1ull << 60;
+            c0 = {0.0f, 0.0f};
+            Z = 1ll << 44;
             summed = false;
-            p = P + static_cast<int64_t>(first + i) * a.ld_p;
-            if (Q) q = Q + static_cast<int64_t>(first + i) * a.ld_q;
-            if (greedy) find_best();
+            row = row_of(i);
+            read = greedy;
+            continue;
+        }
+        left &= left - 1;
+        if (Q) {
+            C += Z;
+            c0 = vf_pair(C);
+            read = true;
         } else if (!greedy) {
-            if (Q) {
-                C += Z >> 10;
-            } else if (x >= 0 && !is_gone(x)) {
-                __syncthreads();
-                if (tid == 0) sm.gone[n_gone] = x;
-                __syncthreads();
-                ++n_gone;
-            }
-            sum_row();
+            drop = i;
+            read = !summed;
         }
     }
     int winner = 0, next = best;
     if (!greedy) {
-        if (!summed) sum_row();
-        if (Z == 0) {                     // nothing is left of the residual: the target's own row
-            C = 0;
-            n_gone = 0;
-            sum_row();
+        uint64_t* all = sm.total[(turn - 1) & 1];
+        if (n_gone) {
+            __syncthreads();
+            if (tid == 0)
+                for (int g = 0; g < n_gone; ++g) {
+                    const int r = row.run_of(sm.gone[g]);
+                    const int64_t w = weight(sm.gone[g]);
+                    all[r / VF_WARPS] -= w;
+                    if (r / VF_WARPS == rank) sm.warp_sum[r % VF_WARPS] -= w;
+                }
+            __syncthreads();
         }
         // the first place whose running sum passes u * Z, that is its whole part: the CTA, its warp's run, the place
-        const uint64_t limit = __umul64hi(vf_fraction(sm.u_next), Z);
-        const uint64_t* all = sm.total[(turn - 1) & 1];
+        const uint64_t limit = __umul64hi(vf_fraction(sm.node.u_next), static_cast<uint64_t>(Z));
         uint64_t before = 0;
         while (winner < ctas && before + all[winner] <= limit) before += all[winner++];
         next = -1;
@@ -276,12 +493,12 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
         } else if (rank == winner) {
             int w = 0;
             while (w < VF_WARPS - 1 && before + sm.warp_sum[w] <= limit) before += sm.warp_sum[w++];
-            const int k0 = min((rank * VF_WARPS + w) * run, a.vocab), k1 = min(k0 + run, a.vocab);
-            const int per = (run + VF_THREADS - 1) / VF_THREADS, m0 = min(k0 + tid * per, k1), m1 = min(m0 + per, k1);
+            const int k0 = row.begin(rank * VF_WARPS + w), k1 = row.end(rank * VF_WARPS + w);
+            const int per = (k1 - k0 + VF_THREADS - 1) / VF_THREADS, m0 = min(k0 + tid * per, k1), m1 = min(m0 + per, k1);
             const auto at = [&](int j) -> uint64_t { return is_gone(j) ? 0 : weight(j); };
-            uint64_t mine = 0;
-            for (int j = m0; j < m1; ++j) mine += at(j);
-            uint64_t upto = mine;
+            uint64_t own = 0;
+            for (int j = m0; j < m1; ++j) own += at(j);
+            uint64_t upto = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -291,8 +508,8 @@ __global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constan
             if (lane == 31) sm.warp_sum[warp] = upto;
             __syncthreads();
             for (int i = 0; i < warp; ++i) before += sm.warp_sum[i];
-            before += upto - mine;
-            if (before <= limit && before + mine > limit)
+            before += upto - own;
+            if (before <= limit && before + own > limit)
                 for (int j = m0; j < m1; ++j) {
                     before += at(j);
                     if (before > limit) {
@@ -324,7 +541,10 @@ template <class T>
 static cudaError_t verify_launch(const VerifyArgs& a, cudaStream_t st) {
     static PerDeviceOnce once;
     once.run([](int) { cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
-    const int ctas = a.d.n_seqs <= 8 ? 16 : 8;
+    // as many CTAs as run at once, two to an SM: 32 greedy sequences of a vocabulary of 128000 take 24.4 us with 16 CTAs
+    // each, 16.6 with 8, 16.9 with 4; 64 sampled ones of 100000 35.7, 17.1 and 11.4; one of 150001 9.4, 10.2 and 12.7
+    int ctas = VF_MOST;
+    while (ctas > 1 && a.d.n_seqs * ctas > 2 * 152) ctas >>= 1;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
