@@ -35,69 +35,121 @@ struct ConvTreeArgs {
     float* log_a;
     float* b;
     int c_conv, n_heads, n_qk_norm, n_q, hv, head_blocks;
+    bool wide;             // rows of qkvz start on 16 bytes
     float eps, q_scale;
 };
 
 constexpr int CT_WARPS = 8;
-constexpr int CT_TOKENS = 8;
+constexpr int CT_TOKENS = 32;              // most tokens of a block
 
-// Block (token run, head group, sequence): a warp per head.  The last slice of
-// y computes the gates.
-template <int CPL>
-__global__ void __launch_bounds__(CT_WARPS * 32) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
-    constexpr int D = CPL * 32;
-    const int s = blockIdx.z;
+// Block (token run, head group, sequence): a warp per head, a thread for 8 of its
+// channels, so that 2 (d = 128) or 4 tokens run side by side, CT_STEP of each in
+// flight.  The taps' weights stay in registers; a raw input is read by up to four
+// tokens, from L1 after the first.  The last slice of y computes the gates.
+template <int D>
+__global__ void __launch_bounds__(CT_WARPS * 32, 2) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
+    constexpr int LANES = D / 8, SIDE = 32 / LANES, STEP = 2;
+    __shared__ int at[CT_TOKENS][4];       // rows of the taps from the sequence's first, oldest first; -1, -2, -3: the conv state
+    __shared__ float tail[CT_WARPS * D * 3];
+    pdl_wait();
+    pdl_trigger();
+    const int s = blockIdx.z, tid = threadIdx.x;
     int first;
     const int n = draft_range(a.d, s, first, g_draft_skipped);
     const int i0 = blockIdx.x * CT_TOKENS, i1 = min(n, i0 + CT_TOKENS);
     if (i0 >= i1) return;
     if (static_cast<int>(blockIdx.y) == a.head_blocks) {
-        for (int e = threadIdx.x; e < (i1 - i0) * a.hv; e += blockDim.x) {
+        for (int e = tid; e < (i1 - i0) * a.hv; e += blockDim.x) {
             const int64_t t = first + i0 + e / a.hv;
             const int h = e % a.hv;
-            gate_values(a.ba[t * a.ld_ba + h], a.ba[t * a.ld_ba + a.hv + h], a.A_log[h], a.dt_bias[h], a.log_a[t * a.hv + h],
-                        a.b[t * a.hv + h]);
+            if (GDN_IN_RANGE(g_draft_error, t < a.d.n_tokens))
+                gate_values(a.ba[t * a.ld_ba + h], a.ba[t * a.ld_ba + a.hv + h], a.A_log[h], a.dt_bias[h], a.log_a[t * a.hv + h],
+                            a.b[t * a.hv + h]);
         }
         return;
     }
-    const int head = blockIdx.y * CT_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (head >= a.n_heads) return;
-    const int c0 = head * D + lane * CPL;
-    const bool norm = head < a.n_qk_norm;
-    for (int i = i0; i < i1; ++i) {
-        // the token, its parent, grandparent and great-grandparent; -1, -2, -3 are the conv state from its newest entry on
-        int at[4];
-        at[3] = i;
+    const int head0 = blockIdx.y * CT_WARPS, heads = min(CT_WARPS, a.n_heads - head0);
+    const int head = head0 + (tid >> 5), lane = tid & 31, sub = lane % LANES, side = lane / LANES;
+    float w[8][4];
+    const int c0 = head * D + 8 * sub;
+    if (head < a.n_heads) {
 #pragma unroll
-        for (int m = 2; m >= 0; --m) at[m] = at[m + 1] < 0 ? at[m + 1] - 1 : draft_parent(draft_ancestors(a.d, first, at[m + 1]));
-        float y[CPL], ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) {
-            const int c = c0 + e;
-            float x[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                x[m] = at[m] < 0 ? a.tail[(static_cast<int64_t>(s) * a.c_conv + c) * 3 + 3 + at[m]]
-                                 : bf16_bits_to_float(a.qkvz[static_cast<int64_t>(first + at[m]) * a.ld_qkvz + c]);
-            const float4 w = *reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(c) * 4);
-            y[e] = conv4_silu(w, x[0], x[1], x[2], x[3]);
-            ss = fmaf(y[e], y[e], ss);
+        for (int e = 0; e < 8; ++e) {
+            const float4 v = *reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(c0 + e) * 4);
+            w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
         }
-        if (norm) {
-            ss = warp_sum(ss);
-            const float r = rsqrtf(ss + a.eps) * (head < a.n_q ? a.q_scale : 1.0f);
-#pragma unroll
-            for (int e = 0; e < CPL; ++e) y[e] *= r;
-        }
-        uint16_t* dst = a.out + static_cast<int64_t>(first + i) * a.c_conv + c0;
-        bool over = norm && !(ss <= 3.0e38f);
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) {
-            over |= !(fabsf(y[e]) <= 65504.0f);
-            if (GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens && c0 + e < a.c_conv)) dst[e] = __half_as_ushort(__float2half_rn(y[e]));
-        }
-        if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
     }
+    if (tid < i1 - i0) {
+        int x = i0 + tid;
+        at[tid][3] = x;
+#pragma unroll
+        for (int m = 2; m >= 0; --m) {
+            x = x < 0 ? x - 1 : draft_parent(draft_ancestors(a.d, first, x));
+            at[tid][m] = x;
+        }
+    }
+    const float* old = a.tail + (static_cast<int64_t>(s) * a.c_conv + head0 * D) * 3;
+    for (int e = tid; e < heads * D * 3; e += blockDim.x) tail[e] = old[e];
+    __syncthreads();
+    if (head >= a.n_heads) return;
+    const bool norm = head < a.n_qk_norm;
+    const float mul = head < a.n_q ? a.q_scale : 1.0f;
+    const float* mine = tail + ((tid >> 5) * D + 8 * sub) * 3;
+    const uint16_t* src = a.qkvz + static_cast<int64_t>(first) * a.ld_qkvz + c0;
+    bool over = false;
+    for (int i = i0 + side; i - side < i1; i += SIDE * STEP) {
+        uint4 x[STEP][4];
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            const int r = min(i + k * SIDE, i1 - 1) - i0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int64_t row = max(at[r][m], 0);
+                if (a.wide) {
+                    x[k][m] = *reinterpret_cast<const uint4*>(src + row * a.ld_qkvz);
+                } else {
+                    const uint2 lo = *reinterpret_cast<const uint2*>(src + row * a.ld_qkvz), hi = *reinterpret_cast<const uint2*>(src + row * a.ld_qkvz + 4);
+                    x[k][m] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            const int r = min(i + k * SIDE, i1 - 1) - i0;
+            float y[8], ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t u = reinterpret_cast<const uint32_t*>(&x[k][m])[e >> 1];
+                    v[m] = __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    if (at[r][m] < 0) v[m] = mine[3 * e + 3 + at[r][m]];
+                y[e] = conv4_silu(make_float4(w[e][0], w[e][1], w[e][2], w[e][3]), v[0], v[1], v[2], v[3]);
+                ss = fmaf(y[e], y[e], ss);
+            }
+            if (norm) {
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float f = rsqrtf(ss + a.eps) * mul;
+                over |= !(ss <= 3.0e38f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= f;
+            }
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf_nan(top, fabsf(y[e]));
+            over |= !(top <= 65504.0f);
+            const int64_t row = first + i + k * SIDE;
+            if (i + k * SIDE < i1 && GDN_IN_RANGE(g_draft_error, row < a.d.n_tokens && c0 + 8 <= a.c_conv))
+                *reinterpret_cast<uint4*>(a.out + row * a.c_conv + c0) =
+                    make_uint4(f16x2_bits(y[0], y[1]), f16x2_bits(y[2], y[3]), f16x2_bits(y[4], y[5]), f16x2_bits(y[6], y[7]));
+        }
+    }
+    if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
 
 cudaError_t launch_conv_tree(const gdn_layer& L, const DraftTokens& d, const uint16_t* qkvz, int64_t ld_qkvz, const float* ba, int64_t ld_ba,
@@ -123,12 +175,9 @@ cudaError_t launch_conv_tree(const gdn_layer& L, const DraftTokens& d, const uin
     a.head_blocks = (a.n_heads + CT_WARPS - 1) / CT_WARPS;
     a.eps = L.eps_l2;
     a.q_scale = L.q_scale;
+    a.wide = reinterpret_cast<uintptr_t>(qkvz) % 16 == 0 && ld_qkvz % 8 == 0;
     const dim3 grid((d.max_new + CT_TOKENS - 1) / CT_TOKENS, a.head_blocks + (L.gate_log_a ? 0 : 1), d.n_seqs);
-    if (L.dk == 128)
-        conv_tree_kernel<4><<<grid, CT_WARPS * 32, 0, st>>>(a);
-    else
-        conv_tree_kernel<2><<<grid, CT_WARPS * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(L.dk == 128 ? conv_tree_kernel<128> : conv_tree_kernel<64>, grid, dim3(CT_WARPS * 32), 0, st, a);
 }
 
 // ------------------------------------------------------------ delta rule
@@ -497,20 +546,24 @@ __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
     return -1;
 }
 
-// Block (value head, sequence): the head's state; blocks past the heads: the conv state of CM_THREADS channels.
-template <int D>
-__global__ void __launch_bounds__(CM_THREADS) commit_kernel(const __grid_constant__ CommitArgs a) {
-    extern __shared__ float cm[];                      // k [path][D], u [path][D]
+// Block (rows of a value head, sequence): a thread has 8 columns of CH rows, all
+// of them loaded before it is known what is accepted (the loads are what bounds
+// the kernel); then a rank-1 update per token of the path, from shared memory.
+// Blocks past the heads: the conv state of CM_THREADS channels.
+template <int D, int CH>
+__global__ void __launch_bounds__(CM_THREADS, 2) commit_kernel(const __grid_constant__ CommitArgs a) {
+    constexpr int COLS = D / 8, STEP = CM_THREADS / COLS, PARTS = D / (STEP * CH);
+    extern __shared__ __align__(16) float cm[];        // k [path][D], then u of the block's rows [path][STEP * CH]
     __shared__ int path[GDN_MAX_NEW];
-    __shared__ float w[GDN_MAX_NEW];
-    __shared__ float la[GDN_MAX_NEW];
-    __shared__ float grow;
-    const int s = blockIdx.y, tid = threadIdx.x;
+    __shared__ Sum2 la[GDN_MAX_NEW + 1];
+    __shared__ float w[GDN_MAX_NEW + 1];
+    pdl_wait();
+    pdl_trigger();
+    const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     int first;
-    const int n = draft_range(a.d, s, first, g_draft_skipped);
-    const int node = commit_node(a, s, n);
-    if (static_cast<int>(blockIdx.x) >= a.hv) {
-        const int c = (blockIdx.x - a.hv) * CM_THREADS + tid;
+    if (static_cast<int>(blockIdx.x) >= a.hv * PARTS) {
+        const int n = draft_range(a.d, s, first, g_draft_skipped), node = commit_node(a, s, n);
+        const int c = (blockIdx.x - a.hv * PARTS) * CM_THREADS + tid;
         if (c >= a.c_conv) return;
         const float* in = a.tail_in + (static_cast<int64_t>(s) * a.c_conv + c) * 3;
         float x[3];
@@ -526,55 +579,91 @@ __global__ void __launch_bounds__(CM_THREADS) commit_kernel(const __grid_constan
         for (int m = 0; m < 3; ++m) out[m] = x[m];
         return;
     }
-    const int h = blockIdx.x, hk = h / a.ratio;
+    const int h = blockIdx.x / PARTS, row0 = blockIdx.x % PARTS * (STEP * CH), hk = h / a.ratio;
+    const int col = tid % COLS * 8, row = tid / COLS;
+    const int64_t base = ((static_cast<int64_t>(s) * a.hv + h) * D + row0 + row) * D + col;
+    uint32_t v[CH][8];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) load32(a.state_in + base + j * STEP * D, v[j]);
+    const int n = draft_range(a.d, s, first, g_draft_skipped), node = commit_node(a, s, n);
     const uint64_t on = node < 0 ? 0ull : draft_ancestors(a.d, first, node) | 1ull << node;
     const int np = __popcll(on);
-    for (int j = tid; j < n; j += CM_THREADS)
-        if (on >> j & 1) {
-            const int at = __popcll(on & ((1ull << j) - 1));
-            path[at] = j;
-            la[at] = clamp_log_a(a.log_a[static_cast<int64_t>(first + j) * a.hv + h]);
+    if (tid < 32) {
+        // the sums of log a over what follows a token on the path (la[0]: over all of it), by doubling
+        for (int j = lane; j < n; j += 32)
+            if (on >> j & 1) {
+                const int at = __popcll(on & ((1ull << j) - 1));
+                path[at] = j;
+                la[at] = {clamp_log_a(a.log_a[static_cast<int64_t>(first + j) * a.hv + h]), 0.0f};
+            }
+        if (lane == 0) la[np] = {0.0f, 0.0f};
+        __syncwarp();
+        for (int step = 1; step < np; step <<= 1) {
+            Sum2 x[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int j = lane + 32 * m;
+                if (j < np) x[m] = j + step < np ? sum2(la[j], la[j + step]) : la[j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (lane + 32 * m < np) la[lane + 32 * m] = x[m];
+            __syncwarp();
         }
-    __syncthreads();
-    for (int j = tid; j <= np; j += CM_THREADS) {      // entry j - 1's decay: what follows it; all of it: the state's
-        double g = 0.0;
-        for (int m = j; m < np; ++m) g += la[m];
-        const float e = expf(static_cast<float>(g));
-        if (j == 0) grow = e;
-        else w[j - 1] = e;
+        for (int j = lane; j <= np; j += 32) w[j] = expf(la[j].hi + la[j].lo);
     }
     __syncthreads();
     float* ks = cm;
     float* us = cm + np * D;
-    for (int e = tid; e < np * D; e += CM_THREADS) {
-        const int64_t t = first + path[e / D];
-        ks[e] = __half2float(__ushort_as_half(a.qkv[t * a.c_conv + a.c_qk + hk * D + e % D]));
-        us[e] = w[e / D] * a.delta[(t * a.hv + h) * D + e % D];
+    for (int e = tid; e < np * COLS; e += CM_THREADS) {
+        const int64_t t = first + path[e / COLS];
+        const uint4 x = *reinterpret_cast<const uint4*>(a.qkv + t * a.c_conv + a.c_qk + hk * D + e % COLS * 8);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
+            *reinterpret_cast<float2*>(ks + e * 8 + 2 * m) = f;
+        }
+    }
+    for (int e = tid; e < np * STEP * CH; e += CM_THREADS) {
+        const int j = e / (STEP * CH), r = e % (STEP * CH);
+        us[e] = w[j + 1] * a.delta[((first + path[j]) * static_cast<int64_t>(a.hv) + h) * D + row0 + r];
     }
     __syncthreads();
-    const int64_t base = (static_cast<int64_t>(s) * a.hv + h) * D * D;
-    for (int e = 4 * tid; e < D * D; e += 4 * CM_THREADS) {
-        float4 v = *reinterpret_cast<const float4*>(a.state_in + base + e);
-        if (np) {
-            v.x *= grow; v.y *= grow; v.z *= grow; v.w *= grow;
+    const float grow = np ? w[0] : 1.0f;
+    float f[CH][8];
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[j][e] = __uint_as_float(v[j][e]) * grow;
+    for (int t = 0; t < np; ++t) {
+        const float4 x = *reinterpret_cast<const float4*>(ks + t * D + col), y = *reinterpret_cast<const float4*>(ks + t * D + col + 4);
+        const float k[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const float u = us[t * STEP * CH + row + j * STEP];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[j][e] = fmaf(u, k[e], f[j][e]);
         }
-        for (int j = 0; j < np; ++j) {
-            const float u = us[j * D + e / D];
-            const float4 k = *reinterpret_cast<const float4*>(ks + j * D + e % D);
-            v.x = fmaf(u, k.x, v.x); v.y = fmaf(u, k.y, v.y); v.z = fmaf(u, k.z, v.z); v.w = fmaf(u, k.w, v.w);
-        }
-        *reinterpret_cast<float4*>(a.state_out + base + e) = v;
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = __float_as_uint(f[j][e]);
+        store32(a.state_out + base + j * STEP * D, v[j]);
     }
 }
 
-template <int D>
+template <int D, int CH>
 static cudaError_t commit_launch(const CommitArgs& a, cudaStream_t st) {
-    constexpr int SMEM = 2 * GDN_MAX_NEW * D * 4;
+    constexpr int STEP = CM_THREADS / (D / 8), PARTS = D / (STEP * CH);
+    constexpr int TOKEN = (D + STEP * CH) * 4;
     static PerDeviceOnce once;
-    once.run([](int) { cudaFuncSetAttribute(commit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
+    once.run([](int) { cudaFuncSetAttribute(commit_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * TOKEN); });
     const int conv_blocks = a.qkvz ? (a.c_conv + CM_THREADS - 1) / CM_THREADS : 0;
-    commit_kernel<D><<<dim3(a.hv + conv_blocks, a.d.n_seqs), CM_THREADS, 2 * a.d.max_new * D * 4, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(commit_kernel<D, CH>, dim3(a.hv * PARTS + conv_blocks, a.d.n_seqs), dim3(CM_THREADS),
+                            static_cast<size_t>(a.d.max_new * TOKEN), st, a);
 }
 
 cudaError_t launch_delta_commit(const gdn_layer& L, const DraftTokens& d, const uint16_t* qkv, const float* log_a, const float* delta,
@@ -596,7 +685,9 @@ cudaError_t launch_delta_commit(const gdn_layer& L, const DraftTokens& d, const 
     a.ratio = L.n_v_heads / L.n_qk_heads;
     a.c_qk = L.n_qk_heads * L.dk;
     a.c_conv = 2 * a.c_qk + L.n_v_heads * L.dv;
-    return L.dk == 128 ? commit_launch<128>(a, st) : commit_launch<64>(a, st);
+    // a quarter of a head's rows to a block where whole heads leave SMs without one
+    if (L.dk == 64) return commit_launch<64, 2>(a, st);
+    return a.hv * d.n_seqs < 2 * 152 ? commit_launch<128, 2>(a, st) : commit_launch<128, 8>(a, st);
 }
 
 int* draft_error_word() {
