@@ -12,20 +12,24 @@ struct DraftTokens {
     int n_tokens, max_new, n_seqs;
 };
 
-// First token and number of tokens of sequence s.  Offsets out of range leave
-// the sequence without tokens and say so in `skipped`.
-__device__ __forceinline__ int draft_range(const DraftTokens& d, int s, int& first, int& skipped) {
-    if (!d.cu) {
-        first = s * d.max_new;
-        return d.max_new;
-    }
-    const int lo = d.cu[s], hi = d.cu[s + 1];
-    first = lo;
+// The tokens of a sequence whose offsets are lo and hi.  Offsets out of range
+// leave the sequence without tokens and say so in `skipped`.
+__device__ __forceinline__ int draft_count(const DraftTokens& d, int lo, int hi, int& skipped) {
     if (lo < 0 || hi < lo || hi > d.n_tokens || hi - lo > d.max_new) {
         atomicCAS(&skipped, 0, static_cast<int>(ERR_INDEX));
         return 0;
     }
     return hi - lo;
+}
+
+// First token and number of tokens of sequence s.
+__device__ __forceinline__ int draft_range(const DraftTokens& d, int s, int& first, int& skipped) {
+    if (!d.cu) {
+        first = s * d.max_new;
+        return d.max_new;
+    }
+    first = d.cu[s];
+    return draft_count(d, first, d.cu[s + 1], skipped);
 }
 
 // The proper ancestors of a sequence's token i (first: its token 0).

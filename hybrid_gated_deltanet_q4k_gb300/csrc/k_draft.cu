@@ -190,7 +190,7 @@ struct DeltaTreeArgs {
     const float* state;    // [n_seqs][hv][D][D]
     uint16_t* o;           // fp16 [n_tokens][hv][D]
     float* delta;          // [n_tokens][hv][D]
-    int hv, ratio, c_qk, c_conv;
+    int hv, ratio, c_qk, c_conv, c_v;
 };
 
 __device__ __forceinline__ float clamp_log_a(float la) { return la < LOG_A_MIN ? LOG_A_MIN : la; }
@@ -214,21 +214,311 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Products of fp32 operands on the tensor cores: tf32 takes the upper 11 bits of
+// each, so an operand is that and a rest, and of the four products the one of the
+// two rests (2^-22 of the whole) is left out.
+struct Tf32 {
+    uint32_t hi, lo;
+    __device__ __forceinline__ explicit Tf32(float x) {
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi));
+    }
+};
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c [16 rows][8 tokens i] += x [16 rows][8 tokens j] m [j][i].  x is laid out as the
+// products are (lane g, t: rows g, g + 8, tokens 2t, 2t + 1), which makes the tokens
+// 2t and 2t + 1 the operands' indices t and t + 4; m0, m1: m[2t][g], m[2t + 1][g].
+__device__ __forceinline__ void mma_rows(float (&c)[4], const float (&x)[4], float m0, float m1) {
+    const Tf32 a0(x[0]), a1(x[2]), a2(x[1]), a3(x[3]), b0(m0), b1(m1);
+    mma_tf32(c, a0.lo, a1.lo, a2.lo, a3.lo, b0.hi, b1.hi);
+    mma_tf32(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.lo, b1.lo);
+    mma_tf32(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
+}
+
+constexpr int DT_U = 20;                    // floats between the tokens of a warp's 16 rows: lanes 2t * 20 + g differ in their banks
+
+// The pieces that both kernels of the delta rule over drafts are made of.
+
+// Rows g and g + 8 of S_0 as operands: columns 8t .. 8t+7 of each 32, a row's
+// largest taken to [2^13, 2^14), then the fp16 number nearest and the one nearest
+// to the rest.  What they lose is 2^-23 of an element or 2^-38 of the largest.
+template <int KB>
+struct StateOperand {
+    uint32_t h0[KB][4], h1[KB][4], l0[KB][4], l1[KB][4];
+    float back[2];
+    // get(m, b, w): the eight columns of block b, of row g (m = 0) or g + 8
+    template <class Get>
+    __device__ __forceinline__ explicit StateOperand(const Get& get) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float top = 0.0f;               // of the numbers; a NaN stays one without it
+            uint32_t w[8];
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                get(m, b, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(__uint_as_float(w[e])));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t e8 = min(max(__float_as_uint(top) >> 23, 14u), 254u);
+            const float scale = __uint_as_float((267u - e8) << 23);
+            back[m] = __uint_as_float((e8 - 13u) << 23);
+            const F2 scale2 = f2(scale, scale);
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                get(m, b, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const F2 x = f2_mul(f2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])), scale2);
+                    float x0, x1;
+                    f2_split(x, x0, x1);
+                    const __half2 hh = __floats2half2_rn(x0, x1);
+                    const float2 f = __half22float2(hh);
+                    f2_split(f2_sub(x, f2(f.x, f.y)), x0, x1);
+                    (m ? h1 : h0)[b][e] = *reinterpret_cast<const uint32_t*>(&hh);
+                    (m ? l1 : l0)[b][e] = f16x2_bits(x0, x1);
+                }
+            }
+        }
+    }
+    // e^{g_i} S_0 times the rows of eight tokens, rows g and g + 8 by tokens 2t and 2t + 1
+    __device__ __forceinline__ void times(const uint4* rows, int sw, float e0, float e1, float (&x)[4]) const {
+        float c[4] = {}, d[4] = {};
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            const uint4 y = rows[(4 * b) ^ sw];
+            mma_f16(c, h0[b][0], h1[b][0], h0[b][1], h1[b][1], y.x, y.y);
+            mma_f16(d, l0[b][0], l1[b][0], l0[b][1], l1[b][1], y.x, y.y);
+            mma_f16(c, h0[b][2], h1[b][2], h0[b][3], h1[b][3], y.z, y.w);
+            mma_f16(d, l0[b][2], l1[b][2], l0[b][3], l1[b][3], y.z, y.w);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] = (c[m] + d[m]) * back[m >> 1] * (m & 1 ? e1 : e0);
+    }
+};
+
+// What all rows of a head share, in shared memory.
+struct DeltaTokens {
+    const uint4 *ks, *qs;    // fp16 rows in units of 16 bytes, unit x of row r at x ^ 4 (r & 1)
+    float *kk, *qk;          // [j][i], pitch floats apart: -e^{g_i - g_j} k_j . k_i, 0 where j is no ancestor of i;
+                             // e^{g_i - g_j} k_j . q_i, where j is one or i itself
+    float* inv;              // per block of 8 tokens [j][i]: u_i = sum_j inv[j][i] r_j
+    uint64_t* anc;           // ancestors
+    uint64_t* uni;           // per block: its ancestors before it
+    Sum2* g;
+    int* up;
+    float* eg;
+    const float* b;
+    int pitch;
+};
+
+// A warp: ancestors in, sums along the paths out.  By doubling: after a round that
+// looked 2^m tokens back, a token holds the sum of the nearest 2^(m + 1) of its
+// path.  mask and log a of the lane's tokens lane and lane + 32.
+__device__ __forceinline__ void delta_sums(const DeltaTokens& d, int n, const uint64_t (&mask)[2], const float (&log_a)[2]) {
+    const int lane = threadIdx.x & 31, np = (n + 7) & ~7;
+    Sum2 sum[2];
+    int up[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int i = lane + 32 * m;
+        const uint64_t x = i < n ? mask[m] & ((1ull << i) - 1) : 0ull;
+        sum[m] = {i < n ? clamp_log_a(log_a[m]) : 0.0f, 0.0f};
+        up[m] = draft_parent(x);
+        if (i < np) {
+            d.anc[i] = x;
+            d.g[i] = sum[m];
+            d.up[i] = up[m];
+        }
+    }
+    __syncwarp();
+    for (int step = 1; step < n; step <<= 1) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (up[m] >= 0) {
+                sum[m] = sum2(sum[m], d.g[up[m]]);
+                up[m] = d.up[up[m]];
+            }
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (lane + 32 * m < np) {
+                d.g[lane + 32 * m] = sum[m];
+                d.up[lane + 32 * m] = up[m];
+            }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        if (lane + 32 * m < np) d.eg[lane + 32 * m] = expf(sum[m].hi + sum[m].lo);
+    if (lane < np / 8) {
+        uint64_t all = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) all |= d.anc[8 * lane + c];
+        d.uni[lane] = all & ((1ull << 8 * lane) - 1);
+    }
+}
+
+// A warp: the products of tokens j = 16 jt .. with the block of tokens i = 8 bi ..
+template <int D>
+__device__ __forceinline__ void delta_products(const DeltaTokens& d, int np, int jt, int bi) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, sw = t ^ (4 * (g & 1));
+    constexpr int UNITS = D / 8;
+    float c[2][2][4] = {};                  // with keys, with queries; two chains each
+    const int j0 = 16 * jt + g;
+    const bool second = 16 * jt + 8 < np;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        const int unit = (4 * b) ^ sw;
+        const uint4 x0 = d.ks[j0 * UNITS + unit], x1 = second ? d.ks[(j0 + 8) * UNITS + unit] : make_uint4(0, 0, 0, 0);
+        const uint4 y = d.ks[(8 * bi + g) * UNITS + unit], z = d.qs[(8 * bi + g) * UNITS + unit];
+        mma_f16(c[0][0], x0.x, x1.x, x0.y, x1.y, y.x, y.y);
+        mma_f16(c[1][0], x0.x, x1.x, x0.y, x1.y, z.x, z.y);
+        mma_f16(c[0][1], x0.z, x1.z, x0.w, x1.w, y.z, y.w);
+        mma_f16(c[1][1], x0.z, x1.z, x0.w, x1.w, z.z, z.w);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int j = j0 + 8 * (m >> 1), i = 8 * bi + 2 * t + (m & 1);
+        if (j >= np) continue;
+        const bool on = d.anc[i] >> j & 1;
+        const float w = expf((d.g[i].hi - d.g[j].hi) + (d.g[i].lo - d.g[j].lo));
+        d.kk[j * d.pitch + i] = on ? -w * (c[0][0][m] + c[0][1][m]) : 0.0f;
+        d.qk[j * d.pitch + i] = on || i == j ? w * (c[1][0][m] + c[1][1][m]) : 0.0f;
+    }
+}
+
+// Eight lanes of a warp: the inverse of block bi's system, a column each.
+__device__ __forceinline__ void delta_inverse(const DeltaTokens& d, int bi) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= 8) return;
+    float m[8][8], out[8];
+    uint32_t on[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        on[i] = static_cast<uint32_t>(d.anc[8 * bi + i] >> 8 * bi);
+#pragma unroll
+        for (int j = 0; j < i; ++j) m[i][j] = d.kk[(8 * bi + j) * d.pitch + 8 * bi + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float sum = i == lane ? 1.0f : 0.0f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) sum = on[i] >> j & 1 ? fmaf(m[i][j], out[j], sum) : sum;
+        out[i] = sum * d.b[8 * bi + i];
+        d.inv[64 * bi + 8 * lane + i] = out[i];
+    }
+}
+
+// A block of 8 tokens of a warp's 16 rows.  r, xq: v - e^g S_0 k and e^g S_0 q, rows
+// g and g + 8 by tokens 2t and 2t + 1; us: the warp's u of earlier tokens; bad: tokens
+// whose u in row lane % 16 is not finite.  Leaves u and o in r's layout.
+__device__ __forceinline__ void delta_block(const DeltaTokens& d, int bi, float (&r)[4], float (&xq)[4], float* us, uint64_t& bad,
+                                            float (&u)[4], float (&o)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint64_t before = d.uni[bi];
+    for (int jb = 0; jb < bi; ++jb) {
+        if (!(before >> 8 * jb & 0xff)) continue;
+        const int j = 8 * jb + 2 * t;
+        const float x[4] = {us[j * DT_U + g], us[(j + 1) * DT_U + g], us[j * DT_U + g + 8], us[(j + 1) * DT_U + g + 8]};
+        mma_rows(r, x, d.kk[j * d.pitch + 8 * bi + g], d.kk[(j + 1) * d.pitch + 8 * bi + g]);
+        mma_rows(xq, x, d.qk[j * d.pitch + 8 * bi + g], d.qk[(j + 1) * d.pitch + 8 * bi + g]);
+    }
+    const int j = 8 * bi + 2 * t;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) u[m] = 0.0f;
+    mma_rows(u, r, d.inv[64 * bi + 16 * t + g], d.inv[64 * bi + 16 * t + 8 + g]);
+    const float sum = ((fabsf(r[0]) + fabsf(r[1])) + (fabsf(r[2]) + fabsf(r[3]))) + ((fabsf(u[0]) + fabsf(u[1])) + (fabsf(u[2]) + fabsf(u[3])));
+    if (!__any_sync(0xffffffffu, bad != 0 || !(sum <= 3.402823466e38f))) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            us[(j + (m & 1)) * DT_U + g + 8 * (m >> 1)] = u[m];
+            o[m] = xq[m];
+        }
+        mma_rows(o, u, d.qk[j * d.pitch + 8 * bi + g], d.qk[(j + 1) * d.pitch + 8 * bi + g]);
+        __syncwarp();
+        return;
+    }
+    // token by token: lane r works on row r, with r and S_0 q by way of the block's place in us
+    const int row = lane & 15;
+    float v[8], w[8], ou[8];
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) us[(j + (m & 1)) * DT_U + g + 8 * (m >> 1)] = pass ? xq[m] : r[m];
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) (pass ? w : v)[c] = us[(8 * bi + c) * DT_U + row];
+        __syncwarp();
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int i = 8 * bi + c;
+        float x = v[c] * d.b[i];
+        if (bad & d.anc[i]) x = __uint_as_float(0x7fffffffu);
+        ou[c] = x;
+        if (!(fabsf(x) <= 3.402823466e38f)) {
+            bad |= 1ull << i;
+            x = 0.0f;
+        }
+        const float* kr = d.kk + i * d.pitch + 8 * bi;
+        const float* qr = d.qk + i * d.pitch + 8 * bi;
+#pragma unroll
+        for (int e = c; e < 8; ++e) {
+            if (e > c) v[e] = fmaf(kr[e], x, v[e]);
+            w[e] = fmaf(qr[e], x, w[e]);
+        }
+        if (bad & (d.anc[i] | 1ull << i)) w[c] = __uint_as_float(0x7fffffffu);
+    }
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {  // o, u, and last the u that others may take
+#pragma unroll
+        for (int c = 0; c < 8; ++c) us[(8 * bi + c) * DT_U + row] = pass == 0 ? w[c] : pass == 2 && (bad >> (8 * bi + c) & 1) ? 0.0f : ou[c];
+        __syncwarp();
+        if (pass < 2) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) (pass ? u : o)[m] = us[(j + (m & 1)) * DT_U + g + 8 * (m >> 1)];
+            __syncwarp();
+        }
+    }
+}
+
+// u and o of a block to global memory; true if an o is beyond fp16.
+__device__ __forceinline__ bool delta_store(const DeltaTreeArgs& a, int first, int n, int bi, int64_t col, const float (&u)[4], const float (&o)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    bool over = false;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int i = 8 * bi + 2 * t + (m & 1);
+        if (i < n && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens)) {
+            const int64_t to = static_cast<int64_t>(first + i) * a.c_v + col + g + 8 * (m >> 1);
+            a.delta[to] = u[m];
+            a.o[to] = __half_as_ushort(__float2half_rn(o[m]));
+            over |= !(fabsf(o[m]) <= 65504.0f);
+        }
+    }
+    return over;
+}
+
 // Shared memory of delta_tree_kernel for np tokens (a multiple of 8) and a
 // number of warps: byte offsets.
-constexpr int DT_STAGE = 336;               // floats per warp, see the kernel
 template <int D>
 struct DeltaTreeSmem {
-    int k, q, kk, qk, u, stage, anc, uni, g, up, eg, b, end;
+    int k, q, kk, qk, inv, u, anc, uni, g, up, eg, b, end;
     __host__ __device__ DeltaTreeSmem(int np, int warps) {
-        k = 0;                              // fp16 rows in units of 16 bytes, unit x of row r at x ^ 4 (r & 1)
+        k = 0;
         q = k + np * D * 2;
-        kk = q + np * D * 2;                // [j][i]: -e^{g_i - g_j} k_j . k_i, 0 where j is no ancestor of i
-        qk = kk + np * np * 4;              // [j][i]: e^{g_i - g_j} k_j . q_i, where j is one or i itself
-        u = qk + np * np * 4;               // per warp [token][16 rows]: v, then u
-        stage = u + warps * np * 64;        // per warp: S_0 k and S_0 q of 8 tokens
-        anc = stage + warps * DT_STAGE * 4;
-        uni = anc + np * 8;                 // per block of 8 tokens: their ancestors before the block
+        kk = q + np * D * 2;
+        qk = kk + np * (np + 4) * 4;        // a pitch of np + 4 for the banks of lanes 2t * pitch + g
+        inv = qk + np * (np + 4) * 4;
+        u = inv + np * 32;                  // per warp [token][16 rows]
+        anc = u + warps * np * DT_U * 4;
+        uni = anc + np * 8;
         g = uni + 64;
         up = g + np * 8;
         eg = up + np * 4;
@@ -237,21 +527,21 @@ struct DeltaTreeSmem {
     }
 };
 
-// A warp holds 16 rows of S_0 for the whole kernel; the rows of u and o follow
-// from them alone, so the CTA's warps meet only for what all rows share, the
-// decayed products of keys and queries.  S_0 is read once, 32 bytes a thread
-// and row at a time, straight into operands of the tensor cores (the k index is
-// permuted alike in both operands: thread t of a quad holds columns 8t .. 8t+7
-// of each 32): each row times a power of two, split into two fp16 numbers, the
-// second taken 2^11 times as large, so that 22 bits of it and more count.  Keys
-// and queries are fp16 as they come.
+// A warp holds 16 rows of S_0; the rows of u and o follow from them alone, so
+// warps meet only for what all rows share, the decayed products of keys and
+// queries.  S_0 is read once, straight into operands of the tensor cores (the k
+// index is permuted alike in both operands: thread t of a quad holds columns 8t ..
+// 8t+7 of each 32).  Keys and queries are fp16 as they come.
 //
-// Tokens go in blocks of 8: the products with S_0 by mma, then what the block's
-// ancestors before it add (one pass over the union of their bits), then the
-// block itself, token by token.  Lane r and lane 16 + r work on row r, the
-// first for u, the second for o.  A u that is not finite is kept out of the
-// sums (0 times it would reach tokens that do not descend from it) and marks
-// its descendants.
+// Tokens go in blocks of 8.  With r_i = v_i - e^{g_i} S_0 k_i + what the ancestors
+// before the block add, the block's u are its unit lower-triangular system's
+// inverse times r; the inverse (8 x 8, the same for all rows, taken once per CTA),
+// the earlier u and the block's own enter as products of fp32 operands on the
+// tensor cores, whose layout never changes in between.  Numbers that are not
+// finite would reach tokens that do not descend from theirs (0 times them), so a
+// warp that meets one goes through the block token by token.
+//
+// This kernel: a CTA for a head, or for part of its rows, of a sequence.
 template <int D>
 __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
     constexpr int KB = D / 32;              // blocks of 32 columns
@@ -262,11 +552,6 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
     const int warps = blockDim.x >> 5, parts = D / (16 * warps);
     const int h = blockIdx.x / parts, part = blockIdx.x % parts, s = blockIdx.y, hk = h / a.ratio;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    int first;
-    const int n = draft_range(a.d, s, first, g_draft_skipped);
-    if (n == 0) return;
-    const int np = (n + 7) & ~7;
-    const DeltaTreeSmem<D> at(np, warps);
     const int r0 = (part * warps + warp) * 16;              // the warp's rows
     uint32_t w0[KB][8], w1[KB][8];                          // rows g and g + 8
     {
@@ -277,227 +562,212 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
             load32(S + 8 * D + 32 * b, w1[b]);
         }
     }
+    int first;
+    const int n = draft_range(a.d, s, first, g_draft_skipped);
+    if (n == 0) return;
+    const int np = (n + 7) & ~7, nb = np / 8;
+    const DeltaTreeSmem<D> at(np, warps);
     uint4* ks = reinterpret_cast<uint4*>(raw + at.k);
     uint4* qs = reinterpret_cast<uint4*>(raw + at.q);
-    float* kk = reinterpret_cast<float*>(raw + at.kk);
-    float* qk = reinterpret_cast<float*>(raw + at.qk);
-    float* us = reinterpret_cast<float*>(raw + at.u) + warp * np * 16;
-    float* stage = reinterpret_cast<float*>(raw + at.stage) + warp * DT_STAGE;
-    uint64_t* anc = reinterpret_cast<uint64_t*>(raw + at.anc);
-    uint64_t* uni = reinterpret_cast<uint64_t*>(raw + at.uni);
-    Sum2* gs = reinterpret_cast<Sum2*>(raw + at.g);
-    int* ups = reinterpret_cast<int*>(raw + at.up);
-    float* eg = reinterpret_cast<float*>(raw + at.eg);
     float* bs = reinterpret_cast<float*>(raw + at.b);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int e = tid; e < np * UNITS; e += blockDim.x) {
-        const int i = e / UNITS, x = e % UNITS;
-        const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv + hk * D + 8 * x;
-        const int to = i * UNITS + (x ^ (4 * (i & 1)));
-        qs[to] = i < n ? *reinterpret_cast<const uint4*>(row) : zero;
-        ks[to] = i < n ? *reinterpret_cast<const uint4*>(row + a.c_qk) : zero;
-    }
-    for (int e = lane; e < 2 * np; e += 32) {               // v of the warp's rows, 8 at a time
-        const int i = e >> 1, r = 8 * (e & 1);
-        const uint4 v = i < n ? *reinterpret_cast<const uint4*>(a.qkv + static_cast<int64_t>(first + i) * a.c_conv + 2 * a.c_qk + h * D + r0 + r)
-                              : zero;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const DeltaTokens d = {ks, qs, reinterpret_cast<float*>(raw + at.kk), reinterpret_cast<float*>(raw + at.qk),
+                           reinterpret_cast<float*>(raw + at.inv), reinterpret_cast<uint64_t*>(raw + at.anc),
+                           reinterpret_cast<uint64_t*>(raw + at.uni), reinterpret_cast<Sum2*>(raw + at.g),
+                           reinterpret_cast<int*>(raw + at.up), reinterpret_cast<float*>(raw + at.eg), bs, np + 4};
+    float* us = reinterpret_cast<float*>(raw + at.u) + warp * np * DT_U;
+    // v of a block, in the products' layout
+    const uint16_t* vs = a.qkv + static_cast<int64_t>(first) * a.c_conv + 2 * a.c_qk + h * D + r0;
+    const auto load_v = [&](int bi, uint16_t (&v)[4]) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[m]));
-            us[i * 16 + r + 2 * m] = f.x;
-            us[i * 16 + r + 2 * m + 1] = f.y;
+            const int i = 8 * bi + 2 * t + (m & 1);
+            v[m] = i < n ? vs[static_cast<int64_t>(i) * a.c_conv + g + 8 * (m >> 1)] : static_cast<uint16_t>(0);
         }
-    }
+    };
+    uint16_t vn[4];
     if (warp == 0) {
-        // sums along the paths by doubling: after a round that looked 2^m tokens
-        // back, a token holds the sum of the nearest 2^(m + 1) of its path
-        Sum2 sum[2];
-        int up[2];
+        uint64_t mask[2];
+        float la[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int i = lane + 32 * m;
-            const bool in = i < n;
-            const uint64_t x = in ? draft_ancestors(a.d, first, i) : 0ull;
-            sum[m] = {in ? clamp_log_a(a.log_a[static_cast<int64_t>(first + i) * a.hv + h]) : 0.0f, 0.0f};
-            up[m] = draft_parent(x);
-            if (i < np) {
-                anc[i] = x;
-                bs[i] = in ? a.b[static_cast<int64_t>(first + i) * a.hv + h] : 0.0f;
-                gs[i] = sum[m];
-                ups[i] = up[m];
-            }
+            const int64_t row = static_cast<int64_t>(first + i) * a.hv + h;
+            mask[m] = i < n && a.d.tree ? a.d.tree[first + i] : ~0ull;
+            la[m] = i < n ? a.log_a[row] : 0.0f;
+            if (i < np) bs[i] = i < n ? a.b[row] : 0.0f;
         }
-        __syncwarp();
-        for (int step = 1; step < n; step <<= 1) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                if (up[m] >= 0) {
-                    sum[m] = sum2(sum[m], gs[up[m]]);
-                    up[m] = ups[up[m]];
-                }
-            __syncwarp();
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                if (lane + 32 * m < np) {
-                    gs[lane + 32 * m] = sum[m];
-                    ups[lane + 32 * m] = up[m];
-                }
-            __syncwarp();
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-            if (lane + 32 * m < np) eg[lane + 32 * m] = expf(sum[m].hi + sum[m].lo);
-        if (lane < np / 8) {
-            uint64_t x = 0;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x |= anc[8 * lane + c];
-            uni[lane] = x & ((1ull << 8 * lane) - 1);
+        delta_sums(d, n, mask, la);
+        load_v(0, vn);
+    } else {
+        load_v(0, vn);
+        for (int e = tid - 32; e < np * UNITS; e += blockDim.x - 32) {
+            const int i = e / UNITS, x = e % UNITS;
+            const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv + hk * D + 8 * x;
+            const int to = i * UNITS + (x ^ (4 * (i & 1)));
+            qs[to] = i < n ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
+            ks[to] = i < n ? *reinterpret_cast<const uint4*>(row + a.c_qk) : make_uint4(0, 0, 0, 0);
         }
     }
+    const StateOperand<KB> S0([&](int m, int b, uint32_t (&w)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = m ? w1[b][e] : w0[b][e];
+    });
     __syncthreads();
     const int sw = t ^ (4 * (g & 1));       // the unit of columns 8t .. 8t+7 in rows of g's parity
-    const int nb = np / 8;
-    // products of the tokens, 16 tokens j by 8 tokens i, with keys and with queries
-    for (int x = warp; x < ((np + 15) / 16) * nb * 2; x += warps) {
-        const int side = x & 1, bi = (x >> 1) % nb, jt = (x >> 1) / nb;
-        if (16 * jt > 8 * bi + 7) continue;
-        float c[4] = {};
-        const uint4* other = side ? qs : ks;
-        const int j0 = 16 * jt + g;
-        const bool second = 16 * jt + 8 < np;
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            const int unit = (4 * b) ^ sw;
-            const uint4 x0 = ks[j0 * UNITS + unit], x1 = second ? ks[(j0 + 8) * UNITS + unit] : zero;
-            const uint4 y = other[(8 * bi + g) * UNITS + unit];
-            mma_f16(c, x0.x, x1.x, x0.y, x1.y, y.x, y.y);
-            mma_f16(c, x0.z, x1.z, x0.w, x1.w, y.z, y.w);
-        }
-        float* out = side ? qk : kk;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int j = j0 + 8 * (m >> 1), i = 8 * bi + 2 * t + (m & 1);
-            if (j >= np) continue;
-            const bool on = (anc[i] >> j & 1) || (side && i == j);
-            const float w = expf((gs[i].hi - gs[j].hi) + (gs[i].lo - gs[j].lo));
-            out[j * np + i] = on ? (side ? w : -w) * c[m] : 0.0f;
-        }
-    }
-    // S_0's operands: row maxima to [2^13, 2^14), then high and low parts
-    uint32_t h0[KB][4], h1[KB][4], l0[KB][4], l1[KB][4];
-    float back[2];
-    {
-        const auto split = [&](const uint32_t (&w)[KB][8], uint32_t (&hi)[KB][4], uint32_t (&lo)[KB][4], float& undo) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = max(top, w[b][e] & 0x7fffffffu);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t e8 = min(max(top >> 23, 14u), 254u);
-            const float scale = __uint_as_float((267u - e8) << 23);
-            undo = __uint_as_float((e8 - 13u) << 23);
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = __uint_as_float(w[b][2 * e]) * scale, y = __uint_as_float(w[b][2 * e + 1]) * scale;
-                    const __half2 hh = __floats2half2_rn(x, y);
-                    const float2 f = __half22float2(hh);
-                    hi[b][e] = *reinterpret_cast<const uint32_t*>(&hh);
-                    lo[b][e] = f16x2_bits((x - f.x) * 2048.0f, (y - f.y) * 2048.0f);
-                }
-        };
-        split(w0, h0, l0, back[0]);
-        split(w1, h1, l1, back[1]);
-    }
+    for (int bi = 0, turn = 0; bi < nb; ++bi)
+        for (int jt = 0; 2 * jt <= bi; ++jt)
+            if ((2 * jt + 1 >= bi || d.uni[bi] >> 16 * jt & 0xffff) && turn++ % warps == warp) delta_products<D>(d, np, jt, bi);
     __syncthreads();
-    const int row = lane & 15, side = lane >> 4;
-    const float* coef = side ? qk : kk;
-    uint64_t bad = 0;                       // tokens whose u in this row is not finite
+    for (int bi = warp; bi < nb; bi += warps) delta_inverse(d, bi);
+    float xk[4], xq[4];
+    const auto with_state = [&](int bi) {
+        const float e0 = d.eg[8 * bi + 2 * t], e1 = d.eg[8 * bi + 2 * t + 1];
+        S0.times(ks + (8 * bi + g) * UNITS, sw, e0, e1, xk);
+        S0.times(qs + (8 * bi + g) * UNITS, sw, e0, e1, xq);
+    };
+    with_state(0);
+    __syncthreads();
+    uint64_t bad = 0;
     bool over = false;
-    float* du = a.delta + (static_cast<int64_t>(first) * a.hv + h) * D + r0 + row;
-    uint16_t* dof = a.o + (static_cast<int64_t>(first) * a.hv + h) * D + r0 + row;
     for (int bi = 0; bi < nb; ++bi) {
+        float r[4], u[4], o[4];
 #pragma unroll
-        for (int sd = 0; sd < 2; ++sd) {
-            float c[4] = {}, d[4] = {};
-            const uint4* other = sd ? qs : ks;
+        for (int m = 0; m < 4; ++m) r[m] = __half2float(__ushort_as_half(vn[m]));
+        if (bi + 1 < nb) load_v(bi + 1, vn);
+        if (bi) with_state(bi);
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                const uint4 y = other[(8 * bi + g) * UNITS + ((4 * b) ^ sw)];
-                mma_f16(c, h0[b][0], h1[b][0], h0[b][1], h1[b][1], y.x, y.y);
-                mma_f16(d, l0[b][0], l1[b][0], l0[b][1], l1[b][1], y.x, y.y);
-                mma_f16(c, h0[b][2], h1[b][2], h0[b][3], h1[b][3], y.z, y.w);
-                mma_f16(d, l0[b][2], l1[b][2], l0[b][3], l1[b][3], y.z, y.w);
-            }
-            // token c of the block at 20 c: the writers' banks differ, and so do the two halves of the readers'
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                stage[176 * sd + 20 * (2 * t + (m & 1)) + g + 8 * (m >> 1)] = fmaf(d[m], 0x1p-11f, c[m]) * back[m >> 1];
-        }
-        __syncwarp();
-        float acc[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float x = stage[176 * side + 20 * c + row] * eg[8 * bi + c];
-            acc[c] = side ? x : us[(8 * bi + c) * 16 + row] - x;
-        }
-        for (uint64_t m = uni[bi]; m; m &= m - 1) {
-            const int j = __ffsll(static_cast<long long>(m)) - 1;
-            const float u = us[j * 16 + row];
-            const float4 x = *reinterpret_cast<const float4*>(coef + j * np + 8 * bi);
-            const float4 y = *reinterpret_cast<const float4*>(coef + j * np + 8 * bi + 4);
-            acc[0] = fmaf(x.x, u, acc[0]);
-            acc[1] = fmaf(x.y, u, acc[1]);
-            acc[2] = fmaf(x.z, u, acc[2]);
-            acc[3] = fmaf(x.w, u, acc[3]);
-            acc[4] = fmaf(y.x, u, acc[4]);
-            acc[5] = fmaf(y.y, u, acc[5]);
-            acc[6] = fmaf(y.z, u, acc[6]);
-            acc[7] = fmaf(y.w, u, acc[7]);
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int i = 8 * bi + c;
-            float u = acc[c] * bs[i];
-            if (bad & anc[i]) u = __uint_as_float(0x7fffffffu);
-            u = __shfl_sync(0xffffffffu, u, row);
-            const bool fine = fabsf(u) <= 3.402823466e38f;
-            const float v = fine ? u : 0.0f;
-            if (!fine) bad |= 1ull << i;
-            const float* cr = coef + i * np + 8 * bi;
-#pragma unroll
-            for (int e = c; e < 8; ++e) acc[e] = fmaf(cr[e], v, acc[e]);
-            if (side == 0) us[i * 16 + row] = v;
-            if (i < n && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens)) {
-                const int64_t to = static_cast<int64_t>(i) * a.hv * D;
-                if (side == 0) {
-                    du[to] = u;
-                } else {
-                    const float o = bad & (anc[i] | 1ull << i) ? __uint_as_float(0x7fffffffu) : acc[c];
-                    over |= !(fabsf(o) <= 65504.0f);
-                    dof[to] = __half_as_ushort(__float2half_rn(o));
-                }
-            }
-        }
-        __syncwarp();
+        for (int m = 0; m < 4; ++m) r[m] -= xk[m];
+        delta_block(d, bi, r, xq, us, bad, u, o);
+        over |= delta_store(a, first, n, bi, h * D + r0, u, o);
     }
     if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
 
+// The same for sequences of up to 8 tokens, a block: S_0 is used once, so its
+// numbers go from the load to the tensor cores without being kept, as two tf32
+// numbers each against keys and queries in fp32 (22 bits of S_0 count, at every
+// size).  Nothing but reading S_0 takes long, so the rest hides behind it: the
+// loads come first, and a warp of its own takes the products of the tokens while
+// the others have S_0 times keys and queries.
+template <int D>
+struct DeltaFewSmem {
+    static constexpr int W = D / 16, ROW = D + 4;           // floats of a row of keys: lanes g * ROW + 8t differ in their banks
+    float k[8][ROW], q[8][ROW];
+    uint4 k16[8 * D / 8], q16[8 * D / 8];                   // as delta_products takes them
+    float kk[8 * 12], qk[8 * 12], inv[64], us[W][8 * DT_U];
+    uint64_t anc[8], uni[8];
+    Sum2 g[8];
+    int up[8];
+    float eg[8], b[8];
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * (D / 16 + 1), D == 128 ? 2 : 4) delta_few_kernel(const __grid_constant__ DeltaTreeArgs a) {
+    using Smem = DeltaFewSmem<D>;
+    constexpr int KB = D / 32, UNITS = D / 8, W = Smem::W;
+    __shared__ __align__(16) Smem sm;
+    pdl_wait();
+    pdl_trigger();
+    const int h = blockIdx.x, s = blockIdx.y, hk = h / a.ratio;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const DeltaTokens d = {sm.k16, sm.q16, sm.kk, sm.qk, sm.inv, sm.anc, sm.uni, sm.g, sm.up, sm.eg, sm.b, 12};
+    int first;
+    if (warp == W) {
+        const int n = draft_range(a.d, s, first, g_draft_skipped);
+        if (n == 0) return;
+        uint64_t mask[2] = {~0ull, 0};
+        float la[2] = {0.0f, 0.0f};
+        const int64_t row = static_cast<int64_t>(first + lane) * a.hv + h;
+        if (lane < n) {
+            if (a.d.tree) mask[0] = a.d.tree[first + lane];
+            la[0] = a.log_a[row];
+        }
+        if (lane < 8) sm.b[lane] = lane < n ? a.b[row] : 0.0f;
+        delta_sums(d, n, mask, la);
+        __syncthreads();
+        delta_products<D>(d, 8, 0, 0);
+        __syncwarp();
+        delta_inverse(d, 0);
+        __syncthreads();
+        return;
+    }
+    uint32_t w[KB][2][8];                                   // rows g and g + 8
+    {
+        const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + warp * 16 + g) * D + 8 * t;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            load32(S + 32 * b, w[b][0]);
+            load32(S + 8 * D + 32 * b, w[b][1]);
+        }
+    }
+    const int n = draft_range(a.d, s, first, g_draft_skipped);
+    if (n == 0) return;
+    const uint16_t* rows = a.qkv + static_cast<int64_t>(first) * a.c_conv;
+    for (int e = tid; e < 8 * UNITS; e += 32 * W) {
+        const int i = e / UNITS, c = e % UNITS, to = i * UNITS + (c ^ (4 * (i & 1)));
+        const uint16_t* row = rows + static_cast<int64_t>(i) * a.c_conv + hk * D + 8 * c;
+        const uint4 zero = make_uint4(0, 0, 0, 0), x = i < n ? *reinterpret_cast<const uint4*>(row) : zero;
+        const uint4 y = i < n ? *reinterpret_cast<const uint4*>(row + a.c_qk) : zero;
+        sm.q16[to] = x;
+        sm.k16[to] = y;
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            *reinterpret_cast<float2*>(&sm.q[i][8 * c + 2 * m]) = __half22float2(*reinterpret_cast<const __half2*>(&xs[m]));
+            *reinterpret_cast<float2*>(&sm.k[i][8 * c + 2 * m]) = __half22float2(*reinterpret_cast<const __half2*>(&ys[m]));
+        }
+    }
+    float r[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int i = 2 * t + (m & 1);
+        r[m] = i < n ? __half2float(__ushort_as_half(rows[static_cast<int64_t>(i) * a.c_conv + 2 * a.c_qk + h * D + warp * 16 + g + 8 * (m >> 1)])) : 0.0f;
+    }
+    __syncthreads();
+    float kh[4] = {}, kl[4] = {}, qh[4] = {}, ql[4] = {};
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+        float ke[8], qe[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            *reinterpret_cast<float4*>(&ke[4 * e]) = *reinterpret_cast<const float4*>(&sm.k[g][32 * b + 8 * t + 4 * e]);
+            *reinterpret_cast<float4*>(&qe[4 * e]) = *reinterpret_cast<const float4*>(&sm.q[g][32 * b + 8 * t + 4 * e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const Tf32 a0(__uint_as_float(w[b][0][e])), a1(__uint_as_float(w[b][1][e])), a2(__uint_as_float(w[b][0][e + 1])),
+                a3(__uint_as_float(w[b][1][e + 1]));
+            const uint32_t k0 = __float_as_uint(ke[e]), k1 = __float_as_uint(ke[e + 1]), q0 = __float_as_uint(qe[e]), q1 = __float_as_uint(qe[e + 1]);
+            mma_tf32(kh, a0.hi, a1.hi, a2.hi, a3.hi, k0, k1);
+            mma_tf32(qh, a0.hi, a1.hi, a2.hi, a3.hi, q0, q1);
+            mma_tf32(kl, a0.lo, a1.lo, a2.lo, a3.lo, k0, k1);
+            mma_tf32(ql, a0.lo, a1.lo, a2.lo, a3.lo, q0, q1);
+        }
+    }
+    __syncthreads();
+    float xq[4], u[4], o[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float e = d.eg[2 * t + (m & 1)];
+        r[m] -= (kh[m] + kl[m]) * e;
+        xq[m] = (qh[m] + ql[m]) * e;
+    }
+    uint64_t bad = 0;
+    delta_block(d, 0, r, xq, sm.us[warp], bad, u, o);
+    if (delta_store(a, first, n, 0, h * D + warp * 16, u, o)) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
+}
+
 template <int D>
 static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
-    const int np = (a.d.max_new + 7) & ~7;
+    const int np = (a.d.max_new + 7) & ~7, heads = a.hv * a.d.n_seqs;
     static PerDeviceOnce once;
     once.run([](int) {
-        cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, 8).end);
+        cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
     });
+    if (a.d.max_new <= 8 && heads > 152) return launch_dependent(delta_few_kernel<D>, dim3(a.hv, a.d.n_seqs), dim3(32 * (D / 16 + 1)), 0, st, a);
     // the whole head in a CTA, or its rows in several where that leaves SMs without one
     int warps = D / 16;
-    while (warps > 2 && a.hv * a.d.n_seqs * (D / 16 / warps) < 152) warps >>= 1;
+    while (warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
     return launch_dependent(delta_tree_kernel<D>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
                             static_cast<size_t>(DeltaTreeSmem<D>(np, warps).end), st, a);
 }
@@ -515,7 +785,8 @@ cudaError_t launch_delta_tree(const gdn_layer& L, const DraftTokens& d, const ui
     a.hv = L.n_v_heads;
     a.ratio = L.n_v_heads / L.n_qk_heads;
     a.c_qk = L.n_qk_heads * L.dk;
-    a.c_conv = 2 * a.c_qk + L.n_v_heads * L.dv;
+    a.c_v = L.n_v_heads * L.dv;
+    a.c_conv = 2 * a.c_qk + a.c_v;
     return L.dk == 128 ? delta_tree_launch<128>(a, st) : delta_tree_launch<64>(a, st);
 }
 
