@@ -19,6 +19,17 @@ static __device__ int g_draft_skipped;    // an offset or node of the caller's, 
 
 constexpr float LOG_A_MIN = -1.0e4f;      // e^-10000 is 0 in fp32, and sums of it stay finite (a = 0: log a = -inf)
 
+// N bytes from global to shared memory, without a register in between.
+template <int N>
+__device__ __forceinline__ void cp_async(void* to, const void* from) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ------------------------------------------------------------ conv
 
 struct ConvTreeArgs {
@@ -34,33 +45,33 @@ struct ConvTreeArgs {
     uint16_t* out;         // fp16 [n_tokens][c_conv]
     float* log_a;
     float* b;
-    int c_conv, n_heads, n_qk_norm, n_q, hv, head_blocks;
+    int c_conv, n_heads, n_qk_norm, n_q, hv, col_blocks;
     bool wide;             // rows of qkvz start on 16 bytes
     float eps, q_scale;
 };
 
-constexpr int CT_WARPS = 8;
-constexpr int CT_TOKENS = 32;              // most tokens of a block
+constexpr int CT_THREADS = 256;
+constexpr int CT_COLS = 512;               // channels of a block
+constexpr int CT_SLOTS = CT_COLS / 8;      // threads of a token
 
-// Block (token run, head group, sequence): a warp per head, a thread for 8 of its
-// channels, so that 2 (d = 128) or 4 tokens run side by side, CT_STEP of each in
-// flight.  The taps' weights stay in registers; a raw input is read by up to four
-// tokens, from L1 after the first.  The last slice of y computes the gates.
+// Block (CT_COLS channels, sequence): all raw inputs of the sequence's tokens to
+// shared memory at once, each read once, and from there to the up to four tokens
+// that have them as a tap.  A thread has 8 channels, their weights in registers, of
+// every fourth token.  The last block of x computes the gates.
 template <int D>
-__global__ void __launch_bounds__(CT_WARPS * 32, 2) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
-    constexpr int LANES = D / 8, SIDE = 32 / LANES, STEP = 2;
-    __shared__ int at[CT_TOKENS][4];       // rows of the taps from the sequence's first, oldest first; -1, -2, -3: the conv state
-    __shared__ float tail[CT_WARPS * D * 3];
+__global__ void __launch_bounds__(CT_THREADS, 2) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
+    extern __shared__ __align__(16) unsigned char raw[];    // raw inputs [token][CT_COLS] bf16, the conv state [CT_COLS][3] fp32
+    __shared__ uint64_t anc[GDN_MAX_NEW];
+    __shared__ int at[GDN_MAX_NEW][4];     // the taps' tokens, oldest first; -1, -2, -3: the conv state
     pdl_wait();
     pdl_trigger();
-    const int s = blockIdx.z, tid = threadIdx.x;
+    const int s = blockIdx.y, tid = threadIdx.x;
     int first;
     const int n = draft_range(a.d, s, first, g_draft_skipped);
-    const int i0 = blockIdx.x * CT_TOKENS, i1 = min(n, i0 + CT_TOKENS);
-    if (i0 >= i1) return;
-    if (static_cast<int>(blockIdx.y) == a.head_blocks) {
-        for (int e = tid; e < (i1 - i0) * a.hv; e += blockDim.x) {
-            const int64_t t = first + i0 + e / a.hv;
+    if (n == 0) return;
+    if (static_cast<int>(blockIdx.x) == a.col_blocks) {
+        for (int e = tid; e < n * a.hv; e += CT_THREADS) {
+            const int64_t t = first + e / a.hv;
             const int h = e % a.hv;
             if (GDN_IN_RANGE(g_draft_error, t < a.d.n_tokens))
                 gate_values(a.ba[t * a.ld_ba + h], a.ba[t * a.ld_ba + a.hv + h], a.A_log[h], a.dt_bias[h], a.log_a[t * a.hv + h],
@@ -68,88 +79,92 @@ __global__ void __launch_bounds__(CT_WARPS * 32, 2) conv_tree_kernel(const __gri
         }
         return;
     }
-    const int head0 = blockIdx.y * CT_WARPS, heads = min(CT_WARPS, a.n_heads - head0);
-    const int head = head0 + (tid >> 5), lane = tid & 31, sub = lane % LANES, side = lane / LANES;
-    float w[8][4];
-    const int c0 = head * D + 8 * sub;
-    if (head < a.n_heads) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 v = *reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(c0 + e) * 4);
-            w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+    const int col0 = blockIdx.x * CT_COLS, slot = tid % CT_SLOTS, c0 = col0 + 8 * slot;
+    const bool in = c0 < a.c_conv;         // heads are whole multiples of 8 channels
+    float* tail = reinterpret_cast<float*>(raw + a.d.max_new * CT_COLS * 2);
+    if (in)
+        for (int i = tid / CT_SLOTS; i < n; i += CT_THREADS / CT_SLOTS) {
+            unsigned char* to = raw + (i * CT_SLOTS + slot) * 16;
+            const uint16_t* src = a.qkvz + static_cast<int64_t>(first + i) * a.ld_qkvz + c0;
+            if (a.wide) {
+                cp_async<16>(to, src);
+            } else {
+                cp_async<8>(to, src);
+                cp_async<8>(to + 8, src + 4);
+            }
         }
-    }
-    if (tid < i1 - i0) {
-        int x = i0 + tid;
+    for (int e = tid; e < CT_COLS * 3; e += CT_THREADS)
+        if (col0 * 3 + e < a.c_conv * 3) cp_async<4>(tail + e, a.tail + (static_cast<int64_t>(s) * a.c_conv + col0) * 3 + e);
+    if (tid < n) anc[tid] = draft_ancestors(a.d, first, tid);
+    float4 w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w[e] = in ? *reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(c0 + e) * 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncthreads();
+    if (tid < n) {
+        int x = tid;
         at[tid][3] = x;
 #pragma unroll
         for (int m = 2; m >= 0; --m) {
-            x = x < 0 ? x - 1 : draft_parent(draft_ancestors(a.d, first, x));
+            x = x < 0 ? x - 1 : draft_parent(anc[x]);
             at[tid][m] = x;
         }
     }
-    const float* old = a.tail + (static_cast<int64_t>(s) * a.c_conv + head0 * D) * 3;
-    for (int e = tid; e < heads * D * 3; e += blockDim.x) tail[e] = old[e];
+    cp_async_wait();
     __syncthreads();
-    if (head >= a.n_heads) return;
+    const int head = c0 / D;
     const bool norm = head < a.n_qk_norm;
     const float mul = head < a.n_q ? a.q_scale : 1.0f;
-    const float* mine = tail + ((tid >> 5) * D + 8 * sub) * 3;
-    const uint16_t* src = a.qkvz + static_cast<int64_t>(first) * a.ld_qkvz + c0;
+    const float* mine = tail + 24 * slot;
     bool over = false;
-    for (int i = i0 + side; i - side < i1; i += SIDE * STEP) {
-        uint4 x[STEP][4];
+    // a warp's lanes share the token
+    for (int i = tid / CT_SLOTS; i < n; i += CT_THREADS / CT_SLOTS) {
+        const int4 taps = *reinterpret_cast<const int4*>(at[i]);
+        const int row[4] = {taps.x, taps.y, taps.z, taps.w};
+        float v[4][8];
 #pragma unroll
-        for (int k = 0; k < STEP; ++k) {
-            const int r = min(i + k * SIDE, i1 - 1) - i0;
+        for (int m = 0; m < 4; ++m) {
+            const uint4 x = *reinterpret_cast<const uint4*>(raw + (max(row[m], 0) * CT_SLOTS + slot) * 16);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int64_t row = max(at[r][m], 0);
-                if (a.wide) {
-                    x[k][m] = *reinterpret_cast<const uint4*>(src + row * a.ld_qkvz);
-                } else {
-                    const uint2 lo = *reinterpret_cast<const uint2*>(src + row * a.ld_qkvz), hi = *reinterpret_cast<const uint2*>(src + row * a.ld_qkvz + 4);
-                    x[k][m] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                }
+            for (int e = 0; e < 4; ++e) {
+                v[m][2 * e] = __uint_as_float(u[e] << 16);
+                v[m][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
             }
+            if (m < 3 && row[m] < 0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[m][e] = mine[3 * e + 3 + row[m]];
+        }
+        float y[8], ss = 0.0f, top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            y[e] = conv4_silu(w[e], v[0][e], v[1][e], v[2][e], v[3][e]);
+            ss = fmaf(y[e], y[e], ss);
         }
 #pragma unroll
-        for (int k = 0; k < STEP; ++k) {
-            const int r = min(i + k * SIDE, i1 - 1) - i0;
-            float y[8], ss = 0.0f;
+        for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (norm) {
+            const float f = rsqrtf(ss + a.eps) * mul;
+            over |= in && !(ss <= 3.0e38f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint32_t u = reinterpret_cast<const uint32_t*>(&x[k][m])[e >> 1];
-                    v[m] = __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
-                }
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    if (at[r][m] < 0) v[m] = mine[3 * e + 3 + at[r][m]];
-                y[e] = conv4_silu(make_float4(w[e][0], w[e][1], w[e][2], w[e][3]), v[0], v[1], v[2], v[3]);
-                ss = fmaf(y[e], y[e], ss);
-            }
-            if (norm) {
-#pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float f = rsqrtf(ss + a.eps) * mul;
-                over |= !(ss <= 3.0e38f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= f;
-            }
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf_nan(top, fabsf(y[e]));
-            over |= !(top <= 65504.0f);
-            const int64_t row = first + i + k * SIDE;
-            if (i + k * SIDE < i1 && GDN_IN_RANGE(g_draft_error, row < a.d.n_tokens && c0 + 8 <= a.c_conv))
-                *reinterpret_cast<uint4*>(a.out + row * a.c_conv + c0) =
-                    make_uint4(f16x2_bits(y[0], y[1]), f16x2_bits(y[2], y[3]), f16x2_bits(y[4], y[5]), f16x2_bits(y[6], y[7]));
+            for (int e = 0; e < 8; ++e) y[e] *= f;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf_nan(top, fabsf(y[e]));
+        over |= in && !(top <= 65504.0f);
+        if (in && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens && c0 + 8 <= a.c_conv))
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(first + i) * a.c_conv + c0) =
+                make_uint4(f16x2_bits(y[0], y[1]), f16x2_bits(y[2], y[3]), f16x2_bits(y[4], y[5]), f16x2_bits(y[6], y[7]));
     }
     if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
+}
+
+template <int D>
+static cudaError_t conv_tree_launch(const ConvTreeArgs& a, dim3 grid, cudaStream_t st) {
+    constexpr int TAIL = CT_COLS * 12;
+    static PerDeviceOnce once;
+    once.run([](int) { cudaFuncSetAttribute(conv_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * CT_COLS * 2 + TAIL); });
+    return launch_dependent(conv_tree_kernel<D>, grid, dim3(CT_THREADS), static_cast<size_t>(a.d.max_new * CT_COLS * 2 + TAIL), st, a);
 }
 
 cudaError_t launch_conv_tree(const gdn_layer& L, const DraftTokens& d, const uint16_t* qkvz, int64_t ld_qkvz, const float* ba, int64_t ld_ba,
@@ -172,12 +187,12 @@ cudaError_t launch_conv_tree(const gdn_layer& L, const DraftTokens& d, const uin
     a.n_qk_norm = 2 * L.n_qk_heads;
     a.n_q = L.n_qk_heads;
     a.hv = L.n_v_heads;
-    a.head_blocks = (a.n_heads + CT_WARPS - 1) / CT_WARPS;
+    a.col_blocks = (a.c_conv + CT_COLS - 1) / CT_COLS;
     a.eps = L.eps_l2;
     a.q_scale = L.q_scale;
     a.wide = reinterpret_cast<uintptr_t>(qkvz) % 16 == 0 && ld_qkvz % 8 == 0;
-    const dim3 grid((d.max_new + CT_TOKENS - 1) / CT_TOKENS, a.head_blocks + (L.gate_log_a ? 0 : 1), d.n_seqs);
-    return launch_dependent(L.dk == 128 ? conv_tree_kernel<128> : conv_tree_kernel<64>, grid, dim3(CT_WARPS * 32), 0, st, a);
+    const dim3 grid(a.col_blocks + (L.gate_log_a ? 0 : 1), d.n_seqs);
+    return L.dk == 128 ? conv_tree_launch<128>(a, grid, st) : conv_tree_launch<64>(a, grid, st);
 }
 
 // ------------------------------------------------------------ delta rule
@@ -492,11 +507,12 @@ __device__ __forceinline__ void delta_block(const DeltaTokens& d, int bi, float 
 __device__ __forceinline__ bool delta_store(const DeltaTreeArgs& a, int first, int n, int bi, int64_t col, const float (&u)[4], const float (&o)[4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     bool over = false;
+    const int64_t at = static_cast<int64_t>(first + 8 * bi + 2 * t) * a.c_v + col + g;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         const int i = 8 * bi + 2 * t + (m & 1);
         if (i < n && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens)) {
-            const int64_t to = static_cast<int64_t>(first + i) * a.c_v + col + g + 8 * (m >> 1);
+            const int64_t to = at + static_cast<int64_t>(m & 1 ? a.c_v : 0) + 8 * (m >> 1);
             a.delta[to] = u[m];
             a.o[to] = __half_as_ushort(__float2half_rn(o[m]));
             over |= !(fabsf(o[m]) <= 65504.0f);
@@ -614,9 +630,16 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
     });
     __syncthreads();
     const int sw = t ^ (4 * (g & 1));       // the unit of columns 8t .. 8t+7 in rows of g's parity
-    for (int bi = 0, turn = 0; bi < nb; ++bi)
-        for (int jt = 0; 2 * jt <= bi; ++jt)
-            if ((2 * jt + 1 >= bi || d.uni[bi] >> 16 * jt & 0xffff) && turn++ % warps == warp) delta_products<D>(d, np, jt, bi);
+    // where a block has ancestors, in turn
+    for (int bi = 0, turn = warp; bi < nb; ++bi) {
+        const uint64_t before = d.uni[bi];
+#pragma unroll 1
+        for (int jt = 0; 2 * jt <= bi; ++jt) {
+            if (2 * jt + 1 < bi && !(before >> 16 * jt & 0xffff)) continue;
+            if (turn == 0) delta_products<D>(d, np, jt, bi);
+            turn = turn == 0 ? warps - 1 : turn - 1;
+        }
+    }
     __syncthreads();
     for (int bi = warp; bi < nb; bi += warps) delta_inverse(d, bi);
     float xk[4], xq[4];
@@ -765,9 +788,10 @@ static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
         cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
     });
     if (a.d.max_new <= 8 && heads > 152) return launch_dependent(delta_few_kernel<D>, dim3(a.hv, a.d.n_seqs), dim3(32 * (D / 16 + 1)), 0, st, a);
-    // the whole head in a CTA, or its rows in several where that leaves SMs without one
+    // the whole head in a CTA, or, where that leaves SMs without one and the tokens' own work is little beside S_0, its
+    // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 19.5)
     int warps = D / 16;
-    while (warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
+    while (np <= 16 && warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
     return launch_dependent(delta_tree_kernel<D>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
                             static_cast<size_t>(DeltaTreeSmem<D>(np, warps).end), st, a);
 }
