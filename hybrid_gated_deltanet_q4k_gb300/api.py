@@ -55,7 +55,8 @@ class DeviceLayer:
         for k in ("conv_w", "A_log", "dt_bias", "norm_w"):
             self.dev[k] = t(params[k].astype(np.float32))
         self.eps_l2, self.eps_rms = eps_l2, eps_rms
-        self._struct = None
+        self._struct, self._dll = None, self.lib.dll
+        self._sizes = (spec.c_conv, spec.n_v_heads, spec.dv)
         self.q_scale = spec.dk ** -0.5 if q_scale is None else q_scale
 
     def struct(self, gate_log_a=None, gate_b=None) -> gl.GdnLayer:
@@ -157,16 +158,6 @@ class DeviceLayer:
                                          gl.ptr(ckpt_conv), gl.ptr(workspace), workspace.numel(),
                                          gl.stream_handle(stream), check=check)
 
-    def _drafts(self, n_seqs: int, n_tokens: int, cu, max_new: int, tree, device: int):
-        """The common arguments of the calls over drafted tokens, checked."""
-        if device < 0:
-            raise ValueError("memory of a CUDA device is required")
-        if cu is not None:
-            _vector(cu, torch.int32, n_seqs + 1, "cu", device)
-        if tree is not None:
-            _vector(tree, torch.int64, n_tokens, "tree", device)
-        return gl.ptr(cu), n_tokens, max_new, gl.ptr(tree), n_seqs
-
     def conv_tree(self, qkvz: torch.Tensor, ba: torch.Tensor | None, conv_state: torch.Tensor, qkv: torch.Tensor,
                   log_a: torch.Tensor | None = None, b: torch.Tensor | None = None, cu: torch.Tensor | None = None, max_new: int = 1,
                   tree: torch.Tensor | None = None, stream=None, check=True) -> int:
@@ -174,18 +165,18 @@ class DeviceLayer:
         ba fp32 [T][2 Hv] are the projection's rows, conv_state fp32 [n_seqs][C_conv][3] is only read; qkv fp16
         [T][C_conv], log_a and b fp32 [T][Hv] are written.  cu int32 [n_seqs + 1] (None: max_new tokens each),
         tree int64 [T] mask words (None: chains)."""
-        sp, dev, t = self.spec, conv_state.get_device(), qkvz.shape[0]
-        ld = _matrix(qkvz, torch.bfloat16, (t, sp.c_conv), "qkvz", dev, wider=True)
-        _block(conv_state, torch.float32, (conv_state.shape[0], sp.c_conv, 3), "conv_state", dev)
-        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
-        if ba is None or log_a is None or b is None:
-            raise ValueError("ba, log_a and b are required")
-        ld_ba = _matrix(ba, torch.float32, (t, 2 * sp.n_v_heads), "ba", dev, wider=True)
-        _block(log_a, torch.float32, (t, sp.n_v_heads), "log_a", dev)
-        _block(b, torch.float32, (t, sp.n_v_heads), "b", dev)
-        return self.lib.gdn_conv_tree(self._ref(), gl.ptr(qkvz), ld, gl.ptr(ba), ld_ba, gl.ptr(conv_state),
-                                      *self._drafts(conv_state.shape[0], t, cu, max_new, tree, dev), gl.ptr(qkv), gl.ptr(log_a),
-                                      gl.ptr(b), gl.stream_handle(stream), check=check)
+        c, hv, _ = self._sizes
+        dev, s, t = conv_state.get_device(), conv_state.shape[0], qkvz.shape[0]
+        ld, ld_ba = _rows(qkvz, torch.bfloat16, c, "qkvz", dev), _rows(ba, torch.float32, 2 * hv, "ba", dev)
+        if not (_all(dev, torch.float32, s * c * 3, conv_state) and _all(dev, torch.float16, t * c, qkv) and
+                _all(dev, torch.float32, t * hv, log_a, b) and ba.shape[0] == t and _drafts_ok(dev, s, t, cu, tree)):
+            _refuse(dev, ("conv_state", conv_state, torch.float32, s * c * 3), ("qkv", qkv, torch.float16, t * c),
+                    ("log_a", log_a, torch.float32, t * hv), ("b", b, torch.float32, t * hv), ("ba", ba, torch.float32, t * ba.shape[1]),
+                    *_drafts_named(s, t, cu, tree))
+        r = self._dll.gdn_conv_tree(self._ref(), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
+                                    cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+                                    qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_handle(stream))
+        return r if not r or not check else self.lib.refused("gdn_conv_tree", r)
 
     def delta_tree(self, qkv: torch.Tensor, log_a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
                    delta: torch.Tensor, cu: torch.Tensor | None = None, max_new: int = 1, tree: torch.Tensor | None = None, stream=None,
@@ -193,16 +184,18 @@ class DeviceLayer:
         """Enqueue gdn_delta_tree: the delta rule over each sequence's drafted tokens from its held state fp32
         [n_seqs][Hv][dv][dk], which stays.  qkv fp16 [T][C_conv], log_a and b fp32 [T][Hv] as conv_tree writes them;
         o fp16 [T][Hv][dv] and delta fp32 [T][Hv][dv] (for delta_commit) are written."""
-        sp, dev, t = self.spec, state.get_device(), qkv.shape[0]
-        _block(state, torch.float32, (state.shape[0], sp.n_v_heads, sp.dv, sp.dk), "state", dev)
-        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
-        for name, x in (("log_a", log_a), ("b", b)):
-            _block(x, torch.float32, (t, sp.n_v_heads), name, dev)
-        for name, x, dtype in (("o", o, torch.float16), ("delta", delta, torch.float32)):
-            _block(x, dtype, (t, sp.n_v_heads, sp.dv), name, dev)
-        return self.lib.gdn_delta_tree(self._ref(), gl.ptr(qkv), gl.ptr(log_a), gl.ptr(b), gl.ptr(state),
-                                       *self._drafts(state.shape[0], t, cu, max_new, tree, dev), gl.ptr(o), gl.ptr(delta),
-                                       gl.stream_handle(stream), check=check)
+        c, hv, d = self._sizes
+        dev, s, t = state.get_device(), state.shape[0], qkv.shape[0]
+        if not (_all(dev, torch.float32, s * hv * d * d, state) and _all(dev, torch.float16, t * c, qkv) and
+                _all(dev, torch.float32, t * hv, log_a, b) and _all(dev, torch.float16, t * hv * d, o) and
+                _all(dev, torch.float32, t * hv * d, delta) and _drafts_ok(dev, s, t, cu, tree)):
+            _refuse(dev, ("state", state, torch.float32, s * hv * d * d), ("qkv", qkv, torch.float16, t * c),
+                    ("log_a", log_a, torch.float32, t * hv), ("b", b, torch.float32, t * hv), ("o", o, torch.float16, t * hv * d),
+                    ("delta", delta, torch.float32, t * hv * d), *_drafts_named(s, t, cu, tree))
+        r = self._dll.gdn_delta_tree(self._ref(), qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), state.data_ptr(),
+                                     cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+                                     o.data_ptr(), delta.data_ptr(), gl.stream_handle(stream))
+        return r if not r or not check else self.lib.refused("gdn_delta_tree", r)
 
     def delta_commit(self, qkv: torch.Tensor, log_a: torch.Tensor, delta: torch.Tensor, node: torch.Tensor, state_in: torch.Tensor,
                      state_out: torch.Tensor, qkvz: torch.Tensor | None = None, conv_in: torch.Tensor | None = None,
@@ -211,40 +204,70 @@ class DeviceLayer:
         """Enqueue gdn_delta_commit: the state (and, with qkvz, the conv state) after token node[s] (int32 [n_seqs], -1:
         unchanged) of each sequence, from what conv_tree and delta_tree were given and left.  The outputs may be
         the inputs."""
-        sp, dev, t, s = self.spec, state_in.get_device(), qkv.shape[0], state_in.shape[0]
-        for name, x in (("state_in", state_in), ("state_out", state_out)):
-            _block(x, torch.float32, (s, sp.n_v_heads, sp.dv, sp.dk), name, dev)
-        _block(qkv, torch.float16, (t, sp.c_conv), "qkv", dev)
-        _block(log_a, torch.float32, (t, sp.n_v_heads), "log_a", dev)
-        _block(delta, torch.float32, (t, sp.n_v_heads, sp.dv), "delta", dev)
-        _vector(node, torch.int32, s, "node", dev)
-        ld = 0
+        c, hv, d = self._sizes
+        dev, s, t, ld = state_in.get_device(), state_in.shape[0], qkv.shape[0], 0
+        ok = (_all(dev, torch.float32, s * hv * d * d, state_in, state_out) and _all(dev, torch.float16, t * c, qkv) and
+              _all(dev, torch.float32, t * hv, log_a) and _all(dev, torch.float32, t * hv * d, delta) and
+              _all(dev, torch.int32, s, node) and _drafts_ok(dev, s, t, cu, tree))
         if qkvz is not None:
-            ld = _matrix(qkvz, torch.bfloat16, (t, sp.c_conv), "qkvz", dev, wider=True)
+            ld = _rows(qkvz, torch.bfloat16, c, "qkvz", dev)
             if conv_in is None or conv_out is None:
                 raise ValueError("conv_in and conv_out are required with qkvz")
-            for name, x in (("conv_in", conv_in), ("conv_out", conv_out)):
-                _block(x, torch.float32, (s, sp.c_conv, 3), name, dev)
+            ok = ok and qkvz.shape[0] == t and _all(dev, torch.float32, s * c * 3, conv_in, conv_out)
         elif conv_in is not None or conv_out is not None:
             raise ValueError("conv_in and conv_out need qkvz")
-        return self.lib.gdn_delta_commit(self._ref(), gl.ptr(qkv), gl.ptr(log_a), gl.ptr(delta),
-                                         *self._drafts(s, t, cu, max_new, tree, dev), gl.ptr(node), gl.ptr(state_in), gl.ptr(state_out),
-                                         gl.ptr(qkvz), ld, gl.ptr(conv_in), gl.ptr(conv_out), gl.stream_handle(stream), check=check)
+        if not ok:
+            more = () if qkvz is None else (("conv_in", conv_in, torch.float32, s * c * 3), ("conv_out", conv_out, torch.float32, s * c * 3),
+                                            ("qkvz", qkvz, torch.bfloat16, t * qkvz.shape[1]))
+            _refuse(dev, ("state_in", state_in, torch.float32, s * hv * d * d), ("state_out", state_out, torch.float32, s * hv * d * d),
+                    ("qkv", qkv, torch.float16, t * c), ("log_a", log_a, torch.float32, t * hv), ("delta", delta, torch.float32, t * hv * d),
+                    ("node", node, torch.int32, s), *more, *_drafts_named(s, t, cu, tree))
+        r = self._dll.gdn_delta_commit(self._ref(), qkv.data_ptr(), log_a.data_ptr(), delta.data_ptr(), cu if cu is None else cu.data_ptr(),
+                                       t, max_new, tree if tree is None else tree.data_ptr(), s, node.data_ptr(), state_in.data_ptr(),
+                                       state_out.data_ptr(), qkvz if qkvz is None else qkvz.data_ptr(), ld,
+                                       conv_in if conv_in is None else conv_in.data_ptr(),
+                                       conv_out if conv_out is None else conv_out.data_ptr(), gl.stream_handle(stream))
+        return r if not r or not check else self.lib.refused("gdn_delta_commit", r)
 
 
-def _block(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: int):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
-        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on device cuda:{device} are required")
+# The checks of the calls that a step makes many times over: all of them in one pass over a few attributes; which one
+# failed is looked up only then (_refuse).
+
+def _all(dev: int, dtype: torch.dtype, n: int, *tensors) -> bool:
+    """Whether all are contiguous, of one type and number of elements, on device ``dev``."""
+    for t in tensors:
+        if t is None or t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return dev >= 0
 
 
-def _matrix(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: int, wider: bool = False) -> int:
-    """Elements between the rows of a matrix (whose rows may have more columns, if ``wider``)."""
-    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != shape[0] or t.get_device() != device or device < 0 or (
-            t.shape[1] < shape[1] if wider else t.shape[1] != shape[1]):
-        raise ValueError(f"{name}: {dtype} {list(shape)} on device cuda:{device} are required")
-    if shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if shape[0] > 1 else t.shape[1]
+def _drafts_ok(dev: int, s: int, t: int, cu, tree) -> bool:
+    return (cu is None or _all(dev, torch.int32, s + 1, cu)) and (tree is None or _all(dev, torch.int64, t, tree))
+
+
+def _drafts_named(s: int, t: int, cu, tree) -> tuple:
+    return (() if cu is None else (("cu", cu, torch.int32, s + 1),)) + (() if tree is None else (("tree", tree, torch.int64, t),))
+
+
+def _refuse(dev: int, *named):
+    """Name the first of (name, tensor, dtype, elements) that is not as required."""
+    if dev < 0:
+        raise ValueError("memory of a CUDA device is required")
+    for name, t, dtype, n in named:
+        if not _all(dev, dtype, n, t):
+            raise ValueError(f"{name}: {n} contiguous {dtype} on device cuda:{dev} are required")
+    raise ValueError("arguments that do not belong together")
+
+
+def _rows(t: torch.Tensor | None, dtype: torch.dtype, width: int, name: str, dev: int) -> int:
+    """Elements between the rows of a matrix of at least ``width`` columns."""
+    if t is None or t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: {dtype} [rows][at least {width}] on device cuda:{dev} is required")
+    n, cols = t.shape
+    ld, one = t.stride()
+    if cols < width or (n and cols > 1 and one != 1):
+        raise ValueError(f"{name}: rows of at least {width} contiguous elements are required")
+    return ld if n > 1 else cols
 
 
 def _heads(t: torch.Tensor, name: str, device: int, width=None) -> int:
@@ -436,11 +459,12 @@ class KvPages:
         if block_table.dtype is not torch.int32 or block_table.dim() != 2 or self._device < 0:
             raise ValueError("block_table: int32 [n_seqs][max_blocks] on a CUDA device is required")
         self.n_seqs = block_table.shape[0]
-        ld = _matrix(block_table, torch.int32, tuple(block_table.shape), "block_table", self._device)
+        ld = _rows(block_table, torch.int32, 1, "block_table", self._device)
         _vector(n_blocks, torch.int32, self.n_seqs, "n_blocks", self._device)
         _vector(free_pages, torch.int32, free_pages.numel(), "free_pages", self._device)
         _vector(n_free, torch.int32, 1, "n_free", self._device)
         self.lib = gl.load(debug=debug)
+        self._dll = self.lib.dll
         self.page_tokens, self.block_table, self.n_blocks, self.free_pages, self.n_free = (page_tokens, block_table, n_blocks,
                                                                                            free_pages, n_free)
         self.struct = gl.GdnKvPages(page_tokens, block_table.shape[1], free_pages.numel(), gl.ptr(block_table), ld,
@@ -458,20 +482,26 @@ class KvPages:
         """Enqueue gdn_kv_extend: pages for n_new int32 [n_seqs] tokens after the lens int32 [n_seqs] held ones; lens_out
         (may be lens), cu int32 [n_seqs + 1], positions int32 [T] and slots int64 [T] are written, T at least the
         number of new tokens.  A sequence that found no pages keeps its length and has slots -1."""
-        n, t = self.n_seqs, positions.numel()
-        for name, x, size in (("lens", lens, n), ("n_new", n_new, n), ("lens_out", lens_out, n), ("cu", cu, n + 1),
-                              ("positions", positions, t)):
-            _vector(x, torch.int32, size, name, self._device)
-        _vector(slots, torch.int64, t, "slots", self._device)
-        if tree is not None:
-            _vector(tree, torch.int64, t, "tree", self._device)
-        return self.lib.gdn_kv_extend(self._ref, gl.ptr(lens), gl.ptr(n_new), n, gl.ptr(tree), t, gl.ptr(lens_out),
-                                      gl.ptr(cu), gl.ptr(positions), gl.ptr(slots), gl.stream_handle(stream), check=check)
+        n, t, dev = self.n_seqs, positions.numel(), self._device
+        if not (_all(dev, torch.int32, n, lens, n_new, lens_out) and _all(dev, torch.int32, n + 1, cu) and
+                _all(dev, torch.int32, t, positions) and _all(dev, torch.int64, t, slots) and
+                (tree is None or _all(dev, torch.int64, t, tree))):
+            _refuse(dev, ("lens", lens, torch.int32, n), ("n_new", n_new, torch.int32, n), ("lens_out", lens_out, torch.int32, n),
+                    ("cu", cu, torch.int32, n + 1), ("positions", positions, torch.int32, t), ("slots", slots, torch.int64, t),
+                    *(() if tree is None else (("tree", tree, torch.int64, t),)))
+        r = self._dll.gdn_kv_extend(self._ref, lens.data_ptr(), n_new.data_ptr(), n, tree if tree is None else tree.data_ptr(), t,
+                                    lens_out.data_ptr(), cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), gl.stream_handle(stream))
+        return r if not r or not check else self.lib.refused("gdn_kv_extend", r)
 
     def trim(self, keep: torch.Tensor, stream=None, check=True) -> int:
         """Enqueue gdn_kv_trim: the pages past the first keep int32 [n_seqs] tokens of each sequence become free."""
-        _vector(keep, torch.int32, self.n_seqs, "keep", self._device)
-        return self.lib.gdn_kv_trim(self._ref, gl.ptr(keep), self.n_seqs, gl.stream_handle(stream), check=check)
+        if not _all(self._device, torch.int32, self.n_seqs, keep):
+            _refuse(self._device, ("keep", keep, torch.int32, self.n_seqs))
+        r = self._dll.gdn_kv_trim(self._ref, keep.data_ptr(), self.n_seqs, gl.stream_handle(stream))
+        return r if not r or not check else self.lib.refused("gdn_kv_trim", r)
+
+
+_PROBABILITIES = {torch.float32: gl.GDN_P_F32, torch.bfloat16: gl.GDN_P_BF16}
 
 
 def verify(p: torch.Tensor, tokens: torch.Tensor, rows: torch.Tensor, ids: torch.Tensor, count: torch.Tensor, node: torch.Tensor,
@@ -482,26 +512,25 @@ def verify(p: torch.Tensor, tokens: torch.Tensor, rows: torch.Tensor, ids: torch
     token, q (the same type) the draft's or None, tokens int32 [T], u fp32 [T] and u_next fp32 [n_seqs] random numbers
     in [0, 1); without them p holds scores and the largest is the choice.  rows and ids int32 [T], count, node and
     next int32 [n_seqs] are written."""
-    dev, s = p.get_device(), count.numel()
-    if p.dtype not in (torch.float32, torch.bfloat16) or p.dim() != 2:
+    dev, s, code = p.get_device(), count.numel(), _PROBABILITIES.get(p.dtype)
+    if code is None or p.dim() != 2:
         raise ValueError("p: fp32 or bf16 [tokens][vocab] is required")
     t, vocab = p.shape
-    ld_p = _matrix(p, p.dtype, (t, vocab), "p", dev)
-    ld_q = 0 if q is None else _matrix(q, p.dtype, (t, vocab), "q", dev)
-    for name, x in (("tokens", tokens), ("rows", rows), ("ids", ids)):
-        _vector(x, torch.int32, t, name, dev)
-    for name, x in (("count", count), ("node", node), ("next", next)):
-        _vector(x, torch.int32, s, name, dev)
+    ld_p, ld_q = _rows(p, p.dtype, 1, "p", dev), 0
+    if q is not None:
+        ld_q = _rows(q, p.dtype, vocab, "q", dev)
+        if q.shape != p.shape:
+            raise ValueError("q: the shape of p is required")
     if (u is None) != (u_next is None):
         raise ValueError("u and u_next: both or neither")
-    if u is not None:
-        _vector(u, torch.float32, t, "u", dev)
-        _vector(u_next, torch.float32, s, "u_next", dev)
-    if cu is not None:
-        _vector(cu, torch.int32, s + 1, "cu", dev)
-    if tree is not None:
-        _vector(tree, torch.int64, t, "tree", dev)
-    code = gl.GDN_P_F32 if p.dtype is torch.float32 else gl.GDN_P_BF16
-    return gl.load(debug=debug).gdn_verify(code, gl.ptr(p), ld_p, gl.ptr(q), ld_q, vocab, gl.ptr(tokens), gl.ptr(cu), t, max_new,
-                                           gl.ptr(tree), s, gl.ptr(u), gl.ptr(u_next), gl.ptr(rows), gl.ptr(ids), gl.ptr(count),
-                                           gl.ptr(node), gl.ptr(next), gl.stream_handle(stream), check=check)
+    if not (_all(dev, torch.int32, t, tokens, rows, ids) and _all(dev, torch.int32, s, count, node, next) and _drafts_ok(dev, s, t, cu, tree) and
+            (u is None or (_all(dev, torch.float32, t, u) and _all(dev, torch.float32, s, u_next)))):
+        _refuse(dev, *((name, x, torch.int32, t) for name, x in (("tokens", tokens), ("rows", rows), ("ids", ids))),
+                *((name, x, torch.int32, s) for name, x in (("count", count), ("node", node), ("next", next))),
+                *(() if u is None else (("u", u, torch.float32, t), ("u_next", u_next, torch.float32, s))), *_drafts_named(s, t, cu, tree))
+    lib = gl.load(debug=debug)
+    r = lib.dll.gdn_verify(code, p.data_ptr(), ld_p, q if q is None else q.data_ptr(), ld_q, vocab, tokens.data_ptr(),
+                           cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+                           u if u is None else u.data_ptr(), u_next if u_next is None else u_next.data_ptr(), rows.data_ptr(),
+                           ids.data_ptr(), count.data_ptr(), node.data_ptr(), next.data_ptr(), gl.stream_handle(stream))
+    return r if not r or not check else lib.refused("gdn_verify", r)

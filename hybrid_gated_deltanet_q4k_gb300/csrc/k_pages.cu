@@ -6,11 +6,9 @@
 // GDN_MAX_SEQS), which every CTA takes for itself: a thread per sequence and
 // two scans.  From there tokens and pages are independent: each finds its
 // sequence by bisection of the sums in shared memory.  What is read by all
-// (lengths, pages held, the stack's height) is written last: by the one CTA, or
-// after a cluster's barrier, or by a second launch that waits for the first.
+// (lengths, pages held, the stack's height) is written last: by the one CTA, or by
+// a second launch that waits for the first.
 #include "common.cuh"
-
-#include <cooperative_groups.h>
 
 namespace gdn {
 
@@ -32,6 +30,7 @@ struct PagesArgs {
 };
 
 constexpr int PG_THREADS = 512;
+constexpr int PG_STEP = 4;
 static_assert(PG_THREADS >= GDN_MAX_SEQS, "a thread per sequence");
 
 __device__ __forceinline__ void pages_bad() { atomicCAS(&g_pages_skipped, 0, static_cast<int>(ERR_INDEX)); }
@@ -112,34 +111,61 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(const __grid_c
     __syncthreads();
     const int used = sm.used;
     if (tokens) {
-        const int step = gridDim.x * PG_THREADS;
-        for (int k = blockIdx.x * PG_THREADS + s; k < used; k += step) {
-            const int q = pages_find(sm.page, a.n_seqs, k);
-            const int64_t to = q * a.p.ld_table + sm.had[q] + (k - sm.page[q]);
-            if (GDN_IN_RANGE(g_pages_error, sm.had[q] >= 0 && sm.had[q] + (k - sm.page[q]) < a.p.max_blocks))
-                a.p.block_table[to] = a.p.free_pages[free - 1 - k];
+        const int64_t step = static_cast<int64_t>(gridDim.x) * PG_THREADS;
+        // PG_STEP at a time, so that their bisections and loads overlap
+        for (int64_t k0 = blockIdx.x * PG_THREADS + s; k0 < used; k0 += PG_STEP * step) {
+            int page[PG_STEP];
+            int64_t to[PG_STEP];
+#pragma unroll
+            for (int e = 0; e < PG_STEP; ++e) {
+                const int k = static_cast<int>(k0 + e * step < used ? k0 + e * step : k0), q = pages_find(sm.page, a.n_seqs, k);
+                const int b = sm.had[q] + (k - sm.page[q]);
+                page[e] = a.p.free_pages[free - 1 - k];
+                to[e] = GDN_IN_RANGE(g_pages_error, sm.had[q] >= 0 && b < a.p.max_blocks) ? q * a.p.ld_table + b : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < PG_STEP; ++e)
+                if (to[e] >= 0) a.p.block_table[to[e]] = page[e];
         }
-        for (int t = blockIdx.x * PG_THREADS + s; t < a.max_tokens; t += step) {
-            int64_t slot = -1;
-            int pos = 0;
-            if (t < sm.total) {
-                const int q = pages_find(sm.first, a.n_seqs, t), i = t - sm.first[q], h = sm.had[q];
+        for (int64_t t0 = blockIdx.x * PG_THREADS + s; t0 < a.max_tokens; t0 += PG_STEP * step) {
+            int64_t slot[PG_STEP];
+            int pos[PG_STEP], page[PG_STEP];
+#pragma unroll
+            for (int e = 0; e < PG_STEP; ++e) {
+                const int64_t t = t0 + e * step;
+                slot[e] = -1;
+                pos[e] = 0;
+                page[e] = -1;
+                if (t >= sm.total) continue;
+                const int q = pages_find(sm.first, a.n_seqs, static_cast<int>(t)), i = static_cast<int>(t) - sm.first[q], h = sm.had[q];
                 const int64_t at = static_cast<int64_t>(sm.len[q]) + i;
                 if (h >= 0) {
                     // a new block's page is where the loop above takes it from
                     const int b = static_cast<int>(at >> shift);
-                    const int page = b < h ? a.p.block_table[q * a.p.ld_table + b] : a.p.free_pages[free - 1 - (sm.page[q] + b - h)];
-                    if (page >= 0 && page < a.p.n_pages) slot = (static_cast<int64_t>(page) << shift) + (at & ((1 << shift) - 1));
-                    else pages_bad();
+                    page[e] = b < h ? a.p.block_table[q * a.p.ld_table + b] : a.p.free_pages[free - 1 - (sm.page[q] + b - h)];
+                    slot[e] = at & ((1 << shift) - 1);
                 }
-                pos = static_cast<int>(at);
+                pos[e] = static_cast<int>(at);
                 if (a.tree) {
-                    if (i < 64) pos = sm.len[q] + __popcll(a.tree[t] & ((1ull << i) - 1));
+                    if (i < 64) pos[e] = sm.len[q] + __popcll(a.tree[t] & ((1ull << i) - 1));
                     else pages_bad();
                 }
             }
-            a.slots[t] = slot;
-            a.positions[t] = pos;
+#pragma unroll
+            for (int e = 0; e < PG_STEP; ++e) {
+                const int64_t t = t0 + e * step;
+                if (t >= a.max_tokens) break;
+                if (slot[e] >= 0) {
+                    if (page[e] >= 0 && page[e] < a.p.n_pages) {
+                        slot[e] += static_cast<int64_t>(page[e]) << shift;
+                    } else {
+                        slot[e] = -1;
+                        pages_bad();
+                    }
+                }
+                a.slots[t] = slot[e];
+                a.positions[t] = pos[e];
+            }
         }
     }
     if (!last) return;
@@ -155,7 +181,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(const __grid_c
     }
 }
 
-__global__ void __launch_bounds__(PG_THREADS) pages_trim_kernel(const __grid_constant__ PagesArgs a) {
+__global__ void __launch_bounds__(PG_THREADS) pages_trim_kernel(const __grid_constant__ PagesArgs a, bool pages, bool last) {
     __shared__ int first[GDN_MAX_SEQS], held[GDN_MAX_SEQS];
     __shared__ int64_t warp_total[GDN_MAX_SEQS / 32];
     __shared__ int64_t sum;
@@ -179,15 +205,22 @@ __global__ void __launch_bounds__(PG_THREADS) pages_trim_kernel(const __grid_con
     const int64_t after = free + sum;
     if (after > a.p.n_pages) pages_bad();
     const int back = static_cast<int>(sum < 0x7fffffff ? sum : 0x7fffffff);
-    for (int64_t k = blockIdx.x * PG_THREADS + s; k < back; k += gridDim.x * PG_THREADS) {
-        const int64_t to = after - 1 - k;
-        if (to >= a.p.n_pages) continue;
-        const int q = pages_find(first, a.n_seqs, static_cast<int>(k));
-        a.p.free_pages[to] = a.p.block_table[q * a.p.ld_table + held[q] + (k - first[q])];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * PG_THREADS;
+    for (int64_t k0 = blockIdx.x * PG_THREADS + s; pages && k0 < back; k0 += PG_STEP * step) {
+        int page[PG_STEP];
+#pragma unroll
+        for (int e = 0; e < PG_STEP; ++e) {
+            const int k = static_cast<int>(k0 + e * step < back ? k0 + e * step : k0), q = pages_find(first, a.n_seqs, k);
+            page[e] = a.p.block_table[q * a.p.ld_table + held[q] + (k - first[q])];
+        }
+#pragma unroll
+        for (int e = 0; e < PG_STEP; ++e) {
+            const int64_t k = k0 + e * step, to = after - 1 - k;
+            if (k < back && to < a.p.n_pages) a.p.free_pages[to] = page[e];
+        }
     }
-    if (gridDim.x > 1) cooperative_groups::this_cluster().sync();
-    else __syncthreads();
-    if (blockIdx.x) return;
+    if (!last) return;
+    __syncthreads();
     if (in) a.p.n_blocks[s] = keep;
     if (s == 0) *a.p.n_free = static_cast<int>(after < a.p.n_pages ? after : a.p.n_pages);
 }
@@ -212,9 +245,8 @@ cudaError_t launch_kv_extend(const gdn_kv_pages& p, const int32_t* lens, const i
     a.positions = positions;
     a.slots = slots;
     // one CTA where its threads have a few tokens each, else all SMs and a second launch for what they read
-    constexpr int FEW = 4 * PG_THREADS;
-    if (max_tokens <= FEW) return launch_dependent(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, true, true);
-    const int64_t want = (max_tokens + 2 * PG_THREADS - 1) / (2 * PG_THREADS);
+    if (max_tokens <= PG_STEP * PG_THREADS) return launch_dependent(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, true, true);
+    const int64_t want = (max_tokens + PG_STEP * PG_THREADS - 1) / (PG_STEP * PG_THREADS);
     const cudaError_t e = launch_dependent(pages_extend_kernel, dim3(static_cast<unsigned>(want < 304 ? want : 304)), dim3(PG_THREADS), 0, st,
                                            a, true, false);
     return e != cudaSuccess ? e : launch_dependent(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, false, true);
@@ -222,21 +254,13 @@ cudaError_t launch_kv_extend(const gdn_kv_pages& p, const int32_t* lens, const i
 
 cudaError_t launch_kv_trim(const gdn_kv_pages& p, const int32_t* keep, int n_seqs, cudaStream_t st) {
     const PagesArgs a = pages_args(p, keep, n_seqs);
-    // a cluster where there may be many pages
-    const unsigned ctas = static_cast<int64_t>(n_seqs) * p.max_blocks > 16 * PG_THREADS ? 8 : 1;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = ctas;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(PG_THREADS);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, pages_trim_kernel, a);
+    // as above, where there may be many pages; few come back in a step of drafts, so the bound on them is far off
+    const int64_t most = static_cast<int64_t>(n_seqs) * p.max_blocks;
+    if (most <= 128 * PG_THREADS) return launch_dependent(pages_trim_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, true, true);
+    const int64_t want = (most + 4 * PG_STEP * PG_THREADS - 1) / (4 * PG_STEP * PG_THREADS);
+    const cudaError_t e = launch_dependent(pages_trim_kernel, dim3(static_cast<unsigned>(want < 304 ? want : 304)), dim3(PG_THREADS), 0, st, a,
+                                           true, false);
+    return e != cudaSuccess ? e : launch_dependent(pages_trim_kernel, dim3(1), dim3(PG_THREADS), 0, st, a, false, true);
 }
 
 int* pages_error_word() {

@@ -142,6 +142,10 @@ class Lib:
     def last_error(self) -> str:
         return self.dll.gdn_last_error().decode()
 
+    def refused(self, name: str, code: int):
+        """Raise for a status that is not GDN_OK."""
+        raise GdnError(name, code, self.last_error())
+
     def _bind(self, name, fn, status):
         def call(*args, check=status):
             r = fn(*args)
@@ -180,13 +184,26 @@ def ptr(t) -> int:
         return t.ctypes.data
 
 
+_raw_stream = None      # torch's current stream of a device, once CUDA is up
+
+
 def stream_handle(stream=None) -> int:
+    global _raw_stream
     if stream is not None:
         return stream.cuda_stream
+    if _raw_stream is not None:         # the handle alone: no stream object is made for a call
+        return _raw_stream(_current_device())
     import torch
-    if torch.cuda.is_initialized():     # the handle alone: no stream object is made for a call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if torch.cuda.is_initialized():
+        _use_raw_streams(torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        return stream_handle()
     return torch.cuda.current_stream().cuda_stream
+
+
+def _use_raw_streams(raw_stream, current_device):
+    global _raw_stream, _current_device
+    _current_device = current_device
+    _raw_stream = raw_stream
 
 
 def make_layer_struct(spec, dev: dict, eps_l2=1e-6, eps_rms=1e-6, q_scale=None, gate_log_a=None, gate_b=None) -> GdnLayer:
