@@ -832,6 +832,7 @@ struct CommitArgs {
 };
 
 constexpr int CM_THREADS = 256;
+constexpr int CM_CHANNELS = 4;             // of the conv state, per thread
 
 // The accepted token of sequence s, -1 where there is none; n: its tokens.
 __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
@@ -844,34 +845,41 @@ __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
 // Block (rows of a value head, sequence): a thread has 8 columns of CH rows, all
 // of them loaded before it is known what is accepted (the loads are what bounds
 // the kernel); then a rank-1 update per token of the path, from shared memory.
-// Blocks past the heads: the conv state of CM_THREADS channels.
+// Blocks past the heads: the conv state, CM_CHANNELS channels a thread.
 template <int D, int CH>
-__global__ void __launch_bounds__(CM_THREADS, 2) commit_kernel(const __grid_constant__ CommitArgs a) {
+__global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(const __grid_constant__ CommitArgs a) {
     constexpr int COLS = D / 8, STEP = CM_THREADS / COLS, PARTS = D / (STEP * CH);
-    extern __shared__ __align__(16) float cm[];        // k [path][D], then u of the block's rows [path][STEP * CH]
-    __shared__ int path[GDN_MAX_NEW];
+    constexpr int ROWS = STEP * CH;
+    extern __shared__ __align__(16) float cm[];        // per token of the path: k [D], then u of the block's rows
     __shared__ Sum2 la[GDN_MAX_NEW + 1];
     __shared__ float w[GDN_MAX_NEW + 1];
     pdl_wait();
     pdl_trigger();
-    const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const int s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int first;
     if (static_cast<int>(blockIdx.x) >= a.hv * PARTS) {
         const int n = draft_range(a.d, s, first, g_draft_skipped), node = commit_node(a, s, n);
-        const int c = (blockIdx.x - a.hv * PARTS) * CM_THREADS + tid;
-        if (c >= a.c_conv) return;
-        const float* in = a.tail_in + (static_cast<int64_t>(s) * a.c_conv + c) * 3;
-        float x[3];
-        int at = node;
+        int at[3];                         // tokens, or -1, -2, -3: the old state from its newest entry on
+        at[2] = node;
 #pragma unroll
-        for (int m = 2; m >= 0; --m) {
-            // at: a token, or -1, -2, -3: the old state from its newest entry on
-            x[m] = at < 0 ? in[3 + at] : bf16_bits_to_float(a.qkvz[static_cast<int64_t>(first + at) * a.ld_qkvz + c]);
-            at = at < 0 ? at - 1 : draft_parent(draft_ancestors(a.d, first, at));
+        for (int m = 1; m >= 0; --m) at[m] = at[m + 1] < 0 ? at[m + 1] - 1 : draft_parent(draft_ancestors(a.d, first, at[m + 1]));
+        const int64_t base = static_cast<int64_t>(s) * a.c_conv;
+        float x[CM_CHANNELS][3];
+#pragma unroll
+        for (int k = 0; k < CM_CHANNELS; ++k) {
+            const int c = ((blockIdx.x - a.hv * PARTS) * CM_CHANNELS + k) * CM_THREADS + tid;
+            if (c >= a.c_conv) break;
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                x[k][m] = at[m] < 0 ? a.tail_in[(base + c) * 3 + 3 + at[m]] : bf16_bits_to_float(a.qkvz[(first + at[m]) * a.ld_qkvz + c]);
         }
-        float* out = a.tail_out + (static_cast<int64_t>(s) * a.c_conv + c) * 3;
 #pragma unroll
-        for (int m = 0; m < 3; ++m) out[m] = x[m];
+        for (int k = 0; k < CM_CHANNELS; ++k) {
+            const int c = ((blockIdx.x - a.hv * PARTS) * CM_CHANNELS + k) * CM_THREADS + tid;
+            if (c >= a.c_conv) break;
+#pragma unroll
+            for (int m = 0; m < 3; ++m) a.tail_out[(base + c) * 3 + m] = x[k][m];
+        }
         return;
     }
     const int h = blockIdx.x / PARTS, row0 = blockIdx.x % PARTS * (STEP * CH), hk = h / a.ratio;
@@ -883,14 +891,25 @@ __global__ void __launch_bounds__(CM_THREADS, 2) commit_kernel(const __grid_cons
     const int n = draft_range(a.d, s, first, g_draft_skipped), node = commit_node(a, s, n);
     const uint64_t on = node < 0 ? 0ull : draft_ancestors(a.d, first, node) | 1ull << node;
     const int np = __popcll(on);
-    if (tid < 32) {
+    // a warp for every eighth token of the path
+    int at = 0;
+    for (uint64_t m = on; m; m &= m - 1, ++at) {
+        if (at % (CM_THREADS / 32) != warp) continue;
+        const int64_t t = first + __ffsll(static_cast<long long>(m)) - 1;
+        float* to = cm + at * (D + ROWS);
+        for (int e = lane; e < COLS; e += 32) {
+            const uint4 x = *reinterpret_cast<const uint4*>(a.qkv + t * a.c_conv + a.c_qk + hk * D + 8 * e);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) *reinterpret_cast<float2*>(to + 8 * e + 2 * c) = __half22float2(*reinterpret_cast<const __half2*>(&u[c]));
+        }
+        for (int e = lane; e < ROWS; e += 32) to[D + e] = a.delta[(t * a.hv + h) * D + row0 + e];
+    }
+    if (warp == 0) {
         // the sums of log a over what follows a token on the path (la[0]: over all of it), by doubling
         for (int j = lane; j < n; j += 32)
-            if (on >> j & 1) {
-                const int at = __popcll(on & ((1ull << j) - 1));
-                path[at] = j;
-                la[at] = {clamp_log_a(a.log_a[static_cast<int64_t>(first + j) * a.hv + h]), 0.0f};
-            }
+            if (on >> j & 1)
+                la[__popcll(on & ((1ull << j) - 1))] = {clamp_log_a(a.log_a[static_cast<int64_t>(first + j) * a.hv + h]), 0.0f};
         if (lane == 0) la[np] = {0.0f, 0.0f};
         __syncwarp();
         for (int step = 1; step < np; step <<= 1) {
@@ -909,23 +928,6 @@ __global__ void __launch_bounds__(CM_THREADS, 2) commit_kernel(const __grid_cons
         for (int j = lane; j <= np; j += 32) w[j] = expf(la[j].hi + la[j].lo);
     }
     __syncthreads();
-    float* ks = cm;
-    float* us = cm + np * D;
-    for (int e = tid; e < np * COLS; e += CM_THREADS) {
-        const int64_t t = first + path[e / COLS];
-        const uint4 x = *reinterpret_cast<const uint4*>(a.qkv + t * a.c_conv + a.c_qk + hk * D + e % COLS * 8);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
-            *reinterpret_cast<float2*>(ks + e * 8 + 2 * m) = f;
-        }
-    }
-    for (int e = tid; e < np * STEP * CH; e += CM_THREADS) {
-        const int j = e / (STEP * CH), r = e % (STEP * CH);
-        us[e] = w[j + 1] * a.delta[((first + path[j]) * static_cast<int64_t>(a.hv) + h) * D + row0 + r];
-    }
-    __syncthreads();
     const float grow = np ? w[0] : 1.0f;
     float f[CH][8];
 #pragma unroll
@@ -933,11 +935,13 @@ __global__ void __launch_bounds__(CM_THREADS, 2) commit_kernel(const __grid_cons
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[j][e] = __uint_as_float(v[j][e]) * grow;
     for (int t = 0; t < np; ++t) {
-        const float4 x = *reinterpret_cast<const float4*>(ks + t * D + col), y = *reinterpret_cast<const float4*>(ks + t * D + col + 4);
+        const float* from = cm + t * (D + ROWS);
+        const float4 x = *reinterpret_cast<const float4*>(from + col), y = *reinterpret_cast<const float4*>(from + col + 4);
         const float k[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const float after = w[t + 1];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const float u = us[t * STEP * CH + row + j * STEP];
+            const float u = from[D + row + j * STEP] * after;
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[j][e] = fmaf(u, k[e], f[j][e]);
         }
@@ -956,7 +960,7 @@ static cudaError_t commit_launch(const CommitArgs& a, cudaStream_t st) {
     constexpr int TOKEN = (D + STEP * CH) * 4;
     static PerDeviceOnce once;
     once.run([](int) { cudaFuncSetAttribute(commit_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * TOKEN); });
-    const int conv_blocks = a.qkvz ? (a.c_conv + CM_THREADS - 1) / CM_THREADS : 0;
+    const int conv_blocks = a.qkvz ? (a.c_conv + CM_CHANNELS * CM_THREADS - 1) / (CM_CHANNELS * CM_THREADS) : 0;
     return launch_dependent(commit_kernel<D, CH>, dim3(a.hv * PARTS + conv_blocks, a.d.n_seqs), dim3(CM_THREADS),
                             static_cast<size_t>(a.d.max_new * TOKEN), st, a);
 }
@@ -980,9 +984,10 @@ cudaError_t launch_delta_commit(const gdn_layer& L, const DraftTokens& d, const 
     a.ratio = L.n_v_heads / L.n_qk_heads;
     a.c_qk = L.n_qk_heads * L.dk;
     a.c_conv = 2 * a.c_qk + L.n_v_heads * L.dv;
-    // a quarter of a head's rows to a block where whole heads leave SMs without one
     if (L.dk == 64) return commit_launch<64, 2>(a, st);
-    return a.hv * d.n_seqs < 2 * 152 ? commit_launch<128, 2>(a, st) : commit_launch<128, 8>(a, st);
+    // 32 rows of a head to a block where that fills the SMs, else 64 (one sequence of 32 heads: 3.2 us, 4.0 with 64; 64
+    // sequences: 61 us with 32 rows, 53 with 64, 68 with 128, which leaves an SM two blocks)
+    return a.hv * d.n_seqs < 2 * 152 ? commit_launch<128, 2>(a, st) : commit_launch<128, 4>(a, st);
 }
 
 int* draft_error_word() {
