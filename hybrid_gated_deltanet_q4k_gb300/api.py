@@ -64,11 +64,16 @@ class DeviceLayer:
         L.q6k_mask = self.q6k_mask
         return L
 
-    def _ref(self):
-        """The layer's struct without drawn gates, made once."""
-        if self._struct is None:
-            self._struct = self.struct()
-        return ctypes.byref(self._struct)
+    def _ref(self, conv: bool = False):
+        """The layer's struct without drawn gates; made once, with what a call of the conv reads as it is now."""
+        st = self._struct
+        if st is None:
+            st = self._struct = self.struct()
+        elif conv:
+            dev = self.dev
+            st.conv_w, st.A_log, st.dt_bias = dev["conv_w"].data_ptr(), dev["A_log"].data_ptr(), dev["dt_bias"].data_ptr()
+            st.eps_l2, st.q_scale = self.eps_l2, self.q_scale
+        return ctypes.byref(st)
 
     def workspace_bytes(self, ubatch_tokens: int) -> int:
         s = self.struct()
@@ -173,9 +178,9 @@ class DeviceLayer:
             _refuse(dev, ("conv_state", conv_state, torch.float32, s * c * 3), ("qkv", qkv, torch.float16, t * c),
                     ("log_a", log_a, torch.float32, t * hv), ("b", b, torch.float32, t * hv), ("ba", ba, torch.float32, t * ba.shape[1]),
                     *_drafts_named(s, t, cu, tree))
-        r = self._dll.gdn_conv_tree(self._ref(), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
+        r = self._dll.gdn_conv_tree(self._ref(True), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
                                     cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
-                                    qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_handle(stream))
+                                    qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_conv_tree", r)
 
     def delta_tree(self, qkv: torch.Tensor, log_a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
@@ -194,7 +199,7 @@ class DeviceLayer:
                     ("delta", delta, torch.float32, t * hv * d), *_drafts_named(s, t, cu, tree))
         r = self._dll.gdn_delta_tree(self._ref(), qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), state.data_ptr(),
                                      cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
-                                     o.data_ptr(), delta.data_ptr(), gl.stream_handle(stream))
+                                     o.data_ptr(), delta.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_delta_tree", r)
 
     def delta_commit(self, qkv: torch.Tensor, log_a: torch.Tensor, delta: torch.Tensor, node: torch.Tensor, state_in: torch.Tensor,
@@ -226,7 +231,7 @@ class DeviceLayer:
                                        t, max_new, tree if tree is None else tree.data_ptr(), s, node.data_ptr(), state_in.data_ptr(),
                                        state_out.data_ptr(), qkvz if qkvz is None else qkvz.data_ptr(), ld,
                                        conv_in if conv_in is None else conv_in.data_ptr(),
-                                       conv_out if conv_out is None else conv_out.data_ptr(), gl.stream_handle(stream))
+                                       conv_out if conv_out is None else conv_out.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_delta_commit", r)
 
 
@@ -490,14 +495,14 @@ class KvPages:
                     ("cu", cu, torch.int32, n + 1), ("positions", positions, torch.int32, t), ("slots", slots, torch.int64, t),
                     *(() if tree is None else (("tree", tree, torch.int64, t),)))
         r = self._dll.gdn_kv_extend(self._ref, lens.data_ptr(), n_new.data_ptr(), n, tree if tree is None else tree.data_ptr(), t,
-                                    lens_out.data_ptr(), cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), gl.stream_handle(stream))
+                                    lens_out.data_ptr(), cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_kv_extend", r)
 
     def trim(self, keep: torch.Tensor, stream=None, check=True) -> int:
         """Enqueue gdn_kv_trim: the pages past the first keep int32 [n_seqs] tokens of each sequence become free."""
         if not _all(self._device, torch.int32, self.n_seqs, keep):
             _refuse(self._device, ("keep", keep, torch.int32, self.n_seqs))
-        r = self._dll.gdn_kv_trim(self._ref, keep.data_ptr(), self.n_seqs, gl.stream_handle(stream))
+        r = self._dll.gdn_kv_trim(self._ref, keep.data_ptr(), self.n_seqs, gl.stream_on(self._device, stream))
         return r if not r or not check else self.lib.refused("gdn_kv_trim", r)
 
 
@@ -532,5 +537,5 @@ def verify(p: torch.Tensor, tokens: torch.Tensor, rows: torch.Tensor, ids: torch
     r = lib.dll.gdn_verify(code, p.data_ptr(), ld_p, q if q is None else q.data_ptr(), ld_q, vocab, tokens.data_ptr(),
                            cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
                            u if u is None else u.data_ptr(), u_next if u_next is None else u_next.data_ptr(), rows.data_ptr(),
-                           ids.data_ptr(), count.data_ptr(), node.data_ptr(), next.data_ptr(), gl.stream_handle(stream))
+                           ids.data_ptr(), count.data_ptr(), node.data_ptr(), next.data_ptr(), gl.stream_on(dev, stream))
     return r if not r or not check else lib.refused("gdn_verify", r)

@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(cons
 #pragma unroll
         for (int k = 0; k < CM_CHANNELS; ++k) {
             const int c = ((blockIdx.x - a.hv * PARTS) * CM_CHANNELS + k) * CM_THREADS + tid;
-            if (c >= a.c_conv) break;
+            if (c >= a.c_conv || !GDN_IN_RANGE(g_draft_error, s < a.d.n_seqs)) break;
 #pragma unroll
             for (int m = 0; m < 3; ++m) a.tail_out[(base + c) * 3 + m] = x[k][m];
         }
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(cons
     for (int j = 0; j < CH; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = __float_as_uint(f[j][e]);
-        store32(a.state_out + base + j * STEP * D, v[j]);
+        if (GDN_IN_RANGE(g_draft_error, s < a.d.n_seqs && h < a.hv && row + j * STEP < D - row0)) store32(a.state_out + base + j * STEP * D, v[j]);
     }
 }
 

@@ -200,6 +200,15 @@ def stream_handle(stream=None) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def stream_on(device: int, stream=None) -> int:
+    """stream_handle for a call on memory of ``device``, which has to be the stream's device: the current one's, or that
+    of ``stream``."""
+    on = stream.device_index if stream is not None else _current_device() if _raw_stream is not None else device
+    if on != device:
+        raise ValueError(f"memory of cuda:{device} in a call on a stream of cuda:{on}")
+    return stream_handle(stream)
+
+
 def _use_raw_streams(raw_stream, current_device):
     global _raw_stream, _current_device
     _current_device = current_device

@@ -198,3 +198,18 @@ def test_wrappers_refuse_host_memory(L):
         dl.delta_commit(qkv, g, u, one, st, st)
     with pytest.raises(ValueError, match="qkvz"):
         dl.conv_tree(torch.zeros(t, 384, dtype=torch.bfloat16), g, torch.zeros(2, 384, 3), qkv, g, g)
+
+
+def test_a_call_is_on_its_memory_s_device(monkeypatch):
+    """Tensors of another device than the stream's are refused, with the current stream and with a given one."""
+    monkeypatch.setattr(gl, "_raw_stream", lambda device: 100 + device)
+    monkeypatch.setattr(gl, "_current_device", lambda: 1, raising=False)
+    assert gl.stream_on(1) == 101
+    with pytest.raises(ValueError, match="cuda:0"):
+        gl.stream_on(0)
+
+    class Stream:
+        device_index, cuda_stream = 0, 7
+    assert gl.stream_on(0, Stream) == 7
+    with pytest.raises(ValueError, match="cuda:1"):
+        gl.stream_on(1, Stream)
