@@ -96,10 +96,16 @@ __global__ void __launch_bounds__(CT_THREADS, 2) conv_tree_kernel(const __grid_c
     for (int e = tid; e < CT_COLS * 3; e += CT_THREADS)
         if (col0 * 3 + e < a.c_conv * 3) cp_async<4>(tail + e, a.tail + (static_cast<int64_t>(s) * a.c_conv + col0) * 3 + e);
     if (tid < n) anc[tid] = draft_ancestors(a.d, first, tid);
-    float4 w[8];
+    F2 w[4][4];                            // taps of channels 2e and 2e + 1
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        w[e] = in ? *reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(c0 + e) * 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < 4; ++e) {
+        const float4* src = reinterpret_cast<const float4*>(a.conv_w + static_cast<int64_t>(in ? c0 + 2 * e : 0) * 4);
+        const float4 x = src[0], y = src[1];
+        w[0][e] = f2(x.x, y.x);
+        w[1][e] = f2(x.y, y.y);
+        w[2][e] = f2(x.z, y.z);
+        w[3][e] = f2(x.w, y.w);
+    }
     __syncthreads();
     if (tid < n) {
         int x = tid;
@@ -121,40 +127,51 @@ __global__ void __launch_bounds__(CT_THREADS, 2) conv_tree_kernel(const __grid_c
     for (int i = tid / CT_SLOTS; i < n; i += CT_THREADS / CT_SLOTS) {
         const int4 taps = *reinterpret_cast<const int4*>(at[i]);
         const int row[4] = {taps.x, taps.y, taps.z, taps.w};
-        float v[4][8];
+        F2 y[4];                           // as conv4_silu has it, two channels at a time
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + (max(row[m], 0) * CT_SLOTS + slot) * 16);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            F2 v[4];
+            if (m < 3 && row[m] < 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[m][2 * e] = __uint_as_float(u[e] << 16);
-                v[m][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                for (int e = 0; e < 4; ++e) v[e] = f2(mine[6 * e + 3 + row[m]], mine[6 * e + 6 + row[m]]);
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(raw + (max(row[m], 0) * CT_SLOTS + slot) * 16);
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = f2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u));
             }
-            if (m < 3 && row[m] < 0)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[m][e] = mine[3 * e + 3 + row[m]];
+            for (int e = 0; e < 4; ++e) y[e] = m ? f2_fma(w[m][e], v[e], y[e]) : f2_mul(w[m][e], v[e]);
         }
-        float y[8], ss = 0.0f, top = 0.0f;
+        F2 sq = f2(0.0f, 0.0f);
+        float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            y[e] = conv4_silu(w[e], v[0][e], v[1][e], v[2][e], v[3][e]);
-            ss = fmaf(y[e], y[e], ss);
+        for (int e = 0; e < 4; ++e) {
+            const float l = -1.4426950408889634f;
+            float t0, t1;
+            f2_split(f2_mul(y[e], f2(l, l)), t0, t1);
+            f2_split(f2_add(f2(ex2_ftz(t0), ex2_ftz(t1)), f2(1.0f, 1.0f)), t0, t1);
+            y[e] = f2_mul(y[e], f2(rcp_ftz(t0), rcp_ftz(t1)));
+            sq = f2_fma(y[e], y[e], sq);
         }
+        float ss, s1;
+        f2_split(sq, ss, s1);
+        ss += s1;
 #pragma unroll
         for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (norm) {
-            const float f = rsqrtf(ss + a.eps) * mul;
-            over |= in && !(ss <= 3.0e38f);
+        const float f = norm ? rsqrtf(ss + a.eps) * mul : 1.0f;
+        uint32_t out[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= f;
+        for (int e = 0; e < 4; ++e) {
+            float y0, y1;
+            f2_split(f2_mul(y[e], f2(f, f)), y0, y1);
+            top = fmaxf_nan(top, fmaxf_nan(fabsf(y0), fabsf(y1)));
+            out[e] = f16x2_bits(y0, y1);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf_nan(top, fabsf(y[e]));
-        over |= in && !(top <= 65504.0f);
+        over |= in && !((norm ? fmaxf_nan(top, ss <= 3.0e38f ? 0.0f : ss) : top) <= 65504.0f);
         if (in && GDN_IN_RANGE(g_draft_error, first + i < a.d.n_tokens && c0 + 8 <= a.c_conv))
             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(first + i) * a.c_conv + c0) =
-                make_uint4(f16x2_bits(y[0], y[1]), f16x2_bits(y[2], y[3]), f16x2_bits(y[4], y[5]), f16x2_bits(y[6], y[7]));
+                make_uint4(out[0], out[1], out[2], out[3]);
     }
     if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
@@ -230,12 +247,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // Products of fp32 operands on the tensor cores: tf32 takes the upper 11 bits of
-// each, so an operand is that and a rest, and of the four products the one of the
-// two rests (2^-22 of the whole) is left out.
+// each, so an operand is the nearest such number and a rest, whose upper 11 bits
+// count (cutting x off instead of rounding it would give the rest x's sign, and
+// what is cut off the rest one direction: 3.7e-7 of S_0 k, not 1e-7).  Of the four
+// products the one of the two rests (2^-24 of the whole) is left out.
 struct Tf32 {
     uint32_t hi, lo;
     __device__ __forceinline__ explicit Tf32(float x) {
-        hi = __float_as_uint(x) & 0xffffe000u;
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
         lo = __float_as_uint(x - __uint_as_float(hi));
     }
 };
