@@ -57,7 +57,10 @@ constexpr int CT_SLOTS = CT_COLS / 8;      // threads of a token
 // Block (CT_COLS channels, sequence): all raw inputs of the sequence's tokens to
 // shared memory at once, each read once, and from there to the up to four tokens
 // that have them as a tap.  A thread has 8 channels, their weights in registers, of
-// every fourth token.  The last block of x computes the gates.
+// every fourth token.  The last block of x computes the gates.  48 trees of 20 to
+// 64 tokens, 8192 channels: 35 us, 2.1 TB/s; with a warp walking a head's tokens
+// from L1 it was 51.  What is left is latency (offsets, then rows, then the taps of
+// up to 16 tokens a thread): a third fewer instructions changed nothing.
 template <int D>
 __global__ void __launch_bounds__(CT_THREADS, 2) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];    // raw inputs [token][CT_COLS] bf16, the conv state [CT_COLS][3] fp32
@@ -576,7 +579,14 @@ struct DeltaTreeSmem {
 // finite would reach tokens that do not descend from theirs (0 times them), so a
 // warp that meets one goes through the block token by token.
 //
-// This kernel: a CTA for a head, or for part of its rows, of a sequence.
+// The products are mma.sync: S_0 goes from registers that loaded it into operands,
+// where tcgen05 would want both halves of it written to shared memory first, twice
+// its bytes, for products of 16 to 128 columns.
+//
+// This kernel: a CTA for a head, or for part of its rows, of a sequence.  24 trees
+// of 24 to 64 tokens over 32 heads of 128: 71 us; S_0 alone could be read in 15.
+// A CTA's phases follow one another (S_0, the tokens' products, the blocks), with
+// two CTAs to an SM and 0.4 instructions issued a cycle and scheduler.
 template <int D>
 __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
     constexpr int KB = D / 32;              // blocks of 32 columns
@@ -690,10 +700,15 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
 // numbers each against keys and queries in fp32 (22 bits of S_0 count, at every
 // size).  Nothing but reading S_0 takes long, so the rest hides behind it: the
 // loads come first, and a warp of its own takes the products of the tokens while
-// the others have S_0 times keys and queries.
+// the others have S_0 times keys and queries.  64 chains of up to 8 tokens over 32
+// heads of 128 (146 MB): 31.4 us, 4.65 TB/s; reading S_0 and nothing else takes
+// 22.8.  With S_0 kept in operands as above it was 52; fetched a head ahead into
+// shared memory by CTAs that stay, 45 (its way through shared memory cost more
+// than the waits it saved).
+constexpr int DF_WARPS = 4;                 // 64 rows of a head to a CTA (31.4 us for 64 chains of up to 8 over 32 heads of 128; 32.5 with 128)
 template <int D>
 struct DeltaFewSmem {
-    static constexpr int W = D / 16, ROW = D + 4;           // floats of a row of keys: lanes g * ROW + 8t differ in their banks
+    static constexpr int W = DF_WARPS, ROW = D + 4;           // floats of a row of keys: lanes g * ROW + 8t differ in their banks
     float k[8][ROW], q[8][ROW];
     uint4 k16[8 * D / 8], q16[8 * D / 8];                   // as delta_products takes them
     float kk[8 * 12], qk[8 * 12], inv[64], us[W][8 * DT_U];
@@ -704,14 +719,15 @@ struct DeltaFewSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(32 * (D / 16 + 1), D == 128 ? 2 : 4) delta_few_kernel(const __grid_constant__ DeltaTreeArgs a) {
+__global__ void __launch_bounds__(32 * (DF_WARPS + 1), 4) delta_few_kernel(const __grid_constant__ DeltaTreeArgs a) {
     using Smem = DeltaFewSmem<D>;
-    constexpr int KB = D / 32, UNITS = D / 8, W = Smem::W;
+    constexpr int KB = D / 32, UNITS = D / 8, W = DF_WARPS, PARTS = D / 16 / W;
     __shared__ __align__(16) Smem sm;
     pdl_wait();
     pdl_trigger();
-    const int h = blockIdx.x, s = blockIdx.y, hk = h / a.ratio;
+    const int h = blockIdx.x / PARTS, s = blockIdx.y, hk = h / a.ratio;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int r0 = (blockIdx.x % PARTS * W + warp) * 16;
     const DeltaTokens d = {sm.k16, sm.q16, sm.kk, sm.qk, sm.inv, sm.anc, sm.uni, sm.g, sm.up, sm.eg, sm.b, 12};
     int first;
     if (warp == W) {
@@ -735,7 +751,7 @@ __global__ void __launch_bounds__(32 * (D / 16 + 1), D == 128 ? 2 : 4) delta_few
     }
     uint32_t w[KB][2][8];                                   // rows g and g + 8
     {
-        const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + warp * 16 + g) * D + 8 * t;
+        const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + r0 + g) * D + 8 * t;
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             load32(S + 32 * b, w[b][0]);
@@ -763,7 +779,7 @@ __global__ void __launch_bounds__(32 * (D / 16 + 1), D == 128 ? 2 : 4) delta_few
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         const int i = 2 * t + (m & 1);
-        r[m] = i < n ? __half2float(__ushort_as_half(rows[static_cast<int64_t>(i) * a.c_conv + 2 * a.c_qk + h * D + warp * 16 + g + 8 * (m >> 1)])) : 0.0f;
+        r[m] = i < n ? __half2float(__ushort_as_half(rows[static_cast<int64_t>(i) * a.c_conv + 2 * a.c_qk + h * D + r0 + g + 8 * (m >> 1)])) : 0.0f;
     }
     __syncthreads();
     float kh[4] = {}, kl[4] = {}, qh[4] = {}, ql[4] = {};
@@ -796,7 +812,7 @@ __global__ void __launch_bounds__(32 * (D / 16 + 1), D == 128 ? 2 : 4) delta_few
     }
     uint64_t bad = 0;
     delta_block(d, 0, r, xq, sm.us[warp], bad, u, o);
-    if (delta_store(a, first, n, 0, h * D + warp * 16, u, o)) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
+    if (delta_store(a, first, n, 0, h * D + r0, u, o)) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
 
 template <int D>
@@ -806,7 +822,8 @@ static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
     once.run([](int) {
         cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
     });
-    if (a.d.max_new <= 8 && heads > 152) return launch_dependent(delta_few_kernel<D>, dim3(a.hv, a.d.n_seqs), dim3(32 * (D / 16 + 1)), 0, st, a);
+    if (a.d.max_new <= 8 && heads > 152)
+        return launch_dependent(delta_few_kernel<D>, dim3(a.hv * (D / 16 / DF_WARPS), a.d.n_seqs), dim3(32 * (DF_WARPS + 1)), 0, st, a);
     // the whole head in a CTA, or, where that leaves SMs without one and the tokens' own work is little beside S_0, its
     // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 19.5)
     int warps = D / 16;
@@ -863,7 +880,9 @@ __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
 
 // Block (rows of a value head, sequence): a thread has 8 columns of CH rows, all
 // of them loaded before it is known what is accepted (the loads are what bounds
-// the kernel); then a rank-1 update per token of the path, from shared memory.
+// the kernel); then a rank-1 update per token of the path, from shared memory.  64
+// sequences of 32 heads of 128 (281 MB): 53 us, 5.3 TB/s; a copy of the states
+// takes 42.
 // Blocks past the heads: the conv state, CM_CHANNELS channels a thread.
 template <int D, int CH>
 __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(const __grid_constant__ CommitArgs a) {

@@ -7,7 +7,9 @@
 // two scans.  From there tokens and pages are independent: each finds its
 // sequence by bisection of the sums in shared memory.  What is read by all
 // (lengths, pages held, the stack's height) is written last: by the one CTA, or by
-// a second launch that waits for the first.
+// a second launch that waits for the first.  A trim and an extension of 64 trees of
+// up to 32 tokens: 8 us, two launches and their chains of loads; of 256 prompts
+// (1.05 million tokens, 65 thousand pages): 20 us, four launches.
 #include "common.cuh"
 
 namespace gdn {
