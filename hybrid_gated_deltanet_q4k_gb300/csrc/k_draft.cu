@@ -657,17 +657,21 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
     } else {
         load_v(0, vn);
         for (int e = tid - 32; e < np * UNITS; e += blockDim.x - 32) {
-            const int i = e / UNITS, x = e % UNITS;
-            const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv + hk * D + 8 * x;
-            const int to = i * UNITS + (x ^ (4 * (i & 1)));
-            qs[to] = i < n ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
-            ks[to] = i < n ? *reinterpret_cast<const uint4*>(row + a.c_qk) : make_uint4(0, 0, 0, 0);
+            const int i = e / UNITS, x = e % UNITS, to = i * UNITS + (x ^ (4 * (i & 1)));
+            if (i < n) {
+                const uint16_t* row = a.qkv + static_cast<int64_t>(first + i) * a.c_conv + hk * D + 8 * x;
+                cp_async<16>(qs + to, row);
+                cp_async<16>(ks + to, row + a.c_qk);
+            } else {
+                qs[to] = ks[to] = make_uint4(0, 0, 0, 0);
+            }
         }
     }
     const StateOperand<KB> S0([&](int m, int b, uint32_t (&w)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = m ? w1[b][e] : w0[b][e];
     });
+    cp_async_wait();
     __syncthreads();
     const int sw = t ^ (4 * (g & 1));       // the unit of columns 8t .. 8t+7 in rows of g's parity
     // where a block has ancestors, in turn
@@ -697,10 +701,10 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
 #pragma unroll
         for (int m = 0; m < 4; ++m) r[m] = __half2float(__ushort_as_half(vn[m]));
         if (bi + 1 < nb) load_v(bi + 1, vn);
-        if (bi) with_state(bi);
 #pragma unroll
         for (int m = 0; m < 4; ++m) r[m] -= xk[m];
         delta_block(d, bi, r, xq, us, bad, u, o);
+        if (bi + 1 < nb) with_state(bi + 1);
         over |= delta_store(a, first, n, bi, h * D + r0, u, o);
     }
     if (over) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
