@@ -50,19 +50,19 @@ struct ConvTreeArgs {
     float eps, q_scale;
 };
 
-constexpr int CT_THREADS = 256;
-constexpr int CT_COLS = 512;               // channels of a block
+constexpr int CT_THREADS = 128;
+constexpr int CT_COLS = 256;               // channels of a block
 constexpr int CT_SLOTS = CT_COLS / 8;      // threads of a token
 
 // Block (CT_COLS channels, sequence): all raw inputs of the sequence's tokens to
 // shared memory at once, each read once, and from there to the up to four tokens
 // that have them as a tap.  A thread has 8 channels, their weights in registers, of
 // every fourth token.  The last block of x computes the gates.  48 trees of 20 to
-// 64 tokens, 8192 channels: 35 us, 2.1 TB/s; with a warp walking a head's tokens
-// from L1 it was 51.  What is left is latency (offsets, then rows, then the taps of
+// 64 tokens, 8192 channels: 33 us, 2.2 TB/s (35 in blocks of 512 channels, 44 with
+// 512 threads); with a warp walking a head's tokens from L1 it was 51.  What is left is latency (offsets, then rows, then the taps of
 // up to 16 tokens a thread): a third fewer instructions changed nothing.
 template <int D>
-__global__ void __launch_bounds__(CT_THREADS, 2) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
+__global__ void __launch_bounds__(CT_THREADS, 6) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];    // raw inputs [token][CT_COLS] bf16, the conv state [CT_COLS][3] fp32
     __shared__ uint64_t anc[GDN_MAX_NEW];
     __shared__ int at[GDN_MAX_NEW][4];     // the taps' tokens, oldest first; -1, -2, -3: the conv state
@@ -595,7 +595,7 @@ struct DeltaTreeSmem {
 // its bytes, for products of 16 to 128 columns.
 //
 // This kernel: a CTA for a head, or for part of its rows, of a sequence.  24 trees
-// of 24 to 64 tokens over 32 heads of 128: 71 us; S_0 alone could be read in 15.
+// of 24 to 64 tokens over 32 heads of 128: 60 us; S_0 alone could be read in 15.
 // A CTA's phases follow one another (S_0, the tokens' products, the blocks), with
 // two CTAs to an SM and 0.4 instructions issued a cycle and scheduler.
 template <int D>
@@ -840,7 +840,7 @@ static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
     if (a.d.max_new <= 8 && heads > 152)
         return launch_dependent(delta_few_kernel<D>, dim3(a.hv * (D / 16 / DF_WARPS), a.d.n_seqs), dim3(32 * (DF_WARPS + 1)), 0, st, a);
     // the whole head in a CTA, or, where that leaves SMs without one and the tokens' own work is little beside S_0, its
-    // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 19.5)
+    // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 18)
     int warps = D / 16;
     while (np <= 16 && warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
     return launch_dependent(delta_tree_kernel<D>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
