@@ -94,12 +94,8 @@ __device__ __forceinline__ int64_t vf_warp_sum(int64_t x) {
     return x;
 }
 __device__ __forceinline__ uint64_t vf_warp_max(uint64_t x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t y = __shfl_xor_sync(0xffffffffu, x, o);
-        x = y > x ? y : x;
-    }
-    return x;
+    const uint32_t hi = static_cast<uint32_t>(x >> 32), a = __reduce_max_sync(0xffffffffu, hi);
+    return static_cast<uint64_t>(a) << 32 | __reduce_max_sync(0xffffffffu, hi == a ? static_cast<uint32_t>(x) : 0u);
 }
 
 // What the decisions need but the sums of rows: read by the first CTA of the
@@ -115,7 +111,8 @@ struct VerifyNodes {
 
 struct VerifySmem {
     VerifyNodes node;
-    uint64_t total[2][VF_MOST];           // the CTAs' sums (or largest scores), by the parity of the row's turn
+    uint64_t total[2][VF_MOST];           // the CTAs' sums, by the parity of the row's turn
+    uint64_t top[2][VF_MOST * VF_WARPS];  // the warps' largest keys, likewise
     uint64_t warp_sum[VF_WARPS];
     int gone[GDN_MAX_NEW];                // rejected certain drafts
     int found;
@@ -375,17 +372,17 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const __grid_cons
         for (int c = 0; c < ctas; ++c) Z += all[c];
         summed = true;
     };
-    // the CTAs' and the block's largest key
+    // the largest key, from warps to warps: what CTAs put together first for sums (fewer numbers go around) takes two
+    // microseconds over six rows here
     const auto top_of_all = [&](uint64_t top) {
+        uint64_t* all = sm.top[turn & 1];
+        ++turn;
         top = vf_warp_max(top);
-        if (lane == 0) sm.warp_sum[warp] = top;
-        __syncthreads();
+        if (lane < ctas) *cluster.map_shared_rank(all + mine, lane) = top;
+        cluster.sync();
         top = 0;
-#pragma unroll
-        for (int i = 0; i < VF_WARPS; ++i) top = sm.warp_sum[i] > top ? sm.warp_sum[i] : top;
-        const uint64_t* all = spread(top);
-        for (int c = 0; c < ctas; ++c) top = all[c] > top ? all[c] : top;
-        return top;
+        for (int r = lane; r < runs; r += 32) top = all[r] > top ? all[r] : top;
+        return vf_warp_max(top);
     };
     const auto find_best = [&]() {
         uint64_t top = vf_top_vectors<T>(row, row.vec(mine) + lane, row.vec(mine + 1));
