@@ -265,9 +265,9 @@ __device__ __forceinline__ bool vf_accepted(Pair c0, float u, Pair z, float q, f
 // CTAs meet once at the start and once per row that is read, their sums sent
 // around before the barrier.  What bounds it is that rows follow one another: a row
 // of 150001 fp32 p and q takes some 2.5 us (the loads' latency, 22 instructions an
-// element, the sums and the barrier), the gathering before the first some 4.  One
-// chain of 5: 9.3 us; 32 greedy chains of up to 6 (128000 bf16): 16.4; 16 trees of
-// 12 to 32: 29.  Decisions in fp64 had been 4 us more for the one chain.
+// element, the sums and the barrier; 1.7 of them with a vocabulary of 1000), the
+// gathering before the first some 4.  One chain of 5: 9.4 us; 32 greedy chains of up
+// to 6 (128000 bf16): 14; 16 trees of 12 to 32: 30.  Decisions in fp64 had been 4 us more for the one chain.
 template <class T>
 __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     namespace cg = cooperative_groups;
@@ -372,8 +372,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const __grid_cons
         for (int c = 0; c < ctas; ++c) Z += all[c];
         summed = true;
     };
-    // the largest key, from warps to warps: what CTAs put together first for sums (fewer numbers go around) takes two
-    // microseconds over six rows here
+    // the largest key, from warps to warps: putting a CTA's together first, as the sums do, takes 0.4 us more a row
     const auto top_of_all = [&](uint64_t top) {
         uint64_t* all = sm.top[turn & 1];
         ++turn;
@@ -542,8 +541,9 @@ template <class T>
 static cudaError_t verify_launch(const VerifyArgs& a, cudaStream_t st) {
     static PerDeviceOnce once;
     once.run([](int) { cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
-    // as many CTAs as run at once, two to an SM: 32 greedy sequences of a vocabulary of 128000 take 24.4 us with 16 CTAs
-    // each, 16.6 with 8, 16.9 with 4; 64 sampled ones of 100000 35.7, 17.1 and 11.4; one of 150001 9.4, 10.2 and 12.7
+    // as many CTAs as run at once, two to an SM: 32 greedy sequences of a vocabulary of 128000 took 24.4 us with 16 CTAs
+    // each, 16.6 with 8, 16.9 with 4; 64 sampled ones of 100000 35.7, 17.1 and 11.4; one of 150001
+    // 9.4, 10.2 and 12.7
     int ctas = VF_MOST;
     while (ctas > 1 && a.d.n_seqs * ctas > 2 * 152) ctas >>= 1;
     cudaLaunchAttribute at[2];
