@@ -1247,9 +1247,11 @@ int gdn_delta_commit(const gdn_layer* layer, const uint16_t* qkv, const float* l
         return fail(GDN_EINVAL, "gdn_delta_commit: node, state_in and state_out (16-byte aligned) required");
     if (n_tokens && (!qkv || !log_a || !delta || !aligned(qkv, 16) || !aligned(delta, 16) || !aligned(log_a, 4)))
         return fail(GDN_EINVAL, "gdn_delta_commit: qkv, log_a and delta (16-byte aligned) required");
-    if (qkvz && (!rows_ok(qkvz, ld_qkvz, s.c_conv) || !conv_in || !conv_out || !aligned(conv_in, 4) || !aligned(conv_out, 4)))
-        return fail(GDN_EINVAL, "gdn_delta_commit: qkvz rows of at least %lld and conv_in, conv_out required", (long long)s.c_conv);
-    if (!qkvz && (conv_in || conv_out)) return fail(GDN_EINVAL, "gdn_delta_commit: a conv state needs qkvz");
+    if (n_tokens && (qkvz != nullptr) != (conv_in != nullptr)) return fail(GDN_EINVAL, "gdn_delta_commit: a conv state and qkvz: both or neither");
+    if ((conv_in != nullptr) != (conv_out != nullptr) || !aligned(conv_in, 4) || !aligned(conv_out, 4))
+        return fail(GDN_EINVAL, "gdn_delta_commit: conv_in and conv_out: both or neither");
+    if (n_tokens && qkvz && !rows_ok(qkvz, ld_qkvz, s.c_conv))
+        return fail(GDN_EINVAL, "gdn_delta_commit: qkvz rows of at least %lld required", (long long)s.c_conv);
     GDN_LAUNCH(launch_delta_commit(*layer, d, qkv, log_a, delta, node, state_in, state_out, qkvz, ld_qkvz, conv_in, conv_out,
                                    static_cast<cudaStream_t>(stream)),
                "gdn_delta_commit");
@@ -1264,8 +1266,9 @@ int gdn_verify(int dtype, const void* p, int64_t ld_p, const void* q, int64_t ld
     if (r) return r;
     if (dtype != GDN_P_F32 && dtype != GDN_P_BF16) return fail(GDN_EINVAL, "gdn_verify: unknown dtype %d", dtype);
     if (vocab < 1 || vocab >= 0x20000000) return fail(GDN_EINVAL, "gdn_verify: 1 <= vocab < 2^29 required (got %lld)", (long long)vocab);
-    if ((u == nullptr) != (u_next == nullptr)) return fail(GDN_EINVAL, "gdn_verify: u and u_next: both or neither");
-    if (!u && q) return fail(GDN_EINVAL, "gdn_verify: the greedy choice takes no q");
+    // without tokens there may be no memory for what they have one of each
+    if (n_tokens && (u == nullptr) != (u_next == nullptr)) return fail(GDN_EINVAL, "gdn_verify: u and u_next: both or neither");
+    if (n_tokens && !u && q) return fail(GDN_EINVAL, "gdn_verify: the greedy choice takes no q");
     if (!count || !node || !next || !aligned(count, 4) || !aligned(node, 4) || !aligned(next, 4))
         return fail(GDN_EINVAL, "gdn_verify: count, node and next required");
     const size_t size = dtype == GDN_P_F32 ? 4 : 2;

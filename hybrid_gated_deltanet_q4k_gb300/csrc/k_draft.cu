@@ -875,9 +875,9 @@ struct CommitArgs {
     const int32_t* node;     // [n_seqs], -1: nothing accepted
     const float* state_in;
     float* state_out;
-    const uint16_t* qkvz;    // null: no conv state
+    const uint16_t* qkvz;
     int64_t ld_qkvz;
-    const float* tail_in;
+    const float* tail_in;    // null: no conv state
     float* tail_out;
     int hv, ratio, c_qk, c_conv;
 };
@@ -1013,7 +1013,7 @@ static cudaError_t commit_launch(const CommitArgs& a, cudaStream_t st) {
     constexpr int TOKEN = (D + STEP * CH) * 4;
     static PerDeviceOnce once;
     once.run([](int) { cudaFuncSetAttribute(commit_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * TOKEN); });
-    const int conv_blocks = a.qkvz ? (a.c_conv + CM_CHANNELS * CM_THREADS - 1) / (CM_CHANNELS * CM_THREADS) : 0;
+    const int conv_blocks = a.tail_in ? (a.c_conv + CM_CHANNELS * CM_THREADS - 1) / (CM_CHANNELS * CM_THREADS) : 0;
     return launch_dependent(commit_kernel<D, CH>, dim3(a.hv * PARTS + conv_blocks, a.d.n_seqs), dim3(CM_THREADS),
                             static_cast<size_t>(a.d.max_new * TOKEN), st, a);
 }

@@ -577,9 +577,9 @@ int gdn_delta_tree(const gdn_layer *layer, const uint16_t *qkv, const float *log
  *               is reported as GDN_EINDEX.
  *   state_in, state_out  fp32 [n_seqs][Hv][dv][dk] (16-byte aligned); may be the
  *               same
- *   qkvz        the rows of gdn_conv_tree, or NULL: no conv state
+ *   qkvz        the rows of gdn_conv_tree
  *   conv_in, conv_out    fp32 [n_seqs][C_conv][3], the conv state before and
- *               after the token; may be the same
+ *               after the token; may be the same.  All three NULL: no conv state
  */
 int gdn_delta_commit(const gdn_layer *layer, const uint16_t *qkv, const float *log_a, const float *delta,
                      const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree, int n_seqs,

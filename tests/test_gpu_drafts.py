@@ -80,7 +80,8 @@ class Case:
         return dict(cu=self.cu_dev, max_new=self.max_new, tree=self.tree)
 
     def qkv(self):
-        return f16_dev(np.concatenate([self.q.reshape(self.t, -1), self.k.reshape(self.t, -1), self.v.reshape(self.t, -1)], axis=1))
+        w, t = self.d, self.t
+        return f16_dev(np.concatenate([self.q.reshape(t, self.hk * w), self.k.reshape(t, self.hk * w), self.v.reshape(t, self.hv * w)], axis=1))
 
     def run_delta(self):
         o, u = Guarded(self.t * self.hv * self.d * 2, 0x5B), Guarded(self.t * self.hv * self.d * 4, 0x5B)
@@ -181,6 +182,21 @@ def test_commit(shape, in_place):
                 assert np.array_equal(s_out[s, h].cpu().numpy(), c.state[s, h])
             else:
                 close(s_out[s, h], ref, steps * 2.0 ** -23 * e)
+
+
+def test_a_commit_without_tokens_passes_the_states_through():
+    c = Case(1, 2, 64, [0, 0], "chain", seed=1)
+    state, tail = torch.full((2, 2, 64, 64), 7.0, device=DEV), torch.full((2, c.spec.c_conv, 3), 7.0, device=DEV)
+    x = torch.empty(0, c.spec.c_conv, dtype=torch.bfloat16, device=DEV)
+    c.dl.delta_commit(c.qkv(), f32_dev(c.log_a), torch.empty(0, 2, 64, device=DEV), torch.tensor([-1, -1], dtype=torch.int32, device=DEV),
+                      f32_dev(c.state), state, x, f32_dev(c.tail), tail, **c.more())
+    sync(c.dl.lib)
+    assert np.array_equal(state.cpu().numpy(), c.state) and np.array_equal(tail.cpu().numpy(), c.tail)
+    # and the other calls have nothing to do
+    none = torch.empty(0, 2, 64, device=DEV)
+    c.dl.delta_tree(c.qkv(), f32_dev(c.log_a), f32_dev(c.b), f32_dev(c.state), none.half(), none, **c.more())
+    c.dl.conv_tree(x, torch.empty(0, 4, device=DEV), f32_dev(c.tail), c.qkv(), f32_dev(c.log_a), f32_dev(c.b), **c.more())
+    sync(c.dl.lib)
 
 
 def test_a_step_is_tokens_one_after_another():
@@ -334,8 +350,9 @@ def test_a_node_outside_its_sequence_counts_as_none(node):
         assert torch.equal(out[0].cpu(), torch.from_numpy(c.state[0]))
 
 
-def test_without_offsets_every_sequence_has_max_new():
-    c = Case(1, 2, 64, [5, 5, 5], "chain", seed=6)
+@pytest.mark.parametrize("hk,hv,lens", [(1, 2, [5, 5, 5]), (16, 64, [7, 7, 7]), (1, 1, [64])])
+def test_without_offsets_every_sequence_has_max_new(hk, hv, lens):
+    c = Case(hk, hv, 64, lens, "chain", seed=6)
     o, u = c.run_delta()
     c.cu_dev = None
     o2, u2 = c.run_delta()

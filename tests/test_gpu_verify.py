@@ -211,6 +211,20 @@ def test_offsets_out_of_range_count_as_empty():
         assert (out[2] == 0).any() and (out[3][out[2] == 0] == -1).all() and (out[4][out[2] == 0] == -1).all()
 
 
+@pytest.mark.parametrize("kind", ["q", "certain", "greedy"])
+def test_without_offsets_every_sequence_has_max_new(kind):
+    c = Case([6, 6, 6], 300, kind, "f32", True, seed=12)
+    want = c.oracle()
+    c.cu = None
+    assert all(np.array_equal(x, y) for x, y in zip(c.run(), want))
+
+
+def test_no_tokens_at_all():
+    c = Case([0, 0], 10, "q", "f32", False, seed=0)
+    rows, ids, count, node, nxt = c.run()
+    assert list(count) == [0, 0] and list(node) == [-1, -1] and list(nxt) == [-1, -1]
+
+
 def test_rows_behind_the_last_sequence_stay():
     c = Case([4, 3, 5], 64, "q", "f32", True, seed=9)
     want = c.oracle()
