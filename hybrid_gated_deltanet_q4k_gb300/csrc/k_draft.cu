@@ -30,6 +30,29 @@ __device__ __forceinline__ void cp_async(void* to, const void* from) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// 32 bytes of a state: one access where the states start on 32 bytes (WIDE), two
+// where they start on 16; the pieces lie whole multiples of 32 behind the start.
+template <bool WIDE>
+__device__ __forceinline__ void load_state(const float* p, uint32_t (&w)[8]) {
+    if constexpr (WIDE) {
+        load32(p, w);
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 4);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_state(float* p, const uint32_t (&w)[8]) {
+    if constexpr (WIDE) {
+        store32(p, w);
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+static bool on_32_bytes(const float* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
 // ------------------------------------------------------------ conv
 
 struct ConvTreeArgs {
@@ -598,7 +621,7 @@ struct DeltaTreeSmem {
 // of 24 to 64 tokens over 32 heads of 128: 60 us; S_0 alone could be read in 15.
 // A CTA's phases follow one another (S_0, the tokens' products, the blocks), with
 // two CTAs to an SM and 0.4 instructions issued a cycle and scheduler.
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
     constexpr int KB = D / 32;              // blocks of 32 columns
     constexpr int UNITS = D / 8;            // 16-byte units of a row of keys
@@ -614,8 +637,8 @@ __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constan
         const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + r0 + g) * D + 8 * t;
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
-            load32(S + 32 * b, w0[b]);
-            load32(S + 8 * D + 32 * b, w1[b]);
+            load_state<WIDE>(S + 32 * b, w0[b]);
+            load_state<WIDE>(S + 8 * D + 32 * b, w1[b]);
         }
     }
     int first;
@@ -733,7 +756,7 @@ struct DeltaFewSmem {
     float eg[8], b[8];
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(32 * (DF_WARPS + 1), 4) delta_few_kernel(const __grid_constant__ DeltaTreeArgs a) {
     using Smem = DeltaFewSmem<D>;
     constexpr int KB = D / 32, UNITS = D / 8, W = DF_WARPS, PARTS = D / 16 / W;
@@ -769,8 +792,8 @@ __global__ void __launch_bounds__(32 * (DF_WARPS + 1), 4) delta_few_kernel(const
         const float* S = a.state + ((static_cast<int64_t>(s) * a.hv + h) * D + r0 + g) * D + 8 * t;
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
-            load32(S + 32 * b, w[b][0]);
-            load32(S + 8 * D + 32 * b, w[b][1]);
+            load_state<WIDE>(S + 32 * b, w[b][0]);
+            load_state<WIDE>(S + 8 * D + 32 * b, w[b][1]);
         }
     }
     const int n = draft_range(a.d, s, first, g_draft_skipped);
@@ -830,20 +853,20 @@ __global__ void __launch_bounds__(32 * (DF_WARPS + 1), 4) delta_few_kernel(const
     if (delta_store(a, first, n, 0, h * D + r0, u, o)) atomicCAS(&g_draft_error, 0, static_cast<int>(ERR_RANGE));
 }
 
-template <int D>
+template <int D, bool WIDE>
 static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
     const int np = (a.d.max_new + 7) & ~7, heads = a.hv * a.d.n_seqs;
     static PerDeviceOnce once;
     once.run([](int) {
-        cudaFuncSetAttribute(delta_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
+        cudaFuncSetAttribute(delta_tree_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
     });
     if (a.d.max_new <= 8 && heads > 152)
-        return launch_dependent(delta_few_kernel<D>, dim3(a.hv * (D / 16 / DF_WARPS), a.d.n_seqs), dim3(32 * (DF_WARPS + 1)), 0, st, a);
+        return launch_dependent(delta_few_kernel<D, WIDE>, dim3(a.hv * (D / 16 / DF_WARPS), a.d.n_seqs), dim3(32 * (DF_WARPS + 1)), 0, st, a);
     // the whole head in a CTA, or, where that leaves SMs without one and the tokens' own work is little beside S_0, its
     // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 18)
     int warps = D / 16;
     while (np <= 16 && warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
-    return launch_dependent(delta_tree_kernel<D>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
+    return launch_dependent(delta_tree_kernel<D, WIDE>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
                             static_cast<size_t>(DeltaTreeSmem<D>(np, warps).end), st, a);
 }
 
@@ -862,7 +885,8 @@ cudaError_t launch_delta_tree(const gdn_layer& L, const DraftTokens& d, const ui
     a.c_qk = L.n_qk_heads * L.dk;
     a.c_v = L.n_v_heads * L.dv;
     a.c_conv = 2 * a.c_qk + a.c_v;
-    return L.dk == 128 ? delta_tree_launch<128>(a, st) : delta_tree_launch<64>(a, st);
+    if (on_32_bytes(state)) return L.dk == 128 ? delta_tree_launch<128, true>(a, st) : delta_tree_launch<64, true>(a, st);
+    return L.dk == 128 ? delta_tree_launch<128, false>(a, st) : delta_tree_launch<64, false>(a, st);
 }
 
 // ------------------------------------------------------------ commit
@@ -899,7 +923,7 @@ __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
 // sequences of 32 heads of 128 (281 MB): 53 us, 5.3 TB/s; a copy of the states
 // takes 42.
 // Blocks past the heads: the conv state, CM_CHANNELS channels a thread.
-template <int D, int CH>
+template <int D, int CH, bool WIDE>
 __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(const __grid_constant__ CommitArgs a) {
     constexpr int COLS = D / 8, STEP = CM_THREADS / COLS, PARTS = D / (STEP * CH);
     constexpr int ROWS = STEP * CH;
@@ -940,7 +964,7 @@ __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(cons
     const int64_t base = ((static_cast<int64_t>(s) * a.hv + h) * D + row0 + row) * D + col;
     uint32_t v[CH][8];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) load32(a.state_in + base + j * STEP * D, v[j]);
+    for (int j = 0; j < CH; ++j) load_state<WIDE>(a.state_in + base + j * STEP * D, v[j]);
     const int n = draft_range(a.d, s, first, g_draft_skipped), node = commit_node(a, s, n);
     const uint64_t on = node < 0 ? 0ull : draft_ancestors(a.d, first, node) | 1ull << node;
     const int np = __popcll(on);
@@ -1003,18 +1027,19 @@ __global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(cons
     for (int j = 0; j < CH; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = __float_as_uint(f[j][e]);
-        if (GDN_IN_RANGE(g_draft_error, s < a.d.n_seqs && h < a.hv && row + j * STEP < D - row0)) store32(a.state_out + base + j * STEP * D, v[j]);
+        if (GDN_IN_RANGE(g_draft_error, s < a.d.n_seqs && h < a.hv && row + j * STEP < D - row0))
+            store_state<WIDE>(a.state_out + base + j * STEP * D, v[j]);
     }
 }
 
-template <int D, int CH>
+template <int D, int CH, bool WIDE>
 static cudaError_t commit_launch(const CommitArgs& a, cudaStream_t st) {
     constexpr int STEP = CM_THREADS / (D / 8), PARTS = D / (STEP * CH);
     constexpr int TOKEN = (D + STEP * CH) * 4;
     static PerDeviceOnce once;
-    once.run([](int) { cudaFuncSetAttribute(commit_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * TOKEN); });
+    once.run([](int) { cudaFuncSetAttribute(commit_kernel<D, CH, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_MAX_NEW * TOKEN); });
     const int conv_blocks = a.tail_in ? (a.c_conv + CM_CHANNELS * CM_THREADS - 1) / (CM_CHANNELS * CM_THREADS) : 0;
-    return launch_dependent(commit_kernel<D, CH>, dim3(a.hv * PARTS + conv_blocks, a.d.n_seqs), dim3(CM_THREADS),
+    return launch_dependent(commit_kernel<D, CH, WIDE>, dim3(a.hv * PARTS + conv_blocks, a.d.n_seqs), dim3(CM_THREADS),
                             static_cast<size_t>(a.d.max_new * TOKEN), st, a);
 }
 
@@ -1037,10 +1062,12 @@ cudaError_t launch_delta_commit(const gdn_layer& L, const DraftTokens& d, const 
     a.ratio = L.n_v_heads / L.n_qk_heads;
     a.c_qk = L.n_qk_heads * L.dk;
     a.c_conv = 2 * a.c_qk + L.n_v_heads * L.dv;
-    if (L.dk == 64) return commit_launch<64, 2>(a, st);
+    const bool wide = on_32_bytes(state_in) && on_32_bytes(state_out);
+    if (L.dk == 64) return wide ? commit_launch<64, 2, true>(a, st) : commit_launch<64, 2, false>(a, st);
     // 32 rows of a head to a block where that fills the SMs, else 64 (one sequence of 32 heads: 3.2 us, 4.0 with 64; 64
     // sequences: 61 us with 32 rows, 53 with 64, 68 with 128, which leaves an SM two blocks)
-    return a.hv * d.n_seqs < 2 * 152 ? commit_launch<128, 2>(a, st) : commit_launch<128, 4>(a, st);
+    if (a.hv * d.n_seqs < 2 * 152) return wide ? commit_launch<128, 2, true>(a, st) : commit_launch<128, 2, false>(a, st);
+    return wide ? commit_launch<128, 4, true>(a, st) : commit_launch<128, 4, false>(a, st);
 }
 
 int* draft_error_word() {
