@@ -88,7 +88,7 @@ template <int D>
 __global__ void __launch_bounds__(CT_THREADS, 6) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];    // raw inputs [token][CT_COLS] bf16, the conv state [CT_COLS][3] fp32
     __shared__ uint64_t anc[GDN_MAX_NEW];
-    __shared__ int at[GDN_MAX_NEW][4];     // the taps' tokens, oldest first; -1, -2, -3: the conv state
+    __shared__ __align__(16) int at[GDN_MAX_NEW][4];     // the taps' tokens, oldest first; -1, -2, -3: the conv state
     pdl_wait();
     pdl_trigger();
     const int s = blockIdx.y, tid = threadIdx.x;
