@@ -178,9 +178,10 @@ class DeviceLayer:
             _refuse(dev, ("conv_state", conv_state, torch.float32, s * c * 3), ("qkv", qkv, torch.float16, t * c),
                     ("log_a", log_a, torch.float32, t * hv), ("b", b, torch.float32, t * hv), ("ba", ba, torch.float32, t * ba.shape[1]),
                     *_drafts_named(s, t, cu, tree))
-        r = self._dll.gdn_conv_tree(self._ref(True), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
-                                    cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
-                                    qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_on(dev, stream))
+        call = gl.entry(self._dll.gdn_conv_tree, dev, stream)
+        r = call(self._ref(True), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
+                 cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+                 qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_conv_tree", r)
 
     def delta_tree(self, qkv: torch.Tensor, log_a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
@@ -197,9 +198,10 @@ class DeviceLayer:
             _refuse(dev, ("state", state, torch.float32, s * hv * d * d), ("qkv", qkv, torch.float16, t * c),
                     ("log_a", log_a, torch.float32, t * hv), ("b", b, torch.float32, t * hv), ("o", o, torch.float16, t * hv * d),
                     ("delta", delta, torch.float32, t * hv * d), *_drafts_named(s, t, cu, tree))
-        r = self._dll.gdn_delta_tree(self._ref(), qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), state.data_ptr(),
-                                     cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
-                                     o.data_ptr(), delta.data_ptr(), gl.stream_on(dev, stream))
+        call = gl.entry(self._dll.gdn_delta_tree, dev, stream)
+        r = call(self._ref(), qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), state.data_ptr(),
+                 cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+                 o.data_ptr(), delta.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_delta_tree", r)
 
     def delta_commit(self, qkv: torch.Tensor, log_a: torch.Tensor, delta: torch.Tensor, node: torch.Tensor, state_in: torch.Tensor,
@@ -227,11 +229,12 @@ class DeviceLayer:
             _refuse(dev, ("state_in", state_in, torch.float32, s * hv * d * d), ("state_out", state_out, torch.float32, s * hv * d * d),
                     ("qkv", qkv, torch.float16, t * c), ("log_a", log_a, torch.float32, t * hv), ("delta", delta, torch.float32, t * hv * d),
                     ("node", node, torch.int32, s), *more, *_drafts_named(s, t, cu, tree))
-        r = self._dll.gdn_delta_commit(self._ref(), qkv.data_ptr(), log_a.data_ptr(), delta.data_ptr(), cu if cu is None else cu.data_ptr(),
-                                       t, max_new, tree if tree is None else tree.data_ptr(), s, node.data_ptr(), state_in.data_ptr(),
-                                       state_out.data_ptr(), qkvz if qkvz is None else qkvz.data_ptr(), ld,
-                                       conv_in if conv_in is None else conv_in.data_ptr(),
-                                       conv_out if conv_out is None else conv_out.data_ptr(), gl.stream_on(dev, stream))
+        call = gl.entry(self._dll.gdn_delta_commit, dev, stream)
+        r = call(self._ref(), qkv.data_ptr(), log_a.data_ptr(), delta.data_ptr(), cu if cu is None else cu.data_ptr(),
+                 t, max_new, tree if tree is None else tree.data_ptr(), s, node.data_ptr(), state_in.data_ptr(),
+                 state_out.data_ptr(), qkvz if qkvz is None else qkvz.data_ptr(), ld,
+                 conv_in if conv_in is None else conv_in.data_ptr(),
+                 conv_out if conv_out is None else conv_out.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_delta_commit", r)
 
 
@@ -494,15 +497,17 @@ class KvPages:
             _refuse(dev, ("lens", lens, torch.int32, n), ("n_new", n_new, torch.int32, n), ("lens_out", lens_out, torch.int32, n),
                     ("cu", cu, torch.int32, n + 1), ("positions", positions, torch.int32, t), ("slots", slots, torch.int64, t),
                     *(() if tree is None else (("tree", tree, torch.int64, t),)))
-        r = self._dll.gdn_kv_extend(self._ref, lens.data_ptr(), n_new.data_ptr(), n, tree if tree is None else tree.data_ptr(), t,
-                                    lens_out.data_ptr(), cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), gl.stream_on(dev, stream))
+        call = gl.entry(self._dll.gdn_kv_extend, dev, stream)
+        r = call(self._ref, lens.data_ptr(), n_new.data_ptr(), n, tree if tree is None else tree.data_ptr(), t,
+                 lens_out.data_ptr(), cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_kv_extend", r)
 
     def trim(self, keep: torch.Tensor, stream=None, check=True) -> int:
         """Enqueue gdn_kv_trim: the pages past the first keep int32 [n_seqs] tokens of each sequence become free."""
         if not _all(self._device, torch.int32, self.n_seqs, keep):
             _refuse(self._device, ("keep", keep, torch.int32, self.n_seqs))
-        r = self._dll.gdn_kv_trim(self._ref, keep.data_ptr(), self.n_seqs, gl.stream_on(self._device, stream))
+        call = gl.entry(self._dll.gdn_kv_trim, self._device, stream)
+        r = call(self._ref, keep.data_ptr(), self.n_seqs, gl.stream_on(self._device, stream))
         return r if not r or not check else self.lib.refused("gdn_kv_trim", r)
 
 
@@ -534,8 +539,9 @@ def verify(p: torch.Tensor, tokens: torch.Tensor, rows: torch.Tensor, ids: torch
                 *((name, x, torch.int32, s) for name, x in (("count", count), ("node", node), ("next", next))),
                 *(() if u is None else (("u", u, torch.float32, t), ("u_next", u_next, torch.float32, s))), *_drafts_named(s, t, cu, tree))
     lib = gl.load(debug=debug)
-    r = lib.dll.gdn_verify(code, p.data_ptr(), ld_p, q if q is None else q.data_ptr(), ld_q, vocab, tokens.data_ptr(),
-                           cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
-                           u if u is None else u.data_ptr(), u_next if u_next is None else u_next.data_ptr(), rows.data_ptr(),
-                           ids.data_ptr(), count.data_ptr(), node.data_ptr(), next.data_ptr(), gl.stream_on(dev, stream))
+    call = gl.entry(lib.dll.gdn_verify, dev, stream)
+    r = call(code, p.data_ptr(), ld_p, q if q is None else q.data_ptr(), ld_q, vocab, tokens.data_ptr(),
+             cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
+             u if u is None else u.data_ptr(), u_next if u_next is None else u_next.data_ptr(), rows.data_ptr(),
+             ids.data_ptr(), count.data_ptr(), node.data_ptr(), next.data_ptr(), gl.stream_on(dev, stream))
     return r if not r or not check else lib.refused("gdn_verify", r)

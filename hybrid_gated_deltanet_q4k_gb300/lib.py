@@ -184,11 +184,10 @@ def ptr(t) -> int:
         return t.ctypes.data
 
 
-_raw_stream = None      # torch's current stream of a device, once CUDA is up
+_raw_stream = _current_device = None      # torch's current stream of a device and its current device, once CUDA is up
 
 
 def stream_handle(stream=None) -> int:
-    global _raw_stream
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:         # the handle alone: no stream object is made for a call
@@ -203,10 +202,26 @@ def stream_handle(stream=None) -> int:
 def stream_on(device: int, stream=None) -> int:
     """stream_handle for a call on memory of ``device``, which has to be the stream's device: the current one's, or that
     of ``stream``."""
-    on = stream.device_index if stream is not None else _current_device() if _raw_stream is not None else device
+    if _raw_stream is None:             # there is memory of the device, so CUDA is up
+        import torch
+        _use_raw_streams(torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    on = stream.device_index if stream is not None else _current_device()
     if on != device:
         raise ValueError(f"memory of cuda:{device} in a call on a stream of cuda:{on}")
     return stream_handle(stream)
+
+
+def entry(fn, device: int, stream):
+    """fn for a call on ``stream``, with ``device`` as the current one meanwhile: a handle of a default stream stands for
+    the current device's, and kernels are set up and launched there."""
+    if stream is None:                  # the current device's, or stream_on refuses the call
+        return fn
+    import torch
+
+    def call(*args):
+        with torch.cuda.device(device):
+            return fn(*args)
+    return call
 
 
 def _use_raw_streams(raw_stream, current_device):
