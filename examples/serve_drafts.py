@@ -5,7 +5,7 @@ back and the new tokens get theirs (``KvPages.trim``, ``extend``); the GDN layer
 (``conv_tree``, ``delta_tree`` between its projections) and so does the attention layer (``RopeTable.apply``,
 ``KvCache.write``, ``attend``); the drafts are verified against the target's probabilities (``verify``); the state
 moves to the accepted token (``delta_commit``) and the accepted keys and values to their final slots
-(``KvCache.write`` with ``rows``).
+(``KvCache.write`` with ``rows``).  A sequence that found no pages is left out on the GPU too, and is as it was.
 
 Random weights stand for the model, and a model without its layers drafts for it.  The example also checks itself:
 every accepted token is decoded again, one at a time (``decode``), and the probabilities are compared.
@@ -87,32 +87,38 @@ class Model:
 class Sequences:
     """States, cache and pages of several sequences, on the GPU."""
 
-    def __init__(self, model, n, tokens, page=16):
+    def __init__(self, model, n, tokens, page=16, n_pages=None):
+        """n_pages: of the pool, where it is to have fewer than all sequences may come to need."""
         sp = model.spec
         self.state = torch.zeros(n, sp.n_v_heads, sp.dv, sp.dk, device=model.device)
         self.conv = torch.zeros(n, sp.c_conv, 3, device=model.device)
         blocks = -(-tokens // page)
-        self.cache = KvCache.new("bf16", n * blocks, model.hkv, page, model.d, device=model.device)
-        self.pages = KvPages.new(n, blocks, n * blocks, page, device=model.device)
+        n_pages = n * blocks if n_pages is None else n_pages
+        self.cache = KvCache.new("bf16", n_pages, model.hkv, page, model.d, device=model.device)
+        self.pages = KvPages.new(n, blocks, n_pages, page, device=model.device)
         self.lens = torch.zeros(n, dtype=torch.int32, device=model.device)
 
 
 def step(model, seqs, tokens, n_new, tree, max_new, u, u_next, draft_p):
     """One round over the tokens [T] of all sequences (the last certain one of each, then its drafts).  Returns the new
-    tokens, how many each sequence has, the target's probabilities and the accepted rows."""
+    tokens, how many each sequence has (0: it found no pages and may try again), the target's probabilities and the
+    accepted rows."""
     t, n = tokens.numel(), n_new.numel()
     ints = lambda k, dtype=torch.int32: torch.empty(k, dtype=dtype, device=model.device)  # noqa: E731
     after, cu, positions, slots = ints(n), ints(n + 1), ints(t), ints(t, torch.int64)
     seqs.pages.trim(seqs.lens)
     seqs.pages.extend(seqs.lens, n_new, after, cu, positions, slots, tree=tree)
+    starved = (after == seqs.lens) & (n_new > 0)            # these have tokens but no slots: nothing of them may stay
     more = dict(cu=cu, max_new=max_new, tree=tree)
     x = model.embed[tokens.long()]
     y, (qkv, log_a, delta, qkvz) = model.gdn_drafts(x, seqs.state, seqs.conv, **more)
     x = model.add(x, y)
-    y, k, v = model.attention(x, positions, slots, seqs.cache, after, seqs.pages.block_table, **more)
+    y, k, v = model.attention(x, positions, slots, seqs.cache, after.masked_fill(starved, 0), seqs.pages.block_table, **more)
     p = model.head(model.add(x, y))
     rows, ids, count, node, nxt = ints(t), ints(t), ints(n), ints(n), ints(n)
     api.verify(p, tokens, rows, ids, count, node, nxt, u=u, u_next=u_next, q=draft_p, **more)
+    node.masked_fill_(starved, -1)
+    count.masked_fill_(starved, 0)
     model.gdn.delta_commit(qkv, log_a, delta, node, seqs.state, seqs.state, qkvz, seqs.conv, seqs.conv, **more)
     seqs.cache.write(k, v, torch.where(rows < 0, torch.full_like(slots, -1), slots), rows=rows)
     seqs.lens += count

@@ -521,6 +521,14 @@ int gdn_attn_cache(const gdn_kv_cache *cache, const uint16_t *q, int64_t ld_q, c
  * gdn_kv_trim gives the other pages back.  Nothing is read back to the host, so
  * a captured graph of the step may be replayed.
  *
+ * A sequence for which there were no pages (lens_out equals lens where n_new is
+ * not 0) keeps its rows in the step, but its tokens have no slots, so what is
+ * computed for them means nothing.  The step leaves it out on the device: a length of 0 in
+ * gdn_attn_cache (its rows become zeros), and between gdn_verify and
+ * gdn_delta_commit a node of -1 and a count of 0.  gdn_kv_write stores nothing at
+ * slots of -1.  Its states, length and pages are then those from before the step,
+ * which may be taken again when there are pages.
+ *
  * Shared by gdn_conv_tree, gdn_delta_tree, gdn_delta_commit and gdn_verify:
  *   cu        device int32 [n_seqs + 1]: sequence s holds the token rows
  *             [cu[s], cu[s+1]) of the n_tokens rows, at most max_new (it may be
@@ -649,7 +657,8 @@ typedef struct gdn_kv_pages {
  * lens[s] tokens and gets n_new[s] more; where its pages do not reach for them it
  * takes pages from the top of the stack, sequences and blocks in order.  The
  * first sequence for which the stack does not reach, and those after it that
- * need a page, get none: their length stays and their tokens get slot -1.
+ * need a page, get none: their length stays and their tokens, which cu still
+ * counts, get slot -1 (above: how a step leaves such a sequence out).
  *   lens, n_new  device int32 [n_seqs], not negative
  *   tree         device uint64 [max_tokens] mask words, or NULL: a token's
  *                position is lens[s] plus the number of its ancestors (NULL: of
