@@ -239,15 +239,19 @@ __device__ __noinline__ uint64_t vf_top_vectors(const VerifyRow<T> row, int v, i
     return at < 0 ? 0 : vf_key(top, at);
 }
 
-// An integer of up to 50 bits times 2^-44 as two floats.
+// An integer below 2^53 times 2^-44 as two floats, off by at most 2^-49 of it: what
+// 63 rejections of a row's sum below 8 come to is below 504 times 2^44.
 struct Pair {
     float hi, lo;
 };
 __device__ __forceinline__ Pair vf_pair(int64_t x) {
-    const float a = static_cast<float>(static_cast<uint32_t>(x >> 26)) * 0x1p-18f;
-    const float b = static_cast<float>(static_cast<uint32_t>(x) & 0x3ffffffu) * 0x1p-44f;
-    const float s = a + b;                // a is 0 or more than b
-    return {s, b - (s - a)};
+    // three parts that a float holds, 23, 15 and 15 bits
+    const uint32_t low = static_cast<uint32_t>(x);
+    const float a = static_cast<float>(static_cast<uint32_t>(x >> 30)) * 0x1p-14f;
+    const float b = static_cast<float>(low >> 15 & 0x7fffu) * 0x1p-29f, c = static_cast<float>(low & 0x7fffu) * 0x1p-44f;
+    const float m = __fadd_rn(b, c), e = __fsub_rn(c, __fsub_rn(m, b));      // b is 0 or more than c
+    const float s = __fadd_rn(a, m);      // a is 0 or more than m
+    return {s, __fadd_rn(__fsub_rn(m, __fsub_rn(s, a)), e)};
 }
 
 // (c0 + u z) q < p, in pairs of floats: sm_103a has next to no units for 64 bits,

@@ -626,8 +626,10 @@ int gdn_delta_commit(const gdn_layer *layer, const uint16_t *qkv, const float *l
  *   next     device int32 [n_seqs]: the token after it, ids' last
  * An empty sequence has count 0, node and next -1.  Where nothing is left of r
  * the next token is drawn from p; where p has nothing either it is -1.
- * A first comparison u q < p is exact, later ones and the sums go by multiples of
- * 2^-44: integers, so that results do not depend on the order of summation.
+ * The sums are integers, multiples of 2^-44, so that results do not depend on the
+ * order of summation.  A first comparison u q < p is exact; later ones take what
+ * was rejected before and the sum as two floats each and are good to 2^-45 of
+ * their sides, for as many rejections and as large sums as the call allows.
  * 1 <= vocab < 2^31 / 4.
  */
 #define GDN_P_F32 0
