@@ -168,11 +168,14 @@ class DeviceLayer:
                   tree: torch.Tensor | None = None, stream=None, check=True) -> int:
         """Enqueue gdn_conv_tree: the conv over each sequence's drafted tokens.  qkvz bf16 [T][at least C_conv] and
         ba fp32 [T][2 Hv] are the projection's rows, conv_state fp32 [n_seqs][C_conv][3] is only read; qkv fp16
-        [T][C_conv], log_a and b fp32 [T][Hv] are written.  cu int32 [n_seqs + 1] (None: max_new tokens each),
-        tree int64 [T] mask words (None: chains)."""
+        [T][C_conv], log_a and b fp32 [T][Hv] are written.  ba, log_a and b all None: the gates are drawn elsewhere, only
+        qkv is written.  cu int32 [n_seqs + 1] (None: max_new tokens each), tree int64 [T] mask words (None: chains)."""
         c, hv, _ = self._sizes
         dev, s, t = conv_state.get_device(), conv_state.shape[0], qkvz.shape[0]
-        ld, ld_ba = _rows(qkvz, torch.bfloat16, c, "qkvz", dev), _rows(ba, torch.float32, 2 * hv, "ba", dev)
+        ld = _rows(qkvz, torch.bfloat16, c, "qkvz", dev)
+        if ba is None and log_a is None and b is None:
+            return self._conv_tree_alone(qkvz, ld, conv_state, qkv, cu, max_new, tree, stream, check)
+        ld_ba = _rows(ba, torch.float32, 2 * hv, "ba", dev)
         if not (_all(dev, torch.float32, s * c * 3, conv_state) and _all(dev, torch.float16, t * c, qkv) and
                 _all(dev, torch.float32, t * hv, log_a, b) and ba.shape[0] == t and _drafts_ok(dev, s, t, cu, tree)):
             _refuse(dev, ("conv_state", conv_state, torch.float32, s * c * 3), ("qkv", qkv, torch.float16, t * c),
@@ -182,6 +185,19 @@ class DeviceLayer:
         r = call(self._ref(True), qkvz.data_ptr(), ld, ba.data_ptr(), ld_ba, conv_state.data_ptr(),
                  cu if cu is None else cu.data_ptr(), t, max_new, tree if tree is None else tree.data_ptr(), s,
                  qkv.data_ptr(), log_a.data_ptr(), b.data_ptr(), gl.stream_on(dev, stream))
+        return r if not r or not check else self.lib.refused("gdn_conv_tree", r)
+
+    def _conv_tree_alone(self, qkvz, ld, conv_state, qkv, cu, max_new, tree, stream, check) -> int:
+        """conv_tree of a layer whose gates are drawn."""
+        c = self._sizes[0]
+        dev, s, t = conv_state.get_device(), conv_state.shape[0], qkvz.shape[0]
+        if not (_all(dev, torch.float32, s * c * 3, conv_state) and _all(dev, torch.float16, t * c, qkv) and _drafts_ok(dev, s, t, cu, tree)):
+            _refuse(dev, ("conv_state", conv_state, torch.float32, s * c * 3), ("qkv", qkv, torch.float16, t * c), *_drafts_named(s, t, cu, tree))
+        st = self.struct()
+        st.gate_log_a = st.gate_b = 16      # that they are drawn is all that matters here
+        call = gl.entry(self._dll.gdn_conv_tree, dev, stream)
+        r = call(ctypes.byref(st), qkvz.data_ptr(), ld, None, 0, conv_state.data_ptr(), cu if cu is None else cu.data_ptr(), t, max_new,
+                 tree if tree is None else tree.data_ptr(), s, qkv.data_ptr(), None, None, gl.stream_on(dev, stream))
         return r if not r or not check else self.lib.refused("gdn_conv_tree", r)
 
     def delta_tree(self, qkv: torch.Tensor, log_a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, o: torch.Tensor,
