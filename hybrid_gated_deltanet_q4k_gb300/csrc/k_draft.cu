@@ -924,7 +924,7 @@ __device__ __forceinline__ int commit_node(const CommitArgs& a, int s, int n) {
 // takes 42.
 // Blocks past the heads: the conv state, CM_CHANNELS channels a thread.
 template <int D, int CH, bool WIDE>
-__global__ void __launch_bounds__(CM_THREADS, CH > 4 ? 2 : 4) commit_kernel(const __grid_constant__ CommitArgs a) {
+__global__ void __launch_bounds__(CM_THREADS, 4) commit_kernel(const __grid_constant__ CommitArgs a) {
     constexpr int COLS = D / 8, STEP = CM_THREADS / COLS, PARTS = D / (STEP * CH);
     constexpr int ROWS = STEP * CH;
     extern __shared__ __align__(16) float cm[];        // per token of the path: k [D], then u of the block's rows
