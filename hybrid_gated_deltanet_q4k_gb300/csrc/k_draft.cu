@@ -296,6 +296,9 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// What counts as finite where products of two parts are taken: from 2^128 - 2^116 =
+// 3.40274e38 on the first part rounds to infinity, and 0 times that is no number.
+constexpr float TF32_MAX = 3.4e38f;
 // c [16 rows][8 tokens i] += x [16 rows][8 tokens j] m [j][i].  x is laid out as the
 // products are (lane g, t: rows g, g + 8, tokens 2t, 2t + 1), which makes the tokens
 // 2t and 2t + 1 the operands' indices t and t + 4; m0, m1: m[2t][g], m[2t + 1][g].
@@ -505,7 +508,7 @@ __device__ __forceinline__ void delta_block(const DeltaTokens& d, int bi, float 
     for (int m = 0; m < 4; ++m) u[m] = 0.0f;
     mma_rows(u, r, d.inv[64 * bi + 16 * t + g], d.inv[64 * bi + 16 * t + 8 + g]);
     const float sum = ((fabsf(r[0]) + fabsf(r[1])) + (fabsf(r[2]) + fabsf(r[3]))) + ((fabsf(u[0]) + fabsf(u[1])) + (fabsf(u[2]) + fabsf(u[3])));
-    if (!__any_sync(0xffffffffu, bad != 0 || !(sum <= 3.402823466e38f))) {
+    if (!__any_sync(0xffffffffu, bad != 0 || !(sum <= TF32_MAX))) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             us[(j + (m & 1)) * DT_U + g + 8 * (m >> 1)] = u[m];
@@ -533,7 +536,7 @@ __device__ __forceinline__ void delta_block(const DeltaTokens& d, int bi, float 
         float x = v[c] * d.b[i];
         if (bad & d.anc[i]) x = __uint_as_float(0x7fffffffu);
         ou[c] = x;
-        if (!(fabsf(x) <= 3.402823466e38f)) {
+        if (!(fabsf(x) <= TF32_MAX)) {
             bad |= 1ull << i;
             x = 0.0f;
         }
