@@ -571,7 +571,12 @@ int gdn_conv_tree(const gdn_layer *layer, const uint16_t *qkvz, int64_t ld_qkvz,
  * In fp32 (products with the state from operands of 22 bits and more); o is
  * rounded once, and a value of it beyond fp16's range is reported as
  * GDN_ERANGE.  log_a = -inf (a = 0) is allowed.  A token depends on its ancestors
- * alone, whatever the others hold.
+ * alone, whatever the others hold.  An element of the state, or a u for the token's
+ * descendants, of 3.4e38 and more may count as infinite.
+ *
+ * q, k and v come rounded to fp16 here (2^-11 of each), where gdn_decode keeps
+ * them in fp32: what a token adds to the state, u k^T, differs from what decoding
+ * the token adds by up to 2^-9 of its terms' absolute values.
  */
 int gdn_delta_tree(const gdn_layer *layer, const uint16_t *qkv, const float *log_a, const float *b, const float *state,
                    const int32_t *cu, int64_t n_tokens, int max_new, const uint64_t *tree, int n_seqs, uint16_t *o,
