@@ -863,12 +863,14 @@ static cudaError_t delta_tree_launch(const DeltaTreeArgs& a, cudaStream_t st) {
     once.run([](int) {
         cudaFuncSetAttribute(delta_tree_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, DeltaTreeSmem<D>(GDN_MAX_NEW, D / 16).end);
     });
-    if (a.d.max_new <= 8 && heads > 152)
+    // up to 8 tokens the kernel for them is the faster one at any number of heads (of 128: 1 head 2.7 us and 3.8, 32 heads
+    // 2.8 and 4.0, 160 4.7 and 5.5, 512 9.9 and 12.1, 2048 31 and 41; of 64: 2.5 and 3.3, 32 heads 2.5 and 3.4, 512 3.8 and 4.5)
+    if (a.d.max_new <= 8)
         return launch_dependent(delta_few_kernel<D, WIDE>, dim3(a.hv * (D / 16 / DF_WARPS), a.d.n_seqs), dim3(32 * (DF_WARPS + 1)), 0, st, a);
-    // the whole head in a CTA, or, where that leaves SMs without one and the tokens' own work is little beside S_0, its
-    // rows in several (32 heads: 4 tokens 4.1 us in four parts, 4.6 whole; 64 tokens 31 and 18)
-    int warps = D / 16;
-    while (np <= 16 && warps > 2 && heads * (D / 16 / warps) < 152) warps >>= 1;
+    // a head of 128 in two CTAs while each finds an SM of its own (76 heads, 16 tokens: 5.2 us in two, 5.7 whole; 64 tokens:
+    // 16.1 and 18.0; 80 heads: 5.9 and 5.7, 19.2 and 18.0), else a CTA a head; in four parts it was never faster, a head of
+    // 64 not in two
+    const int warps = D == 128 && 2 * heads <= 152 ? 4 : D / 16;
     return launch_dependent(delta_tree_kernel<D, WIDE>, dim3(a.hv * (D / 16 / warps), a.d.n_seqs), dim3(32 * warps),
                             static_cast<size_t>(DeltaTreeSmem<D>(np, warps).end), st, a);
 }
