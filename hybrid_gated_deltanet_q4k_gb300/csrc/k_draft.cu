@@ -1069,9 +1069,10 @@ cudaError_t launch_delta_commit(const gdn_layer& L, const DraftTokens& d, const 
     a.c_conv = 2 * a.c_qk + L.n_v_heads * L.dv;
     const bool wide = on_32_bytes(state_in) && on_32_bytes(state_out);
     if (L.dk == 64) return wide ? commit_launch<64, 2, true>(a, st) : commit_launch<64, 2, false>(a, st);
-    // 32 rows of a head to a block where that fills the SMs, else 64 (one sequence of 32 heads: 3.2 us, 4.0 with 64; 64
-    // sequences: 61 us with 32 rows, 53 with 64, 68 with 128, which leaves an SM two blocks)
-    if (a.hv * d.n_seqs < 2 * 152) return wide ? commit_launch<128, 2, true>(a, st) : commit_launch<128, 2, false>(a, st);
+    // 32 rows of a head to a block while there are few heads, else 64 (paths of up to 32 tokens, us with 32 and with 64: 32
+    // heads 3.1 and 3.8, 160 5.8 and 6.4, 192 7.0 and 6.8, 224 8.6 and 7.9, 512 18.3 and 16.9, 2048 60 and 53; 128 rows leave
+    // an SM two blocks: 68)
+    if (a.hv * d.n_seqs < 192) return wide ? commit_launch<128, 2, true>(a, st) : commit_launch<128, 2, false>(a, st);
     return wide ? commit_launch<128, 4, true>(a, st) : commit_launch<128, 4, false>(a, st);
 }
 

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("lens,kind", [([5, 2, 8, 1, 3, 0, 4, 6, 7, 33], "tree"), ([64, 2, 8, 1, 3, 8, 4, 6, 0, 5], "chain")])
 def test_the_commit_of_a_batch(lens, kind):
-    """32 heads of 128 and ten sequences, 320 heads in all: from 304 on a block takes 64 rows.  The tolerance is that of
+    """32 heads of 128 and ten sequences, 320 heads in all: from 192 on a block takes 64 rows.  The tolerance is that of
     the commit's other tests: a step of 2^-23 of the sum of absolute values per token of the path, and four."""
     c = Case(16, 32, 128, lens, kind, seed=17, pad=1)
     rng = np.random.default_rng(4)
