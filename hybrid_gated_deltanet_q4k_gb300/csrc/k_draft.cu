@@ -82,8 +82,9 @@ constexpr int CT_SLOTS = CT_COLS / 8;      // threads of a token
 // that have them as a tap.  A thread has 8 channels, their weights in registers, of
 // every fourth token.  The last block of x computes the gates.  48 trees of 20 to
 // 64 tokens, 8192 channels: 33 us, 2.2 TB/s (35 in blocks of 512 channels, 44 with
-// 512 threads); with a warp walking a head's tokens from L1 it was 51.  What is left is latency (offsets, then rows, then the taps of
-// up to 16 tokens a thread): a third fewer instructions changed nothing.
+// 512 threads); with a warp walking a head's tokens from L1 it was 51.  What bounds it is this order of a block's work: all
+// copies, a wait for all of them, then up to 16 tokens a thread, so that loads and arithmetic do not overlap within a
+// block (DRAM 14 %, 0.39 instructions issued a cycle and scheduler); a third fewer instructions changed nothing.
 template <int D>
 __global__ void __launch_bounds__(CT_THREADS, 6) conv_tree_kernel(const __grid_constant__ ConvTreeArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];    // raw inputs [token][CT_COLS] bf16, the conv state [CT_COLS][3] fp32
@@ -622,8 +623,10 @@ struct DeltaTreeSmem {
 //
 // This kernel: a CTA for a head, or for part of its rows, of a sequence.  24 trees
 // of 24 to 64 tokens over 32 heads of 128: 60 us; S_0 alone could be read in 15.
-// A CTA's phases follow one another (S_0, the tokens' products, the blocks), with
-// two CTAs to an SM and 0.4 instructions issued a cycle and scheduler.
+// A CTA's phases follow one another (S_0, the tokens' products, the blocks in turn:
+// 16300 of 51000 cycles of 64 tokens are these), with two CTAs to an SM and 0.47
+// instructions issued a cycle and scheduler.  At the 128 registers that two CTAs
+// leave a thread, heads of 128 spill 16 bytes.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256, 2) delta_tree_kernel(const __grid_constant__ DeltaTreeArgs a) {
     constexpr int KB = D / 32;              // blocks of 32 columns

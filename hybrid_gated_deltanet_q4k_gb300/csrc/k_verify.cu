@@ -271,7 +271,9 @@ __device__ __forceinline__ bool vf_accepted(Pair c0, float u, Pair z, float q, f
 // of 150001 fp32 p and q takes some 2.5 us (the loads' latency, 22 instructions an
 // element, the sums and the barrier; 1.7 of them with a vocabulary of 1000), the
 // gathering before the first some 4.  One chain of 5: 9.4 us; 32 greedy chains of up
-// to 6 (128000 bf16): 14; 16 trees of 12 to 32: 30.  Decisions in fp64 had been 4 us more for the one chain.
+// to 6 (128000 bf16): 14; 16 trees of 12 to 32: 30.  Certain drafts (no q): the same
+// trees 20, 32 chains of 2 to 6 (128000 bf16) 9.5.  Decisions in fp64 had been 4 us
+// more for the one chain.
 template <class T>
 __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     namespace cg = cooperative_groups;
