@@ -214,8 +214,8 @@ def stream_on(device: int, stream=None) -> int:
 def entry(fn, device: int, stream):
     """fn for a call on ``stream``, with ``device`` as the current one meanwhile: a handle of a default stream stands for
     the current device's, and kernels are set up and launched there."""
-    if stream is None:                  # the current device's, or stream_on refuses the call
-        return fn
+    if stream is None or (_current_device is not None and _current_device() == device):
+        return fn                       # without a stream: the current device's, or stream_on refuses the call
     import torch
 
     def call(*args):
